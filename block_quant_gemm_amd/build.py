@@ -3,11 +3,17 @@
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = ["csrc/quant.hip", "csrc/gemm.hip", "csrc/api.hip"]
+SOURCES = ["csrc/quant.hip", "csrc/gemm.hip", "csrc/latent.hip", "csrc/attention.hip",
+           "csrc/api.hip"]
 LIB = os.path.join(PKG, "libmxq.so")
+# Loop-carried accumulators stay whole vectors: split into scalars, they are
+# copied between the two halves of the register file in every iteration.
+EXTRA_FLAGS = {s: ["-mllvm", "-amdgpu-codegenprepare-break-large-phis=0"]
+               for s in ("csrc/latent.hip", "csrc/attention.hip")}
 
 
 def source_digest():
@@ -32,22 +38,36 @@ def hipcc():
 def build(verbose=False):
     """Compile every source for gfx950 into block_quant_gemm_amd/libmxq.so."""
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           "-I" + os.path.join(ROOT, "include"),
-           # keep FP32 arithmetic off the packed-FP32 instructions
-           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-           "-o", tmp] + [os.path.join(PKG, s) for s in SOURCES]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    msgs = [l for l in (r.stderr or "").splitlines()
-            if "packed-fp32-ops' is not a recognized feature" not in l]
-    if r.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
-    if verbose and msgs:
-        print("\n".join(msgs), file=sys.stderr)
+    common = [hipcc(), "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+              "-I" + os.path.join(ROOT, "include"),
+              # keep FP32 arithmetic off the packed-FP32 instructions
+              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
+    with tempfile.TemporaryDirectory() as d:
+        objs = [os.path.join(d, os.path.basename(s) + ".o") for s in SOURCES]
+        cmds = [common + EXTRA_FLAGS.get(s, []) + ["-c", os.path.join(PKG, s), "-o", o]
+                for s, o in zip(SOURCES, objs)]
+        _run(cmds, verbose)
+        _run([[hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs], verbose)
     os.replace(tmp, LIB)
     return LIB
+
+
+def _run(cmds, verbose):
+    """Runs the commands at once; raises if one fails."""
+    procs = []
+    for c in cmds:
+        if verbose:
+            print(" ".join(c), flush=True)
+        procs.append(subprocess.Popen(c, stdout=subprocess.DEVNULL, stderr=subprocess.PIPE,
+                                      text=True))
+    errs = [p.communicate()[1] for p in procs]
+    for p, err in zip(procs, errs):
+        msgs = [l for l in (err or "").splitlines()
+                if "packed-fp32-ops' is not a recognized feature" not in l]
+        if p.returncode != 0:
+            raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
+        if verbose and msgs:
+            print("\n".join(msgs), file=sys.stderr)
 
 
 if __name__ == "__main__":

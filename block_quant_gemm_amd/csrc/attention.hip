@@ -1,0 +1,1082 @@
+// Expanded latent attention for gfx950: softmax attention over sequences packed
+// row by row, forward and backward, whose keys are a per-head part (128 columns)
+// beside a rotary part (64 columns) that all heads share.  BF16 operands on the
+// BF16 matrix instruction, FP32 sums and softmax statistics.
+//
+// With z = scale * (q . k) over the visible keys of a row:
+//   m = max z,  l = sum exp(z - m),  o = sum exp(z - m) v / l,  lse = m + ln l
+//   P = exp(z - lse),  dP = dO V^T,  D = rowsum(dO * o) = rowsum(P * dP)
+//   dS = P * (dP - D),  dQ = scale * dS K,  dK = scale * dS^T Q,  dV = P^T dO
+//
+// One shape serves the three kernels.  Each wavefront keeps the rows of its
+// own side in registers (queries in the forward and dQ kernels, keys in the
+// dK/dV kernel) and walks the other side in tiles of 64 rows that the whole
+// workgroup stages in LDS.  The logits are formed transposed, with the
+// wavefront's own row along the lanes, so a row's maximum and sum are a
+// reduction over registers and one exchange between the two lane halves, and
+// the probabilities are already in the operand layout of the second product:
+// the matrix instruction leaves lane (n, h) the rows 8a + 4h + b (a, b = 0..3)
+// of its column, and the second product's slab of 16 takes its elements in that
+// same order, with the staged tile read transposed (ds_read_b64_tr_b16) to match.
+// Probabilities and dS never pass through memory.
+
+#include "common.h"
+
+namespace mxq {
+
+namespace {
+
+constexpr int kNope = MXQ_NOPE_DIM, kRope = MXQ_ROPE_DIM, kVal = MXQ_VALUE_DIM;
+constexpr int kQk = kNope + kRope;              // 192
+constexpr int kSteps = kQk / 16, kVSteps = kVal / 16;   // 16-deep steps of the two products
+constexpr int kBN = 64;                         // rows of a staged tile
+constexpr int kThr = 256;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// The reference that a row's exponentials are taken against follows the
+// running maximum only when that is more than this many powers of two ahead:
+// any reference gives the same quotients, 2^8 times the largest loses no bits,
+// and the sums are then hardly ever rescaled.
+constexpr float kSlack = 8.0f;
+// The backward kernels form P and dS 2^24 times too large (a shift of the
+// exponent's argument) and scale the finished sums back, so that probabilities
+// far below a row's largest do not underflow FP32.
+constexpr float kShift = 24.0f, kUnshift = 1.0f / 16777216.0f;
+
+// One operand: rows of `ld` elements, heads `ldh` elements apart.
+struct Op {
+  const uint16_t* p;
+  int64_t ld, ldh;
+};
+struct OpOut {
+  uint16_t* p;
+  int64_t ld, ldh;
+};
+
+struct AttnArgs {
+  Op q, kn, v, o, dout;
+  const uint16_t* kr;
+  int64_t ldr;
+  const int64_t* offq;
+  const int64_t* offk;
+  int32_t B, H, causal;
+  int64_t Tq, Tk;
+  float scale;
+  OpOut out, dq, dkn, dv;
+  uint16_t* dkr;
+  int64_t lddr;
+  float* lse;
+  int64_t ldl;
+  float* delta;                                  // [H, Tq]
+  float* rope_part;                              // [H, Tk, 64]
+};
+
+// ---------------------------------------------------------------------------
+// Packed sequences.  Offsets are clamped into the rows that exist, so a
+// malformed table never leads outside the buffers.
+// ---------------------------------------------------------------------------
+
+struct SeqTile {
+  int64_t q0, k0;                                // the sequence's first rows
+  int lq, lk;                                    // and lengths
+  int row0;                                      // first row of this tile in the sequence
+  bool ok;
+};
+
+__device__ __forceinline__ int64_t clamp_off(int64_t o, int64_t n) { return o < 0 ? 0 : o > n ? n : o; }
+
+__device__ __forceinline__ int64_t bcast64(int64_t v, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)v >> 32), lane);
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// Tile t of the list of all sequences' tiles of `rows` rows (of the keys with
+// KEYS, of the queries without); a causal sequence's query tiles come last
+// first, the ones with the most keys.  Every wavefront works it out for itself.
+template <bool KEYS>
+__device__ __forceinline__ SeqTile find_tile(const AttnArgs& a, uint32_t t, int rows) {
+  SeqTile s{};
+  const int lane = threadIdx.x & 63;
+  uint32_t before = 0;
+  for (int32_t base = 0; base < a.B; base += 64) {
+    const int32_t b = base + lane;
+    int64_t q0 = 0, k0 = 0, lq = 0, lk = 0;
+    if (b < a.B) {
+      q0 = a.offq ? clamp_off(a.offq[b], a.Tq) : 0;
+      lq = (a.offq ? clamp_off(a.offq[b + 1], a.Tq) : a.Tq) - q0;
+      k0 = a.offk ? clamp_off(a.offk[b], a.Tk) : 0;
+      lk = (a.offk ? clamp_off(a.offk[b + 1], a.Tk) : a.Tk) - k0;
+      lq = lq < 0 ? 0 : lq;
+      lk = lk < 0 ? 0 : lk;
+    }
+    const uint32_t n = (uint32_t)(((KEYS ? lk : lq) + rows - 1) / rows);
+    uint32_t incl = n;
+#pragma unroll
+    for (int sh = 1; sh < 64; sh <<= 1) {
+      const uint32_t u = __shfl_up(incl, sh, 64);
+      if (lane >= sh) incl += u;
+    }
+    const uint64_t past = __ballot(t < before + incl);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      s.q0 = bcast64(q0, at);
+      s.k0 = bcast64(k0, at);
+      s.lq = (int)bcast64(lq, at);
+      s.lk = (int)bcast64(lk, at);
+      const uint32_t nn = (uint32_t)__builtin_amdgcn_readlane((int)n, at);
+      const uint32_t first = before + (uint32_t)__builtin_amdgcn_readlane((int)incl, at) - nn;
+      const uint32_t i = t - first;
+      s.row0 = (int)((!KEYS && a.causal ? nn - 1 - i : i) * (uint32_t)rows);
+      s.ok = true;
+      return s;
+    }
+    before += (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
+  }
+  return s;
+}
+
+// ---------------------------------------------------------------------------
+// Staged tiles: 64 rows of the other side as three sub-tiles, N (128 columns),
+// R (the 64 rotary columns) and Y (128 columns), copied from memory straight
+// into LDS.  The 16-byte units of a row are permuted by an XOR with a function
+// of the row, chosen for both ways the tiles are read: 16 rows at one unit (the
+// first products' operand) and 4 consecutive rows at 4 consecutive units (the
+// transposed reads) each cover the 16 units of a 256-byte bank line once.  Rows
+// past the end read as zeros through the descriptors' range check.
+// ---------------------------------------------------------------------------
+
+constexpr int kNB = kBN * 256, kRB = kBN * 128;  // bytes of N (and Y) and of R
+constexpr int kTile = 2 * kNB + kRB;             // 40 KB
+constexpr int kOffR = kNB, kOffY = kNB + kRB;
+
+__device__ __forceinline__ uint32_t f_wide(uint32_t r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
+__device__ __forceinline__ uint32_t f_rope(uint32_t r) {   // bits 1..3 of r, reversed
+  return ((r & 2) << 1) | ((r & 4) >> 1) | ((r & 8) >> 3);
+}
+
+__device__ __forceinline__ i32x4 uniform(i32x4 r) {
+  i32x4 u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u[i] = __builtin_amdgcn_readfirstlane(r[i]);
+  return u;
+}
+
+// 16 bytes a lane from descriptor offset `off + step` to LDS byte m0 + 16 lane.
+// Not tracked by the compiler: tile_wait() orders it.
+__device__ __forceinline__ void dma16(i32x4 r, uint32_t lds, uint32_t off, uint32_t step) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :: "s"(lds), "v"(off), "s"(r), "s"(step) : "memory");
+}
+
+// This lane's part of the copies.  Wavefront w copies the 1 KB pieces w, w + 4,
+// .. of each sub-tile (4 rows of N or Y, 8 rows of R), so a lane's unit is the
+// same in every piece and only the row advances.
+struct Copy {
+  uint32_t n, r, y;                              // offset in the first piece
+  uint32_t dn, dr, dy;                           // from piece to piece (uniform)
+  uint32_t ldn, ldr, ldy;                        // row strides in bytes
+  uint32_t lds;                                  // wavefront's LDS byte in a tile
+};
+
+__device__ __forceinline__ Copy copy_plan(const void* lds, int64_t ldn, int64_t ldr, int64_t ldy) {
+  Copy c;
+  const uint32_t l = threadIdx.x & 63;
+  const uint32_t w = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  c.ldn = (uint32_t)ldn * 2; c.ldr = (uint32_t)ldr * 2; c.ldy = (uint32_t)ldy * 2;
+  const uint32_t r4 = 4 * w + (l >> 4), r8 = 8 * w + (l >> 3);
+  const uint32_t uw = ((l & 15) ^ f_wide(r4)) * 16, ur = ((l & 7) ^ f_rope(r8)) * 16;
+  c.n = r4 * c.ldn + uw;
+  c.r = r8 * c.ldr + ur;
+  c.y = r4 * c.ldy + uw;
+  c.dn = 16 * c.ldn; c.dr = 32 * c.ldr; c.dy = 16 * c.ldy;
+  c.lds = (uint32_t)reinterpret_cast<uintptr_t>(lds) + w * 1024;
+  return c;
+}
+
+// Bytes of `rows` rows (0 at least, 64 at most) of `ld` bytes, the last one `width`.
+__device__ __forceinline__ uint32_t span(int rows, uint32_t ld, uint32_t width) {
+  const int r = rows > kBN ? kBN : rows;
+  return r > 0 ? (uint32_t)(r - 1) * ld + width : 0u;
+}
+
+// Starts the copy of rows row0 .. row0 + 63 of `rows` to tile buffer `buf`.
+__device__ __forceinline__ void tile_copy(const Copy& c, const uint16_t* n, const uint16_t* r,
+                                          const uint16_t* y, int row0, int rows, int buf) {
+  const uint8_t* pn = reinterpret_cast<const uint8_t*>(n) + (int64_t)row0 * c.ldn;
+  const uint8_t* pr = reinterpret_cast<const uint8_t*>(r) + (int64_t)row0 * c.ldr;
+  const uint8_t* py = reinterpret_cast<const uint8_t*>(y) + (int64_t)row0 * c.ldy;
+  const i32x4 dn = uniform(make_rsrc(pn, span(rows - row0, c.ldn, 256)));
+  const i32x4 dr = uniform(make_rsrc(pr, span(rows - row0, c.ldr, 128)));
+  const i32x4 dy = uniform(make_rsrc(py, span(rows - row0, c.ldy, 256)));
+  const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)(c.lds + buf * kTile));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dma16(dn, lds + i * 4096, c.n, i * c.dn);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) dma16(dr, lds + kOffR + i * 4096, c.r, i * c.dr);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dma16(dy, lds + kOffY + i * 4096, c.y, i * c.dy);
+}
+
+// Every copy this wavefront started has landed, and so, past the barrier, has
+// every other wavefront's; and all reads before it are done.
+__device__ __forceinline__ void tile_wait() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+}
+
+// Rows of the wavefront's own side as operands: lane (n, h) holds columns
+// 16 s + 8 h .. + 7 of row n for each step s, from step 8 on of `pr`; rows past
+// the end are zeros.
+template <int STEPS>
+__device__ __forceinline__ void own_rows(bf16x8 (&f)[STEPS], const uint16_t* p, int64_t ld,
+                                         const uint16_t* pr, int64_t ldr, int row, int rows) {
+  const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row < rows)
+      v = *reinterpret_cast<const uint4*>(s < 8 ? p + (int64_t)row * ld + s * 16 + h * 8
+                                                : pr + (int64_t)row * ldr + (s - 8) * 16 + h * 8);
+    f[s] = __builtin_bit_cast(bf16x8, v);
+  }
+}
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+// Where a lane reads in a tile.  Each step or column block only flips bits of
+// the unit, so one base a kind of read serves them all.
+struct Reads {
+  uint32_t n, r;                                 // first products: N or Y, and R
+  uint32_t tn, tr;                               // transposed: N or Y, and R
+};
+
+__device__ __forceinline__ Reads read_plan() {
+  const uint32_t l = threadIdx.x & 63, n = l & 31, h = l >> 5, g = l >> 4, i = l & 15;
+  Reads p;
+  p.n = n * 256 + ((h ^ f_wide(n)) << 4);
+  p.r = n * 128 + ((h ^ f_rope(n)) << 4);
+  // each 16 lanes read 4 rows of 16 columns and receive one column of 4 rows each
+  const uint32_t row = 4 * (g >> 1) + (i >> 2), u = 2 * (g & 1) + ((i & 3) >> 1);
+  p.tn = row * 256 + ((u ^ f_wide(row)) << 4) + (i & 1) * 8;
+  p.tr = row * 128 + ((u ^ f_rope(row)) << 4) + (i & 1) * 8;
+  return p;
+}
+
+// First products: rows 32 sub .. + 31 of a tile, columns 16 s .. + 15.
+__device__ __forceinline__ bf16x8 x_frag(const uint8_t* t, const Reads& p, int sub, int s) {
+  return s < 8 ? *reinterpret_cast<const bf16x8*>(t + (p.n ^ (s << 5)) + sub * 8192)
+               : *reinterpret_cast<const bf16x8*>(t + kOffR + (p.r ^ ((s - 8) << 5)) + sub * 4096);
+}
+__device__ __forceinline__ bf16x8 y_frag(const uint8_t* t, const Reads& p, int sub, int s) {
+  return *reinterpret_cast<const bf16x8*>(t + kOffY + (p.n ^ (s << 5)) + sub * 8192);
+}
+
+// Second products: columns 32 d .. + 31 of the tile's rows 16 j .. + 15,
+// transposed: lane (c, h) gets rows 16 j + 4 h + 0..3 and 16 j + 8 + 4 h + 0..3
+// of column 32 d + c.
+__device__ __forceinline__ bf16x8 tr_pair(const uint8_t* a, const uint8_t* b) {
+  const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)a);
+  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)b);
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+__device__ __forceinline__ bf16x8 x_tr(const uint8_t* t, const Reads& p, int j, int d) {
+  if (d < 4) {
+    const uint32_t o = p.tn ^ (d << 6);
+    return tr_pair(t + o + j * 4096, t + (o ^ 32) + 2048 + j * 4096);
+  }
+  const uint32_t o = p.tr ^ ((d - 4) << 6);
+  return tr_pair(t + kOffR + o + j * 2048, t + kOffR + (o ^ 16) + 1024 + j * 2048);
+}
+__device__ __forceinline__ bf16x8 y_tr(const uint8_t* t, const Reads& p, int j, int d) {
+  const uint32_t o = p.tn ^ (d << 6);
+  return tr_pair(t + kOffY + o + j * 4096, t + kOffY + (o ^ 32) + 2048 + j * 4096);
+}
+
+__device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// The tile row that register i of a 32-row block holds in lane half h.
+__device__ __forceinline__ int reg_row(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
+
+// 8 FP32 values rounded to BF16 (registers 8 j .. 8 j + 7 of a block: slab j).
+__device__ __forceinline__ bf16x8 slab(const f32x16& p, int j) {
+  uint4 w;
+  w.x = bf16x2_bits(p[8 * j], p[8 * j + 1]);
+  w.y = bf16x2_bits(p[8 * j + 2], p[8 * j + 3]);
+  w.z = bf16x2_bits(p[8 * j + 4], p[8 * j + 5]);
+  w.w = bf16x2_bits(p[8 * j + 6], p[8 * j + 7]);
+  return __builtin_bit_cast(bf16x8, w);
+}
+
+__device__ __forceinline__ float half_max(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]),
+                         __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
+// Transposed result blocks to memory: lane (n, h) holds columns reg_row(i, h)
+// of each 32-column block of its row, 4 consecutive ones a store.
+__device__ __forceinline__ void store_block(const f32x16& b, float mul, uint16_t* p) {
+  const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint2 w;
+    w.x = bf16x2_bits(b[4 * i] * mul, b[4 * i + 1] * mul);
+    w.y = bf16x2_bits(b[4 * i + 2] * mul, b[4 * i + 3] * mul);
+    *reinterpret_cast<uint2*>(p + 8 * i + 4 * h) = w;
+  }
+}
+
+template <int NT>
+__device__ __forceinline__ bool any_nonfinite(const f32x16 (&acc)[NT]) {
+  bool bad = false;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) bad |= !(__builtin_fabsf(acc[t][i]) < __builtin_inff());
+  return bad;
+}
+
+// ---------------------------------------------------------------------------
+// Rows redone by themselves.  A hidden key's probability is an exact 0, but the
+// matrix unit still multiplies it, and 0 * NaN or 0 * infinity would reach
+// rows that the mask keeps apart.  Such a product always leaves a NaN, so rows
+// whose result is not finite are computed again over their visible keys (or
+// queries) alone, one wavefront a row, before they are written.  Costs the plain
+// path one check of the results; a row with finite operands never comes here.
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float bf(const uint16_t* p) {
+  return __builtin_bit_cast(float, (uint32_t)*p << 16);
+}
+
+// Sum of x[i] * y[i] over n columns, by one lane.
+__device__ __forceinline__ float dot(const uint16_t* x, const uint16_t* y, int n) {
+  float s = 0.0f;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) s = __builtin_fmaf(bf(x + i), bf(y + i), s);
+  return s;
+}
+
+__device__ __forceinline__ float lane_of(float x, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) x = __builtin_fmaxf(x, __shfl_xor(x, s, 64));
+  return x;
+}
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) x += __shfl_xor(x, s, 64);
+  return x;
+}
+
+// A head's operands of one sequence.
+struct Head {
+  const uint16_t *q, *kn, *kr, *v, *o, *g;       // g: the output's gradient
+  const float *lse, *delta;
+};
+__device__ __forceinline__ Head head_of(const AttnArgs& a, const SeqTile& s, int head) {
+  Head x;
+  x.q = a.q.p + s.q0 * a.q.ld + head * a.q.ldh;
+  x.kn = a.kn.p + s.k0 * a.kn.ld + head * a.kn.ldh;
+  x.kr = a.kr + s.k0 * a.ldr;
+  x.v = a.v.p + s.k0 * a.v.ld + head * a.v.ldh;
+  x.o = a.o.p + s.q0 * a.o.ld + head * a.o.ldh;
+  x.g = a.dout.p + s.q0 * a.dout.ld + head * a.dout.ldh;
+  x.lse = a.lse + head * a.ldl + s.q0;
+  x.delta = a.delta + head * a.Tq + s.q0;
+  return x;
+}
+__device__ __forceinline__ float logit2(const AttnArgs& a, const Head& x, int i, int j) {
+  const uint16_t* q = x.q + (int64_t)i * a.q.ld;
+  return (dot(q, x.kn + (int64_t)j * a.kn.ld, kNope) + dot(q + kNope, x.kr + (int64_t)j * a.ldr, kRope)) *
+         (a.scale * kLog2e);
+}
+
+// Output row i of a head, over its `keys` first keys.
+__device__ __forceinline__ void redo_output(const AttnArgs& a, const SeqTile& s, int head, int i, int keys) {
+  const Head x = head_of(a, s, head);
+  const int l = threadIdx.x & 63;
+  float m = -__builtin_inff(), sum = 0.0f, o0 = 0.0f, o1 = 0.0f;
+#pragma unroll 1
+  for (int j0 = 0; j0 < keys; j0 += 64) {
+    const int n = keys - j0 < 64 ? keys - j0 : 64;
+    const float z = l < n ? logit2(a, x, i, j0 + l) : -__builtin_inff();
+    const float mn = __builtin_fmaxf(m, wave_max(z));
+    const float ref = mn == -__builtin_inff() ? 0.0f : mn;
+    const float alpha = __builtin_amdgcn_exp2f(m - ref);
+    const float p = l < n ? __builtin_amdgcn_exp2f(z - ref) : 0.0f;
+    m = mn;
+    sum = sum * alpha + wave_sum(p);
+    o0 *= alpha;
+    o1 *= alpha;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      const uint16_t* v = x.v + (int64_t)(j0 + j) * a.v.ld + 2 * l;
+      const float pj = lane_of(p, j);
+      o0 = __builtin_fmaf(pj, bf(v), o0);
+      o1 = __builtin_fmaf(pj, bf(v + 1), o1);
+    }
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  *reinterpret_cast<uint32_t*>(a.out.p + (s.q0 + i) * a.out.ld + head * a.out.ldh + 2 * l) =
+      bf16x2_bits(o0 * inv, o1 * inv);
+}
+
+// Query gradient row i of a head, over its `keys` first keys: lane l has
+// columns l, l + 64 and l + 128.
+__device__ __forceinline__ void redo_dq(const AttnArgs& a, const SeqTile& s, int head, int i, int keys) {
+  const Head x = head_of(a, s, head);
+  const int l = threadIdx.x & 63;
+  const float lse2 = x.lse[i] * kLog2e;
+  const uint16_t* gi = x.g + (int64_t)i * a.dout.ld;
+  float delta = 0.0f;
+#pragma unroll 1
+  for (int j = l; j < keys; j += 64)
+    delta = __builtin_fmaf(__builtin_amdgcn_exp2f(logit2(a, x, i, j) - lse2),
+                           dot(gi, x.v + (int64_t)j * a.v.ld, kVal), delta);
+  delta = wave_sum(delta);
+  float d0 = 0.0f, d1 = 0.0f, d2 = 0.0f;
+#pragma unroll 1
+  for (int j0 = 0; j0 < keys; j0 += 64) {
+    const int n = keys - j0 < 64 ? keys - j0 : 64;
+    float ds = 0.0f;
+    if (l < n)
+      ds = __builtin_amdgcn_exp2f(logit2(a, x, i, j0 + l) - lse2) *
+           (dot(gi, x.v + (int64_t)(j0 + l) * a.v.ld, kVal) - delta);
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      const float d = lane_of(ds, j);
+      const uint16_t* k = x.kn + (int64_t)(j0 + j) * a.kn.ld + l;
+      d0 = __builtin_fmaf(d, bf(k), d0);
+      d1 = __builtin_fmaf(d, bf(k + 64), d1);
+      d2 = __builtin_fmaf(d, bf(x.kr + (int64_t)(j0 + j) * a.ldr + l), d2);
+    }
+  }
+  uint16_t* p = a.dq.p + (s.q0 + i) * a.dq.ld + head * a.dq.ldh + l;
+  p[0] = (uint16_t)bf16x2_bits(d0 * a.scale, 0.0f);
+  p[64] = (uint16_t)bf16x2_bits(d1 * a.scale, 0.0f);
+  p[128] = (uint16_t)bf16x2_bits(d2 * a.scale, 0.0f);
+}
+
+// Gradients of key and value row j of a head, over the queries from `first` on.
+__device__ __forceinline__ void redo_dkv(const AttnArgs& a, const SeqTile& s, int head, int j, int first) {
+  const Head x = head_of(a, s, head);
+  const int l = threadIdx.x & 63;
+  const uint16_t* vj = x.v + (int64_t)j * a.v.ld;
+  float k0 = 0.0f, k1 = 0.0f, k2 = 0.0f, v0 = 0.0f, v1 = 0.0f;
+#pragma unroll 1
+  for (int i0 = first; i0 < s.lq; i0 += 64) {
+    const int n = s.lq - i0 < 64 ? s.lq - i0 : 64;
+    float p = 0.0f, ds = 0.0f;
+    if (l < n) {
+      const int i = i0 + l;
+      p = __builtin_amdgcn_exp2f(logit2(a, x, i, j) - x.lse[i] * kLog2e);
+      ds = p * (dot(x.g + (int64_t)i * a.dout.ld, vj, kVal) - x.delta[i]);
+    }
+#pragma unroll 1
+    for (int u = 0; u < n; ++u) {
+      const float pu = lane_of(p, u), du = lane_of(ds, u);
+      const uint16_t* q = x.q + (int64_t)(i0 + u) * a.q.ld + l;
+      const uint16_t* g = x.g + (int64_t)(i0 + u) * a.dout.ld + l;
+      k0 = __builtin_fmaf(du, bf(q), k0);
+      k1 = __builtin_fmaf(du, bf(q + 64), k1);
+      k2 = __builtin_fmaf(du, bf(q + 128), k2);
+      v0 = __builtin_fmaf(pu, bf(g), v0);
+      v1 = __builtin_fmaf(pu, bf(g + 64), v1);
+    }
+  }
+  const int64_t row = s.k0 + j;
+  uint16_t* dv = a.dv.p + row * a.dv.ld + head * a.dv.ldh + l;
+  uint16_t* dk = a.dkn.p + row * a.dkn.ld + head * a.dkn.ldh + l;
+  dv[0] = (uint16_t)bf16x2_bits(v0, 0.0f);
+  dv[64] = (uint16_t)bf16x2_bits(v1, 0.0f);
+  dk[0] = (uint16_t)bf16x2_bits(k0 * a.scale, 0.0f);
+  dk[64] = (uint16_t)bf16x2_bits(k1 * a.scale, 0.0f);
+  a.rope_part[(head * a.Tk + row) * kRope + l] = k2;
+}
+
+// Keys that query row i sees.
+__device__ __forceinline__ int keys_seen(const AttnArgs& a, const SeqTile& s, int i) {
+  if (!a.causal) return s.lk;
+  const int64_t e = (int64_t)i + s.lk - s.lq + 1;
+  return e < 0 ? 0 : e < s.lk ? (int)e : s.lk;
+}
+
+// ---------------------------------------------------------------------------
+// Forward.  A workgroup takes 128 QT query rows of one head, 32 QT a wavefront.
+// ---------------------------------------------------------------------------
+
+template <int QT>
+__global__ __launch_bounds__(kThr, QT == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTile];
+  constexpr int BM = 128 * QT;
+  const int head = blockIdx.x % a.H;
+  const SeqTile st = find_tile<false>(a, blockIdx.x / a.H, BM);
+  if (!st.ok) return;                              // uniform over the workgroup
+  const int l = threadIdx.x & 63, n = l & 31, h = l >> 5;
+  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wrow0 = st.row0 + w * 32 * QT;         // the wavefront's first row
+  const uint16_t* kn = a.kn.p + st.k0 * a.kn.ld + head * a.kn.ldh;
+  const uint16_t* kr = a.kr + st.k0 * a.ldr;
+  const uint16_t* v = a.v.p + st.k0 * a.v.ld + head * a.v.ldh;
+  const Copy cp = copy_plan(lds, a.kn.ld, a.ldr, a.v.ld);
+  const Reads rp = read_plan();
+
+  // keys that any row of the workgroup sees, and the wavefront's first and last row
+  const int last = (st.row0 + BM < st.lq ? st.row0 + BM : st.lq) - 1;
+  const int kend = keys_seen(a, st, last);
+  const int wfirst = keys_seen(a, st, wrow0), wlast = keys_seen(a, st, wrow0 + 32 * QT - 1);
+  if (kend > 0) tile_copy(cp, kn, kr, v, 0, st.lk, 0);
+
+  bf16x8 q[QT][kSteps];
+  int lim[QT];
+  const uint16_t* qp = a.q.p + st.q0 * a.q.ld + head * a.q.ldh;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    own_rows(q[t], qp, a.q.ld, qp + kNope, a.q.ld, wrow0 + 32 * t + n, st.lq);
+    lim[t] = keys_seen(a, st, wrow0 + 32 * t + n);
+  }
+  f32x16 o[QT][4] = {};
+  float m[QT], sum[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) m[t] = -__builtin_inff(), sum[t] = 0.0f;
+
+  const float c = a.scale * kLog2e;
+  int buf = 0;
+  for (int k0 = 0; k0 < kend; k0 += kBN, buf ^= 1) {
+    tile_wait();
+    if (k0 + kBN < kend) tile_copy(cp, kn, kr, v, k0 + kBN, st.lk, buf ^ 1);
+    if (k0 >= wlast) continue;                     // nothing seen by this wavefront
+    const uint8_t* tile = lds + buf * kTile;
+    f32x16 s[QT][2] = {};
+#pragma unroll
+    for (int kk = 0; kk < kSteps; ++kk) {
+      const bf16x8 k0f = x_frag(tile, rp, 0, kk), k1f = x_frag(tile, rp, 1, kk);
+#pragma unroll
+      for (int t = 0; t < QT; ++t) {
+        s[t][0] = mfma(k0f, q[t][kk], s[t][0]);
+        s[t][1] = mfma(k1f, q[t][kk], s[t][1]);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);             // keeps the phases' registers apart
+    if (k0 + kBN > wfirst) {                       // some row does not see all of the tile
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (k0 + 32 * b + reg_row(i, h) >= lim[t]) s[t][b][i] = -__builtin_inff();
+    }
+    bf16x8 p[QT][4];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      float mx = s[t][0][0];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        mx = __builtin_fmaxf(mx, s[t][0][i]);
+        mx = __builtin_fmaxf(mx, s[t][1][i]);
+      }
+      mx = half_max(mx) * c;
+      if (__builtin_expect(__ballot(mx > m[t] + kSlack) != 0, 0)) {
+        const float mn = __builtin_fmaxf(m[t], mx);
+        const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m[t] - mn);
+        m[t] = mn;
+        sum[t] *= alpha;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) o[t][d] *= alpha;
+      }
+      const float mc = m[t] == -__builtin_inff() ? 0.0f : m[t];   // nothing seen yet: all zeros
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][b][i], c, -mc));
+          s[t][b][i] = e;
+          sum[t] += e;
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[t][j] = slab(s[t][j >> 1], j & 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const bf16x8 vf = y_tr(tile, rp, j, d);
+#pragma unroll
+        for (int t = 0; t < QT; ++t) o[t][d] = mfma(vf, p[t][j], o[t][d]);
+      }
+  }
+  uint64_t redo[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    const int row = wrow0 + 32 * t + n;
+    const float total = half_sum(sum[t]);
+    // a row that sees nothing: zeros, and minus infinity
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    redo[t] = __ballot(any_nonfinite(o[t]) && row < st.lq);
+    if (row < st.lq) {
+      uint16_t* p = a.out.p + (st.q0 + row) * a.out.ld + head * a.out.ldh;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) store_block(o[t][d], inv, p + 32 * d);
+      if (h == 0)
+        a.lse[head * a.ldl + st.q0 + row] =
+            total == 0.0f ? -__builtin_inff() : kLn2 * (m[t] + __builtin_amdgcn_logf(total));
+    }
+  }
+  if (!a.causal) return;
+#pragma unroll 1
+  for (int t = 0; t < QT; ++t) {
+    uint32_t rows = (uint32_t)redo[t] | (uint32_t)(redo[t] >> 32);
+    while (rows) {
+      const int i = wrow0 + 32 * t + __builtin_ctz(rows);
+      rows &= rows - 1;
+      redo_output(a, st, head, i, keys_seen(a, st, i));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward, queries: dQ and D, which the keys' kernel reads.
+//
+// D is wanted before the loop that could sum it.  The BF16 output gives it but
+// for the output's rounding, d = rowsum(dO * o), and that is not good enough where
+// few keys hold a row's weight (dS is then a difference of nearly equal
+// numbers).  With dS' = P * (dP - d), the row sum r of dS' is D - d, and
+//   dQ = scale * (dS' K - r (P K)):
+// the products P K and dS' K share the reads of K, which bound this kernel.
+// ---------------------------------------------------------------------------
+
+template <int QT>
+__global__ __launch_bounds__(kThr, 1) void k_attn_dq(AttnArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTile];
+  constexpr int BM = 128 * QT;
+  const int head = blockIdx.x % a.H;
+  const SeqTile st = find_tile<false>(a, blockIdx.x / a.H, BM);
+  if (!st.ok) return;
+  const int l = threadIdx.x & 63, n = l & 31, h = l >> 5;
+  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wrow0 = st.row0 + w * 32 * QT;
+  const Head x = head_of(a, st, head);
+  const Copy cp = copy_plan(lds, a.kn.ld, a.ldr, a.v.ld);
+  const Reads rp = read_plan();
+  const int last = (st.row0 + BM < st.lq ? st.row0 + BM : st.lq) - 1;
+  const int kend = keys_seen(a, st, last);
+  const int wfirst = keys_seen(a, st, wrow0), wlast = keys_seen(a, st, wrow0 + 32 * QT - 1);
+  if (kend > 0) tile_copy(cp, x.kn, x.kr, x.v, 0, st.lk, 0);
+
+  bf16x8 q[QT][kSteps], g[QT][kVSteps];
+  float lse2[QT], delta[QT];                       // lse in powers of two; D
+  int lim[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    const int row = wrow0 + 32 * t + n;
+    lim[t] = keys_seen(a, st, row);
+    own_rows(q[t], x.q, a.q.ld, x.q + kNope, a.q.ld, row, st.lq);
+    own_rows(g[t], x.g, a.dout.ld, nullptr, 0, row, st.lq);
+    bf16x8 of[kVSteps];
+    own_rows(of, x.o, a.o.ld, nullptr, 0, row, st.lq);
+    float d = 0.0f;
+#pragma unroll
+    for (int s = 0; s < kVSteps; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d = __builtin_fmaf((float)of[s][e], (float)g[t][s][e], d);
+    delta[t] = half_sum(d);
+    float z = -__builtin_inff();
+    if (row < st.lq) z = x.lse[row];
+    lse2[t] = z == -__builtin_inff() ? __builtin_inff() : z * kLog2e - kShift;   // no keys: P = 0
+  }
+
+  f32x16 dq[QT][6] = {}, pk[QT][6] = {};
+  float rest[QT] = {};                             // row sums of dS'
+  const float c = a.scale * kLog2e;
+  int buf = 0;
+  for (int k0 = 0; k0 < kend; k0 += kBN, buf ^= 1) {
+    tile_wait();
+    if (k0 + kBN < kend) tile_copy(cp, x.kn, x.kr, x.v, k0 + kBN, st.lk, buf ^ 1);
+    if (k0 >= wlast) continue;
+    const uint8_t* tile = lds + buf * kTile;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      f32x16 s[QT] = {}, dp[QT] = {};
+#pragma unroll
+      for (int kk = 0; kk < kSteps; ++kk) {
+        const bf16x8 f = x_frag(tile, rp, b, kk);
+#pragma unroll
+        for (int t = 0; t < QT; ++t) s[t] = mfma(f, q[t][kk], s[t]);
+      }
+#pragma unroll
+      for (int kk = 0; kk < kVSteps; ++kk) {
+        const bf16x8 f = y_frag(tile, rp, b, kk);
+#pragma unroll
+        for (int t = 0; t < QT; ++t) dp[t] = mfma(f, g[t][kk], dp[t]);
+      }
+      __builtin_amdgcn_sched_barrier(0);           // keeps the phases' registers apart
+      bf16x8 pf[QT][2], ds[QT][2];
+#pragma unroll
+      for (int t = 0; t < QT; ++t) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], c, -lse2[t]));
+          s[t][i] = p;
+          dp[t][i] = p * (dp[t][i] - delta[t]);
+        }
+        if (k0 + kBN > wfirst) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (k0 + 32 * b + reg_row(i, h) >= lim[t]) s[t][i] = 0.0f, dp[t][i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) rest[t] += dp[t][i];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) pf[t][j] = slab(s[t], j), ds[t][j] = slab(dp[t], j);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int d = 0; d < 6; ++d) {
+          const bf16x8 f = x_tr(tile, rp, 2 * b + j, d);
+#pragma unroll
+          for (int t = 0; t < QT; ++t) {
+            dq[t][d] = mfma(f, ds[t][j], dq[t][d]);
+            pk[t][d] = mfma(f, pf[t][j], pk[t][d]);
+          }
+        }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    const int row = wrow0 + 32 * t + n;
+    const float r = half_sum(rest[t]) * kUnshift;
+#pragma unroll
+    for (int d = 0; d < 6; ++d) dq[t][d] -= pk[t][d] * r;
+    if (row < st.lq && h == 0) a.delta[head * a.Tq + st.q0 + row] = delta[t] + r;
+  }
+  uint64_t redo[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    const int row = wrow0 + 32 * t + n;
+    redo[t] = __ballot(any_nonfinite(dq[t]) && row < st.lq);
+    if (row < st.lq) {
+      uint16_t* p = a.dq.p + (st.q0 + row) * a.dq.ld + head * a.dq.ldh;
+#pragma unroll
+      for (int d = 0; d < 6; ++d) store_block(dq[t][d], a.scale * kUnshift, p + 32 * d);
+    }
+  }
+  if (!a.causal) return;
+#pragma unroll 1
+  for (int t = 0; t < QT; ++t) {
+    uint32_t rows = (uint32_t)redo[t] | (uint32_t)(redo[t] >> 32);
+    while (rows) {
+      const int i = wrow0 + 32 * t + __builtin_ctz(rows);
+      rows &= rows - 1;
+      redo_dq(a, st, head, i, keys_seen(a, st, i));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward, keys: dK, dV.  A workgroup takes 128 keys of one head, 32 a
+// wavefront, and walks the queries that see them.  The rotary part of dK is
+// summed over the heads by k_attn_drope, from one FP32 part a head, in head order.
+// ---------------------------------------------------------------------------
+
+__global__ __launch_bounds__(kThr, 1) void k_attn_dkv(AttnArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTile];
+  __shared__ __attribute__((aligned(16))) float stat[2][2][kBN];   // lse (powers of two), D
+  constexpr int BM = 128;
+  const int head = blockIdx.x % a.H;
+  const SeqTile st = find_tile<true>(a, blockIdx.x / a.H, BM);
+  if (!st.ok) return;
+  const int l = threadIdx.x & 63, n = l & 31, h = l >> 5;
+  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wkey = st.row0 + w * 32, row = wkey + n;   // the wavefront's keys, this lane's
+  const int diff = st.lk - st.lq;                  // query i sees keys j <= i + diff
+  const Head x = head_of(a, st, head);
+  const Copy cp = copy_plan(lds, a.q.ld, a.q.ld, a.dout.ld);
+  const Reads rp = read_plan();
+
+  // queries from lim on see this lane's key; the tile starts at the first that sees any
+  const int lim = !a.causal || row - diff < 0 ? 0 : row - diff;
+  int q0 = 0;
+  if (a.causal) {
+    const int f = st.row0 - diff;
+    q0 = f <= 0 ? 0 : f >= st.lq ? st.lq : f;
+    q0 = q0 / kBN * kBN;
+  }
+  const int wlim = !a.causal ? 0 : wkey - diff;    // first query that sees the wavefront's first key
+  // lse and D of a tile's queries, one value a lane of the first two wavefronts
+  auto stat_of = [&](int r0) {
+    const int i = r0 + l;
+    float z = 0.0f;
+    if (w < 2 && i < st.lq) z = w == 0 ? x.lse[i] : x.delta[i];
+    return z;
+  };
+  float z = 0.0f;
+  if (q0 < st.lq) {
+    z = stat_of(q0);
+    tile_copy(cp, x.q, x.q + kNope, x.g, q0, st.lq, 0);
+  }
+  bf16x8 k[kSteps], v[kVSteps];
+  own_rows(k, x.kn, a.kn.ld, x.kr, a.ldr, row, st.lk);
+  own_rows(v, x.v, a.v.ld, nullptr, 0, row, st.lk);
+
+  f32x16 dk[6] = {}, dv[4] = {};
+  const float c = a.scale * kLog2e;
+  int buf = 0;
+  for (; q0 < st.lq; q0 += kBN, buf ^= 1) {
+    if (w == 0)
+      stat[buf][0][l] = z == -__builtin_inff() ? __builtin_inff() : z * kLog2e - kShift;   // no keys: P = 0
+    else if (w == 1)
+      stat[buf][1][l] = z;
+    tile_wait();
+    if (q0 + kBN < st.lq) {
+      z = stat_of(q0 + kBN);
+      tile_copy(cp, x.q, x.q + kNope, x.g, q0 + kBN, st.lq, buf ^ 1);
+    }
+    if (q0 + kBN <= wlim) continue;                // no query here sees the wavefront's keys
+    const bool partial = q0 + kBN > st.lq || q0 < wlim + 31;
+    const uint8_t* tile = lds + buf * kTile;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      f32x16 s = {}, dp = {};
+#pragma unroll
+      for (int kk = 0; kk < kSteps; ++kk) s = mfma(x_frag(tile, rp, b, kk), k[kk], s);
+#pragma unroll
+      for (int kk = 0; kk < kVSteps; ++kk) dp = mfma(y_frag(tile, rp, b, kk), v[kk], dp);
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+        const int r4 = 32 * b + 8 * q4 + 4 * h;
+        const f32x4 ls = *reinterpret_cast<const f32x4*>(&stat[buf][0][r4]);
+        const f32x4 dl = *reinterpret_cast<const f32x4*>(&stat[buf][1][r4]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 4 * q4 + e;
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -ls[e]));
+          s[i] = p;
+          dp[i] = p * (dp[i] - dl[e]);
+        }
+      }
+      if (partial) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int qi = q0 + 32 * b + reg_row(i, h);
+          if (qi < lim || qi >= st.lq) s[i] = 0.0f, dp[i] = 0.0f;
+        }
+      }
+      const bf16x8 pf[2] = {slab(s, 0), slab(s, 1)}, df[2] = {slab(dp, 0), slab(dp, 1)};
+      __builtin_amdgcn_sched_barrier(0);           // keeps the phases' registers apart
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) dv[d] = mfma(y_tr(tile, rp, 2 * b + j, d), pf[j], dv[d]);
+#pragma unroll
+        for (int d = 0; d < 6; ++d) dk[d] = mfma(x_tr(tile, rp, 2 * b + j, d), df[j], dk[d]);
+      }
+    }
+  }
+  const uint64_t bad = __ballot((any_nonfinite(dk) || any_nonfinite(dv)) && row < st.lk);
+  if (row < st.lk) {
+    const int64_t kr = st.k0 + row;
+    uint16_t* pv = a.dv.p + kr * a.dv.ld + head * a.dv.ldh;
+    uint16_t* pk = a.dkn.p + kr * a.dkn.ld + head * a.dkn.ldh;
+    float* rp2 = a.rope_part + (head * a.Tk + kr) * kRope;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      store_block(dv[d], kUnshift, pv + 32 * d);
+      store_block(dk[d], a.scale * kUnshift, pk + 32 * d);
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x16 b = dk[4 + t] * kUnshift;
+        *reinterpret_cast<f32x4*>(rp2 + 32 * t + 8 * i + 4 * h) =
+            f32x4{b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]};
+      }
+  }
+  if (!a.causal) return;
+  uint32_t rows = (uint32_t)bad | (uint32_t)(bad >> 32);
+  while (rows) {
+    const int j = wkey + __builtin_ctz(rows);
+    rows &= rows - 1;
+    redo_dkv(a, st, head, j, j - diff < 0 ? 0 : j - diff);
+  }
+}
+
+// dk_rope[t] = scale * sum over heads, in head order, rounded once.  Four
+// columns a lane.  Rows outside every sequence get unspecified values.
+__global__ __launch_bounds__(kThr) void k_attn_drope(AttnArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * kThr + threadIdx.x;
+  const int64_t t = i / (kRope / 4);
+  const int c = (int)(i % (kRope / 4)) * 4;
+  if (t >= a.Tk) return;
+  const float* p = a.rope_part + t * kRope + c;
+  f32x4 s = {};
+  for (int h = 0; h < a.H; ++h) s += *reinterpret_cast<const f32x4*>(p + h * a.Tk * kRope);
+  uint2 w;
+  w.x = bf16x2_bits(s[0] * a.scale, s[1] * a.scale);
+  w.y = bf16x2_bits(s[2] * a.scale, s[3] * a.scale);
+  *reinterpret_cast<uint2*>(a.dkr + t * a.lddr + c) = w;
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+constexpr int64_t kMaxRows = INT64_C(1) << 30, kMaxStride = INT64_C(1) << 23;
+
+inline bool aligned16(const void* p) { return ((uintptr_t)p % 16) == 0; }
+inline int launch_status() { return hipGetLastError() == hipSuccess ? MXQ_OK : MXQ_ERR_HIP; }
+
+// Strides of a [rows, heads, cols] operand: 16-byte rows that do not overlap
+// in the last dimension.
+int check_op(const void* p, int64_t rows, int64_t ld, int64_t ldh, int cols) {
+  if (rows == 0) return MXQ_OK;                    // nothing is read or written
+  if (!p) return MXQ_ERR_NULL;
+  // a staged tile's 64 rows are addressed with 32-bit byte offsets
+  if (ld < cols || ldh < cols || ld > kMaxStride) return MXQ_ERR_SHAPE;
+  if (ld % 8 != 0 || ldh % 8 != 0 || !aligned16(p)) return MXQ_ERR_ALIGN;
+  return MXQ_OK;
+}
+
+#define MXQ_TRY(expr)                  \
+  do {                                 \
+    const int st_ = (expr);            \
+    if (st_ != MXQ_OK) return st_;     \
+  } while (0)
+
+int check_attn(const mxq_latent_attn* d, AttnArgs* a) {
+  if (!d) return MXQ_ERR_NULL;
+  if (d->H < 1 || d->H > 65536 || d->Tq < 0 || d->Tk < 0 || d->Tq > kMaxRows || d->Tk > kMaxRows)
+    return MXQ_ERR_SHAPE;
+  if (d->causal != 0 && d->causal != 1) return MXQ_ERR_ARG;
+  if (!(d->scale > 0.0f) || d->scale > 3.4e38f) return MXQ_ERR_ARG;
+  if ((d->offsets_q == nullptr) != (d->offsets_k == nullptr)) return MXQ_ERR_NULL;
+  if (d->offsets_q && (d->B < 1 || d->B > 65536)) return MXQ_ERR_SHAPE;
+  MXQ_TRY(check_op(d->q, d->Tq, d->ldq, d->ldq_head, kQk));
+  MXQ_TRY(check_op(d->k_nope, d->Tk, d->ldk, d->ldk_head, kNope));
+  MXQ_TRY(check_op(d->k_rope, d->Tk, d->ldr, kRope, kRope));
+  MXQ_TRY(check_op(d->v, d->Tk, d->ldv, d->ldv_head, kVal));
+  *a = AttnArgs{};
+  a->q = {d->q, d->ldq, d->ldq_head};
+  a->kn = {d->k_nope, d->ldk, d->ldk_head};
+  a->v = {d->v, d->ldv, d->ldv_head};
+  a->kr = d->k_rope;
+  a->ldr = d->ldr;
+  a->offq = d->offsets_q;
+  a->offk = d->offsets_k;
+  a->B = d->offsets_q ? d->B : 1;
+  a->H = d->H;
+  a->causal = d->causal;
+  a->Tq = d->Tq;
+  a->Tk = d->Tk;
+  a->scale = d->scale;
+  return MXQ_OK;
+}
+
+// Workgroups that hold every sequence's tiles of `rows` rows, for all heads.
+int grid_of(int64_t T, int64_t rows, const AttnArgs& a, uint32_t* n) {
+  const int64_t g = sat_mul(T / rows + a.B, a.H);
+  if (g > 0x7FFFFFFFLL) return MXQ_ERR_SHAPE;
+  *n = (uint32_t)g;
+  return MXQ_OK;
+}
+
+// 256-row query tiles halve the LDS reads of each product; 128-row tiles keep
+// more CUs busy when there are few rows.
+bool big_tiles(const AttnArgs&) { return false; }
+
+}  // namespace
+
+}  // namespace mxq
+
+using namespace mxq;
+
+extern "C" int latent_attention(const mxq_latent_attn* d, uint16_t* o, int64_t ldo,
+                                int64_t ldo_head, float* lse, int64_t ldl, hipStream_t stream) {
+  AttnArgs a;
+  MXQ_TRY(check_attn(d, &a));
+  MXQ_TRY(check_op(o, a.Tq, ldo, ldo_head, kVal));
+  if (a.Tq > 0 && !lse) return MXQ_ERR_NULL;
+  if (ldl < a.Tq) return MXQ_ERR_SHAPE;
+  if ((uintptr_t)lse % 4 != 0) return MXQ_ERR_ALIGN;
+  if (a.Tq == 0) return MXQ_OK;
+  a.out = {o, ldo, ldo_head};
+  a.lse = lse;
+  a.ldl = ldl;
+  uint32_t n;
+  const bool big = big_tiles(a);
+  MXQ_TRY(grid_of(a.Tq, big ? 256 : 128, a, &n));
+  if (big)
+    hipLaunchKernelGGL(k_attn_fwd<1>, dim3(n), dim3(kThr), 0, stream, a);
+  else
+    hipLaunchKernelGGL(k_attn_fwd<1>, dim3(n), dim3(kThr), 0, stream, a);
+  return launch_status();
+}
+
+extern "C" int latent_attention_backward(
+    const mxq_latent_attn* d, const uint16_t* o, int64_t ldo, int64_t ldo_head, const float* lse,
+    int64_t ldl, const uint16_t* dout, int64_t lddo, int64_t lddo_head, uint16_t* dq, int64_t lddq,
+    int64_t lddq_head, uint16_t* dk_nope, int64_t lddk, int64_t lddk_head, uint16_t* dk_rope,
+    int64_t lddr, uint16_t* dv, int64_t lddv, int64_t lddv_head, void* workspace,
+    size_t workspace_bytes, hipStream_t stream) {
+  AttnArgs a;
+  MXQ_TRY(check_attn(d, &a));
+  MXQ_TRY(check_op(o, a.Tq, ldo, ldo_head, kVal));
+  MXQ_TRY(check_op(dout, a.Tq, lddo, lddo_head, kVal));
+  MXQ_TRY(check_op(dq, a.Tq, lddq, lddq_head, kQk));
+  MXQ_TRY(check_op(dk_nope, a.Tk, lddk, lddk_head, kNope));
+  MXQ_TRY(check_op(dk_rope, a.Tk, lddr, kRope, kRope));
+  MXQ_TRY(check_op(dv, a.Tk, lddv, lddv_head, kVal));
+  if (a.Tq > 0 && !lse) return MXQ_ERR_NULL;
+  if (ldl < a.Tq) return MXQ_ERR_SHAPE;
+  if ((uintptr_t)lse % 4 != 0) return MXQ_ERR_ALIGN;
+  const size_t need = latent_backward_workspace(a.Tq, a.Tk, a.H);
+  if (workspace_bytes < need) return MXQ_ERR_WORKSPACE;
+  if (need > 0 && !workspace) return MXQ_ERR_NULL;
+  if (!aligned16(workspace)) return MXQ_ERR_ALIGN;
+  uint32_t nq, nk, nr;
+  const bool big = big_tiles(a);
+  MXQ_TRY(grid_of(a.Tq, big ? 256 : 128, a, &nq));
+  MXQ_TRY(grid_of(a.Tk, 128, a, &nk));
+  nr = (uint32_t)((a.Tk * (kRope / 4) + kThr - 1) / kThr);     // at most 2^26
+  a.o = {o, ldo, ldo_head};
+  a.dout = {dout, lddo, lddo_head};
+  a.lse = const_cast<float*>(lse);
+  a.ldl = ldl;
+  a.dq = {dq, lddq, lddq_head};
+  a.dkn = {dk_nope, lddk, lddk_head};
+  a.dv = {dv, lddv, lddv_head};
+  a.dkr = dk_rope;
+  a.lddr = lddr;
+  a.rope_part = static_cast<float*>(workspace);
+  a.delta = a.rope_part + a.H * a.Tk * kRope;
+  if (a.Tq > 0) {
+    if (big)
+      hipLaunchKernelGGL(k_attn_dq<1>, dim3(nq), dim3(kThr), 0, stream, a);
+    else
+      hipLaunchKernelGGL(k_attn_dq<1>, dim3(nq), dim3(kThr), 0, stream, a);
+    MXQ_TRY(launch_status());
+  }
+  if (a.Tk > 0) {
+    hipLaunchKernelGGL(k_attn_dkv, dim3(nk), dim3(kThr), 0, stream, a);
+    MXQ_TRY(launch_status());
+    hipLaunchKernelGGL(k_attn_drope, dim3(nr), dim3(kThr), 0, stream, a);
+    MXQ_TRY(launch_status());
+  }
+  return MXQ_OK;
+}

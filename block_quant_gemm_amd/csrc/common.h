@@ -20,6 +20,48 @@ inline int64_t sat_add(int64_t a, int64_t b) {
   return __builtin_add_overflow(a, b, &r) ? INT64_MAX : r;
 }
 
+// Tokens of a tile of the latent cache's absorbed attention.
+#define MXQ_LATENT_TILE 64
+
+// How mx_latent_decode splits its work: 16 R query rows a workgroup (R = 1 if
+// that holds a request's S * H rows, else 2 and as many row tiles), and along the batch's 64-token tiles runs of one length that stay
+// inside a request.  With `runs` runs' worth of tiles there are at most
+// runs + B runs: `grid` workgroups, two a CU where their registers allow it, and
+// a workspace of one part each (512 sums, a maximum and a total a row).
+// grid = 0: too large.
+struct LatentDecodePlan {
+  int R;
+  uint32_t row_tiles, runs, grid;
+  int64_t part_rows;
+  size_t bytes;
+};
+inline LatentDecodePlan latent_decode_plan(int64_t B, int64_t S, int64_t H, int64_t max_len) {
+  LatentDecodePlan p{};
+  if (B < 1 || S < 1 || H < 1 || max_len < 0 || sat_mul(S, H) > 65536) return p;
+  const int64_t rows = S * H;
+  p.R = rows <= 16 ? 1 : 2;
+  p.row_tiles = (uint32_t)((rows + 16 * p.R - 1) / (16 * p.R));
+  const int64_t tiles = sat_mul(B, max_len > 0 ? sat_add(max_len, MXQ_LATENT_TILE - 1) / MXQ_LATENT_TILE : 1);
+  if (tiles > 0x3FFFFFFFLL) return p;
+  int64_t want = (p.R == 1 ? 512 : 256) / (int64_t)p.row_tiles;
+  if (want < 2) want = 2;
+  const int64_t runs = want - B > want / 2 ? want - B : want / 2;
+  p.runs = (uint32_t)runs;
+  p.grid = (uint32_t)(runs + B < tiles ? runs + B : tiles);
+  p.part_rows = (int64_t)p.grid * p.row_tiles * 16 * p.R;
+  if (p.part_rows > (INT64_C(1) << 40)) return LatentDecodePlan{};
+  p.bytes = (size_t)p.part_rows * (MXQ_LATENT_DIM + 2) * sizeof(float);
+  return p;
+}
+
+// Workspace of latent_attention_backward: the rotary key's gradient of each
+// head, and D of each row, both FP32.  SIZE_MAX when it does not fit.
+inline size_t latent_backward_workspace(int64_t Tq, int64_t Tk, int64_t H) {
+  if (Tq < 0 || Tk < 0 || H < 1) return 0;
+  const int64_t words = sat_add(sat_mul(sat_mul(H, Tk), MXQ_ROPE_DIM), sat_mul(H, Tq));
+  return words > INT64_MAX / (int64_t)sizeof(float) ? SIZE_MAX : (size_t)words * sizeof(float);
+}
+
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -86,6 +128,59 @@ __device__ __forceinline__ uint32_t cvt2_e4m3_sat(float a, float b, uint32_t old
   a = __builtin_amdgcn_fmed3f(a, -448.0f, 448.0f);
   b = __builtin_amdgcn_fmed3f(b, -448.0f, 448.0f);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, (int)old, HI);
+}
+
+// One MX block of 32 BF16 values held by a DPP quad, 8 per lane: the E8M0
+// scale code from the block's largest magnitude (every lane of the quad gets
+// it) and the lane's 8 E4M3 codes.
+__device__ __forceinline__ void quant8(uint4 v, uint32_t& lo, uint32_t& hi, uint32_t& code) {
+  u16x2 m = __builtin_elementwise_max(absmax2(v.x, v.y), absmax2(v.z, v.w));
+  uint32_t am = m.x > m.y ? m.x : m.y;
+  uint32_t o = dpp_u32(am, kQuadXor1);
+  am = am > o ? am : o;
+  o = dpp_u32(am, kQuadXor2);
+  am = am > o ? am : o;
+  code = mx_scale_code(am);
+  if (code == 0xFFu) {                 // NaN or Inf in the block
+    lo = hi = 0x7F7F7F7Fu;
+    return;
+  }
+  float inv = mx_inv_scale(code);      // x * 2^-e is exact in FP32
+  lo = cvt2_e4m3_sat<false>(bf16_lo(v.x) * inv, bf16_hi(v.x) * inv, 0u);
+  lo = cvt2_e4m3_sat<true>(bf16_lo(v.y) * inv, bf16_hi(v.y) * inv, lo);
+  hi = cvt2_e4m3_sat<false>(bf16_lo(v.z) * inv, bf16_hi(v.z) * inv, 0u);
+  hi = cvt2_e4m3_sat<true>(bf16_lo(v.w) * inv, bf16_hi(v.w) * inv, hi);
+}
+
+// E8M0 code c as the FP32 scale operand of the scaled conversions, which
+// take its exponent field: 2^(c - 127); 0xFF (a NaN block) turns every
+// converted value into NaN.
+__device__ __forceinline__ float e8m0_f32(uint32_t c) { return __builtin_bit_cast(float, c << 23); }
+
+// Eight E4M3 codes (bytes of w0, then w1) times 2^(c - 127) as BF16, element
+// i from byte i.  Exact while the product is a normal or subnormal BF16
+// value with its bits intact: scale codes 3..246.
+__device__ __forceinline__ bf16x8 widen8_bf16(uint32_t w0, uint32_t w1, float s) {
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, false);
+  const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, true);
+  const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, false);
+  const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, true);
+  const bf16x4 lo = __builtin_shufflevector(p0, p1, 0, 1, 2, 3);
+  const bf16x4 hi = __builtin_shufflevector(p2, p3, 0, 1, 2, 3);
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Buffer descriptor for gfx9: 48-bit base, stride 0, num_records bytes (range
+// checked: loads at or past it read 0), data format word 0x00020000.
+__device__ __forceinline__ i32x4 make_rsrc(const void* p, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  i32x4 r;
+  r[0] = (int)(uint32_t)a;
+  r[1] = (int)((a >> 32) & 0xFFFFu);
+  r[2] = (int)bytes;
+  r[3] = 0x00020000;
+  return r;
 }
 
 }  // namespace mxq

@@ -67,18 +67,6 @@ __device__ __forceinline__ void static_for(F&& f) { static_for_range<0, N>(f); }
 
 enum GemmKind { kDense = 0, kVarM = 1, kVarK = 2 };
 
-// Buffer descriptor for gfx9: 48-bit base, stride 0, num_records bytes (range
-// checked: loads at or past it read 0), data format word 0x00020000.
-__device__ __forceinline__ i32x4 make_rsrc(const void* p, uint32_t bytes) {
-  const uint64_t a = reinterpret_cast<uint64_t>(p);
-  i32x4 r;
-  r[0] = (int)(uint32_t)a;
-  r[1] = (int)((a >> 32) & 0xFFFFu);
-  r[2] = (int)bytes;
-  r[3] = 0x00020000;
-  return r;
-}
-
 // Asynchronous loads straight into LDS (issued as inline assembly: the
 // compiler does not track them; the k loop's explicit vmcnt waits and
 // barriers order them; nothing else in these kernels uses m0).  16 bytes per
@@ -300,25 +288,6 @@ __device__ __forceinline__ uint32_t mx_block_f32(const float (&v)[32], uint32_t 
     out[d] = code == 0xFFu ? 0x7F7F7F7Fu : w;
   }
   return code;
-}
-
-// E8M0 code c as the FP32 scale operand of the scaled conversions, which
-// take its exponent field: 2^(c - 127); 0xFF (a NaN block) turns every
-// converted value into NaN.
-__device__ __forceinline__ float e8m0_f32(uint32_t c) { return __builtin_bit_cast(float, c << 23); }
-
-// Eight E4M3 codes (bytes of w0, then w1) times 2^(c - 127) as BF16, element
-// i from byte i.  Exact while the product is a normal or subnormal BF16
-// value with its bits intact: scale codes 3..246.
-__device__ __forceinline__ bf16x8 widen8_bf16(uint32_t w0, uint32_t w1, float s) {
-  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-  const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, false);
-  const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, true);
-  const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, false);
-  const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, true);
-  const bf16x4 lo = __builtin_shufflevector(p0, p1, 0, 1, 2, 3);
-  const bf16x4 hi = __builtin_shufflevector(p2, p3, 0, 1, 2, 3);
-  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 // The MFMA operand of tile row r for one k-step: 16-byte chunks c0 and c1.

@@ -1,0 +1,752 @@
+// The MX latent cache for gfx950: writing tokens into it, reading them back,
+// and the absorbed attention of decoding tokens that reads it.
+//
+// A slot keeps a token's latent vector c (512 values) as E4M3 codes with one
+// E8M0 scale per 32 values, and its rotary key (64 values) in BF16: 656 bytes
+// instead of 1152.  Absorbed attention multiplies the queries by the latent
+// vector itself, which is both key (with the rotary key beside it) and value:
+//   z[r, t] = scale * (q[r, :512] . c[t] + q[r, 512:] . k_rope[t])
+//   o[r]    = sum_t softmax(z[r])_t c[t]
+// so one read of a slot serves every head and every query token of a request.
+
+#include "common.h"
+
+namespace mxq {
+
+namespace {
+
+constexpr int kLat = MXQ_LATENT_DIM, kRope = MXQ_ROPE_DIM, kBlocks = kLat / 32;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kThr = 256;
+
+struct Cache {
+  uint8_t* codes;
+  uint8_t* scales;
+  uint16_t* rope;
+  int64_t ldc, lds, ldr, slots;
+};
+
+// ---------------------------------------------------------------------------
+// Write and read.  One wavefront a token: lane l holds latent values
+// 8 l .. 8 l + 7 (a DPP quad one block), lanes 0-7 also the rotary key's 16
+// bytes 16 l.  U tokens a wavefront are in flight at once.
+// ---------------------------------------------------------------------------
+
+template <int U>
+__global__ __launch_bounds__(kThr) void k_latent_write(const uint16_t* __restrict__ c, int64_t ldc,
+                                                       const uint16_t* __restrict__ k_rope,
+                                                       int64_t ldr,
+                                                       const int64_t* __restrict__ slots, int64_t T,
+                                                       Cache k) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t0 = ((int64_t)blockIdx.x * (kThr / 64) + (threadIdx.x >> 6)) * U;
+  uint4 v[U], r[U];
+  int64_t s[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t t = t0 + u;
+    s[u] = -1;
+    v[u] = r[u] = make_uint4(0, 0, 0, 0);
+    if (t < T) {
+      s[u] = slots[t];
+      v[u] = *reinterpret_cast<const uint4*>(c + t * ldc + lane * 8);
+      if (lane < 8) r[u] = *reinterpret_cast<const uint4*>(k_rope + t * ldr + lane * 8);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    uint32_t lo, hi, code;
+    quant8(v[u], lo, hi, code);
+    if (s[u] < 0 || s[u] >= k.slots) continue;
+    *reinterpret_cast<uint2*>(k.codes + s[u] * k.ldc + lane * 8) = make_uint2(lo, hi);
+    if ((lane & 3) == 0) k.scales[s[u] * k.lds + (lane >> 2)] = (uint8_t)code;
+    if (lane < 8) *reinterpret_cast<uint4*>(k.rope + s[u] * k.ldr + lane * 8) = r[u];
+  }
+}
+
+// Two codes of a dword (HI: bytes 2-3) times the scale 2^(e - 127), rounded to
+// BF16 once.  Formed in FP32, so that the smallest scales' values round instead
+// of losing bits in the conversion.
+template <bool HI>
+__device__ __forceinline__ uint32_t decode2(uint32_t w, float s) {
+  const f32x2 f = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, HI);
+  return bf16x2_bits(f[0] * s, f[1] * s);
+}
+
+// 2^(e - 127) as FP32: e = 0 is the subnormal 2^-127, e = 0xFF NaN.
+__device__ __forceinline__ float scale_f32(uint32_t e) {
+  return __builtin_bit_cast(float, e == 0u ? 0x00400000u : e == 0xFFu ? 0x7FC00000u : e << 23);
+}
+
+template <int U>
+__global__ __launch_bounds__(kThr) void k_latent_read(Cache k, const int64_t* __restrict__ slots,
+                                                      int64_t T, uint16_t* __restrict__ c,
+                                                      int64_t ldc, uint16_t* __restrict__ k_rope,
+                                                      int64_t ldr) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t0 = ((int64_t)blockIdx.x * (kThr / 64) + (threadIdx.x >> 6)) * U;
+  int64_t s[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) s[u] = t0 + u < T ? slots[t0 + u] : -1;
+  uint2 v[U];
+  uint4 r[U];
+  uint32_t e[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    v[u] = make_uint2(0, 0);
+    r[u] = make_uint4(0, 0, 0, 0);
+    e[u] = 127;
+    if (s[u] >= 0 && s[u] < k.slots) {
+      v[u] = *reinterpret_cast<const uint2*>(k.codes + s[u] * k.ldc + lane * 8);
+      e[u] = k.scales[s[u] * k.lds + (lane >> 2)];
+      if (lane < 8) r[u] = *reinterpret_cast<const uint4*>(k.rope + s[u] * k.ldr + lane * 8);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t t = t0 + u;
+    if (t >= T) continue;
+    const float f = scale_f32(e[u]);
+    uint4 w;
+    w.x = decode2<false>(v[u].x, f);
+    w.y = decode2<true>(v[u].x, f);
+    w.z = decode2<false>(v[u].y, f);
+    w.w = decode2<true>(v[u].y, f);
+    *reinterpret_cast<uint4*>(c + t * ldc + lane * 8) = w;
+    if (lane < 8) *reinterpret_cast<uint4*>(k_rope + t * ldr + lane * 8) = r[u];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Absorbed attention of decoding tokens.
+//
+// The rows of one request are its query tokens' heads (row s * H + h).  A
+// workgroup takes 16 R of them and a run of one request's 64-token tiles; all
+// runs are about equally long, so ragged lengths balance, and a request with
+// more than one leaves parts (FP32 sums, maximum and total) for
+// k_decode_merge.  A tile's codes are widened to BF16 once, into LDS, exactly
+// (the scale folded in), and serve all rows as keys and again, read
+// transposed, as values:
+//   logits  wavefront w takes tokens 16 w .. 16 w + 15 against all rows,
+//           queries in registers;
+//   values  wavefront w takes 128 latent columns for all rows and 64 tokens.
+// So each wavefront reads the tile once per product whatever R is.  Both
+// products leave the query row along the lanes, and a lane's probabilities go
+// to the same lane of the other wavefronts.
+// ---------------------------------------------------------------------------
+
+constexpr int kTok = MXQ_LATENT_TILE;            // tokens of a tile
+constexpr int kUnits = (kLat + kRope) / 8;       // 16-byte units of a widened row: 72
+constexpr int kRowB = kUnits * 16;               // 1152 bytes
+constexpr int kSteps = (kLat + kRope) / 32;      // 18 steps of 32 columns
+constexpr int kWaves = kThr / 64;
+constexpr int kCl = kTok * 32 / kThr, kRl = kTok * 8 / kThr;   // 8 code and 2 rotary loads a lane
+
+struct DecodeArgs {
+  const uint16_t* q;
+  int64_t ldq_seq, ldq_tok, ldq_head;
+  Cache k;
+  const int32_t* pages;
+  int64_t ldp;
+  int64_t npages;                                // pages in the pool
+  uint32_t page, page_mul, page_shift;           // t / page == t * page_mul >> page_shift
+  int32_t max_pages;                             // entries in a row of `pages`
+  const int64_t* lens;
+  int32_t B, S, H, rows;
+  int64_t max_len;
+  float scale;
+  uint32_t runs;                                 // runs to aim at
+  uint16_t* o;
+  int64_t ldo_seq, ldo_tok, ldo_head;
+  float* lse;                                    // [B, S, H]
+  float* part_o;                                 // [grid.x][row tiles][16 R][512]
+  float* part_ml;                                // [grid.x][row tiles][16 R][2]
+};
+
+// Units of a widened row go to slots so that a lane that widens 16 codes
+// (units 2 i, 2 i + 1) stores each half beside its neighbours' halves: unit
+// 2 i is slot i, unit 2 i + 1 slot 32 + i, the rotary key's units 64..71 stay.
+// The sum over columns takes any order, so queries are loaded in slot order;
+// results are stored back in unit order.
+__device__ __forceinline__ int slot_unit(int s) {
+  return s < 32 ? 2 * s : s < 64 ? 2 * (s - 32) + 1 : s;
+}
+// Slots of row r are permuted by an XOR: 16 rows at one slot, and 8 consecutive
+// rows at 2 consecutive slots (transposed reads), cover a 256-byte bank line once.
+__device__ __forceinline__ uint32_t fd(uint32_t r) { return (((r >> 1) & 3) << 1) | ((r >> 3) & 1); }
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// Maximum / sum over the four 16-lane groups.
+__device__ __forceinline__ float groups_max(float x) {
+  uint32_t u = __builtin_bit_cast(uint32_t, x);
+  auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  x = __builtin_fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+  u = __builtin_bit_cast(uint32_t, x);
+  r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+__device__ __forceinline__ float groups_sum(float x) {
+  uint32_t u = __builtin_bit_cast(uint32_t, x);
+  auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  x = __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+  u = __builtin_bit_cast(uint32_t, x);
+  r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
+// Tokens of sequence b, cut to max_len, and its tiles: at least one, so that
+// an empty sequence's rows are written too.
+__device__ __forceinline__ int seq_len(const DecodeArgs& a, int32_t b) {
+  const int64_t n = a.lens[b];
+  return (int)(n < 0 ? 0 : n > a.max_len ? a.max_len : n);
+}
+__device__ __forceinline__ uint32_t seq_tiles(int len) {
+  return len > 0 ? (uint32_t)((len + kTok - 1) / kTok) : 1u;
+}
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {   // inclusive
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int sh = 1; sh < 64; sh <<= 1) {
+    const uint32_t u = __shfl_up(x, sh, 64);
+    if (lane >= sh) x += u;
+  }
+  return x;
+}
+__device__ __forceinline__ uint32_t last_lane(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+
+// Tiles of a run: `runs` runs hold the whole batch's tiles (each sequence adds
+// at most one run that is shorter).
+__device__ __forceinline__ uint32_t run_tiles(const DecodeArgs& a) {
+  const int lane = threadIdx.x & 63;
+  uint32_t t = 0;
+  for (int32_t base = 0; base < a.B; base += 64)
+    t += last_lane(wave_scan(base + lane < a.B ? seq_tiles(seq_len(a, base + lane)) : 0u));
+  return (t + a.runs - 1) / a.runs;
+}
+// Runs of sequence base + lane (0 past the batch).
+__device__ __forceinline__ uint32_t seq_runs(const DecodeArgs& a, int32_t base, uint32_t per) {
+  const int32_t b = base + (int32_t)(threadIdx.x & 63);
+  return b < a.B ? (seq_tiles(seq_len(a, b)) + per - 1) / per : 0u;
+}
+
+// The slot of token t of a request with this page table, or -1: past the end,
+// or a page outside the pool.
+__device__ __forceinline__ int32_t slot_of(const DecodeArgs& a, const int32_t* pages, uint32_t t, int len) {
+  if (t >= (uint32_t)len) return -1;
+  const uint32_t p = (uint32_t)(((uint64_t)t * a.page_mul) >> a.page_shift);
+  if (p >= (uint32_t)a.max_pages) return -1;
+  const int32_t pg = pages[p];
+  if (pg < 0 || pg >= a.npages) return -1;
+  return (int32_t)((int64_t)pg * a.page + (t - p * a.page));
+}
+
+// One row's part over the tokens [t0, t1), by one wavefront and without the
+// matrix unit: hidden tokens are left out instead of multiplied by 0.  Lane l
+// returns columns 8 l .. 8 l + 7.  For rows whose plain result is not finite.
+__device__ __forceinline__ void redo_part(const DecodeArgs& a, int32_t b, int row, int len, int t0,
+                                          int t1, float (&o)[8], float& m, float& sum) {
+  const int l = threadIdx.x & 63;
+  const int sq = row / a.H, h = row - sq * a.H;
+  const uint16_t* q = a.q + (int64_t)b * a.ldq_seq + (int64_t)sq * a.ldq_tok + (int64_t)h * a.ldq_head;
+  const int32_t* pages = a.pages + (int64_t)b * a.ldp;
+  const float c = a.scale * kLog2e;
+  m = -__builtin_inff();
+  sum = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = 0.0f;
+#pragma unroll 1
+  for (int base = t0; base < t1; base += 64) {
+    const int n = t1 - base < 64 ? t1 - base : 64;
+    const int32_t s = l < n ? slot_of(a, pages, (uint32_t)(base + l), len) : -1;
+    float z = -__builtin_inff();
+    if (l < n) {
+      z = 0.0f;
+      if (s >= 0) {
+#pragma unroll 1
+        for (int i = 0; i < kLat; ++i) {
+          const float f = __builtin_amdgcn_cvt_f32_fp8((int)a.k.codes[s * a.k.ldc + i], 0) *
+                          scale_f32(a.k.scales[s * a.k.lds + i / 32]);
+          z = __builtin_fmaf(f, bf16_lo(q[i]), z);
+        }
+#pragma unroll 1
+        for (int i = 0; i < kRope; ++i)
+          z = __builtin_fmaf(bf16_lo(a.k.rope[s * a.k.ldr + i]), bf16_lo(q[kLat + i]), z);
+      }
+      z *= c;
+    }
+    float mx = z;
+#pragma unroll
+    for (int sh = 32; sh > 0; sh >>= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, sh, 64));
+    const float mn = __builtin_fmaxf(m, mx);
+    const float ref = mn == -__builtin_inff() ? 0.0f : mn;
+    const float alpha = __builtin_amdgcn_exp2f(m - ref);
+    const float p = l < n ? __builtin_amdgcn_exp2f(z - ref) : 0.0f;
+    m = mn;
+    float ps = p;
+#pragma unroll
+    for (int sh = 32; sh > 0; sh >>= 1) ps += __shfl_xor(ps, sh, 64);
+    sum = sum * alpha + ps;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= alpha;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      const int32_t sj = __builtin_amdgcn_readlane(s, j);
+      if (sj < 0) continue;
+      const float pj = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, p), j));
+      const float f = scale_f32(a.k.scales[sj * a.k.lds + l / 4]) * pj;
+      const uint2 w = *reinterpret_cast<const uint2*>(a.k.codes + sj * a.k.ldc + 8 * l);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        o[e] = __builtin_fmaf(__builtin_amdgcn_cvt_f32_fp8((int)((e < 4 ? w.x : w.y) >> (8 * (e & 3))), 0), f, o[e]);
+    }
+  }
+}
+
+// Four latent columns of a finished row.
+__device__ __forceinline__ uint2 bf16x4_bits(f32x4 v, float mul) {
+  return make_uint2(bf16x2_bits(v[0] * mul, v[1] * mul), bf16x2_bits(v[2] * mul, v[3] * mul));
+}
+
+template <int R>
+__global__ __launch_bounds__(kThr, R == 1 ? 2 : 1) void k_decode(DecodeArgs a) {
+  __shared__ __attribute__((aligned(256))) uint8_t tile[kTok * kRowB];
+  __shared__ __attribute__((aligned(16))) uint2 s_p[kWaves][R][64];
+  __shared__ float s_max[kWaves][R * 16];
+  __shared__ int32_t s_slot[2][kTok];
+  __shared__ uint32_t s_redo[R * 16];
+  const int tid = threadIdx.x, l = tid & 63, n = l & 15, g = l >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rt = blockIdx.y;
+
+  // the request and the run of its tiles that this workgroup takes
+  const uint32_t per = run_tiles(a);
+  int32_t b = -1;
+  uint32_t k = 0, nrun = 0;                        // run k of nrun
+  {
+    uint32_t before = 0;
+    for (int32_t base = 0; base < a.B; base += 64) {
+      const uint32_t own = seq_runs(a, base, per), incl = wave_scan(own);
+      const uint64_t past = __ballot(blockIdx.x < before + incl);
+      if (past) {
+        const int at = __builtin_ctzll(past);
+        b = base + at;
+        nrun = (uint32_t)__builtin_amdgcn_readlane((int)own, at);
+        k = blockIdx.x - before - (uint32_t)__builtin_amdgcn_readlane((int)(incl - own), at);
+        break;
+      }
+      before += last_lane(incl);
+    }
+  }
+  if (b < 0) return;                               // uniform over the workgroup
+  const int len = seq_len(a, b);
+  const uint32_t ntile = seq_tiles(len);
+  const uint32_t i0 = (uint32_t)((uint64_t)k * ntile / nrun);
+  const uint32_t i1 = (uint32_t)((uint64_t)(k + 1) * ntile / nrun);   // > i0: nrun <= ntile
+  const int32_t* pages = a.pages + (int64_t)b * a.ldp;
+
+  // where this lane writes and reads in the tile (bytes); what varies from
+  // step to step are constants and single bits
+  const uint32_t r0 = tid >> 5, ch = tid & 31;
+  const uint32_t wr = r0 * kRowB + ((ch ^ fd(r0)) << 4);
+  const uint32_t wrr = (tid >> 3) * kRowB + ((64 + ((tid & 7) ^ fd(tid >> 3))) << 4);
+  const uint32_t rk = (16 * w + n) * kRowB + ((g ^ fd(n)) << 4);
+  const uint32_t trow = 4 * g + (n >> 2);
+  const uint32_t rv = trow * kRowB + w * 256 + ((((n & 3) >> 1) ^ fd(trow)) << 4) + (n & 1) * 8;
+
+  auto put_slot = [&](uint32_t i) {                // slots of tile i, by the first wavefront
+    if (w == 0) s_slot[i & 1][l] = i < i1 ? slot_of(a, pages, i * kTok + l, len) : -1;
+  };
+  uint4 sc[kCl], sr[kRl];
+  uint32_t se[kCl];
+  auto load = [&](uint32_t i) {
+#pragma unroll
+    for (int j = 0; j < kCl; ++j) {
+      const int32_t s = s_slot[i & 1][j * 8 + r0];
+      sc[j] = make_uint4(0, 0, 0, 0);
+      se[j] = 127;
+      if (s >= 0) {
+        sc[j] = *reinterpret_cast<const uint4*>(a.k.codes + s * a.k.ldc + ch * 16);
+        se[j] = a.k.scales[s * a.k.lds + (ch >> 1)];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kRl; ++j) {
+      const int32_t s = s_slot[i & 1][j * 32 + (tid >> 3)];
+      sr[j] = make_uint4(0, 0, 0, 0);
+      if (s >= 0) sr[j] = *reinterpret_cast<const uint4*>(a.k.rope + s * a.k.ldr + (tid & 7) * 8);
+    }
+  };
+  put_slot(i0);
+  put_slot(i0 + 1);
+  if (tid < 16 * R) s_redo[tid] = 0;
+
+  // queries: lane (n, g) holds slot 4 kk + g of row n for each step kk
+  bf16x8 q[R][kSteps];
+  int lim[R];                                      // tokens below lim are seen by this lane's row
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int row = (rt * R + r) * 16 + n;
+    const int s = row / a.H, h = row - s * a.H;
+    const bool ok = row < a.rows;
+    lim[r] = ok ? len - (a.S - 1 - s) : 0;
+    const uint16_t* qp = a.q + (int64_t)b * a.ldq_seq + (int64_t)s * a.ldq_tok + (int64_t)h * a.ldq_head;
+#pragma unroll
+    for (int kk = 0; kk < kSteps; ++kk) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (ok) v = *reinterpret_cast<const uint4*>(qp + slot_unit(4 * kk + g) * 8);
+      q[r][kk] = __builtin_bit_cast(bf16x8, v);
+    }
+  }
+  f32x4 o[R][8] = {};
+  float m[R], sum[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) m[r] = -__builtin_inff(), sum[r] = 0.0f;
+  const float c = a.scale * kLog2e;
+  __syncthreads();
+  load(i0);
+  for (uint32_t i = i0; i < i1; ++i) {
+    __syncthreads();                               // the last tile is consumed
+#pragma unroll
+    for (int j = 0; j < kCl; ++j) {
+      const float f = e8m0_f32(se[j]);
+      uint8_t* p = tile + (wr ^ ((j & 1) << 4)) + j * (8 * kRowB);
+      *reinterpret_cast<bf16x8*>(p) = widen8_bf16(sc[j].x, sc[j].y, f);
+      *reinterpret_cast<bf16x8*>(p + 512) = widen8_bf16(sc[j].z, sc[j].w, f);
+    }
+#pragma unroll
+    for (int j = 0; j < kRl; ++j)
+      *reinterpret_cast<uint4*>(tile + wrr + j * (32 * kRowB)) = sr[j];
+    __syncthreads();
+    if (i + 1 < i1) load(i + 1);
+
+    f32x4 s[R] = {};
+#pragma unroll
+    for (int kk = 0; kk < kSteps; ++kk) {
+      const bf16x8 kf = *reinterpret_cast<const bf16x8*>(tile + (rk ^ ((kk & 1) << 6)) + (kk >> 1) * 128);
+#pragma unroll
+      for (int r = 0; r < R; ++r) s[r] = mfma16(kf, q[r][kk], s[r]);
+    }
+    const int tok0 = (int)(i * kTok) + 16 * w + 4 * g;   // this lane's 4 tokens
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (tok0 + e >= lim[r]) s[r][e] = -__builtin_inff();
+      const float mx = groups_max(__builtin_fmaxf(__builtin_fmaxf(s[r][0], s[r][1]),
+                                                  __builtin_fmaxf(s[r][2], s[r][3])));
+      if (g == 0) s_max[w][r * 16 + n] = mx;
+    }
+    __syncthreads();
+    put_slot(i + 2);                               // its loads are a whole tile away
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float mn = m[r];
+#pragma unroll
+      for (int x = 0; x < kWaves; ++x) mn = __builtin_fmaxf(mn, s_max[x][r * 16 + n] * c);
+      if (__ballot(mn != m[r])) {
+        const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mn);
+        m[r] = mn;
+        sum[r] *= alpha;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) o[r][d] *= alpha;
+      }
+      const float mc = mn == -__builtin_inff() ? 0.0f : mn;
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][e], c, -mc));
+        sum[r] += p[e];
+      }
+      s_p[w][r][l] = make_uint2(bf16x2_bits(p[0], p[1]), bf16x2_bits(p[2], p[3]));
+    }
+    __syncthreads();
+    // values: tokens 4 g + 0..3 of two wavefronts' 16 a step of 32
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      bf16x8 pf[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint2 x = s_p[2 * j][r][l], y = s_p[2 * j + 1][r][l];
+        pf[r] = __builtin_bit_cast(bf16x8, make_uint4(x.x, x.y, y.x, y.y));
+      }
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        const uint8_t* p = tile + (rv ^ ((d & 3) << 5)) + (d >> 2) * 128 + j * (32 * kRowB);
+        const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
+        const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 16 * kRowB));
+        const bf16x8 vf = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+        for (int r = 0; r < R; ++r) o[r][d] = mfma16(vf, pf[r], o[r][d]);
+      }
+    }
+  }
+
+  // totals of all wavefronts' tokens; rows to redo
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float x = groups_sum(sum[r]);
+    if (g == 0) s_max[w][r * 16 + n] = x;
+    // Query tokens that do not see a tile's last tokens still multiply them, by
+    // 0; a NaN or infinity there leaves a NaN, and the row is redone.
+    bool bad = false;
+#pragma unroll
+    for (int d = 0; d < 8; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) bad |= !(__builtin_fabsf(o[r][d][e]) < __builtin_inff());
+    if (bad && a.S > 1) s_redo[r * 16 + n] = 1;
+  }
+  __syncthreads();
+  const int64_t part = ((int64_t)blockIdx.x * gridDim.y + rt) * (16 * R);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float total = 0.0f;
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) total += s_max[x][r * 16 + n];
+    const int row = (rt * R + r) * 16 + n;
+    const bool mine = row < a.rows && s_redo[r * 16 + n] == 0;
+    if (nrun == 1) {
+      const int sq = row / a.H, h = row - sq * a.H;
+      uint16_t* op = a.o + (int64_t)b * a.ldo_seq + (int64_t)sq * a.ldo_tok + (int64_t)h * a.ldo_head;
+      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+      if (mine) {
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+          *reinterpret_cast<uint2*>(op + slot_unit(16 * w + 2 * d + (g >> 1)) * 8 + 4 * (g & 1)) =
+              bf16x4_bits(o[r][d], inv);
+      }
+      if (mine && w == 0 && g == 0)
+        a.lse[(int64_t)b * a.rows + row] =
+            total == 0.0f ? -__builtin_inff() : kLn2 * (m[r] + __builtin_amdgcn_logf(total));
+    } else {
+      const int64_t pr = part + r * 16 + n;
+      if (mine) {
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+          *reinterpret_cast<f32x4*>(a.part_o + pr * kLat + slot_unit(16 * w + 2 * d + (g >> 1)) * 8 +
+                                    4 * (g & 1)) = o[r][d];
+      }
+      if (mine && w == 0 && g == 0) {
+        a.part_ml[2 * pr] = m[r];
+        a.part_ml[2 * pr + 1] = total;
+      }
+    }
+  }
+  if (a.S == 1) return;
+#pragma unroll 1
+  for (int y = w; y < 16 * R; y += kWaves) {
+    if (s_redo[y] == 0) continue;                  // uniform over the wavefront
+    const int row = rt * R * 16 + y, sq = row / a.H, h = row - sq * a.H;
+    if (row >= a.rows) continue;
+    const int seen = len - (a.S - 1 - sq), end = (int)(i1 * kTok);
+    float v[8], mm, total;
+    redo_part(a, b, row, len, (int)(i0 * kTok), seen < end ? seen : end, v, mm, total);
+    if (nrun == 1) {
+      uint16_t* op = a.o + (int64_t)b * a.ldo_seq + (int64_t)sq * a.ldo_tok + (int64_t)h * a.ldo_head;
+      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+      for (int e = 0; e < 8; e += 4)
+        *reinterpret_cast<uint2*>(op + 8 * l + e) = bf16x4_bits(f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]}, inv);
+      if (l == 0)
+        a.lse[(int64_t)b * a.rows + row] =
+            total == 0.0f ? -__builtin_inff() : kLn2 * (mm + __builtin_amdgcn_logf(total));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a.part_o[(part + y) * kLat + 8 * l + e] = v[e];
+      if (l == 0) {
+        a.part_ml[2 * (part + y)] = mm;
+        a.part_ml[2 * (part + y) + 1] = total;
+      }
+    }
+  }
+}
+
+// Joins the parts of the requests that more than one workgroup worked on, in
+// their order: with M = max m, o = sum 2^(m - M) O / sum 2^(m - M) l.  One
+// workgroup a row, 128 lanes of 4 columns, 4 such groups taking every 4th part.
+__global__ __launch_bounds__(512) void k_decode_merge(DecodeArgs a, uint32_t nrt, int rows_per_tile) {
+  __shared__ __attribute__((aligned(16))) float s_o[3][kLat];
+  __shared__ float s_l[4];
+  const int32_t b = (int32_t)(blockIdx.x / (uint32_t)a.rows);
+  const int row = (int)(blockIdx.x % (uint32_t)a.rows);
+  const uint32_t per = run_tiles(a);
+  uint32_t g0 = 0, n = 0;                          // the request's first run, and runs
+  for (int32_t base = 0; base <= b; base += 64) {
+    const uint32_t own = seq_runs(a, base, per), incl = wave_scan(own);
+    if (b < base + 64) {
+      g0 += (uint32_t)__builtin_amdgcn_readlane((int)(incl - own), b - base);
+      n = (uint32_t)__builtin_amdgcn_readlane((int)own, b - base);
+    } else {
+      g0 += last_lane(incl);
+    }
+  }
+  if (n == 1) return;                              // written whole; uniform
+  const int rt = row / rows_per_tile, rr = row % rows_per_tile;
+  auto part_row = [&](uint32_t x) { return ((int64_t)(g0 + x) * nrt + rt) * rows_per_tile + rr; };
+  float mx = -__builtin_inff();
+  for (uint32_t x = threadIdx.x & 63; x < n; x += 64)
+    mx = __builtin_fmaxf(mx, a.part_ml[2 * part_row(x)]);
+#pragma unroll
+  for (int sh = 32; sh > 0; sh >>= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, sh, 64));
+  const float ref = mx == -__builtin_inff() ? 0.0f : mx;
+  const int grp = threadIdx.x >> 7, d = (threadIdx.x & 127) * 4;
+  f32x4 acc = {};
+  float lsum = 0.0f;
+#pragma unroll 4
+  for (uint32_t x = grp; x < n; x += 4) {
+    const int64_t pr = part_row(x);
+    const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * pr] - ref);
+    lsum = __builtin_fmaf(f, a.part_ml[2 * pr + 1], lsum);
+    const f32x4 v = *reinterpret_cast<const f32x4*>(a.part_o + pr * kLat + d);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(f, v[e], acc[e]);
+  }
+  if (grp > 0) *reinterpret_cast<f32x4*>(&s_o[grp - 1][d]) = acc;
+  if ((threadIdx.x & 127) == 0) s_l[grp] = lsum;
+  __syncthreads();
+  if (grp > 0) return;
+#pragma unroll
+  for (int y = 0; y < 3; ++y) acc += *reinterpret_cast<const f32x4*>(&s_o[y][d]);
+  const float total = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+  const int sq = row / a.H, h = row - sq * a.H;
+  uint16_t* op = a.o + (int64_t)b * a.ldo_seq + (int64_t)sq * a.ldo_tok + (int64_t)h * a.ldo_head;
+  *reinterpret_cast<uint2*>(op + d) = bf16x4_bits(acc, total == 0.0f ? 0.0f : 1.0f / total);
+  if (threadIdx.x == 0)
+    a.lse[(int64_t)b * a.rows + row] =
+        total == 0.0f ? -__builtin_inff() : kLn2 * (ref + __builtin_amdgcn_logf(total));
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+inline bool aligned16(const void* p) { return ((uintptr_t)p % 16) == 0; }
+inline int launch_status() { return hipGetLastError() == hipSuccess ? MXQ_OK : MXQ_ERR_HIP; }
+
+#define MXQ_TRY(expr)              \
+  do {                             \
+    const int st_ = (expr);        \
+    if (st_ != MXQ_OK) return st_; \
+  } while (0)
+
+int check_cache(const mxq_latent_cache* d, Cache* k) {
+  if (!d) return MXQ_ERR_NULL;
+  // slots are held in 32 bits; addresses in 64
+  if (d->slots < 0 || d->slots > 0x7FFFFFFFLL) return MXQ_ERR_SHAPE;
+  if (d->slots > 0 && (!d->codes || !d->scales || !d->k_rope)) return MXQ_ERR_NULL;
+  if (d->ld_codes < kLat || d->ld_scales < kBlocks || d->ld_rope < kRope) return MXQ_ERR_SHAPE;
+  if (d->ld_codes % 16 != 0 || d->ld_rope % 8 != 0 || !aligned16(d->codes) || !aligned16(d->k_rope))
+    return MXQ_ERR_ALIGN;
+  *k = {d->codes, d->scales, d->k_rope, d->ld_codes, d->ld_scales, d->ld_rope, d->slots};
+  return MXQ_OK;
+}
+
+int check_rows(const uint16_t* c, int64_t ldc, const uint16_t* r, int64_t ldr, const int64_t* slots,
+               int64_t T) {
+  if (T < 0 || T > 0x7FFFFFFFLL) return MXQ_ERR_SHAPE;
+  if (T == 0) return MXQ_OK;
+  if (!c || !r || !slots) return MXQ_ERR_NULL;
+  if (ldc < kLat || ldr < kRope) return MXQ_ERR_SHAPE;
+  if (ldc % 8 != 0 || ldr % 8 != 0 || !aligned16(c) || !aligned16(r) || (uintptr_t)slots % 8 != 0)
+    return MXQ_ERR_ALIGN;
+  return MXQ_OK;
+}
+
+}  // namespace
+
+}  // namespace mxq
+
+using namespace mxq;
+
+extern "C" int mx_latent_cache_write(const uint16_t* c, int64_t ldc, const uint16_t* k_rope,
+                                     int64_t ldr, const int64_t* slots, int64_t T,
+                                     const mxq_latent_cache* cache, hipStream_t stream) {
+  Cache k;
+  MXQ_TRY(check_cache(cache, &k));
+  MXQ_TRY(check_rows(c, ldc, k_rope, ldr, slots, T));
+  if (T == 0) return MXQ_OK;
+  hipLaunchKernelGGL(k_latent_write<1>, dim3((uint32_t)((T + 3) / 4)), dim3(kThr), 0, stream, c,
+                     ldc, k_rope, ldr, slots, T, k);
+  return launch_status();
+}
+
+extern "C" int mx_latent_cache_read(const mxq_latent_cache* cache, const int64_t* slots, int64_t T,
+                                    uint16_t* c, int64_t ldc, uint16_t* k_rope, int64_t ldr,
+                                    hipStream_t stream) {
+  Cache k;
+  MXQ_TRY(check_cache(cache, &k));
+  MXQ_TRY(check_rows(c, ldc, k_rope, ldr, slots, T));
+  if (T == 0) return MXQ_OK;
+  hipLaunchKernelGGL(k_latent_read<1>, dim3((uint32_t)((T + 3) / 4)), dim3(kThr), 0, stream, k,
+                     slots, T, c, ldc, k_rope, ldr);
+  return launch_status();
+}
+
+extern "C" int mx_latent_decode(const uint16_t* q, int64_t ldq_seq, int64_t ldq_tok,
+                                int64_t ldq_head, const mxq_latent_cache* cache,
+                                const int32_t* pages, int64_t ld_pages, int32_t max_pages,
+                                int32_t page_size, const int64_t* lens, int32_t B, int32_t S,
+                                int32_t H, int64_t max_len, float scale, uint16_t* o,
+                                int64_t ldo_seq, int64_t ldo_tok, int64_t ldo_head, float* lse,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  DecodeArgs a{};
+  MXQ_TRY(check_cache(cache, &a.k));
+  if (B < 0 || S < 1 || H < 1 || max_pages < 0 || page_size < 1 || max_len < 0) return MXQ_ERR_SHAPE;
+  if (sat_mul(S, H) > 65536 || sat_mul(B, sat_mul(S, H)) > 0x7FFFFFFFLL) return MXQ_ERR_SHAPE;
+  // tokens are counted in 32 bits, and every sequence's pages must be in the table
+  if (max_len > (INT64_C(1) << 30) || max_len > sat_mul(max_pages, page_size)) return MXQ_ERR_SHAPE;
+  if (!(scale > 0.0f) || scale > 3.4e38f) return MXQ_ERR_ARG;
+  if (B == 0) return MXQ_OK;
+  if (ldq_head < kLat + kRope || ldq_tok < kLat + kRope || ldq_seq < kLat + kRope ||
+      ldo_head < kLat || ldo_tok < kLat || ldo_seq < kLat || ld_pages < max_pages)
+    return MXQ_ERR_SHAPE;
+  if (!q || !lens || !o || !lse || (max_len > 0 && !pages)) return MXQ_ERR_NULL;
+  if (ldq_seq % 8 != 0 || ldq_tok % 8 != 0 || ldq_head % 8 != 0 || ldo_seq % 4 != 0 ||
+      ldo_tok % 4 != 0 || ldo_head % 4 != 0 || !aligned16(q) || (uintptr_t)o % 8 != 0 ||
+      (uintptr_t)lens % 8 != 0 || (uintptr_t)lse % 4 != 0 || (uintptr_t)pages % 4 != 0)
+    return MXQ_ERR_ALIGN;
+  const LatentDecodePlan p = latent_decode_plan(B, S, H, max_len);
+  if (p.grid == 0) return MXQ_ERR_SHAPE;
+  if (workspace_bytes < p.bytes) return MXQ_ERR_WORKSPACE;
+  if (!workspace) return MXQ_ERR_NULL;
+  if (!aligned16(workspace)) return MXQ_ERR_ALIGN;
+  a.q = q;
+  a.ldq_seq = ldq_seq; a.ldq_tok = ldq_tok; a.ldq_head = ldq_head;
+  a.pages = pages; a.ldp = ld_pages; a.npages = a.k.slots / page_size; a.max_pages = max_pages;
+  a.page = (uint32_t)page_size;
+  // t / page for t < 2^31: with 2^e >= page, ceil(2^(31 + e) / page) times t
+  // exceeds the exact quotient by less than 1 / page
+  uint32_t e = 0;
+  while ((UINT64_C(1) << e) < (uint64_t)page_size) ++e;
+  a.page_shift = 31 + e;
+  a.page_mul = (uint32_t)(((UINT64_C(1) << (31 + e)) + page_size - 1) / page_size);
+  a.lens = lens;
+  a.B = B; a.S = S; a.H = H; a.rows = S * H;
+  a.max_len = max_len;
+  a.scale = scale;
+  a.o = o;
+  a.ldo_seq = ldo_seq; a.ldo_tok = ldo_tok; a.ldo_head = ldo_head;
+  a.lse = lse;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = a.part_o + p.part_rows * kLat;
+  a.runs = p.runs;
+  const dim3 grid(p.grid, p.row_tiles);
+  if (p.R == 1)
+    hipLaunchKernelGGL(k_decode<1>, grid, dim3(kThr), 0, stream, a);
+  else
+    hipLaunchKernelGGL(k_decode<2>, grid, dim3(kThr), 0, stream, a);
+  MXQ_TRY(launch_status());
+  if (p.grid > 1) {
+    const dim3 rows((uint32_t)((int64_t)B * a.rows));
+    hipLaunchKernelGGL(k_decode_merge, rows, dim3(512), 0, stream, a, p.row_tiles, 16 * p.R);
+  }
+  return launch_status();
+}

@@ -48,25 +48,6 @@ __device__ __forceinline__ void store_stream(void* p, uint2 v) {
   __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(p));
 }
 
-__device__ __forceinline__ void quant8(uint4 v, uint32_t& lo, uint32_t& hi, uint32_t& code) {
-  u16x2 m = __builtin_elementwise_max(absmax2(v.x, v.y), absmax2(v.z, v.w));
-  uint32_t am = m.x > m.y ? m.x : m.y;
-  uint32_t o = dpp_u32(am, kQuadXor1);
-  am = am > o ? am : o;
-  o = dpp_u32(am, kQuadXor2);
-  am = am > o ? am : o;
-  code = mx_scale_code(am);
-  if (code == 0xFFu) {                 // NaN or Inf in the block
-    lo = hi = 0x7F7F7F7Fu;
-    return;
-  }
-  float inv = mx_inv_scale(code);      // x * 2^-e is exact in FP32
-  lo = cvt2_e4m3_sat<false>(bf16_lo(v.x) * inv, bf16_hi(v.x) * inv, 0u);
-  lo = cvt2_e4m3_sat<true>(bf16_lo(v.y) * inv, bf16_hi(v.y) * inv, lo);
-  hi = cvt2_e4m3_sat<false>(bf16_lo(v.z) * inv, bf16_hi(v.z) * inv, 0u);
-  hi = cvt2_e4m3_sat<true>(bf16_lo(v.w) * inv, bf16_hi(v.w) * inv, hi);
-}
-
 // Up to kRowBatch matrices in one launch: item i owns the global segment
 // groups [first, first + ceil(total / kRowUnroll) * kRowUnroll), so a group of
 // kRowUnroll consecutive segments never straddles two items.
@@ -1076,13 +1057,15 @@ extern "C" int mx_quantize_dual_batch(const mxq_dual_item* items, int32_t n,
   return launch_colwise<true, false>(b, stream);
 }
 
-extern "C" size_t mxq_workspace_size(int op, int64_t n, int64_t a1, int64_t, int64_t) {
+extern "C" size_t mxq_workspace_size(int op, int64_t n, int64_t a1, int64_t a2, int64_t a3) {
   if (op == MXQ_WS_PER_TENSOR) return n > 0 ? kPtBlocks * sizeof(uint32_t) : 0;
   if (op == MXQ_WS_PER_GROUP && n >= 0 && a1 > 0) {   // n = rows, a1 = groups
     const int64_t words = sat_add(n, a1);
     return words > INT64_MAX / (int64_t)sizeof(uint32_t) ? SIZE_MAX
                                                           : (size_t)words * sizeof(uint32_t);
   }
+  if (op == MXQ_WS_LATENT_DECODE) return latent_decode_plan(n, a1, a2, a3).bytes;
+  if (op == MXQ_WS_LATENT_BACKWARD) return latent_backward_workspace(n, a1, a2);
   return 0;
 }
 

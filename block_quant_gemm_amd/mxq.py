@@ -1,6 +1,7 @@
 """ctypes binding of libmxq.so.
 
-Argument marshalling only: every function below checks nothing itself,
+Argument marshalling only: every function below checks nothing itself (the
+latent-attention calls, which take many related tensors, check their shapes),
 allocates its outputs with torch (device memory is the caller's), passes raw
 device pointers and the current HIP stream to the C function of the same
 name, and raises if the library returns an error.  All arithmetic happens in
@@ -17,11 +18,13 @@ LIB_PATH = os.path.join(_HERE, "libmxq.so")
 
 OUT_BF16, OUT_FP32 = 0, 1
 ACC_MFMA_FP8, ACC_FP32 = 0, 1
-WS_PER_TENSOR, WS_PER_GROUP = 0, 1
+WS_PER_TENSOR, WS_PER_GROUP, WS_LATENT_DECODE, WS_LATENT_BACKWARD = 0, 1, 2, 3
 
 _i64, _i32, _p, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
+_f32 = ctypes.c_float
 ROWWISE_BATCH_MAX = 4
 DUAL_BATCH_MAX = 4
+LATENT_DIM, ROPE_DIM, NOPE_DIM, VALUE_DIM = 512, 64, 128, 128
 
 
 class RowwiseItem(ctypes.Structure):
@@ -36,6 +39,20 @@ class DualItem(ctypes.Structure):
                 ("E", _i32), ("q", _p), ("ldq", _i64), ("scale", _p), ("lds", _i64),
                 ("qT", _p), ("ldqT", _i64), ("M_cap", _i64), ("scaleT", _p), ("ldsT", _i64),
                 ("offsets_padded", _p)]
+
+
+class LatentCacheArg(ctypes.Structure):
+    """mxq_latent_cache of mxq.h."""
+    _fields_ = [("codes", _p), ("ld_codes", _i64), ("scales", _p), ("ld_scales", _i64),
+                ("k_rope", _p), ("ld_rope", _i64), ("slots", _i64)]
+
+
+class LatentAttnArg(ctypes.Structure):
+    """mxq_latent_attn of mxq.h."""
+    _fields_ = [("q", _p), ("ldq", _i64), ("ldq_head", _i64), ("k_nope", _p), ("ldk", _i64),
+                ("ldk_head", _i64), ("k_rope", _p), ("ldr", _i64), ("v", _p), ("ldv", _i64),
+                ("ldv_head", _i64), ("offsets_q", _p), ("offsets_k", _p), ("Tq", _i64),
+                ("Tk", _i64), ("B", _i32), ("H", _i32), ("scale", _f32), ("causal", _i32)]
 
 
 _SIGS = {
@@ -93,6 +110,18 @@ _SIGS = {
     "mx_grouped_gemm_wgrad": (ctypes.c_int, [_p, _p, _i64, _i64, _p, _p, _i64, _i64, _p,
                                              _i32, _i64, _i64, _p, _i64, ctypes.c_int,
                                              ctypes.c_int, _p]),
+    "mx_latent_cache_write": (ctypes.c_int, [_p, _i64, _p, _i64, _p, _i64,
+                                             ctypes.POINTER(LatentCacheArg), _p]),
+    "mx_latent_cache_read": (ctypes.c_int, [ctypes.POINTER(LatentCacheArg), _p, _i64, _p, _i64,
+                                            _p, _i64, _p]),
+    "mx_latent_decode": (ctypes.c_int, [_p, _i64, _i64, _i64, ctypes.POINTER(LatentCacheArg), _p,
+                                        _i64, _i32, _i32, _p, _i32, _i32, _i32, _i64, _f32, _p,
+                                        _i64, _i64, _i64, _p, _p, _sz, _p]),
+    "latent_attention": (ctypes.c_int, [ctypes.POINTER(LatentAttnArg), _p, _i64, _i64, _p, _i64,
+                                        _p]),
+    "latent_attention_backward": (ctypes.c_int, [ctypes.POINTER(LatentAttnArg), _p, _i64, _i64, _p,
+                                                 _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64,
+                                                 _i64, _p, _i64, _p, _i64, _i64, _p, _sz, _p]),
     "mxq_workspace_size": (_sz, [ctypes.c_int, _i64, _i64, _i64, _i64]),
     "mxq_validate_offsets": (ctypes.c_int, [_p, _i32, _i64, _p]),
 }
@@ -675,6 +704,193 @@ def mx_grouped_gemm_wgrad(at, at_scale, bt, bt_scale, offsets_padded, out_dtype=
                                         _ptr(offsets_padded), E, N, K, _ptr(c),
                                         c.stride(1), out_dtype, accum, _stream()))
     return c
+
+
+# ---------------------------------------------------------------------------
+# latent attention
+# ---------------------------------------------------------------------------
+
+def _shaped(name, t, dtype, *shape):
+    """Raises unless t has this dtype, this shape (None: any size) and adjacent
+    values along its last dimension: the C calls take addresses and strides
+    and cannot see a tensor that is too small."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1 and t.numel():
+        raise ValueError(f"{name}: the last dimension has to be contiguous")
+    return t
+
+
+def latent_cache(slots, device="cuda"):
+    """An empty MX latent cache of `slots` slots: (codes uint8 [slots, 512],
+    scales uint8 [slots, 16], k_rope BF16 [slots, 64]), all zeros."""
+    return (torch.zeros((slots, LATENT_DIM), dtype=torch.uint8, device=device),
+            torch.zeros((slots, LATENT_DIM // 32), dtype=torch.uint8, device=device),
+            torch.zeros((slots, ROPE_DIM), dtype=torch.bfloat16, device=device))
+
+
+def _cache_arg(cache):
+    codes, scales, k_rope = cache
+    n = codes.shape[0]
+    _shaped("cache codes", codes, torch.uint8, n, LATENT_DIM)
+    _shaped("cache scales", scales, torch.uint8, n, LATENT_DIM // 32)
+    _shaped("cache k_rope", k_rope, torch.bfloat16, n, ROPE_DIM)
+    return LatentCacheArg(codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0),
+                          k_rope.data_ptr(), k_rope.stride(0), n)
+
+
+def mx_latent_cache_write(c, k_rope, slots, cache):
+    """Quantizes T tokens into the cache: slot slots[t] (int64, device; outside
+    the cache: skipped) gets c[t] (BF16 [T, 512]) as MX codes and scales, and
+    k_rope[t] (BF16 [T, 64]).  Returns the cache."""
+    T = c.shape[0]
+    _shaped("c", c, torch.bfloat16, T, LATENT_DIM)
+    _shaped("k_rope", k_rope, torch.bfloat16, T, ROPE_DIM)
+    _shaped("slots", slots, torch.int64, T)
+    _check(load().mx_latent_cache_write(c.data_ptr(), c.stride(0), k_rope.data_ptr(),
+                                        k_rope.stride(0), slots.data_ptr(), T, _cache_arg(cache),
+                                        _stream()))
+    return cache
+
+
+def mx_latent_cache_read(cache, slots, c=None, k_rope=None):
+    """The tokens in the slots `slots` (int64 [T], device; outside the cache:
+    zeros).  Returns (c BF16 [T, 512], k_rope BF16 [T, 64])."""
+    T = slots.shape[0]
+    _shaped("slots", slots, torch.int64, T)
+    if c is None:
+        c = torch.empty((T, LATENT_DIM), dtype=torch.bfloat16, device=slots.device)
+    if k_rope is None:
+        k_rope = torch.empty((T, ROPE_DIM), dtype=torch.bfloat16, device=slots.device)
+    _shaped("c", c, torch.bfloat16, T, LATENT_DIM)
+    _shaped("k_rope", k_rope, torch.bfloat16, T, ROPE_DIM)
+    _check(load().mx_latent_cache_read(_cache_arg(cache), slots.data_ptr(), T, c.data_ptr(),
+                                       c.stride(0), k_rope.data_ptr(), k_rope.stride(0),
+                                       _stream()))
+    return c, k_rope
+
+
+def mx_latent_decode(q, cache, pages, lens, page_size, max_len, scale, o=None, lse=None,
+                     workspace=None):
+    """Absorbed attention of S decoding tokens a request over the MX latent cache.
+
+    q BF16 [B, S, H, 576]; pages int32 [B, max_pages] (token t of request b is
+    in slot pages[b, t // page_size] * page_size + t % page_size); lens int64
+    [B] cached tokens, the S query tokens among them (the last); max_len: host
+    bound of lens.  Returns (o BF16 [B, S, H, 512], lse float32 [B, S, H])."""
+    B, S, H, _ = q.shape
+    _shaped("q", q, torch.bfloat16, B, S, H, LATENT_DIM + ROPE_DIM)
+    _shaped("pages", pages, torch.int32, B, None)
+    _shaped("lens", lens, torch.int64, B)
+    if o is None:
+        o = torch.empty((B, S, H, LATENT_DIM), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, S, H), dtype=torch.float32, device=q.device)
+    _shaped("o", o, torch.bfloat16, B, S, H, LATENT_DIM)
+    _shaped("lse", lse, torch.float32, B, S, H)
+    if not lse.is_contiguous():
+        raise ValueError("lse: has to be contiguous")
+    lib = load()
+    if workspace is None:
+        workspace = torch.empty(lib.mxq_workspace_size(WS_LATENT_DECODE, B, S, H, max_len),
+                                dtype=torch.uint8, device=q.device)
+    _check(lib.mx_latent_decode(
+        q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), _cache_arg(cache), pages.data_ptr(),
+        pages.stride(0), pages.shape[1], page_size, lens.data_ptr(), B, S, H, max_len, scale,
+        o.data_ptr(), o.stride(0), o.stride(1), o.stride(2), lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _stream()))
+    return o, lse
+
+
+def _attn_arg(q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal):
+    Tq, H, _ = q.shape
+    Tk = k_nope.shape[0]
+    _shaped("q", q, torch.bfloat16, Tq, H, NOPE_DIM + ROPE_DIM)
+    _shaped("k_nope", k_nope, torch.bfloat16, Tk, H, NOPE_DIM)
+    _shaped("k_rope", k_rope, torch.bfloat16, Tk, ROPE_DIM)
+    _shaped("v", v, torch.bfloat16, Tk, H, VALUE_DIM)
+    B = 0
+    if offsets_k is None:
+        offsets_k = offsets_q
+    if offsets_q is not None:
+        B = offsets_q.numel() - 1
+        _shaped("offsets_q", offsets_q, torch.int64, B + 1)
+    if offsets_k is not None:
+        _shaped("offsets_k", offsets_k, torch.int64, B + 1)
+    return LatentAttnArg(
+        q.data_ptr(), q.stride(0), q.stride(1), k_nope.data_ptr(), k_nope.stride(0),
+        k_nope.stride(1), k_rope.data_ptr(), k_rope.stride(0), v.data_ptr(), v.stride(0),
+        v.stride(1), None if offsets_q is None else offsets_q.data_ptr(),
+        None if offsets_k is None else offsets_k.data_ptr(), Tq, Tk, B, H, scale, int(causal))
+
+
+def latent_attention(q, k_nope, k_rope, v, offsets_q=None, offsets_k=None, scale=None, causal=True,
+                     o=None, lse=None):
+    """Expanded latent attention over packed sequences.
+
+    q BF16 [Tq, H, 192] (128 columns for k_nope, then 64 for k_rope); k_nope
+    and v BF16 [Tk, H, 128], any row and head strides (e.g. the halves of one
+    [Tk, H, 256] projection); k_rope BF16 [Tk, 64], shared by the heads;
+    offsets_q, offsets_k int64 [B+1] on the device (offsets_k defaults to
+    offsets_q; both None: one sequence); scale defaults to 192 ** -0.5.
+    Returns (o BF16 [Tq, H, 128], lse float32 [H, Tq])."""
+    if scale is None:
+        scale = (NOPE_DIM + ROPE_DIM) ** -0.5
+    Tq, H, _ = q.shape
+    arg = _attn_arg(q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal)
+    if o is None:
+        o = torch.empty((Tq, H, VALUE_DIM), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
+    _shaped("o", o, torch.bfloat16, Tq, H, VALUE_DIM)
+    _shaped("lse", lse, torch.float32, H, Tq)
+    _check(load().latent_attention(arg, o.data_ptr(), o.stride(0), o.stride(1), lse.data_ptr(),
+                                   lse.stride(0), _stream()))
+    return o, lse
+
+
+def latent_attention_backward(dout, q, k_nope, k_rope, v, o, lse, offsets_q=None, offsets_k=None,
+                              scale=None, causal=True, dq=None, dk_nope=None, dk_rope=None, dv=None,
+                              workspace=None):
+    """Gradients of latent_attention from that of its output (BF16 [Tq, H, 128]).
+
+    The other arguments are the forward call's and its results o and lse.
+    Returns (dq, dk_nope, dk_rope, dv), shaped as their operands; dk_nope and dv
+    are the halves of one [Tk, H, 256] buffer unless they are given."""
+    if scale is None:
+        scale = (NOPE_DIM + ROPE_DIM) ** -0.5
+    Tq, H, _ = q.shape
+    Tk = k_nope.shape[0]
+    arg = _attn_arg(q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal)
+    _shaped("dout", dout, torch.bfloat16, Tq, H, VALUE_DIM)
+    _shaped("o", o, torch.bfloat16, Tq, H, VALUE_DIM)
+    _shaped("lse", lse, torch.float32, H, Tq)
+    dev = q.device
+    if dq is None:
+        dq = torch.empty((Tq, H, NOPE_DIM + ROPE_DIM), dtype=torch.bfloat16, device=dev)
+    if dk_nope is None or dv is None:
+        dkv = torch.empty((Tk, H, NOPE_DIM + VALUE_DIM), dtype=torch.bfloat16, device=dev)
+        dk_nope = dkv[..., :NOPE_DIM] if dk_nope is None else dk_nope
+        dv = dkv[..., NOPE_DIM:] if dv is None else dv
+    if dk_rope is None:
+        dk_rope = torch.empty((Tk, ROPE_DIM), dtype=torch.bfloat16, device=dev)
+    _shaped("dq", dq, torch.bfloat16, Tq, H, NOPE_DIM + ROPE_DIM)
+    _shaped("dk_nope", dk_nope, torch.bfloat16, Tk, H, NOPE_DIM)
+    _shaped("dk_rope", dk_rope, torch.bfloat16, Tk, ROPE_DIM)
+    _shaped("dv", dv, torch.bfloat16, Tk, H, VALUE_DIM)
+    lib = load()
+    if workspace is None:
+        workspace = torch.empty(lib.mxq_workspace_size(WS_LATENT_BACKWARD, Tq, Tk, H, 0),
+                                dtype=torch.uint8, device=dev)
+    _check(lib.latent_attention_backward(
+        arg, o.data_ptr(), o.stride(0), o.stride(1), lse.data_ptr(), lse.stride(0),
+        dout.data_ptr(), dout.stride(0), dout.stride(1), dq.data_ptr(), dq.stride(0), dq.stride(1),
+        dk_nope.data_ptr(), dk_nope.stride(0), dk_nope.stride(1), dk_rope.data_ptr(),
+        dk_rope.stride(0), dv.data_ptr(), dv.stride(0), dv.stride(1), workspace.data_ptr(),
+        workspace.numel(), _stream()))
+    return dq, dk_nope, dk_rope, dv
 
 
 def validate_offsets(offsets, M):

@@ -609,12 +609,213 @@ MXQ_API int fp8_grouped_gemm_wgrad_per_group(const uint8_t* at, const float* a_s
                                      hipStream_t stream);
 
 /* ------------------------------------------------------------------------ *
+ * Latent attention                                                          *
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Attention whose keys and values come from one latent vector a token, with
+ * the dimensions of the MLA projections: a latent vector of 512 values and a
+ * rotary key of 64 (the 2048 -> 576 projection), and per head 128 key columns
+ * beside the rotary key, and 128 value columns.
+ *
+ * Two forms.  Expanded (training, prefill): every head has its own keys and
+ * values, products of the latent vector; latent_attention and its gradient.
+ * Absorbed (decoding): the heads' key projection has been multiplied into the
+ * queries, which then meet the latent vector itself; mx_latent_decode, on a
+ * cache that holds the latent vectors as MX blocks.
+ */
+#define MXQ_LATENT_DIM 512
+#define MXQ_ROPE_DIM 64
+#define MXQ_NOPE_DIM 128
+#define MXQ_VALUE_DIM 128
+
+/*
+ * The MX latent cache: `slots` slots of one token each, in three arrays.  A
+ * slot's 512 latent values are E4M3 codes with one E8M0 scale per 32 (the MX
+ * rule above, row-wise); its rotary key stays in BF16.  Which slot holds which
+ * token is the caller's: pages of page_size consecutive slots, page p being
+ * slots [p * page_size, (p + 1) * page_size).
+ *   codes     : device, E4M3 [slots, 512], row stride ld_codes bytes (% 16 == 0),
+ *               16-byte aligned.
+ *   scales    : device, E8M0 [slots, 16], row stride ld_scales bytes.
+ *   k_rope    : device, BF16 [slots, 64], row stride ld_rope elements
+ *               (% 8 == 0), 16-byte aligned.
+ *   slots     : at most 2^31 - 1.
+ */
+typedef struct mxq_latent_cache {
+  uint8_t* codes;
+  int64_t ld_codes;
+  uint8_t* scales;
+  int64_t ld_scales;
+  uint16_t* k_rope;
+  int64_t ld_rope;
+  int64_t slots;
+} mxq_latent_cache;
+
+/*
+ * Quantizes T tokens into the cache: slot slots[t] receives exactly the codes
+ * and scales that mx_quantize_rowwise gives c's row t, and k_rope's row t.
+ *   c      : device, BF16 [T, 512], row stride ldc elements (% 8 == 0), 16-byte
+ *            aligned.
+ *   k_rope : device, BF16 [T, 64], row stride ldr elements (% 8 == 0), 16-byte
+ *            aligned.  Both may be column ranges of one [T, 576] projection.
+ *   slots  : device int64 [T].  A slot outside [0, cache->slots) is not written
+ *            (-1 for padding tokens).  A slot named twice holds one of the two
+ *            tokens' values, possibly a mixture.
+ *   cache  : host struct, read during the call only.
+ * Other slots keep their contents.  T == 0 is a no-op.
+ */
+MXQ_API int mx_latent_cache_write(const uint16_t* c, int64_t ldc, const uint16_t* k_rope,
+                          int64_t ldr, const int64_t* slots, int64_t T,
+                          const mxq_latent_cache* cache, hipStream_t stream);
+
+/*
+ * Reads T slots back: row t of c receives code * 2^(scale - 127) of slot
+ * slots[t], rounded to BF16 to nearest even (exact unless the product is
+ * below BF16's normal range), NaN for a block whose scale is 0xFF, and row t of
+ * k_rope its rotary key.  A slot outside [0, cache->slots) reads as zeros.
+ *   c, k_rope : device, BF16 [T, 512] and [T, 64], strides and alignment as for
+ *               mx_latent_cache_write.
+ *   slots     : device int64 [T].
+ * T == 0 is a no-op.
+ */
+MXQ_API int mx_latent_cache_read(const mxq_latent_cache* cache, const int64_t* slots, int64_t T,
+                         uint16_t* c, int64_t ldc, uint16_t* k_rope, int64_t ldr,
+                         hipStream_t stream);
+
+/*
+ * Absorbed attention of decoding tokens over the MX latent cache.  For request
+ * b with n = min(lens[b], max_len) cached tokens, query token s of S and head h:
+ *   z[t] = scale * (q[b,s,h,:512] . c[t] + q[b,s,h,512:] . k_rope[t])
+ *   o[b,s,h,:] = sum_t softmax(z)_t c[t],   lse[b,s,h] = ln sum_t exp(z[t])
+ * over the tokens t < n - (S - 1 - s): the S query tokens are the request's
+ * last S tokens, already in the cache, and each sees itself and what precedes
+ * it.  A row that sees nothing gets zeros and minus infinity.
+ * c[t] is the cached block's value, widened exactly; the products are exact,
+ * sums, maxima and totals are FP32, and the probabilities are rounded to BF16 for
+ * the second product.  Results do not depend on timing (no atomics).
+ *   q          : device, BF16 [B, S, H, 576], strides ldq_seq, ldq_tok,
+ *                ldq_head elements (each >= 576, % 8 == 0), 16-byte aligned.
+ *   pages      : device int32 [B, max_pages], row stride ld_pages: token t of
+ *                request b is in slot pages[b][t / page_size] * page_size +
+ *                t % page_size.  Entries past the request's tokens are not read.
+ *                A page outside the pool gives that row unspecified values but
+ *                never an access outside the cache.
+ *   page_size  : >= 1, any number.
+ *   lens       : device int64 [B].
+ *   max_len    : host bound of the lengths, <= max_pages * page_size and 2^30;
+ *                it sets the split of the work, longer requests are cut to it.
+ *   scale      : > 0, finite.
+ *   o          : device, BF16 [B, S, H, 512], strides ldo_* elements (each
+ *                >= 512, % 4 == 0), 8-byte aligned.
+ *   lse        : device float [B, S, H], contiguous.
+ *   workspace  : device scratch of at least mxq_workspace_size(
+ *                MXQ_WS_LATENT_DECODE, B, S, H, max_len) bytes, 16-byte aligned.
+ * S * H <= 65536.  B == 0 is a no-op.
+ */
+MXQ_API int mx_latent_decode(const uint16_t* q, int64_t ldq_seq, int64_t ldq_tok, int64_t ldq_head,
+                     const mxq_latent_cache* cache, const int32_t* pages, int64_t ld_pages,
+                     int32_t max_pages, int32_t page_size, const int64_t* lens, int32_t B,
+                     int32_t S, int32_t H, int64_t max_len, float scale, uint16_t* o,
+                     int64_t ldo_seq, int64_t ldo_tok, int64_t ldo_head, float* lse,
+                     void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The operands of expanded latent attention over B sequences packed row by row.
+ *   q       : device, BF16 [Tq, H, 192]: 128 columns that meet k_nope, then 64
+ *             that meet k_rope; row stride ldq, head stride ldq_head elements.
+ *   k_nope  : device, BF16 [Tk, H, 128] (ldk, ldk_head).
+ *   k_rope  : device, BF16 [Tk, 64] (ldr), shared by all heads.
+ *   v       : device, BF16 [Tk, H, 128] (ldv, ldv_head).  k_nope and v may be
+ *             the two halves of one [Tk, H, 256] projection.
+ *   offsets_q, offsets_k : device int64 [B+1]: sequence b has query rows
+ *             [offsets_q[b], offsets_q[b+1]) and key rows [offsets_k[b],
+ *             offsets_k[b+1]); non-decreasing, within [0, Tq] and [0, Tk].  Both
+ *             NULL: one sequence of all rows (B is then ignored).  Malformed
+ *             tables give unspecified values but never an access outside the
+ *             buffers.
+ *   H       : 1 .. 65536.  B: 1 .. 65536.  Tq, Tk: at most 2^30.
+ *   scale   : > 0, finite.
+ *   causal  : 0, or 1: query i of a sequence with lq queries and lk keys sees
+ *             keys j <= i + lk - lq (the queries are the last lq tokens).
+ * Strides are multiples of 8 and pointers 16-byte aligned.
+ */
+typedef struct mxq_latent_attn {
+  const uint16_t* q;
+  int64_t ldq, ldq_head;
+  const uint16_t* k_nope;
+  int64_t ldk, ldk_head;
+  const uint16_t* k_rope;
+  int64_t ldr;
+  const uint16_t* v;
+  int64_t ldv, ldv_head;
+  const int64_t* offsets_q;
+  const int64_t* offsets_k;
+  int64_t Tq, Tk;
+  int32_t B, H;
+  float scale;
+  int32_t causal;
+} mxq_latent_attn;
+
+/*
+ * Expanded latent attention, forward:
+ *   z[i,j] = scale * (q_nope[i] . k_nope[j] + q_rope[i] . k_rope[j]),
+ *   o[i] = sum_j softmax(z[i])_j v[j],   lse[i] = ln sum_j exp(z[i,j])
+ * over the visible keys of row i's own sequence, for each head.  Keys that a
+ * row does not see do not reach it, whatever they hold.  A row that sees
+ * nothing gets zeros and minus infinity.  Sums, maxima and totals are FP32,
+ * the probabilities are rounded to BF16 for the second product.
+ *   attn : host struct, read during the call only.
+ *   o    : device, BF16 [Tq, H, 128], strides ldo, ldo_head (% 8 == 0), 16-byte
+ *          aligned.
+ *   lse  : device float [H, Tq], row stride ldl >= Tq.
+ * Rows outside every sequence are not written.
+ */
+MXQ_API int latent_attention(const mxq_latent_attn* attn, uint16_t* o, int64_t ldo, int64_t ldo_head,
+                     float* lse, int64_t ldl, hipStream_t stream);
+
+/*
+ * Gradient of latent_attention: with P = exp(z - lse), dP = dO V^T,
+ * D = rowsum(P * dP) and dS = P * (dP - D),
+ *   dq = scale * dS K,  dk = scale * dS^T Q,  dv = P^T dO,
+ * the rotary key's gradient summed over the heads.  D does not inherit the
+ * rounding of o (which only starts it).  FP32 sums; P and dS are
+ * rounded to BF16 for the products; results do not depend on timing (no
+ * atomics).  Every row of a sequence is written, with zeros where nothing
+ * reaches it.
+ *   attn     : as for latent_attention, with the same values.
+ *   o, lse   : latent_attention's results.
+ *   dout     : device, BF16 [Tq, H, 128] (lddo, lddo_head), the gradient of o.
+ *   dq, dk_nope, dk_rope, dv : device, BF16, shaped as q, k_nope, k_rope and v;
+ *              dk_nope and dv may be the two halves of one [Tk, H, 256] buffer.
+ *   workspace: device scratch of at least mxq_workspace_size(
+ *              MXQ_WS_LATENT_BACKWARD, Tq, Tk, H, 0) bytes, 16-byte aligned.
+ * Strides are multiples of 8 and pointers 16-byte aligned.  Rows outside every
+ * sequence get unspecified values in dk_rope and are not written elsewhere.
+ */
+MXQ_API int latent_attention_backward(const mxq_latent_attn* attn, const uint16_t* o, int64_t ldo,
+                              int64_t ldo_head, const float* lse, int64_t ldl,
+                              const uint16_t* dout, int64_t lddo, int64_t lddo_head,
+                              uint16_t* dq, int64_t lddq, int64_t lddq_head,
+                              uint16_t* dk_nope, int64_t lddk, int64_t lddk_head,
+                              uint16_t* dk_rope, int64_t lddr,
+                              uint16_t* dv, int64_t lddv, int64_t lddv_head,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ *
  * Helpers                                                                   *
  * ------------------------------------------------------------------------ */
 
 /* Workspace kinds: per-tensor quantization (n = elements), per-group
- * quantization (n = rows, a1 = groups). */
-enum { MXQ_WS_PER_TENSOR = 0, MXQ_WS_PER_GROUP = 1 };
+ * quantization (n = rows, a1 = groups), absorbed latent attention (n = B,
+ * a1 = S, a2 = H, a3 = max_len), expanded latent attention's gradient (n = Tq,
+ * a1 = Tk, a2 = H). */
+enum {
+  MXQ_WS_PER_TENSOR = 0,
+  MXQ_WS_PER_GROUP = 1,
+  MXQ_WS_LATENT_DECODE = 2,
+  MXQ_WS_LATENT_BACKWARD = 3
+};
 
 /* Workspace bytes an operation needs (0 if none). */
 MXQ_API size_t mxq_workspace_size(int op, int64_t n, int64_t a1, int64_t a2, int64_t a3);
