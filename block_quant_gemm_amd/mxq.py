@@ -9,7 +9,9 @@ the library's HIP kernels; there is no other code path.
 """
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -39,20 +41,6 @@ class DualItem(ctypes.Structure):
                 ("E", _i32), ("q", _p), ("ldq", _i64), ("scale", _p), ("lds", _i64),
                 ("qT", _p), ("ldqT", _i64), ("M_cap", _i64), ("scaleT", _p), ("ldsT", _i64),
                 ("offsets_padded", _p)]
-
-
-class LatentCacheArg(ctypes.Structure):
-    """mxq_latent_cache of mxq.h."""
-    _fields_ = [("codes", _p), ("ld_codes", _i64), ("scales", _p), ("ld_scales", _i64),
-                ("k_rope", _p), ("ld_rope", _i64), ("slots", _i64)]
-
-
-class LatentAttnArg(ctypes.Structure):
-    """mxq_latent_attn of mxq.h."""
-    _fields_ = [("q", _p), ("ldq", _i64), ("ldq_head", _i64), ("k_nope", _p), ("ldk", _i64),
-                ("ldk_head", _i64), ("k_rope", _p), ("ldr", _i64), ("v", _p), ("ldv", _i64),
-                ("ldv_head", _i64), ("offsets_q", _p), ("offsets_k", _p), ("Tq", _i64),
-                ("Tk", _i64), ("B", _i32), ("H", _i32), ("scale", _f32), ("causal", _i32)]
 
 
 _SIGS = {
@@ -111,15 +99,15 @@ _SIGS = {
                                              _i32, _i64, _i64, _p, _i64, ctypes.c_int,
                                              ctypes.c_int, _p]),
     "mx_latent_cache_write": (ctypes.c_int, [_p, _i64, _p, _i64, _p, _i64,
-                                             ctypes.POINTER(LatentCacheArg), _p]),
-    "mx_latent_cache_read": (ctypes.c_int, [ctypes.POINTER(LatentCacheArg), _p, _i64, _p, _i64,
+                                             _p, _p]),
+    "mx_latent_cache_read": (ctypes.c_int, [_p, _p, _i64, _p, _i64,
                                             _p, _i64, _p]),
-    "mx_latent_decode": (ctypes.c_int, [_p, _i64, _i64, _i64, ctypes.POINTER(LatentCacheArg), _p,
+    "mx_latent_decode": (ctypes.c_int, [_p, _i64, _i64, _i64, _p, _p,
                                         _i64, _i32, _i32, _p, _i32, _i32, _i32, _i64, _f32, _p,
                                         _i64, _i64, _i64, _p, _p, _sz, _p]),
-    "latent_attention": (ctypes.c_int, [ctypes.POINTER(LatentAttnArg), _p, _i64, _i64, _p, _i64,
+    "latent_attention": (ctypes.c_int, [_p, _p, _i64, _i64, _p, _i64,
                                         _p]),
-    "latent_attention_backward": (ctypes.c_int, [ctypes.POINTER(LatentAttnArg), _p, _i64, _i64, _p,
+    "latent_attention_backward": (ctypes.c_int, [_p, _p, _i64, _i64, _p,
                                                  _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64,
                                                  _i64, _p, _i64, _p, _i64, _i64, _p, _sz, _p]),
     "mxq_workspace_size": (_sz, [ctypes.c_int, _i64, _i64, _i64, _i64]),
@@ -163,6 +151,11 @@ def _ptr(t):
 
 def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _raw_stream():
+    """The current stream's handle, without the stream object around it."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _bf16_bits(x):
@@ -710,17 +703,31 @@ def mx_grouped_gemm_wgrad(at, at_scale, bt, bt_scale, offsets_padded, out_dtype=
 # latent attention
 # ---------------------------------------------------------------------------
 
-def _shaped(name, t, dtype, *shape):
-    """Raises unless t has this dtype, this shape (None: any size) and adjacent
+# These calls are short enough for their marshalling to count, so it is kept lean:
+# the C structs are packed as bytes, shapes are compared as tuples, and buffers
+# come from new_empty.
+_CACHE_STRUCT = struct.Struct("PqPqPqq")                  # mxq_latent_cache of mxq.h
+_ATTN_STRUCT = struct.Struct("PqqPqqPqPqqPPqqiifi")       # mxq_latent_attn of mxq.h
+_BF16, _U8, _I64, _F32 = torch.bfloat16, torch.uint8, torch.int64, torch.float32
+
+
+def _rows(name, t, dtype, shape):
+    """The strides of t.  Raises unless t has this dtype and shape and adjacent
     values along its last dimension: the C calls take addresses and strides
     and cannot see a tensor that is too small."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.numel():
+    s = t.stride()
+    if s[-1] != 1 and t.numel() and shape[-1] != 1:
         raise ValueError(f"{name}: the last dimension has to be contiguous")
-    return t
+    return s
+
+
+@functools.lru_cache(maxsize=1024)
+def _latent_workspace(op, n, a1, a2, a3):
+    return workspace_size(op, n, a1, a2, a3)
 
 
 def latent_cache(slots, device="cuda"):
@@ -734,11 +741,11 @@ def latent_cache(slots, device="cuda"):
 def _cache_arg(cache):
     codes, scales, k_rope = cache
     n = codes.shape[0]
-    _shaped("cache codes", codes, torch.uint8, n, LATENT_DIM)
-    _shaped("cache scales", scales, torch.uint8, n, LATENT_DIM // 32)
-    _shaped("cache k_rope", k_rope, torch.bfloat16, n, ROPE_DIM)
-    return LatentCacheArg(codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0),
-                          k_rope.data_ptr(), k_rope.stride(0), n)
+    sc = _rows("cache codes", codes, _U8, (n, 512))
+    ss = _rows("cache scales", scales, _U8, (n, 16))
+    sr = _rows("cache k_rope", k_rope, _BF16, (n, 64))
+    return _CACHE_STRUCT.pack(codes.data_ptr(), sc[0], scales.data_ptr(), ss[0],
+                              k_rope.data_ptr(), sr[0], n)
 
 
 def mx_latent_cache_write(c, k_rope, slots, cache):
@@ -746,12 +753,13 @@ def mx_latent_cache_write(c, k_rope, slots, cache):
     the cache: skipped) gets c[t] (BF16 [T, 512]) as MX codes and scales, and
     k_rope[t] (BF16 [T, 64]).  Returns the cache."""
     T = c.shape[0]
-    _shaped("c", c, torch.bfloat16, T, LATENT_DIM)
-    _shaped("k_rope", k_rope, torch.bfloat16, T, ROPE_DIM)
-    _shaped("slots", slots, torch.int64, T)
-    _check(load().mx_latent_cache_write(c.data_ptr(), c.stride(0), k_rope.data_ptr(),
-                                        k_rope.stride(0), slots.data_ptr(), T, _cache_arg(cache),
-                                        _stream()))
+    sc = _rows("c", c, _BF16, (T, 512))
+    sr = _rows("k_rope", k_rope, _BF16, (T, 64))
+    _rows("slots", slots, _I64, (T,))
+    st = load().mx_latent_cache_write(c.data_ptr(), sc[0], k_rope.data_ptr(), sr[0],
+                                      slots.data_ptr(), T, _cache_arg(cache), _raw_stream())
+    if st:
+        _check(st)
     return cache
 
 
@@ -759,16 +767,17 @@ def mx_latent_cache_read(cache, slots, c=None, k_rope=None):
     """The tokens in the slots `slots` (int64 [T], device; outside the cache:
     zeros).  Returns (c BF16 [T, 512], k_rope BF16 [T, 64])."""
     T = slots.shape[0]
-    _shaped("slots", slots, torch.int64, T)
+    _rows("slots", slots, _I64, (T,))
     if c is None:
-        c = torch.empty((T, LATENT_DIM), dtype=torch.bfloat16, device=slots.device)
+        c = cache[2].new_empty((T, 512))
     if k_rope is None:
-        k_rope = torch.empty((T, ROPE_DIM), dtype=torch.bfloat16, device=slots.device)
-    _shaped("c", c, torch.bfloat16, T, LATENT_DIM)
-    _shaped("k_rope", k_rope, torch.bfloat16, T, ROPE_DIM)
-    _check(load().mx_latent_cache_read(_cache_arg(cache), slots.data_ptr(), T, c.data_ptr(),
-                                       c.stride(0), k_rope.data_ptr(), k_rope.stride(0),
-                                       _stream()))
+        k_rope = cache[2].new_empty((T, 64))
+    sc = _rows("c", c, _BF16, (T, 512))
+    sr = _rows("k_rope", k_rope, _BF16, (T, 64))
+    st = load().mx_latent_cache_read(_cache_arg(cache), slots.data_ptr(), T, c.data_ptr(), sc[0],
+                                     k_rope.data_ptr(), sr[0], _raw_stream())
+    if st:
+        _check(st)
     return c, k_rope
 
 
@@ -781,49 +790,51 @@ def mx_latent_decode(q, cache, pages, lens, page_size, max_len, scale, o=None, l
     [B] cached tokens, the S query tokens among them (the last); max_len: host
     bound of lens.  Returns (o BF16 [B, S, H, 512], lse float32 [B, S, H])."""
     B, S, H, _ = q.shape
-    _shaped("q", q, torch.bfloat16, B, S, H, LATENT_DIM + ROPE_DIM)
-    _shaped("pages", pages, torch.int32, B, None)
-    _shaped("lens", lens, torch.int64, B)
+    sq = _rows("q", q, _BF16, (B, S, H, 576))
+    width = pages.shape[-1]
+    sp = _rows("pages", pages, torch.int32, (B, width))
+    _rows("lens", lens, _I64, (B,))
     if o is None:
-        o = torch.empty((B, S, H, LATENT_DIM), dtype=torch.bfloat16, device=q.device)
+        o = q.new_empty((B, S, H, 512))
     if lse is None:
-        lse = torch.empty((B, S, H), dtype=torch.float32, device=q.device)
-    _shaped("o", o, torch.bfloat16, B, S, H, LATENT_DIM)
-    _shaped("lse", lse, torch.float32, B, S, H)
+        lse = q.new_empty((B, S, H), dtype=_F32)
+    so = _rows("o", o, _BF16, (B, S, H, 512))
+    _rows("lse", lse, _F32, (B, S, H))
     if not lse.is_contiguous():
         raise ValueError("lse: has to be contiguous")
-    lib = load()
     if workspace is None:
-        workspace = torch.empty(lib.mxq_workspace_size(WS_LATENT_DECODE, B, S, H, max_len),
-                                dtype=torch.uint8, device=q.device)
-    _check(lib.mx_latent_decode(
-        q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), _cache_arg(cache), pages.data_ptr(),
-        pages.stride(0), pages.shape[1], page_size, lens.data_ptr(), B, S, H, max_len, scale,
-        o.data_ptr(), o.stride(0), o.stride(1), o.stride(2), lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), _stream()))
+        workspace = q.new_empty(_latent_workspace(WS_LATENT_DECODE, B, S, H, max_len), dtype=_U8)
+    st = load().mx_latent_decode(
+        q.data_ptr(), sq[0], sq[1], sq[2], _cache_arg(cache), pages.data_ptr(), sp[0], width,
+        page_size, lens.data_ptr(), B, S, H, max_len, scale, o.data_ptr(), so[0], so[1], so[2],
+        lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream())
+    if st:
+        _check(st)
     return o, lse
 
 
 def _attn_arg(q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal):
     Tq, H, _ = q.shape
     Tk = k_nope.shape[0]
-    _shaped("q", q, torch.bfloat16, Tq, H, NOPE_DIM + ROPE_DIM)
-    _shaped("k_nope", k_nope, torch.bfloat16, Tk, H, NOPE_DIM)
-    _shaped("k_rope", k_rope, torch.bfloat16, Tk, ROPE_DIM)
-    _shaped("v", v, torch.bfloat16, Tk, H, VALUE_DIM)
-    B = 0
+    sq = _rows("q", q, _BF16, (Tq, H, 192))
+    sk = _rows("k_nope", k_nope, _BF16, (Tk, H, 128))
+    sr = _rows("k_rope", k_rope, _BF16, (Tk, 64))
+    sv = _rows("v", v, _BF16, (Tk, H, 128))
     if offsets_k is None:
         offsets_k = offsets_q
+    B = oq = ok = 0
     if offsets_q is not None:
-        B = offsets_q.numel() - 1
-        _shaped("offsets_q", offsets_q, torch.int64, B + 1)
+        B = offsets_q.shape[0] - 1
+        _rows("offsets_q", offsets_q, _I64, (B + 1,))
+        oq = offsets_q.data_ptr()
     if offsets_k is not None:
-        _shaped("offsets_k", offsets_k, torch.int64, B + 1)
-    return LatentAttnArg(
-        q.data_ptr(), q.stride(0), q.stride(1), k_nope.data_ptr(), k_nope.stride(0),
-        k_nope.stride(1), k_rope.data_ptr(), k_rope.stride(0), v.data_ptr(), v.stride(0),
-        v.stride(1), None if offsets_q is None else offsets_q.data_ptr(),
-        None if offsets_k is None else offsets_k.data_ptr(), Tq, Tk, B, H, scale, int(causal))
+        _rows("offsets_k", offsets_k, _I64, (B + 1,))
+        ok = offsets_k.data_ptr()
+    if scale is None:
+        scale = (NOPE_DIM + ROPE_DIM) ** -0.5
+    return _ATTN_STRUCT.pack(q.data_ptr(), sq[0], sq[1], k_nope.data_ptr(), sk[0], sk[1],
+                             k_rope.data_ptr(), sr[0], v.data_ptr(), sv[0], sv[1], oq, ok, Tq, Tk,
+                             B, H, scale, int(causal))
 
 
 def latent_attention(q, k_nope, k_rope, v, offsets_q=None, offsets_k=None, scale=None, causal=True,
@@ -836,18 +847,18 @@ def latent_attention(q, k_nope, k_rope, v, offsets_q=None, offsets_k=None, scale
     offsets_q, offsets_k int64 [B+1] on the device (offsets_k defaults to
     offsets_q; both None: one sequence); scale defaults to 192 ** -0.5.
     Returns (o BF16 [Tq, H, 128], lse float32 [H, Tq])."""
-    if scale is None:
-        scale = (NOPE_DIM + ROPE_DIM) ** -0.5
     Tq, H, _ = q.shape
     arg = _attn_arg(q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal)
     if o is None:
-        o = torch.empty((Tq, H, VALUE_DIM), dtype=torch.bfloat16, device=q.device)
+        o = q.new_empty((Tq, H, 128))
     if lse is None:
-        lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
-    _shaped("o", o, torch.bfloat16, Tq, H, VALUE_DIM)
-    _shaped("lse", lse, torch.float32, H, Tq)
-    _check(load().latent_attention(arg, o.data_ptr(), o.stride(0), o.stride(1), lse.data_ptr(),
-                                   lse.stride(0), _stream()))
+        lse = q.new_empty((H, Tq), dtype=_F32)
+    so = _rows("o", o, _BF16, (Tq, H, 128))
+    sl = _rows("lse", lse, _F32, (H, Tq))
+    st = load().latent_attention(arg, o.data_ptr(), so[0], so[1], lse.data_ptr(), sl[0],
+                                 _raw_stream())
+    if st:
+        _check(st)
     return o, lse
 
 
@@ -859,37 +870,33 @@ def latent_attention_backward(dout, q, k_nope, k_rope, v, o, lse, offsets_q=None
     The other arguments are the forward call's and its results o and lse.
     Returns (dq, dk_nope, dk_rope, dv), shaped as their operands; dk_nope and dv
     are the halves of one [Tk, H, 256] buffer unless they are given."""
-    if scale is None:
-        scale = (NOPE_DIM + ROPE_DIM) ** -0.5
     Tq, H, _ = q.shape
     Tk = k_nope.shape[0]
     arg = _attn_arg(q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal)
-    _shaped("dout", dout, torch.bfloat16, Tq, H, VALUE_DIM)
-    _shaped("o", o, torch.bfloat16, Tq, H, VALUE_DIM)
-    _shaped("lse", lse, torch.float32, H, Tq)
-    dev = q.device
+    sg = _rows("dout", dout, _BF16, (Tq, H, 128))
+    so = _rows("o", o, _BF16, (Tq, H, 128))
+    sl = _rows("lse", lse, _F32, (H, Tq))
     if dq is None:
-        dq = torch.empty((Tq, H, NOPE_DIM + ROPE_DIM), dtype=torch.bfloat16, device=dev)
+        dq = q.new_empty((Tq, H, 192))
     if dk_nope is None or dv is None:
-        dkv = torch.empty((Tk, H, NOPE_DIM + VALUE_DIM), dtype=torch.bfloat16, device=dev)
-        dk_nope = dkv[..., :NOPE_DIM] if dk_nope is None else dk_nope
-        dv = dkv[..., NOPE_DIM:] if dv is None else dv
+        dkv = q.new_empty((Tk, H, 256))
+        dk_nope = dkv[..., :128] if dk_nope is None else dk_nope
+        dv = dkv[..., 128:] if dv is None else dv
     if dk_rope is None:
-        dk_rope = torch.empty((Tk, ROPE_DIM), dtype=torch.bfloat16, device=dev)
-    _shaped("dq", dq, torch.bfloat16, Tq, H, NOPE_DIM + ROPE_DIM)
-    _shaped("dk_nope", dk_nope, torch.bfloat16, Tk, H, NOPE_DIM)
-    _shaped("dk_rope", dk_rope, torch.bfloat16, Tk, ROPE_DIM)
-    _shaped("dv", dv, torch.bfloat16, Tk, H, VALUE_DIM)
-    lib = load()
+        dk_rope = q.new_empty((Tk, 64))
+    sdq = _rows("dq", dq, _BF16, (Tq, H, 192))
+    sdk = _rows("dk_nope", dk_nope, _BF16, (Tk, H, 128))
+    sdr = _rows("dk_rope", dk_rope, _BF16, (Tk, 64))
+    sdv = _rows("dv", dv, _BF16, (Tk, H, 128))
     if workspace is None:
-        workspace = torch.empty(lib.mxq_workspace_size(WS_LATENT_BACKWARD, Tq, Tk, H, 0),
-                                dtype=torch.uint8, device=dev)
-    _check(lib.latent_attention_backward(
-        arg, o.data_ptr(), o.stride(0), o.stride(1), lse.data_ptr(), lse.stride(0),
-        dout.data_ptr(), dout.stride(0), dout.stride(1), dq.data_ptr(), dq.stride(0), dq.stride(1),
-        dk_nope.data_ptr(), dk_nope.stride(0), dk_nope.stride(1), dk_rope.data_ptr(),
-        dk_rope.stride(0), dv.data_ptr(), dv.stride(0), dv.stride(1), workspace.data_ptr(),
-        workspace.numel(), _stream()))
+        workspace = q.new_empty(_latent_workspace(WS_LATENT_BACKWARD, Tq, Tk, H, 0), dtype=_U8)
+    st = load().latent_attention_backward(
+        arg, o.data_ptr(), so[0], so[1], lse.data_ptr(), sl[0], dout.data_ptr(), sg[0], sg[1],
+        dq.data_ptr(), sdq[0], sdq[1], dk_nope.data_ptr(), sdk[0], sdk[1], dk_rope.data_ptr(),
+        sdr[0], dv.data_ptr(), sdv[0], sdv[1], workspace.data_ptr(), workspace.numel(),
+        _raw_stream())
+    if st:
+        _check(st)
     return dq, dk_nope, dk_rope, dv
 
 
