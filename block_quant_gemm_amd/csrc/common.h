@@ -23,14 +23,14 @@ inline int64_t sat_add(int64_t a, int64_t b) {
 // Tokens of a tile of the latent cache's absorbed attention.
 #define MXQ_LATENT_TILE 64
 
-// How mx_latent_decode splits its work: 16 R query rows a workgroup (R = 1 if
-// that holds a request's S * H rows, else 2 and as many row tiles), and along the batch's 64-token tiles runs of one length that stay
+// How mx_latent_decode splits its work: `rows` query rows a workgroup (the
+// smallest of 16, 32 and 64 that holds a request's S * H rows, else 64 and as many
+// row tiles), and along the batch's 64-token tiles runs of one length that stay
 // inside a request.  With `runs` runs' worth of tiles there are at most
-// runs + B runs: `grid` workgroups, two a CU where their registers allow it, and
-// a workspace of one part each (512 sums, a maximum and a total a row).
-// grid = 0: too large.
+// runs + B runs: `grid` workgroups, and a workspace of one part each (512
+// sums, a maximum and a total a row) and 8 bytes a request.  grid = 0: too large.
 struct LatentDecodePlan {
-  int R;
+  int rows;
   uint32_t row_tiles, runs, grid;
   int64_t part_rows;
   size_t bytes;
@@ -38,19 +38,19 @@ struct LatentDecodePlan {
 inline LatentDecodePlan latent_decode_plan(int64_t B, int64_t S, int64_t H, int64_t max_len) {
   LatentDecodePlan p{};
   if (B < 1 || S < 1 || H < 1 || max_len < 0 || sat_mul(S, H) > 65536) return p;
-  const int64_t rows = S * H;
-  p.R = rows <= 16 ? 1 : 2;
-  p.row_tiles = (uint32_t)((rows + 16 * p.R - 1) / (16 * p.R));
+  p.rows = S * H <= 16 ? 16 : S * H <= 32 ? 32 : 64;
+  p.row_tiles = (uint32_t)((S * H + p.rows - 1) / p.rows);
   const int64_t tiles = sat_mul(B, max_len > 0 ? sat_add(max_len, MXQ_LATENT_TILE - 1) / MXQ_LATENT_TILE : 1);
   if (tiles > 0x3FFFFFFFLL) return p;
-  int64_t want = (p.R == 1 ? 512 : 256) / (int64_t)p.row_tiles;
+  // workgroups of 16 rows have four wavefronts, two to a CU; the others have eight
+  int64_t want = (p.rows == 16 ? 512 : 256) / (int64_t)p.row_tiles;
   if (want < 2) want = 2;
   const int64_t runs = want - B > want / 2 ? want - B : want / 2;
   p.runs = (uint32_t)runs;
   p.grid = (uint32_t)(runs + B < tiles ? runs + B : tiles);
-  p.part_rows = (int64_t)p.grid * p.row_tiles * 16 * p.R;
+  p.part_rows = (int64_t)p.grid * p.row_tiles * p.rows;
   if (p.part_rows > (INT64_C(1) << 40)) return LatentDecodePlan{};
-  p.bytes = (size_t)p.part_rows * (MXQ_LATENT_DIM + 2) * sizeof(float);
+  p.bytes = (size_t)p.part_rows * (MXQ_LATENT_DIM + 2) * sizeof(float) + (size_t)B * 8;
   return p;
 }
 

@@ -121,7 +121,8 @@ __global__ __launch_bounds__(kThr) void k_latent_read(Cache k, const int64_t* __
 // Absorbed attention of decoding tokens.
 //
 // The rows of one request are its query tokens' heads (row s * H + h).  A
-// workgroup takes 16 R of them and a run of one request's 64-token tiles; all
+// workgroup takes 16 R G of them (G groups of four wavefronts with 16 R each) and
+// a run of one request's 64-token tiles; all
 // runs are about equally long, so ragged lengths balance, and a request with
 // more than one leaves parts (FP32 sums, maximum and total) for
 // k_decode_merge.  A tile's codes are widened to BF16 once, into LDS, exactly
@@ -130,9 +131,9 @@ __global__ __launch_bounds__(kThr) void k_latent_read(Cache k, const int64_t* __
 //   logits  wavefront w takes tokens 16 w .. 16 w + 15 against all rows,
 //           queries in registers;
 //   values  wavefront w takes 128 latent columns for all rows and 64 tokens.
-// So each wavefront reads the tile once per product whatever R is.  Both
+// So each group reads the tile once per product whatever R is.  Both
 // products leave the query row along the lanes, and a lane's probabilities go
-// to the same lane of the other wavefronts.
+// to the same lane of the other wavefronts of its group.
 // ---------------------------------------------------------------------------
 
 constexpr int kTok = MXQ_LATENT_TILE;            // tokens of a tile
@@ -140,7 +141,6 @@ constexpr int kUnits = (kLat + kRope) / 8;       // 16-byte units of a widened r
 constexpr int kRowB = kUnits * 16;               // 1152 bytes
 constexpr int kSteps = (kLat + kRope) / 32;      // 18 steps of 32 columns
 constexpr int kWaves = kThr / 64;
-constexpr int kCl = kTok * 32 / kThr, kRl = kTok * 8 / kThr;   // 8 code and 2 rotary loads a lane
 
 struct DecodeArgs {
   const uint16_t* q;
@@ -159,8 +159,9 @@ struct DecodeArgs {
   uint16_t* o;
   int64_t ldo_seq, ldo_tok, ldo_head;
   float* lse;                                    // [B, S, H]
-  float* part_o;                                 // [grid.x][row tiles][16 R][512]
-  float* part_ml;                                // [grid.x][row tiles][16 R][2]
+  float* part_o;                                 // [grid.x][row tiles][rows][512]
+  float* part_ml;                                // [grid.x][row tiles][rows][2]
+  uint2* runs_of;                                // [B]: a request's first run, and runs
 };
 
 // Units of a widened row go to slots so that a lane that widens 16 codes
@@ -315,15 +316,21 @@ __device__ __forceinline__ uint2 bf16x4_bits(f32x4 v, float mul) {
   return make_uint2(bf16x2_bits(v[0] * mul, v[1] * mul), bf16x2_bits(v[2] * mul, v[3] * mul));
 }
 
-template <int R>
-__global__ __launch_bounds__(kThr, R == 1 ? 2 : 1) void k_decode(DecodeArgs a) {
+template <int R, int G>
+__global__ __launch_bounds__(kThr * G, R * G == 1 ? 2 : G) void k_decode(DecodeArgs a) {
+  constexpr int kRows = 16 * R * G;                // query rows of the workgroup
+  constexpr int kCl = kTok * 32 / (kThr * G), kRl = kTok * 8 / (kThr * G);   // loads a lane
   __shared__ __attribute__((aligned(256))) uint8_t tile[kTok * kRowB];
-  __shared__ __attribute__((aligned(16))) uint2 s_p[kWaves][R][64];
-  __shared__ float s_max[kWaves][R * 16];
+  __shared__ __attribute__((aligned(16))) uint2 s_p[kWaves][R * G][64];
+  __shared__ float s_max[kWaves][kRows];
   __shared__ int32_t s_slot[2][kTok];
-  __shared__ uint32_t s_redo[R * 16];
+  __shared__ uint32_t s_redo[kRows];
+  // steps of the queries held in registers; the others are read from LDS, in lane order
+  constexpr int KQ = R == 1 ? kSteps : kSteps / 2;
+  __shared__ __attribute__((aligned(16))) uint4 s_q[R * G][KQ < kSteps ? kSteps - KQ : 1][KQ < kSteps ? 64 : 1];
   const int tid = threadIdx.x, l = tid & 63, n = l & 15, g = l >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int w = wave & 3, rg = (wave >> 2) * R;    // part of the tile; first of its 16-row groups
   const int rt = blockIdx.y;
 
   // the request and the run of its tiles that this workgroup takes
@@ -346,6 +353,7 @@ __global__ __launch_bounds__(kThr, R == 1 ? 2 : 1) void k_decode(DecodeArgs a) {
     }
   }
   if (b < 0) return;                               // uniform over the workgroup
+  if (k == 0 && rt == 0 && tid == 0) a.runs_of[b] = make_uint2(blockIdx.x, nrun);   // for the merge
   const int len = seq_len(a, b);
   const uint32_t ntile = seq_tiles(len);
   const uint32_t i0 = (uint32_t)((uint64_t)k * ntile / nrun);
@@ -362,14 +370,14 @@ __global__ __launch_bounds__(kThr, R == 1 ? 2 : 1) void k_decode(DecodeArgs a) {
   const uint32_t rv = trow * kRowB + w * 256 + ((((n & 3) >> 1) ^ fd(trow)) << 4) + (n & 1) * 8;
 
   auto put_slot = [&](uint32_t i) {                // slots of tile i, by the first wavefront
-    if (w == 0) s_slot[i & 1][l] = i < i1 ? slot_of(a, pages, i * kTok + l, len) : -1;
+    if (wave == 0) s_slot[i & 1][l] = i < i1 ? slot_of(a, pages, i * kTok + l, len) : -1;
   };
   uint4 sc[kCl], sr[kRl];
   uint32_t se[kCl];
   auto load = [&](uint32_t i) {
 #pragma unroll
     for (int j = 0; j < kCl; ++j) {
-      const int32_t s = s_slot[i & 1][j * 8 + r0];
+      const int32_t s = s_slot[i & 1][j * (8 * G) + r0];
       sc[j] = make_uint4(0, 0, 0, 0);
       se[j] = 127;
       if (s >= 0) {
@@ -379,31 +387,34 @@ __global__ __launch_bounds__(kThr, R == 1 ? 2 : 1) void k_decode(DecodeArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < kRl; ++j) {
-      const int32_t s = s_slot[i & 1][j * 32 + (tid >> 3)];
+      const int32_t s = s_slot[i & 1][j * (32 * G) + (tid >> 3)];
       sr[j] = make_uint4(0, 0, 0, 0);
       if (s >= 0) sr[j] = *reinterpret_cast<const uint4*>(a.k.rope + s * a.k.ldr + (tid & 7) * 8);
     }
   };
   put_slot(i0);
   put_slot(i0 + 1);
-  if (tid < 16 * R) s_redo[tid] = 0;
+  if (tid < kRows) s_redo[tid] = 0;
 
   // queries: lane (n, g) holds slot 4 kk + g of row n for each step kk
-  bf16x8 q[R][kSteps];
+  bf16x8 q[R][KQ];
   int lim[R];                                      // tokens below lim are seen by this lane's row
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int row = (rt * R + r) * 16 + n;
+    const int row = rt * kRows + (rg + r) * 16 + n;
     const int s = row / a.H, h = row - s * a.H;
     const bool ok = row < a.rows;
     lim[r] = ok ? len - (a.S - 1 - s) : 0;
     const uint16_t* qp = a.q + (int64_t)b * a.ldq_seq + (int64_t)s * a.ldq_tok + (int64_t)h * a.ldq_head;
-#pragma unroll
-    for (int kk = 0; kk < kSteps; ++kk) {
+    auto step = [&](int kk) {
       uint4 v = make_uint4(0, 0, 0, 0);
       if (ok) v = *reinterpret_cast<const uint4*>(qp + slot_unit(4 * kk + g) * 8);
-      q[r][kk] = __builtin_bit_cast(bf16x8, v);
-    }
+      return v;
+    };
+#pragma unroll
+    for (int kk = 0; kk < KQ; ++kk) q[r][kk] = __builtin_bit_cast(bf16x8, step(kk));
+    if (KQ < kSteps)
+      for (int kk = KQ + w; kk < kSteps; kk += 4) s_q[rg + r][kk - KQ][l] = step(kk);
   }
   f32x4 o[R][8] = {};
   float m[R], sum[R];
@@ -417,13 +428,13 @@ __global__ __launch_bounds__(kThr, R == 1 ? 2 : 1) void k_decode(DecodeArgs a) {
 #pragma unroll
     for (int j = 0; j < kCl; ++j) {
       const float f = e8m0_f32(se[j]);
-      uint8_t* p = tile + (wr ^ ((j & 1) << 4)) + j * (8 * kRowB);
+      uint8_t* p = tile + (G == 1 ? wr ^ ((j & 1) << 4) : wr) + j * (8 * G * kRowB);
       *reinterpret_cast<bf16x8*>(p) = widen8_bf16(sc[j].x, sc[j].y, f);
       *reinterpret_cast<bf16x8*>(p + 512) = widen8_bf16(sc[j].z, sc[j].w, f);
     }
 #pragma unroll
     for (int j = 0; j < kRl; ++j)
-      *reinterpret_cast<uint4*>(tile + wrr + j * (32 * kRowB)) = sr[j];
+      *reinterpret_cast<uint4*>(tile + wrr + j * (32 * G * kRowB)) = sr[j];
     __syncthreads();
     if (i + 1 < i1) load(i + 1);
 
@@ -432,7 +443,9 @@ __global__ __launch_bounds__(kThr, R == 1 ? 2 : 1) void k_decode(DecodeArgs a) {
     for (int kk = 0; kk < kSteps; ++kk) {
       const bf16x8 kf = *reinterpret_cast<const bf16x8*>(tile + (rk ^ ((kk & 1) << 6)) + (kk >> 1) * 128);
 #pragma unroll
-      for (int r = 0; r < R; ++r) s[r] = mfma16(kf, q[r][kk], s[r]);
+      for (int r = 0; r < R; ++r)
+        s[r] = mfma16(kf, kk < KQ ? q[r][kk < KQ ? kk : 0]
+                                  : __builtin_bit_cast(bf16x8, s_q[rg + r][kk < KQ ? 0 : kk - KQ][l]), s[r]);
     }
     const int tok0 = (int)(i * kTok) + 16 * w + 4 * g;   // this lane's 4 tokens
 #pragma unroll
@@ -442,7 +455,7 @@ __global__ __launch_bounds__(kThr, R == 1 ? 2 : 1) void k_decode(DecodeArgs a) {
         if (tok0 + e >= lim[r]) s[r][e] = -__builtin_inff();
       const float mx = groups_max(__builtin_fmaxf(__builtin_fmaxf(s[r][0], s[r][1]),
                                                   __builtin_fmaxf(s[r][2], s[r][3])));
-      if (g == 0) s_max[w][r * 16 + n] = mx;
+      if (g == 0) s_max[w][(rg + r) * 16 + n] = mx;
     }
     __syncthreads();
     put_slot(i + 2);                               // its loads are a whole tile away
@@ -450,7 +463,7 @@ __global__ __launch_bounds__(kThr, R == 1 ? 2 : 1) void k_decode(DecodeArgs a) {
     for (int r = 0; r < R; ++r) {
       float mn = m[r];
 #pragma unroll
-      for (int x = 0; x < kWaves; ++x) mn = __builtin_fmaxf(mn, s_max[x][r * 16 + n] * c);
+      for (int x = 0; x < kWaves; ++x) mn = __builtin_fmaxf(mn, s_max[x][(rg + r) * 16 + n] * c);
       if (__ballot(mn != m[r])) {
         const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mn);
         m[r] = mn;
@@ -465,7 +478,7 @@ __global__ __launch_bounds__(kThr, R == 1 ? 2 : 1) void k_decode(DecodeArgs a) {
         p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][e], c, -mc));
         sum[r] += p[e];
       }
-      s_p[w][r][l] = make_uint2(bf16x2_bits(p[0], p[1]), bf16x2_bits(p[2], p[3]));
+      s_p[w][rg + r][l] = make_uint2(bf16x2_bits(p[0], p[1]), bf16x2_bits(p[2], p[3]));
     }
     __syncthreads();
     // values: tokens 4 g + 0..3 of two wavefronts' 16 a step of 32
@@ -474,7 +487,7 @@ __global__ __launch_bounds__(kThr, R == 1 ? 2 : 1) void k_decode(DecodeArgs a) {
       bf16x8 pf[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const uint2 x = s_p[2 * j][r][l], y = s_p[2 * j + 1][r][l];
+        const uint2 x = s_p[2 * j][rg + r][l], y = s_p[2 * j + 1][rg + r][l];
         pf[r] = __builtin_bit_cast(bf16x8, make_uint4(x.x, x.y, y.x, y.y));
       }
 #pragma unroll
@@ -494,7 +507,7 @@ __global__ __launch_bounds__(kThr, R == 1 ? 2 : 1) void k_decode(DecodeArgs a) {
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const float x = groups_sum(sum[r]);
-    if (g == 0) s_max[w][r * 16 + n] = x;
+    if (g == 0) s_max[w][(rg + r) * 16 + n] = x;
     // Query tokens that do not see a tile's last tokens still multiply them, by
     // 0; a NaN or infinity there leaves a NaN, and the row is redone.
     bool bad = false;
@@ -502,17 +515,17 @@ __global__ __launch_bounds__(kThr, R == 1 ? 2 : 1) void k_decode(DecodeArgs a) {
     for (int d = 0; d < 8; ++d)
 #pragma unroll
       for (int e = 0; e < 4; ++e) bad |= !(__builtin_fabsf(o[r][d][e]) < __builtin_inff());
-    if (bad && a.S > 1) s_redo[r * 16 + n] = 1;
+    if (bad && a.S > 1) s_redo[(rg + r) * 16 + n] = 1;
   }
   __syncthreads();
-  const int64_t part = ((int64_t)blockIdx.x * gridDim.y + rt) * (16 * R);
+  const int64_t part = ((int64_t)blockIdx.x * gridDim.y + rt) * kRows;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     float total = 0.0f;
 #pragma unroll
-    for (int x = 0; x < kWaves; ++x) total += s_max[x][r * 16 + n];
-    const int row = (rt * R + r) * 16 + n;
-    const bool mine = row < a.rows && s_redo[r * 16 + n] == 0;
+    for (int x = 0; x < kWaves; ++x) total += s_max[x][(rg + r) * 16 + n];
+    const int row = rt * kRows + (rg + r) * 16 + n;
+    const bool mine = row < a.rows && s_redo[(rg + r) * 16 + n] == 0;
     if (nrun == 1) {
       const int sq = row / a.H, h = row - sq * a.H;
       uint16_t* op = a.o + (int64_t)b * a.ldo_seq + (int64_t)sq * a.ldo_tok + (int64_t)h * a.ldo_head;
@@ -527,7 +540,7 @@ __global__ __launch_bounds__(kThr, R == 1 ? 2 : 1) void k_decode(DecodeArgs a) {
         a.lse[(int64_t)b * a.rows + row] =
             total == 0.0f ? -__builtin_inff() : kLn2 * (m[r] + __builtin_amdgcn_logf(total));
     } else {
-      const int64_t pr = part + r * 16 + n;
+      const int64_t pr = part + (rg + r) * 16 + n;
       if (mine) {
 #pragma unroll
         for (int d = 0; d < 8; ++d)
@@ -542,9 +555,9 @@ __global__ __launch_bounds__(kThr, R == 1 ? 2 : 1) void k_decode(DecodeArgs a) {
   }
   if (a.S == 1) return;
 #pragma unroll 1
-  for (int y = w; y < 16 * R; y += kWaves) {
+  for (int y = wave; y < kRows; y += kWaves * G) {
     if (s_redo[y] == 0) continue;                  // uniform over the wavefront
-    const int row = rt * R * 16 + y, sq = row / a.H, h = row - sq * a.H;
+    const int row = rt * kRows + y, sq = row / a.H, h = row - sq * a.H;
     if (row >= a.rows) continue;
     const int seen = len - (a.S - 1 - sq), end = (int)(i1 * kTok);
     float v[8], mm, total;
@@ -577,17 +590,8 @@ __global__ __launch_bounds__(512) void k_decode_merge(DecodeArgs a, uint32_t nrt
   __shared__ float s_l[4];
   const int32_t b = (int32_t)(blockIdx.x / (uint32_t)a.rows);
   const int row = (int)(blockIdx.x % (uint32_t)a.rows);
-  const uint32_t per = run_tiles(a);
-  uint32_t g0 = 0, n = 0;                          // the request's first run, and runs
-  for (int32_t base = 0; base <= b; base += 64) {
-    const uint32_t own = seq_runs(a, base, per), incl = wave_scan(own);
-    if (b < base + 64) {
-      g0 += (uint32_t)__builtin_amdgcn_readlane((int)(incl - own), b - base);
-      n = (uint32_t)__builtin_amdgcn_readlane((int)own, b - base);
-    } else {
-      g0 += last_lane(incl);
-    }
-  }
+  const uint2 runs = a.runs_of[b];
+  const uint32_t g0 = runs.x, n = runs.y;
   if (n == 1) return;                              // written whole; uniform
   const int rt = row / rows_per_tile, rr = row % rows_per_tile;
   auto part_row = [&](uint32_t x) { return ((int64_t)(g0 + x) * nrt + rt) * rows_per_tile + rr; };
@@ -737,16 +741,19 @@ extern "C" int mx_latent_decode(const uint16_t* q, int64_t ldq_seq, int64_t ldq_
   a.lse = lse;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = a.part_o + p.part_rows * kLat;
+  a.runs_of = reinterpret_cast<uint2*>(a.part_ml + p.part_rows * 2);
   a.runs = p.runs;
   const dim3 grid(p.grid, p.row_tiles);
-  if (p.R == 1)
-    hipLaunchKernelGGL(k_decode<1>, grid, dim3(kThr), 0, stream, a);
+  if (p.rows == 16)
+    hipLaunchKernelGGL((k_decode<1, 1>), grid, dim3(kThr), 0, stream, a);
+  else if (p.rows == 32)
+    hipLaunchKernelGGL((k_decode<1, 2>), grid, dim3(2 * kThr), 0, stream, a);
   else
-    hipLaunchKernelGGL(k_decode<2>, grid, dim3(kThr), 0, stream, a);
+    hipLaunchKernelGGL((k_decode<2, 2>), grid, dim3(2 * kThr), 0, stream, a);
   MXQ_TRY(launch_status());
   if (p.grid > 1) {
     const dim3 rows((uint32_t)((int64_t)B * a.rows));
-    hipLaunchKernelGGL(k_decode_merge, rows, dim3(512), 0, stream, a, p.row_tiles, 16 * p.R);
+    hipLaunchKernelGGL(k_decode_merge, rows, dim3(512), 0, stream, a, p.row_tiles, p.rows);
   }
   return launch_status();
 }
