@@ -168,9 +168,9 @@ __device__ __forceinline__ void dma16(i32x4 r, uint32_t lds, uint32_t off, uint3
                :: "s"(lds), "v"(off), "s"(r), "s"(step) : "memory");
 }
 
-// This lane's part of the copies.  Wavefront w copies the 1 KB pieces w, w + 4,
-// .. of each sub-tile (4 rows of N or Y, 8 rows of R), so a lane's unit is the
-// same in every piece and only the row advances.
+// This lane's part of the copies.  Of NW wavefronts, w copies the 1 KB pieces w,
+// w + NW, .. of each sub-tile (4 rows of N or Y, 8 rows of R), so a lane's unit
+// is the same in every piece and only the row advances.
 struct Copy {
   uint32_t n, r, y;                              // offset in the first piece
   uint32_t dn, dr, dy;                           // from piece to piece (uniform)
@@ -178,6 +178,7 @@ struct Copy {
   uint32_t lds;                                  // wavefront's LDS byte in a tile
 };
 
+template <int NW>
 __device__ __forceinline__ Copy copy_plan(const void* lds, int64_t ldn, int64_t ldr, int64_t ldy) {
   Copy c;
   const uint32_t l = threadIdx.x & 63;
@@ -188,7 +189,7 @@ __device__ __forceinline__ Copy copy_plan(const void* lds, int64_t ldn, int64_t 
   c.n = r4 * c.ldn + uw;
   c.r = r8 * c.ldr + ur;
   c.y = r4 * c.ldy + uw;
-  c.dn = 16 * c.ldn; c.dr = 32 * c.ldr; c.dy = 16 * c.ldy;
+  c.dn = 4 * NW * c.ldn; c.dr = 8 * NW * c.ldr; c.dy = 4 * NW * c.ldy;
   c.lds = (uint32_t)reinterpret_cast<uintptr_t>(lds) + w * 1024;
   return c;
 }
@@ -200,6 +201,7 @@ __device__ __forceinline__ uint32_t span(int rows, uint32_t ld, uint32_t width) 
 }
 
 // Starts the copy of rows row0 .. row0 + 63 of `rows` to tile buffer `buf`.
+template <int NW>
 __device__ __forceinline__ void tile_copy(const Copy& c, const uint16_t* n, const uint16_t* r,
                                           const uint16_t* y, int row0, int rows, int buf) {
   const uint8_t* pn = reinterpret_cast<const uint8_t*>(n) + (int64_t)row0 * c.ldn;
@@ -210,11 +212,11 @@ __device__ __forceinline__ void tile_copy(const Copy& c, const uint16_t* n, cons
   const i32x4 dy = uniform(make_rsrc(py, span(rows - row0, c.ldy, 256)));
   const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)(c.lds + buf * kTile));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dma16(dn, lds + i * 4096, c.n, i * c.dn);
+  for (int i = 0; i < 16 / NW; ++i) dma16(dn, lds + i * (NW * 1024), c.n, i * c.dn);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) dma16(dr, lds + kOffR + i * 4096, c.r, i * c.dr);
+  for (int i = 0; i < 8 / NW; ++i) dma16(dr, lds + kOffR + i * (NW * 1024), c.r, i * c.dr);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dma16(dy, lds + kOffY + i * 4096, c.y, i * c.dy);
+  for (int i = 0; i < 16 / NW; ++i) dma16(dy, lds + kOffY + i * (NW * 1024), c.y, i * c.dy);
 }
 
 // Every copy this wavefront started has landed, and so, past the barrier, has
@@ -280,21 +282,36 @@ __device__ __forceinline__ bf16x8 tr_pair(const uint8_t* a, const uint8_t* b) {
   const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)b);
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
-__device__ __forceinline__ bf16x8 x_tr(const uint8_t* t, const Reads& p, int j, int d) {
-  if (d < 4) {
-    const uint32_t o = p.tn ^ (d << 6);
-    return tr_pair(t + o + j * 4096, t + (o ^ 32) + 2048 + j * 4096);
-  }
-  const uint32_t o = p.tr ^ ((d - 4) << 6);
-  return tr_pair(t + kOffR + o + j * 2048, t + kOffR + (o ^ 16) + 1024 + j * 2048);
-}
-__device__ __forceinline__ bf16x8 y_tr(const uint8_t* t, const Reads& p, int j, int d) {
+// From a sub-tile of 128 columns (N or Y) or of 64 (R) at t.
+__device__ __forceinline__ bf16x8 wide_tr(const uint8_t* t, const Reads& p, int j, int d) {
   const uint32_t o = p.tn ^ (d << 6);
-  return tr_pair(t + kOffY + o + j * 4096, t + kOffY + (o ^ 32) + 2048 + j * 4096);
+  return tr_pair(t + o + j * 4096, t + (o ^ 32) + 2048 + j * 4096);
+}
+__device__ __forceinline__ bf16x8 rope_tr(const uint8_t* t, const Reads& p, int j, int d) {
+  const uint32_t o = p.tr ^ (d << 6);
+  return tr_pair(t + o + j * 2048, t + (o ^ 16) + 1024 + j * 2048);
 }
 
 __device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// A run of products with their tile operands read DEPTH ahead: read(i) gives
+// operand i, use(i, operand) multiplies it.  The scheduling barriers keep that
+// order: left alone, the compiler reads each operand right before its use, and
+// every product waits out the LDS latency.
+template <int N, int DEPTH, class Read, class Use>
+__device__ __forceinline__ void pipelined(Read read, Use use) {
+  bf16x8 f[N];
+#pragma unroll
+  for (int i = 0; i < DEPTH && i < N; ++i) f[i] = read(i);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i + DEPTH < N) f[i + DEPTH] = read(i + DEPTH);
+    use(i, f[i]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
 // The tile row that register i of a 32-row block holds in lane half h.
@@ -345,13 +362,26 @@ __device__ __forceinline__ bool any_nonfinite(const f32x16 (&acc)[NT]) {
   return bad;
 }
 
+__device__ __forceinline__ bool frag_nonfinite(bf16x8 f) {
+  const uint4 w = __builtin_bit_cast(uint4, f);
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+    bad |= (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+  }
+  return bad;
+}
+
 // ---------------------------------------------------------------------------
 // Rows redone by themselves.  A hidden key's probability is an exact 0, but the
 // matrix unit still multiplies it, and 0 * NaN or 0 * infinity would reach
 // rows that the mask keeps apart.  Such a product always leaves a NaN, so rows
 // whose result is not finite are computed again over their visible keys (or
 // queries) alone, one wavefront a row, before they are written.  Costs the plain
-// path one check of the results; a row with finite operands never comes here.
+// path one check of the results; a row with finite operands never comes here,
+// nor one whose own operand or visible logits are already not finite (its result
+// is not either, and redoing all of them would make a diverged model crawl).
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ float bf(const uint16_t* p) {
@@ -514,141 +544,123 @@ __device__ __forceinline__ int keys_seen(const AttnArgs& a, const SeqTile& s, in
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  A workgroup takes 128 QT query rows of one head, 32 QT a wavefront.
+// Forward.  A workgroup of four wavefronts takes 128 query rows of one head, 32 a
+// wavefront; two workgroups share a CU, so that one's exponentials run beside
+// the other's products.
 // ---------------------------------------------------------------------------
 
-template <int QT>
-__global__ __launch_bounds__(kThr, QT == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
+__global__ __launch_bounds__(kThr, 2) void k_attn_fwd(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTile];
-  constexpr int BM = 128 * QT;
+  constexpr int BM = 128;
   const int head = blockIdx.x % a.H;
   const SeqTile st = find_tile<false>(a, blockIdx.x / a.H, BM);
   if (!st.ok) return;                              // uniform over the workgroup
   const int l = threadIdx.x & 63, n = l & 31, h = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int wrow0 = st.row0 + w * 32 * QT;         // the wavefront's first row
+  const int wrow0 = st.row0 + w * 32, row = wrow0 + n;   // the wavefront's first row, this lane's
   const uint16_t* kn = a.kn.p + st.k0 * a.kn.ld + head * a.kn.ldh;
   const uint16_t* kr = a.kr + st.k0 * a.ldr;
   const uint16_t* v = a.v.p + st.k0 * a.v.ld + head * a.v.ldh;
-  const Copy cp = copy_plan(lds, a.kn.ld, a.ldr, a.v.ld);
+  const Copy cp = copy_plan<4>(lds, a.kn.ld, a.ldr, a.v.ld);
   const Reads rp = read_plan();
 
   // keys that any row of the workgroup sees, and the wavefront's first and last row
   const int last = (st.row0 + BM < st.lq ? st.row0 + BM : st.lq) - 1;
   const int kend = keys_seen(a, st, last);
-  const int wfirst = keys_seen(a, st, wrow0), wlast = keys_seen(a, st, wrow0 + 32 * QT - 1);
-  if (kend > 0) tile_copy(cp, kn, kr, v, 0, st.lk, 0);
+  const int wfirst = keys_seen(a, st, wrow0), wlast = keys_seen(a, st, wrow0 + 31);
+  const int lim = keys_seen(a, st, row);
+  if (kend > 0) tile_copy<4>(cp, kn, kr, v, 0, st.lk, 0);
 
-  bf16x8 q[QT][kSteps];
-  int lim[QT];
+  bf16x8 q[kSteps];
   const uint16_t* qp = a.q.p + st.q0 * a.q.ld + head * a.q.ldh;
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    own_rows(q[t], qp, a.q.ld, qp + kNope, a.q.ld, wrow0 + 32 * t + n, st.lq);
-    lim[t] = keys_seen(a, st, wrow0 + 32 * t + n);
-  }
-  f32x16 o[QT][4] = {};
-  float m[QT], sum[QT];
-#pragma unroll
-  for (int t = 0; t < QT; ++t) m[t] = -__builtin_inff(), sum[t] = 0.0f;
-
+  own_rows(q, qp, a.q.ld, qp + kNope, a.q.ld, row, st.lq);
+  f32x16 o[4] = {};
+  float m = -__builtin_inff(), sum = 0.0f;         // reference (powers of two), total
   const float c = a.scale * kLog2e;
   int buf = 0;
   for (int k0 = 0; k0 < kend; k0 += kBN, buf ^= 1) {
     tile_wait();
-    if (k0 + kBN < kend) tile_copy(cp, kn, kr, v, k0 + kBN, st.lk, buf ^ 1);
+    if (k0 + kBN < kend) tile_copy<4>(cp, kn, kr, v, k0 + kBN, st.lk, buf ^ 1);
     if (k0 >= wlast) continue;                     // nothing seen by this wavefront
     const uint8_t* tile = lds + buf * kTile;
-    f32x16 s[QT][2] = {};
-#pragma unroll
-    for (int kk = 0; kk < kSteps; ++kk) {
-      const bf16x8 k0f = x_frag(tile, rp, 0, kk), k1f = x_frag(tile, rp, 1, kk);
-#pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        s[t][0] = mfma(k0f, q[t][kk], s[t][0]);
-        s[t][1] = mfma(k1f, q[t][kk], s[t][1]);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);             // keeps the phases' registers apart
+    f32x16 s[2] = {};
+    pipelined<2 * kSteps, 6>([&](int i) { return x_frag(tile, rp, i & 1, i >> 1); },
+                             [&](int i, bf16x8 f) { s[i & 1] = mfma(f, q[i >> 1], s[i & 1]); });
     if (k0 + kBN > wfirst) {                       // some row does not see all of the tile
-#pragma unroll
-      for (int t = 0; t < QT; ++t)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (k0 + 32 * b + reg_row(i, h) >= lim[t]) s[t][b][i] = -__builtin_inff();
-    }
-    bf16x8 p[QT][4];
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
-      float mx = s[t][0][0];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        mx = __builtin_fmaxf(mx, s[t][0][i]);
-        mx = __builtin_fmaxf(mx, s[t][1][i]);
-      }
-      mx = half_max(mx) * c;
-      if (__builtin_expect(__ballot(mx > m[t] + kSlack) != 0, 0)) {
-        const float mn = __builtin_fmaxf(m[t], mx);
-        const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m[t] - mn);
-        m[t] = mn;
-        sum[t] *= alpha;
-#pragma unroll
-        for (int d = 0; d < 4; ++d) o[t][d] *= alpha;
-      }
-      const float mc = m[t] == -__builtin_inff() ? 0.0f : m[t];   // nothing seen yet: all zeros
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][b][i], c, -mc));
-          s[t][b][i] = e;
-          sum[t] += e;
-        }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) p[t][j] = slab(s[t][j >> 1], j & 1);
+        for (int i = 0; i < 16; ++i)
+          if (k0 + 32 * b + reg_row(i, h) >= lim) s[b][i] = -__builtin_inff();
     }
-    __builtin_amdgcn_sched_barrier(0);
+    float mx = s[0][0];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      mx = __builtin_fmaxf(mx, s[0][i]);
+      mx = __builtin_fmaxf(mx, s[1][i]);
+    }
+    mx = half_max(mx) * c;
+    if (__builtin_expect(__ballot(mx > m + kSlack) != 0, 0)) {
+      const float mn = __builtin_fmaxf(m, mx);
+      const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      sum *= alpha;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] *= alpha;
+    }
+    const float mc = m == -__builtin_inff() ? 0.0f : m;   // nothing seen yet: all zeros
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], c, -mc));
+        s[b][i] = e;
+        sum += e;
+      }
+    bf16x8 p[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = slab(s[j >> 1], j & 1);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const bf16x8 vf = y_tr(tile, rp, j, d);
-#pragma unroll
-        for (int t = 0; t < QT; ++t) o[t][d] = mfma(vf, p[t][j], o[t][d]);
-      }
+      for (int d = 0; d < 4; ++d) o[d] = mfma(wide_tr(tile + kOffY, rp, j, d), p[j], o[d]);
   }
-  uint64_t redo[QT];
+  const float total = half_sum(sum);
+  // a row that sees nothing: zeros, and minus infinity
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const uint64_t bad = __ballot(any_nonfinite(o) && row < st.lq && total == total);
+  if (row < st.lq) {
+    uint16_t* p = a.out.p + (st.q0 + row) * a.out.ld + head * a.out.ldh;
 #pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    const int row = wrow0 + 32 * t + n;
-    const float total = half_sum(sum[t]);
-    // a row that sees nothing: zeros, and minus infinity
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    redo[t] = __ballot(any_nonfinite(o[t]) && row < st.lq);
-    if (row < st.lq) {
-      uint16_t* p = a.out.p + (st.q0 + row) * a.out.ld + head * a.out.ldh;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) store_block(o[t][d], inv, p + 32 * d);
-      if (h == 0)
-        a.lse[head * a.ldl + st.q0 + row] =
-            total == 0.0f ? -__builtin_inff() : kLn2 * (m[t] + __builtin_amdgcn_logf(total));
-    }
+    for (int d = 0; d < 4; ++d) store_block(o[d], inv, p + 32 * d);
+    if (h == 0)
+      a.lse[head * a.ldl + st.q0 + row] =
+          total == 0.0f ? -__builtin_inff() : kLn2 * (m + __builtin_amdgcn_logf(total));
   }
   if (!a.causal) return;
-#pragma unroll 1
-  for (int t = 0; t < QT; ++t) {
-    uint32_t rows = (uint32_t)redo[t] | (uint32_t)(redo[t] >> 32);
-    while (rows) {
-      const int i = wrow0 + 32 * t + __builtin_ctz(rows);
-      rows &= rows - 1;
-      redo_output(a, st, head, i, keys_seen(a, st, i));
-    }
+  uint32_t redo = (uint32_t)bad | (uint32_t)(bad >> 32);
+  while (redo) {
+    const int i = wrow0 + __builtin_ctz(redo);
+    redo &= redo - 1;
+    redo_output(a, st, head, i, keys_seen(a, st, i));
   }
 }
 
 // ---------------------------------------------------------------------------
+// Backward.  Eight wavefronts, two a SIMD: a pair shares 32 rows of the
+// workgroup's 128.  Of each tile of 64, one of the pair forms P and dS against
+// the first 32 rows, the other against the last, and they hand each other the
+// operands through LDS (as they are, in lane order).  Then each takes half of
+// the result's columns over all 64.  That halves the sums a wavefront holds,
+// which is what lets two of them share a SIMD: one's exponentials run beside
+// the other's products.
+// ---------------------------------------------------------------------------
+
+constexpr int kBwdThr = 512, kPairs = 4;
+struct Exchange {
+  uint4 f[kPairs][2][4][64];                     // pair, half, P slabs and dS slabs, lane
+};
+
 // Backward, queries: dQ and D, which the keys' kernel reads.
 //
 // D is wanted before the loop that could sum it.  The BF16 output gives it but
@@ -656,158 +668,152 @@ __global__ __launch_bounds__(kThr, QT == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) 
 // few keys hold a row's weight (dS is then a difference of nearly equal
 // numbers).  With dS' = P * (dP - d), the row sum r of dS' is D - d, and
 //   dQ = scale * (dS' K - r (P K)):
-// the products P K and dS' K share the reads of K, which bound this kernel.
-// ---------------------------------------------------------------------------
-
-template <int QT>
-__global__ __launch_bounds__(kThr, 1) void k_attn_dq(AttnArgs a) {
+// the products P K and dS' K share the reads of K.
+__global__ __launch_bounds__(kBwdThr, 2) void k_attn_dq(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTile];
-  constexpr int BM = 128 * QT;
+  __shared__ __attribute__((aligned(16))) Exchange ex;
+  __shared__ float s_rest[kPairs][2][32];
+  __shared__ uint32_t s_bad[kPairs][2];
+  constexpr int BM = 32 * kPairs;
   const int head = blockIdx.x % a.H;
   const SeqTile st = find_tile<false>(a, blockIdx.x / a.H, BM);
   if (!st.ok) return;
   const int l = threadIdx.x & 63, n = l & 31, h = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int wrow0 = st.row0 + w * 32 * QT;
+  const int pair = w & 3, half = w >> 2;
+  const int wrow0 = st.row0 + pair * 32, row = wrow0 + n;
   const Head x = head_of(a, st, head);
-  const Copy cp = copy_plan(lds, a.kn.ld, a.ldr, a.v.ld);
-  const Reads rp = read_plan();
+  const Copy cp = copy_plan<8>(lds, a.kn.ld, a.ldr, a.v.ld);
+  Reads rp = read_plan();
   const int last = (st.row0 + BM < st.lq ? st.row0 + BM : st.lq) - 1;
   const int kend = keys_seen(a, st, last);
-  const int wfirst = keys_seen(a, st, wrow0), wlast = keys_seen(a, st, wrow0 + 32 * QT - 1);
-  if (kend > 0) tile_copy(cp, x.kn, x.kr, x.v, 0, st.lk, 0);
+  const int wfirst = keys_seen(a, st, wrow0), wlast = keys_seen(a, st, wrow0 + 31);
+  const int lim = keys_seen(a, st, row);
+  if (kend > 0) tile_copy<8>(cp, x.kn, x.kr, x.v, 0, st.lk, 0);
 
-  bf16x8 q[QT][kSteps], g[QT][kVSteps];
-  float lse2[QT], delta[QT];                       // lse in powers of two; D
-  int lim[QT];
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    const int row = wrow0 + 32 * t + n;
-    lim[t] = keys_seen(a, st, row);
-    own_rows(q[t], x.q, a.q.ld, x.q + kNope, a.q.ld, row, st.lq);
-    own_rows(g[t], x.g, a.dout.ld, nullptr, 0, row, st.lq);
+  bf16x8 q[kSteps], g[kVSteps];
+  own_rows(q, x.q, a.q.ld, x.q + kNope, a.q.ld, row, st.lq);
+  own_rows(g, x.g, a.dout.ld, nullptr, 0, row, st.lq);
+  float delta = 0.0f;                              // d
+  {
     bf16x8 of[kVSteps];
     own_rows(of, x.o, a.o.ld, nullptr, 0, row, st.lq);
-    float d = 0.0f;
 #pragma unroll
     for (int s = 0; s < kVSteps; ++s)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d = __builtin_fmaf((float)of[s][e], (float)g[t][s][e], d);
-    delta[t] = half_sum(d);
-    float z = -__builtin_inff();
-    if (row < st.lq) z = x.lse[row];
-    lse2[t] = z == -__builtin_inff() ? __builtin_inff() : z * kLog2e - kShift;   // no keys: P = 0
+      for (int e = 0; e < 8; ++e) delta = __builtin_fmaf((float)of[s][e], (float)g[s][e], delta);
+    delta = half_sum(delta);
   }
+  float lse2 = row < st.lq ? x.lse[row] : -__builtin_inff();   // in powers of two
+  lse2 = lse2 == -__builtin_inff() ? __builtin_inff() : lse2 * kLog2e - kShift;   // no keys: P = 0
 
-  f32x16 dq[QT][6] = {}, pk[QT][6] = {};
-  float rest[QT] = {};                             // row sums of dS'
+  // this wavefront's columns: N blocks 2 half, 2 half + 1 and R block half
+  f32x16 dq[3] = {}, pk[3] = {};
+  float rest = 0.0f;                               // row sum of this half's dS'
   const float c = a.scale * kLog2e;
   int buf = 0;
   for (int k0 = 0; k0 < kend; k0 += kBN, buf ^= 1) {
     tile_wait();
-    if (k0 + kBN < kend) tile_copy(cp, x.kn, x.kr, x.v, k0 + kBN, st.lk, buf ^ 1);
-    if (k0 >= wlast) continue;
+    if (k0 + kBN < kend) tile_copy<8>(cp, x.kn, x.kr, x.v, k0 + kBN, st.lk, buf ^ 1);
+    const bool live = k0 < wlast;                  // the same for both of a pair
     const uint8_t* tile = lds + buf * kTile;
+    // the units' addresses are formed again in every tile: kept, they cost too many registers
+    asm volatile("" : "+v"(rp.n), "+v"(rp.r), "+v"(rp.tn), "+v"(rp.tr));
+    if (live) {
+      f32x16 s = {}, dp = {};
+      // the two chains alternate while both last
+      pipelined<kSteps + kVSteps, 4>(
+          [&](int i) {
+            return i < 2 * kVSteps && (i & 1) ? y_frag(tile, rp, half, i >> 1)
+                                              : x_frag(tile, rp, half, i < 2 * kVSteps ? i >> 1 : i - kVSteps);
+          },
+          [&](int i, bf16x8 f) {
+            if (i < 2 * kVSteps && (i & 1))
+              dp = mfma(f, g[i >> 1], dp);
+            else
+              s = mfma(f, q[i < 2 * kVSteps ? i >> 1 : i - kVSteps], s);
+          });
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      f32x16 s[QT] = {}, dp[QT] = {};
+      for (int i = 0; i < 16; ++i) {
+        s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse2));
+        dp[i] = s[i] * (dp[i] - delta);
+      }
+      if (k0 + kBN > wfirst) {
 #pragma unroll
-      for (int kk = 0; kk < kSteps; ++kk) {
-        const bf16x8 f = x_frag(tile, rp, b, kk);
-#pragma unroll
-        for (int t = 0; t < QT; ++t) s[t] = mfma(f, q[t][kk], s[t]);
+        for (int i = 0; i < 16; ++i)
+          if (k0 + 32 * half + reg_row(i, h) >= lim) s[i] = 0.0f, dp[i] = 0.0f;
       }
 #pragma unroll
-      for (int kk = 0; kk < kVSteps; ++kk) {
-        const bf16x8 f = y_frag(tile, rp, b, kk);
+      for (int i = 0; i < 16; ++i) rest += dp[i];
 #pragma unroll
-        for (int t = 0; t < QT; ++t) dp[t] = mfma(f, g[t][kk], dp[t]);
+      for (int j = 0; j < 2; ++j) {
+        ex.f[pair][half][j][l] = __builtin_bit_cast(uint4, slab(s, j));
+        ex.f[pair][half][2 + j][l] = __builtin_bit_cast(uint4, slab(dp, j));
       }
-      __builtin_amdgcn_sched_barrier(0);           // keeps the phases' registers apart
-      bf16x8 pf[QT][2], ds[QT][2];
-#pragma unroll
-      for (int t = 0; t < QT; ++t) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], c, -lse2[t]));
-          s[t][i] = p;
-          dp[t][i] = p * (dp[t][i] - delta[t]);
-        }
-        if (k0 + kBN > wfirst) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (k0 + 32 * b + reg_row(i, h) >= lim[t]) s[t][i] = 0.0f, dp[t][i] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) rest[t] += dp[t][i];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) pf[t][j] = slab(s[t], j), ds[t][j] = slab(dp[t], j);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int d = 0; d < 6; ++d) {
-          const bf16x8 f = x_tr(tile, rp, 2 * b + j, d);
-#pragma unroll
-          for (int t = 0; t < QT; ++t) {
-            dq[t][d] = mfma(f, ds[t][j], dq[t][d]);
-            pk[t][d] = mfma(f, pf[t][j], pk[t][d]);
-          }
-        }
+    }
+    __syncthreads();
+    if (live) {
+      bf16x8 p[4], ds[4];
+      pipelined<12, 3>(
+          [&](int i) {
+            const int j = i / 3, d = i % 3;
+            if (d == 0) {
+              p[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][j & 1][l]);
+              ds[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][2 + (j & 1)][l]);
+            }
+            return d < 2 ? wide_tr(tile, rp, j, 2 * half + d) : rope_tr(tile + kOffR, rp, j, half);
+          },
+          [&](int i, bf16x8 f) {
+            dq[i % 3] = mfma(f, ds[i / 3], dq[i % 3]);
+            pk[i % 3] = mfma(f, p[i / 3], pk[i % 3]);
+          });
     }
   }
+  rest = half_sum(rest);
+  if (h == 0) s_rest[pair][half][n] = rest;
+  __syncthreads();
+  const float r = (s_rest[pair][0][n] + s_rest[pair][1][n]) * kUnshift;
 #pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    const int row = wrow0 + 32 * t + n;
-    const float r = half_sum(rest[t]) * kUnshift;
+  for (int d = 0; d < 3; ++d) dq[d] -= pk[d] * r;
+  const uint64_t bad = __ballot(any_nonfinite(dq) && row < st.lq && lse2 == lse2 && delta == delta);
+  if (l == 0) s_bad[pair][half] = a.causal ? (uint32_t)bad | (uint32_t)(bad >> 32) : 0u;
+  __syncthreads();
+  uint32_t redo = s_bad[pair][0] | s_bad[pair][1];
+  if (row < st.lq && h == 0 && half == 0) a.delta[head * a.Tq + st.q0 + row] = delta + r;
+  if (row < st.lq && !((redo >> n) & 1)) {
+    uint16_t* p = a.dq.p + (st.q0 + row) * a.dq.ld + head * a.dq.ldh;
 #pragma unroll
-    for (int d = 0; d < 6; ++d) dq[t][d] -= pk[t][d] * r;
-    if (row < st.lq && h == 0) a.delta[head * a.Tq + st.q0 + row] = delta[t] + r;
+    for (int d = 0; d < 2; ++d) store_block(dq[d], a.scale * kUnshift, p + 64 * half + 32 * d);
+    store_block(dq[2], a.scale * kUnshift, p + kNope + 32 * half);
   }
-  uint64_t redo[QT];
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    const int row = wrow0 + 32 * t + n;
-    redo[t] = __ballot(any_nonfinite(dq[t]) && row < st.lq);
-    if (row < st.lq) {
-      uint16_t* p = a.dq.p + (st.q0 + row) * a.dq.ld + head * a.dq.ldh;
-#pragma unroll
-      for (int d = 0; d < 6; ++d) store_block(dq[t][d], a.scale * kUnshift, p + 32 * d);
-    }
-  }
-  if (!a.causal) return;
-#pragma unroll 1
-  for (int t = 0; t < QT; ++t) {
-    uint32_t rows = (uint32_t)redo[t] | (uint32_t)(redo[t] >> 32);
-    while (rows) {
-      const int i = wrow0 + 32 * t + __builtin_ctz(rows);
-      rows &= rows - 1;
-      redo_dq(a, st, head, i, keys_seen(a, st, i));
-    }
+  if (half) return;
+  while (redo) {
+    const int i = wrow0 + __builtin_ctz(redo);
+    redo &= redo - 1;
+    redo_dq(a, st, head, i, keys_seen(a, st, i));
   }
 }
 
-// ---------------------------------------------------------------------------
-// Backward, keys: dK, dV.  A workgroup takes 128 keys of one head, 32 a
-// wavefront, and walks the queries that see them.  The rotary part of dK is
-// summed over the heads by k_attn_drope, from one FP32 part a head, in head order.
-// ---------------------------------------------------------------------------
-
-__global__ __launch_bounds__(kThr, 1) void k_attn_dkv(AttnArgs a) {
+// Backward, keys: dK, dV, walking the queries that see the workgroup's keys.  The
+// rotary part of dK is summed over the heads by k_attn_drope, from one FP32 part
+// a head, in head order.
+__global__ __launch_bounds__(kBwdThr, 2) void k_attn_dkv(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTile];
+  __shared__ __attribute__((aligned(16))) Exchange ex;
   __shared__ __attribute__((aligned(16))) float stat[2][2][kBN];   // lse (powers of two), D
-  constexpr int BM = 128;
+  __shared__ uint32_t s_bad[kPairs][2];
+  constexpr int BM = 32 * kPairs;
   const int head = blockIdx.x % a.H;
   const SeqTile st = find_tile<true>(a, blockIdx.x / a.H, BM);
   if (!st.ok) return;
   const int l = threadIdx.x & 63, n = l & 31, h = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int wkey = st.row0 + w * 32, row = wkey + n;   // the wavefront's keys, this lane's
+  const int pair = w & 3, half = w >> 2;
+  const int wkey = st.row0 + pair * 32, row = wkey + n;   // the pair's keys, this lane's
   const int diff = st.lk - st.lq;                  // query i sees keys j <= i + diff
   const Head x = head_of(a, st, head);
-  const Copy cp = copy_plan(lds, a.q.ld, a.q.ld, a.dout.ld);
-  const Reads rp = read_plan();
+  const Copy cp = copy_plan<8>(lds, a.q.ld, a.q.ld, a.dout.ld);
+  Reads rp = read_plan();
 
   // queries from lim on see this lane's key; the tile starts at the first that sees any
   const int lim = !a.causal || row - diff < 0 ? 0 : row - diff;
@@ -817,7 +823,7 @@ __global__ __launch_bounds__(kThr, 1) void k_attn_dkv(AttnArgs a) {
     q0 = f <= 0 ? 0 : f >= st.lq ? st.lq : f;
     q0 = q0 / kBN * kBN;
   }
-  const int wlim = !a.causal ? 0 : wkey - diff;    // first query that sees the wavefront's first key
+  const int wlim = !a.causal ? 0 : wkey - diff;    // first query that sees the pair's first key
   // lse and D of a tile's queries, one value a lane of the first two wavefronts
   auto stat_of = [&](int r0) {
     const int i = r0 + l;
@@ -828,13 +834,16 @@ __global__ __launch_bounds__(kThr, 1) void k_attn_dkv(AttnArgs a) {
   float z = 0.0f;
   if (q0 < st.lq) {
     z = stat_of(q0);
-    tile_copy(cp, x.q, x.q + kNope, x.g, q0, st.lq, 0);
+    tile_copy<8>(cp, x.q, x.q + kNope, x.g, q0, st.lq, 0);
   }
   bf16x8 k[kSteps], v[kVSteps];
   own_rows(k, x.kn, a.kn.ld, x.kr, a.ldr, row, st.lk);
   own_rows(v, x.v, a.v.ld, nullptr, 0, row, st.lk);
 
-  f32x16 dk[6] = {}, dv[4] = {};
+  // this wavefront's columns: all of dV (half 0) or of dK's own part (half 1), and
+  // block `half` of the rotary part
+  f32x16 wide[4] = {}, rope = {};
+  const uint32_t side = half ? 0 : kOffY, op = half ? 2 : 0;   // queries and dS, or dO and P
   const float c = a.scale * kLog2e;
   int buf = 0;
   for (; q0 < st.lq; q0 += kBN, buf ^= 1) {
@@ -845,74 +854,98 @@ __global__ __launch_bounds__(kThr, 1) void k_attn_dkv(AttnArgs a) {
     tile_wait();
     if (q0 + kBN < st.lq) {
       z = stat_of(q0 + kBN);
-      tile_copy(cp, x.q, x.q + kNope, x.g, q0 + kBN, st.lq, buf ^ 1);
+      tile_copy<8>(cp, x.q, x.q + kNope, x.g, q0 + kBN, st.lq, buf ^ 1);
     }
-    if (q0 + kBN <= wlim) continue;                // no query here sees the wavefront's keys
-    const bool partial = q0 + kBN > st.lq || q0 < wlim + 31;
+    const bool live = q0 + kBN > wlim;             // some query here sees the pair's keys
     const uint8_t* tile = lds + buf * kTile;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    // the units' addresses are formed again in every tile: kept, they cost too many registers
+    asm volatile("" : "+v"(rp.n), "+v"(rp.r), "+v"(rp.tn), "+v"(rp.tr));
+    if (live) {
       f32x16 s = {}, dp = {};
-#pragma unroll
-      for (int kk = 0; kk < kSteps; ++kk) s = mfma(x_frag(tile, rp, b, kk), k[kk], s);
-#pragma unroll
-      for (int kk = 0; kk < kVSteps; ++kk) dp = mfma(y_frag(tile, rp, b, kk), v[kk], dp);
+      // the two chains alternate while both last
+      pipelined<kSteps + kVSteps, 4>(
+          [&](int i) {
+            return i < 2 * kVSteps && (i & 1) ? y_frag(tile, rp, half, i >> 1)
+                                              : x_frag(tile, rp, half, i < 2 * kVSteps ? i >> 1 : i - kVSteps);
+          },
+          [&](int i, bf16x8 f) {
+            if (i < 2 * kVSteps && (i & 1))
+              dp = mfma(f, v[i >> 1], dp);
+            else
+              s = mfma(f, k[i < 2 * kVSteps ? i >> 1 : i - kVSteps], s);
+          });
 #pragma unroll
       for (int q4 = 0; q4 < 4; ++q4) {
-        const int r4 = 32 * b + 8 * q4 + 4 * h;
+        const int r4 = 32 * half + 8 * q4 + 4 * h;
         const f32x4 ls = *reinterpret_cast<const f32x4*>(&stat[buf][0][r4]);
         const f32x4 dl = *reinterpret_cast<const f32x4*>(&stat[buf][1][r4]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = 4 * q4 + e;
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -ls[e]));
-          s[i] = p;
-          dp[i] = p * (dp[i] - dl[e]);
+          s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -ls[e]));
+          dp[i] = s[i] * (dp[i] - dl[e]);
         }
       }
-      if (partial) {
+      if (q0 + kBN > st.lq || q0 < wlim + 31) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int qi = q0 + 32 * b + reg_row(i, h);
+          const int qi = q0 + 32 * half + reg_row(i, h);
           if (qi < lim || qi >= st.lq) s[i] = 0.0f, dp[i] = 0.0f;
         }
       }
-      const bf16x8 pf[2] = {slab(s, 0), slab(s, 1)}, df[2] = {slab(dp, 0), slab(dp, 1)};
-      __builtin_amdgcn_sched_barrier(0);           // keeps the phases' registers apart
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int d = 0; d < 4; ++d) dv[d] = mfma(y_tr(tile, rp, 2 * b + j, d), pf[j], dv[d]);
-#pragma unroll
-        for (int d = 0; d < 6; ++d) dk[d] = mfma(x_tr(tile, rp, 2 * b + j, d), df[j], dk[d]);
+        ex.f[pair][half][j][l] = __builtin_bit_cast(uint4, slab(s, j));
+        ex.f[pair][half][2 + j][l] = __builtin_bit_cast(uint4, slab(dp, j));
       }
     }
+    __syncthreads();
+    if (live) {
+      bf16x8 f0[4], ds[4];
+      pipelined<20, 3>(
+          [&](int i) {
+            const int j = i / 5, d = i % 5;
+            if (d == 0) f0[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][op + (j & 1)][l]);
+            if (d == 4) ds[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][2 + (j & 1)][l]);
+            return d < 4 ? wide_tr(tile + side, rp, j, d) : rope_tr(tile + kOffR, rp, j, half);
+          },
+          [&](int i, bf16x8 f) {
+            if (i % 5 < 4)
+              wide[i % 5] = mfma(f, f0[i / 5], wide[i % 5]);
+            else
+              rope = mfma(f, ds[i / 5], rope);
+          });
+    }
   }
-  const uint64_t bad = __ballot((any_nonfinite(dk) || any_nonfinite(dv)) && row < st.lk);
-  if (row < st.lk) {
+  bool nf = any_nonfinite(wide), own = false;      // own: the key itself is not finite
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) own |= frag_nonfinite(k[i]);
+#pragma unroll
+  for (int i = 0; i < kVSteps; ++i) own |= frag_nonfinite(v[i]);
+  own = __shfl_xor((int)own, 32, 64) | (int)own;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) nf |= !(__builtin_fabsf(rope[i]) < __builtin_inff());
+  const uint64_t bad = __ballot(nf && row < st.lk && !own);
+  __syncthreads();
+  if (l == 0) s_bad[pair][half] = a.causal ? (uint32_t)bad | (uint32_t)(bad >> 32) : 0u;
+  __syncthreads();
+  uint32_t redo = s_bad[pair][0] | s_bad[pair][1];
+  if (row < st.lk && !((redo >> n) & 1)) {
     const int64_t kr = st.k0 + row;
-    uint16_t* pv = a.dv.p + kr * a.dv.ld + head * a.dv.ldh;
-    uint16_t* pk = a.dkn.p + kr * a.dkn.ld + head * a.dkn.ldh;
-    float* rp2 = a.rope_part + (head * a.Tk + kr) * kRope;
+    uint16_t* p = half ? a.dkn.p + kr * a.dkn.ld + head * a.dkn.ldh : a.dv.p + kr * a.dv.ld + head * a.dv.ldh;
+    const float mul = half ? a.scale * kUnshift : kUnshift;
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      store_block(dv[d], kUnshift, pv + 32 * d);
-      store_block(dk[d], a.scale * kUnshift, pk + 32 * d);
-    }
+    for (int d = 0; d < 4; ++d) store_block(wide[d], mul, p + 32 * d);
+    float* pr = a.rope_part + (head * a.Tk + kr) * kRope + 32 * half + 4 * h;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x16 b = dk[4 + t] * kUnshift;
-        *reinterpret_cast<f32x4*>(rp2 + 32 * t + 8 * i + 4 * h) =
-            f32x4{b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]};
-      }
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<f32x4*>(pr + 8 * i) =
+          f32x4{rope[4 * i], rope[4 * i + 1], rope[4 * i + 2], rope[4 * i + 3]} * kUnshift;
   }
-  if (!a.causal) return;
-  uint32_t rows = (uint32_t)bad | (uint32_t)(bad >> 32);
-  while (rows) {
-    const int j = wkey + __builtin_ctz(rows);
-    rows &= rows - 1;
+  if (half) return;
+  while (redo) {
+    const int j = wkey + __builtin_ctz(redo);
+    redo &= redo - 1;
     redo_dkv(a, st, head, j, j - diff < 0 ? 0 : j - diff);
   }
 }
@@ -996,10 +1029,6 @@ int grid_of(int64_t T, int64_t rows, const AttnArgs& a, uint32_t* n) {
   return MXQ_OK;
 }
 
-// 256-row query tiles halve the LDS reads of each product; 128-row tiles keep
-// more CUs busy when there are few rows.
-bool big_tiles(const AttnArgs&) { return false; }
-
 }  // namespace
 
 }  // namespace mxq
@@ -1019,12 +1048,8 @@ extern "C" int latent_attention(const mxq_latent_attn* d, uint16_t* o, int64_t l
   a.lse = lse;
   a.ldl = ldl;
   uint32_t n;
-  const bool big = big_tiles(a);
-  MXQ_TRY(grid_of(a.Tq, big ? 256 : 128, a, &n));
-  if (big)
-    hipLaunchKernelGGL(k_attn_fwd<1>, dim3(n), dim3(kThr), 0, stream, a);
-  else
-    hipLaunchKernelGGL(k_attn_fwd<1>, dim3(n), dim3(kThr), 0, stream, a);
+  MXQ_TRY(grid_of(a.Tq, 128, a, &n));
+  hipLaunchKernelGGL(k_attn_fwd, dim3(n), dim3(kThr), 0, stream, a);
   return launch_status();
 }
 
@@ -1050,8 +1075,7 @@ extern "C" int latent_attention_backward(
   if (need > 0 && !workspace) return MXQ_ERR_NULL;
   if (!aligned16(workspace)) return MXQ_ERR_ALIGN;
   uint32_t nq, nk, nr;
-  const bool big = big_tiles(a);
-  MXQ_TRY(grid_of(a.Tq, big ? 256 : 128, a, &nq));
+  MXQ_TRY(grid_of(a.Tq, 128, a, &nq));
   MXQ_TRY(grid_of(a.Tk, 128, a, &nk));
   nr = (uint32_t)((a.Tk * (kRope / 4) + kThr - 1) / kThr);     // at most 2^26
   a.o = {o, ldo, ldo_head};
@@ -1066,14 +1090,11 @@ extern "C" int latent_attention_backward(
   a.rope_part = static_cast<float*>(workspace);
   a.delta = a.rope_part + a.H * a.Tk * kRope;
   if (a.Tq > 0) {
-    if (big)
-      hipLaunchKernelGGL(k_attn_dq<1>, dim3(nq), dim3(kThr), 0, stream, a);
-    else
-      hipLaunchKernelGGL(k_attn_dq<1>, dim3(nq), dim3(kThr), 0, stream, a);
+    hipLaunchKernelGGL(k_attn_dq, dim3(nq), dim3(kBwdThr), 0, stream, a);
     MXQ_TRY(launch_status());
   }
   if (a.Tk > 0) {
-    hipLaunchKernelGGL(k_attn_dkv, dim3(nk), dim3(kThr), 0, stream, a);
+    hipLaunchKernelGGL(k_attn_dkv, dim3(nk), dim3(kBwdThr), 0, stream, a);
     MXQ_TRY(launch_status());
     hipLaunchKernelGGL(k_attn_drope, dim3(nr), dim3(kThr), 0, stream, a);
     MXQ_TRY(launch_status());
