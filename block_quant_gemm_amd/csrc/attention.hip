@@ -110,12 +110,7 @@ __device__ __forceinline__ SeqTile find_tile(const AttnArgs& a, uint32_t t, int 
       lk = lk < 0 ? 0 : lk;
     }
     const uint32_t n = (uint32_t)(((KEYS ? lk : lq) + rows - 1) / rows);
-    uint32_t incl = n;
-#pragma unroll
-    for (int sh = 1; sh < 64; sh <<= 1) {
-      const uint32_t u = __shfl_up(incl, sh, 64);
-      if (lane >= sh) incl += u;
-    }
+    const uint32_t incl = wave_scan(n);
     const uint64_t past = __ballot(t < before + incl);
     if (past) {
       const int at = __builtin_ctzll(past);

@@ -91,6 +91,22 @@ __device__ __forceinline__ uint32_t dpp_u32(uint32_t v, int ctrl_xor1_or_2) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kQuadXor2, 0xF, 0xF, false);
 }
 
+// Inclusive sum over the lanes up to this one, all 64 lanes active: within rows
+// of 16 by shifts, then rows 0 and 2 into 1 and 3, then the lower half into the
+// upper.  Register moves only.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xF, 0xF, true);   // row_shr 1
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xF, 0xF, true);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xF, 0xF, true);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xF, 0xF, true);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xA, 0xF, false);  // row_bcast 15
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xC, 0xF, false);  // row_bcast 31
+  return x;
+}
+__device__ __forceinline__ uint32_t lane_u32(uint32_t x, int lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, lane);
+}
+
 // Packed max of the magnitudes of two BF16 values held in one dword.  The
 // sign bits are cleared, so integer order equals magnitude order, and every
 // NaN pattern (0x7F81..0x7FFF) compares above Inf (0x7F80) above all finite

@@ -210,32 +210,11 @@ __device__ __forceinline__ int seq_len(const DecodeArgs& a, int32_t b) {
 __device__ __forceinline__ uint32_t seq_tiles(int len) {
   return len > 0 ? (uint32_t)((len + kTok - 1) / kTok) : 1u;
 }
-__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {   // inclusive
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int sh = 1; sh < 64; sh <<= 1) {
-    const uint32_t u = __shfl_up(x, sh, 64);
-    if (lane >= sh) x += u;
-  }
-  return x;
-}
-__device__ __forceinline__ uint32_t last_lane(uint32_t x) {
-  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
-}
 
-// Tiles of a run: `runs` runs hold the whole batch's tiles (each sequence adds
-// at most one run that is shorter).
-__device__ __forceinline__ uint32_t run_tiles(const DecodeArgs& a) {
-  const int lane = threadIdx.x & 63;
-  uint32_t t = 0;
-  for (int32_t base = 0; base < a.B; base += 64)
-    t += last_lane(wave_scan(base + lane < a.B ? seq_tiles(seq_len(a, base + lane)) : 0u));
-  return (t + a.runs - 1) / a.runs;
-}
-// Runs of sequence base + lane (0 past the batch).
-__device__ __forceinline__ uint32_t seq_runs(const DecodeArgs& a, int32_t base, uint32_t per) {
+// This lane's sequence base + lane: its tiles, 0 past the batch.
+__device__ __forceinline__ uint32_t lane_tiles(const DecodeArgs& a, int32_t base) {
   const int32_t b = base + (int32_t)(threadIdx.x & 63);
-  return b < a.B ? (seq_tiles(seq_len(a, b)) + per - 1) / per : 0u;
+  return b < a.B ? seq_tiles(seq_len(a, b)) : 0u;
 }
 
 // The slot of token t of a request with this page table, or -1: past the end,
@@ -334,22 +313,29 @@ __global__ __launch_bounds__(kThr * G, R * G == 1 ? 2 : G) void k_decode(DecodeA
   const int rt = blockIdx.y;
 
   // the request and the run of its tiles that this workgroup takes
-  const uint32_t per = run_tiles(a);
+  // (`runs` runs hold the whole batch's tiles; each sequence adds at most one
+  // run that is shorter)
   int32_t b = -1;
   uint32_t k = 0, nrun = 0;                        // run k of nrun
   {
+    const uint32_t first = lane_tiles(a, 0);       // of the first 64 sequences, kept
+    uint32_t total = 0;
+    for (int32_t base = 0; base < a.B; base += 64)
+      total += lane_u32(wave_scan(base == 0 ? first : lane_tiles(a, base)), 63);
+    const uint32_t per = (total + a.runs - 1) / a.runs;
     uint32_t before = 0;
     for (int32_t base = 0; base < a.B; base += 64) {
-      const uint32_t own = seq_runs(a, base, per), incl = wave_scan(own);
+      const uint32_t own = ((base == 0 ? first : lane_tiles(a, base)) + per - 1) / per;
+      const uint32_t incl = wave_scan(own);
       const uint64_t past = __ballot(blockIdx.x < before + incl);
       if (past) {
         const int at = __builtin_ctzll(past);
         b = base + at;
-        nrun = (uint32_t)__builtin_amdgcn_readlane((int)own, at);
-        k = blockIdx.x - before - (uint32_t)__builtin_amdgcn_readlane((int)(incl - own), at);
+        nrun = lane_u32(own, at);
+        k = blockIdx.x - before - lane_u32(incl - own, at);
         break;
       }
-      before += last_lane(incl);
+      before += lane_u32(incl, 63);
     }
   }
   if (b < 0) return;                               // uniform over the workgroup
@@ -584,10 +570,12 @@ __global__ __launch_bounds__(kThr * G, R * G == 1 ? 2 : G) void k_decode(DecodeA
 
 // Joins the parts of the requests that more than one workgroup worked on, in
 // their order: with M = max m, o = sum 2^(m - M) O / sum 2^(m - M) l.  One
-// workgroup a row, 128 lanes of 4 columns, 4 such groups taking every 4th part.
-__global__ __launch_bounds__(512) void k_decode_merge(DecodeArgs a, uint32_t nrt, int rows_per_tile) {
-  __shared__ __attribute__((aligned(16))) float s_o[3][kLat];
-  __shared__ float s_l[4];
+// workgroup a row, 128 lanes of 4 columns, GROUPS such groups taking every
+// GROUPS-th part.
+template <int GROUPS>
+__global__ __launch_bounds__(128 * GROUPS) void k_decode_merge(DecodeArgs a, uint32_t nrt, int rows_per_tile) {
+  __shared__ __attribute__((aligned(16))) float s_o[GROUPS > 1 ? GROUPS - 1 : 1][kLat];
+  __shared__ float s_l[GROUPS];
   const int32_t b = (int32_t)(blockIdx.x / (uint32_t)a.rows);
   const int row = (int)(blockIdx.x % (uint32_t)a.rows);
   const uint2 runs = a.runs_of[b];
@@ -605,7 +593,7 @@ __global__ __launch_bounds__(512) void k_decode_merge(DecodeArgs a, uint32_t nrt
   f32x4 acc = {};
   float lsum = 0.0f;
 #pragma unroll 4
-  for (uint32_t x = grp; x < n; x += 4) {
+  for (uint32_t x = grp; x < n; x += GROUPS) {
     const int64_t pr = part_row(x);
     const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * pr] - ref);
     lsum = __builtin_fmaf(f, a.part_ml[2 * pr + 1], lsum);
@@ -618,8 +606,10 @@ __global__ __launch_bounds__(512) void k_decode_merge(DecodeArgs a, uint32_t nrt
   __syncthreads();
   if (grp > 0) return;
 #pragma unroll
-  for (int y = 0; y < 3; ++y) acc += *reinterpret_cast<const f32x4*>(&s_o[y][d]);
-  const float total = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+  for (int y = 0; y < GROUPS - 1; ++y) acc += *reinterpret_cast<const f32x4*>(&s_o[y][d]);
+  float total = 0.0f;
+#pragma unroll
+  for (int y = 0; y < GROUPS; ++y) total += s_l[y];
   const int sq = row / a.H, h = row - sq * a.H;
   uint16_t* op = a.o + (int64_t)b * a.ldo_seq + (int64_t)sq * a.ldo_tok + (int64_t)h * a.ldo_head;
   *reinterpret_cast<uint2*>(op + d) = bf16x4_bits(acc, total == 0.0f ? 0.0f : 1.0f / total);
@@ -752,8 +742,12 @@ extern "C" int mx_latent_decode(const uint16_t* q, int64_t ldq_seq, int64_t ldq_
     hipLaunchKernelGGL((k_decode<2, 2>), grid, dim3(2 * kThr), 0, stream, a);
   MXQ_TRY(launch_status());
   if (p.grid > 1) {
+    // parts a request: about runs / B; few rows with many parts take more groups
     const dim3 rows((uint32_t)((int64_t)B * a.rows));
-    hipLaunchKernelGGL(k_decode_merge, rows, dim3(512), 0, stream, a, p.row_tiles, p.rows);
+    if (p.runs / (uint32_t)B >= 16)
+      hipLaunchKernelGGL(k_decode_merge<8>, rows, dim3(1024), 0, stream, a, p.row_tiles, p.rows);
+    else
+      hipLaunchKernelGGL(k_decode_merge<2>, rows, dim3(256), 0, stream, a, p.row_tiles, p.rows);
   }
   return launch_status();
 }
