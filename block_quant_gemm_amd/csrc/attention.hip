@@ -291,24 +291,6 @@ __device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// A run of products with their tile operands read DEPTH ahead: read(i) gives
-// operand i, use(i, operand) multiplies it.  The scheduling barriers keep that
-// order: left alone, the compiler reads each operand right before its use, and
-// every product waits out the LDS latency.
-template <int N, int DEPTH, class Read, class Use>
-__device__ __forceinline__ void pipelined(Read read, Use use) {
-  bf16x8 f[N];
-#pragma unroll
-  for (int i = 0; i < DEPTH && i < N; ++i) f[i] = read(i);
-  __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (i + DEPTH < N) f[i + DEPTH] = read(i + DEPTH);
-    use(i, f[i]);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-}
-
 // The tile row that register i of a 32-row block holds in lane half h.
 __device__ __forceinline__ int reg_row(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
 

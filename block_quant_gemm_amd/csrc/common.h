@@ -107,6 +107,24 @@ __device__ __forceinline__ uint32_t lane_u32(uint32_t x, int lane) {
   return (uint32_t)__builtin_amdgcn_readlane((int)x, lane);
 }
 
+// A run of products with their tile operands read DEPTH ahead: read(i) gives
+// operand i, use(i, operand) multiplies it.  The scheduling barriers keep that
+// order: left alone, the compiler reads each operand right before its use, and
+// every product waits out the LDS latency.
+template <int N, int DEPTH, class Read, class Use>
+__device__ __forceinline__ void pipelined(Read read, Use use) {
+  decltype(read(0)) f[N];
+#pragma unroll
+  for (int i = 0; i < DEPTH && i < N; ++i) f[i] = read(i);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i + DEPTH < N) f[i + DEPTH] = read(i + DEPTH);
+    use(i, f[i]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
 // Packed max of the magnitudes of two BF16 values held in one dword.  The
 // sign bits are cleared, so integer order equals magnitude order, and every
 // NaN pattern (0x7F81..0x7FFF) compares above Inf (0x7F80) above all finite

@@ -305,7 +305,7 @@ __global__ __launch_bounds__(kThr * G, R * G == 1 ? 2 : G) void k_decode(DecodeA
   __shared__ int32_t s_slot[2][kTok];
   __shared__ uint32_t s_redo[kRows];
   // steps of the queries held in registers; the others are read from LDS, in lane order
-  constexpr int KQ = R == 1 ? kSteps : kSteps / 2;
+  constexpr int KQ = R == 1 ? kSteps : 4;
   __shared__ __attribute__((aligned(16))) uint4 s_q[R * G][KQ < kSteps ? kSteps - KQ : 1][KQ < kSteps ? 64 : 1];
   const int tid = threadIdx.x, l = tid & 63, n = l & 15, g = l >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -358,24 +358,29 @@ __global__ __launch_bounds__(kThr * G, R * G == 1 ? 2 : G) void k_decode(DecodeA
   auto put_slot = [&](uint32_t i) {                // slots of tile i, by the first wavefront
     if (wave == 0) s_slot[i & 1][l] = i < i1 ? slot_of(a, pages, i * kTok + l, len) : -1;
   };
+  // Loads are unconditional (an absent token's from slot 0) so that they leave
+  // together; `gone` marks what has to be zeroed when the tile is widened.
   uint4 sc[kCl], sr[kRl];
-  uint32_t se[kCl];
+  uint32_t se[kCl], gone = ~0u;
   auto load = [&](uint32_t i) {
+    int32_t s[kCl], t[kRl];
+#pragma unroll
+    for (int j = 0; j < kCl; ++j) s[j] = s_slot[i & 1][j * (8 * G) + r0];
+#pragma unroll
+    for (int j = 0; j < kRl; ++j) t[j] = s_slot[i & 1][j * (32 * G) + (tid >> 3)];
+    gone = 0;
 #pragma unroll
     for (int j = 0; j < kCl; ++j) {
-      const int32_t s = s_slot[i & 1][j * (8 * G) + r0];
-      sc[j] = make_uint4(0, 0, 0, 0);
-      se[j] = 127;
-      if (s >= 0) {
-        sc[j] = *reinterpret_cast<const uint4*>(a.k.codes + s * a.k.ldc + ch * 16);
-        se[j] = a.k.scales[s * a.k.lds + (ch >> 1)];
-      }
+      gone |= s[j] < 0 ? 1u << j : 0u;
+      const int32_t x = s[j] < 0 ? 0 : s[j];
+      sc[j] = *reinterpret_cast<const uint4*>(a.k.codes + x * a.k.ldc + ch * 16);
+      se[j] = a.k.scales[x * a.k.lds + (ch >> 1)];
     }
 #pragma unroll
     for (int j = 0; j < kRl; ++j) {
-      const int32_t s = s_slot[i & 1][j * (32 * G) + (tid >> 3)];
-      sr[j] = make_uint4(0, 0, 0, 0);
-      if (s >= 0) sr[j] = *reinterpret_cast<const uint4*>(a.k.rope + s * a.k.ldr + (tid & 7) * 8);
+      gone |= t[j] < 0 ? 256u << j : 0u;
+      const int32_t x = t[j] < 0 ? 0 : t[j];
+      sr[j] = *reinterpret_cast<const uint4*>(a.k.rope + x * a.k.ldr + (tid & 7) * 8);
     }
   };
   put_slot(i0);
@@ -408,9 +413,17 @@ __global__ __launch_bounds__(kThr * G, R * G == 1 ? 2 : G) void k_decode(DecodeA
   for (int r = 0; r < R; ++r) m[r] = -__builtin_inff(), sum[r] = 0.0f;
   const float c = a.scale * kLog2e;
   __syncthreads();
-  load(i0);
+  if (a.k.slots > 0) load(i0);
   for (uint32_t i = i0; i < i1; ++i) {
     __syncthreads();                               // the last tile is consumed
+    if (__ballot(gone != 0)) {
+#pragma unroll
+      for (int j = 0; j < kCl; ++j)
+        if ((gone >> j) & 1) sc[j] = make_uint4(0, 0, 0, 0), se[j] = 127;
+#pragma unroll
+      for (int j = 0; j < kRl; ++j)
+        if ((gone >> (8 + j)) & 1) sr[j] = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int j = 0; j < kCl; ++j) {
       const float f = e8m0_f32(se[j]);
@@ -422,17 +435,35 @@ __global__ __launch_bounds__(kThr * G, R * G == 1 ? 2 : G) void k_decode(DecodeA
     for (int j = 0; j < kRl; ++j)
       *reinterpret_cast<uint4*>(tile + wrr + j * (32 * G * kRowB)) = sr[j];
     __syncthreads();
-    if (i + 1 < i1) load(i + 1);
+    if (i + 1 < i1 && a.k.slots > 0) load(i + 1);
 
-    f32x4 s[R] = {};
+    f32x4 s[R] = {}, s2[R] = {};                   // two chains a row group
+    struct Step {
+      bf16x8 k, q[R];
+    };
+    pipelined<kSteps, (R == 1 ? 4 : 3)>(
+        [&](int kk) {
+          Step x;
+          x.k = *reinterpret_cast<const bf16x8*>(tile + (rk ^ ((kk & 1) << 6)) + (kk >> 1) * 128);
+          if (kk >= KQ) {
 #pragma unroll
-    for (int kk = 0; kk < kSteps; ++kk) {
-      const bf16x8 kf = *reinterpret_cast<const bf16x8*>(tile + (rk ^ ((kk & 1) << 6)) + (kk >> 1) * 128);
+            for (int r = 0; r < R; ++r)
+              x.q[r] = __builtin_bit_cast(bf16x8, s_q[rg + r][kk < KQ ? 0 : kk - KQ][l]);
+          }
+          return x;
+        },
+        [&](int kk, const Step& x) {
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-        s[r] = mfma16(kf, kk < KQ ? q[r][kk < KQ ? kk : 0]
-                                  : __builtin_bit_cast(bf16x8, s_q[rg + r][kk < KQ ? 0 : kk - KQ][l]), s[r]);
-    }
+          for (int r = 0; r < R; ++r) {
+            const bf16x8 qf = kk < KQ ? q[r][kk < KQ ? kk : 0] : x.q[r];
+            if (kk & 1)
+              s2[r] = mfma16(x.k, qf, s2[r]);
+            else
+              s[r] = mfma16(x.k, qf, s[r]);
+          }
+        });
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[r] += s2[r];
     const int tok0 = (int)(i * kTok) + 16 * w + 4 * g;   // this lane's 4 tokens
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -468,24 +499,26 @@ __global__ __launch_bounds__(kThr * G, R * G == 1 ? 2 : G) void k_decode(DecodeA
     }
     __syncthreads();
     // values: tokens 4 g + 0..3 of two wavefronts' 16 a step of 32
+    bf16x8 pf[2][R];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      bf16x8 pf[R];
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const uint2 x = s_p[2 * j][rg + r][l], y = s_p[2 * j + 1][rg + r][l];
-        pf[r] = __builtin_bit_cast(bf16x8, make_uint4(x.x, x.y, y.x, y.y));
+        pf[j][r] = __builtin_bit_cast(bf16x8, make_uint4(x.x, x.y, y.x, y.y));
       }
+    pipelined<16, (R == 1 ? 4 : 3)>(
+        [&](int i2) {
+          const int j = i2 >> 3, d = i2 & 7;
+          const uint8_t* p = tile + (rv ^ ((d & 3) << 5)) + (d >> 2) * 128 + j * (32 * kRowB);
+          const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
+          const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 16 * kRowB));
+          return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+        },
+        [&](int i2, bf16x8 vf) {
 #pragma unroll
-      for (int d = 0; d < 8; ++d) {
-        const uint8_t* p = tile + (rv ^ ((d & 3) << 5)) + (d >> 2) * 128 + j * (32 * kRowB);
-        const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
-        const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 16 * kRowB));
-        const bf16x8 vf = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-        for (int r = 0; r < R; ++r) o[r][d] = mfma16(vf, pf[r], o[r][d]);
-      }
-    }
+          for (int r = 0; r < R; ++r) o[r][i2 & 7] = mfma16(vf, pf[i2 >> 3][r], o[r][i2 & 7]);
+        });
   }
 
   // totals of all wavefronts' tokens; rows to redo
