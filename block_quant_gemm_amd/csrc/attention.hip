@@ -947,7 +947,7 @@ __global__ __launch_bounds__(kThr) void k_attn_drope(AttnArgs a) {
 // Host side
 // ---------------------------------------------------------------------------
 
-constexpr int64_t kMaxRows = INT64_C(1) << 30, kMaxStride = INT64_C(1) << 23;
+constexpr int64_t kMaxRows = INT64_C(1) << 27, kMaxStride = INT64_C(1) << 23;
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p % 16) == 0; }
 inline int launch_status() { return hipGetLastError() == hipSuccess ? MXQ_OK : MXQ_ERR_HIP; }
@@ -998,10 +998,11 @@ int check_attn(const mxq_latent_attn* d, AttnArgs* a) {
   return MXQ_OK;
 }
 
-// Workgroups that hold every sequence's tiles of `rows` rows, for all heads.
+// Workgroups that hold every sequence's tiles of `rows` rows, for all heads.  A
+// launch has fewer than 2^32 work items, of which a workgroup has up to 512.
 int grid_of(int64_t T, int64_t rows, const AttnArgs& a, uint32_t* n) {
   const int64_t g = sat_mul(T / rows + a.B, a.H);
-  if (g > 0x7FFFFFFFLL) return MXQ_ERR_SHAPE;
+  if (g >= (INT64_C(1) << 23)) return MXQ_ERR_SHAPE;
   *n = (uint32_t)g;
   return MXQ_OK;
 }
@@ -1054,7 +1055,7 @@ extern "C" int latent_attention_backward(
   uint32_t nq, nk, nr;
   MXQ_TRY(grid_of(a.Tq, 128, a, &nq));
   MXQ_TRY(grid_of(a.Tk, 128, a, &nk));
-  nr = (uint32_t)((a.Tk * (kRope / 4) + kThr - 1) / kThr);     // at most 2^26
+  nr = (uint32_t)((a.Tk * (kRope / 4) + kThr - 1) / kThr);     // at most 2^23
   a.o = {o, ldo, ldo_head};
   a.dout = {dout, lddo, lddo_head};
   a.lse = const_cast<float*>(lse);

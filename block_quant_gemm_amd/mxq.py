@@ -153,9 +153,13 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _raw_stream():
-    """The current stream's handle, without the stream object around it."""
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+def _raw_stream(t):
+    """The handle of the current stream, which has to be on t's GPU, without the
+    stream object around it."""
+    dev = torch._C._cuda_getDevice()
+    if t.get_device() != dev:
+        raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{dev}")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _bf16_bits(x):
@@ -712,9 +716,11 @@ _BF16, _U8, _I64, _F32 = torch.bfloat16, torch.uint8, torch.int64, torch.float32
 
 
 def _rows(name, t, dtype, shape):
-    """The strides of t.  Raises unless t has this dtype and shape and adjacent
-    values along its last dimension: the C calls take addresses and strides
-    and cannot see a tensor that is too small."""
+    """The strides of t.  Raises unless t is in GPU memory, has this dtype and shape,
+    and adjacent values along its last dimension: the C calls take addresses and
+    strides and can see neither a host address nor a tensor that is too small."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a tensor on the GPU, got {t.device}")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -757,7 +763,7 @@ def mx_latent_cache_write(c, k_rope, slots, cache):
     sr = _rows("k_rope", k_rope, _BF16, (T, 64))
     _rows("slots", slots, _I64, (T,))
     st = load().mx_latent_cache_write(c.data_ptr(), sc[0], k_rope.data_ptr(), sr[0],
-                                      slots.data_ptr(), T, _cache_arg(cache), _raw_stream())
+                                      slots.data_ptr(), T, _cache_arg(cache), _raw_stream(c))
     if st:
         _check(st)
     return cache
@@ -775,7 +781,7 @@ def mx_latent_cache_read(cache, slots, c=None, k_rope=None):
     sc = _rows("c", c, _BF16, (T, 512))
     sr = _rows("k_rope", k_rope, _BF16, (T, 64))
     st = load().mx_latent_cache_read(_cache_arg(cache), slots.data_ptr(), T, c.data_ptr(), sc[0],
-                                     k_rope.data_ptr(), sr[0], _raw_stream())
+                                     k_rope.data_ptr(), sr[0], _raw_stream(slots))
     if st:
         _check(st)
     return c, k_rope
@@ -804,10 +810,11 @@ def mx_latent_decode(q, cache, pages, lens, page_size, max_len, scale, o=None, l
         raise ValueError("lse: has to be contiguous")
     if workspace is None:
         workspace = q.new_empty(_latent_workspace(WS_LATENT_DECODE, B, S, H, max_len), dtype=_U8)
+    _rows("workspace", workspace, _U8, (workspace.numel(),))
     st = load().mx_latent_decode(
         q.data_ptr(), sq[0], sq[1], sq[2], _cache_arg(cache), pages.data_ptr(), sp[0], width,
         page_size, lens.data_ptr(), B, S, H, max_len, scale, o.data_ptr(), so[0], so[1], so[2],
-        lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream())
+        lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(q))
     if st:
         _check(st)
     return o, lse
@@ -856,7 +863,7 @@ def latent_attention(q, k_nope, k_rope, v, offsets_q=None, offsets_k=None, scale
     so = _rows("o", o, _BF16, (Tq, H, 128))
     sl = _rows("lse", lse, _F32, (H, Tq))
     st = load().latent_attention(arg, o.data_ptr(), so[0], so[1], lse.data_ptr(), sl[0],
-                                 _raw_stream())
+                                 _raw_stream(q))
     if st:
         _check(st)
     return o, lse
@@ -890,11 +897,12 @@ def latent_attention_backward(dout, q, k_nope, k_rope, v, o, lse, offsets_q=None
     sdv = _rows("dv", dv, _BF16, (Tk, H, 128))
     if workspace is None:
         workspace = q.new_empty(_latent_workspace(WS_LATENT_BACKWARD, Tq, Tk, H, 0), dtype=_U8)
+    _rows("workspace", workspace, _U8, (workspace.numel(),))
     st = load().latent_attention_backward(
         arg, o.data_ptr(), so[0], so[1], lse.data_ptr(), sl[0], dout.data_ptr(), sg[0], sg[1],
         dq.data_ptr(), sdq[0], sdq[1], dk_nope.data_ptr(), sdk[0], sdk[1], dk_rope.data_ptr(),
         sdr[0], dv.data_ptr(), sdv[0], sdv[1], workspace.data_ptr(), workspace.numel(),
-        _raw_stream())
+        _raw_stream(q))
     if st:
         _check(st)
     return dq, dk_nope, dk_rope, dv

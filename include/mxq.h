@@ -1,5 +1,6 @@
 /*
- * mxq.h — MX-FP8 block quantization and (grouped) GEMM on AMD MI355X (gfx950).
+ * mxq.h — MX-FP8 block quantization, (grouped) GEMM and latent attention on
+ * AMD MI355X (gfx950).
  *
  * C ABI of libmxq.so.  Every pointer argument marked "device" is an address in
  * GPU memory; the library never allocates, frees or keeps any caller buffer.
@@ -628,6 +629,7 @@ MXQ_API int fp8_grouped_gemm_wgrad_per_group(const uint8_t* at, const float* a_s
 #define MXQ_ROPE_DIM 64
 #define MXQ_NOPE_DIM 128
 #define MXQ_VALUE_DIM 128
+#define MXQ_LATENT_MAX_TOKENS (1 << 25)   /* of one cache write or read */
 
 /*
  * The MX latent cache: `slots` slots of one token each, in three arrays.  A
@@ -663,7 +665,7 @@ typedef struct mxq_latent_cache {
  *            (-1 for padding tokens).  A slot named twice holds one of the two
  *            tokens' values, possibly a mixture.
  *   cache  : host struct, read during the call only.
- * Other slots keep their contents.  T == 0 is a no-op.
+ * Other slots keep their contents.  T == 0 is a no-op; T <= MXQ_LATENT_MAX_TOKENS.
  */
 MXQ_API int mx_latent_cache_write(const uint16_t* c, int64_t ldc, const uint16_t* k_rope,
                           int64_t ldr, const int64_t* slots, int64_t T,
@@ -677,7 +679,7 @@ MXQ_API int mx_latent_cache_write(const uint16_t* c, int64_t ldc, const uint16_t
  *   c, k_rope : device, BF16 [T, 512] and [T, 64], strides and alignment as for
  *               mx_latent_cache_write.
  *   slots     : device int64 [T].
- * T == 0 is a no-op.
+ * T == 0 is a no-op; T <= MXQ_LATENT_MAX_TOKENS.
  */
 MXQ_API int mx_latent_cache_read(const mxq_latent_cache* cache, const int64_t* slots, int64_t T,
                          uint16_t* c, int64_t ldc, uint16_t* k_rope, int64_t ldr,
@@ -711,7 +713,7 @@ MXQ_API int mx_latent_cache_read(const mxq_latent_cache* cache, const int64_t* s
  *   lse        : device float [B, S, H], contiguous.
  *   workspace  : device scratch of at least mxq_workspace_size(
  *                MXQ_WS_LATENT_DECODE, B, S, H, max_len) bytes, 16-byte aligned.
- * S * H <= 65536.  B == 0 is a no-op.
+ * S * H <= 65536 and B * S * H < 2^24.  B == 0 is a no-op.
  */
 MXQ_API int mx_latent_decode(const uint16_t* q, int64_t ldq_seq, int64_t ldq_tok, int64_t ldq_head,
                      const mxq_latent_cache* cache, const int32_t* pages, int64_t ld_pages,
@@ -734,7 +736,8 @@ MXQ_API int mx_latent_decode(const uint16_t* q, int64_t ldq_seq, int64_t ldq_tok
  *             NULL: one sequence of all rows (B is then ignored).  Malformed
  *             tables give unspecified values but never an access outside the
  *             buffers.
- *   H       : 1 .. 65536.  B: 1 .. 65536.  Tq, Tk: at most 2^30.
+ *   H       : 1 .. 65536.  B: 1 .. 65536.  Tq, Tk: at most 2^27, and
+ *             (Tq / 128 + B) * H and (Tk / 128 + B) * H less than 2^23.
  *   scale   : > 0, finite.
  *   causal  : 0, or 1: query i of a sequence with lq queries and lk keys sees
  *             keys j <= i + lk - lq (the queries are the last lq tokens).
