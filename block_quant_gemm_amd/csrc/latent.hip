@@ -31,9 +31,9 @@ struct Cache {
 // of slot number), no arithmetic that shows.  One wavefront a token: lane l
 // holds latent values 8 l .. 8 l + 7 (a DPP quad one block of 32), so a token's
 // codes are one 512-byte store and its row of BF16 one 1 KB load; lanes 0-7
-// carry the rotary key's 16 bytes 16 l.  A token a wavefront, and eight
-// workgroups a CU, keep enough loads in flight: 16384 tokens are written in 6.4 us
-// (4.6 TB/s) and 65521 read in 19.4 us (6.1 TB/s, above a large copy's 5.0).
+// carry the rotary key's 16 bytes 16 l.  16384 tokens are written in 6.4 us
+// (4.6 TB/s); 65521 are read in 28.2 us (4.2 TB/s), 19.6 us (6.1 TB/s) when the
+// last-level cache holds them from the call before.  A large copy reaches 5.0 TB/s.
 // ---------------------------------------------------------------------------
 
 __global__ __launch_bounds__(kThr) void k_latent_write(const uint16_t* __restrict__ c, int64_t ldc,
@@ -70,30 +70,55 @@ __device__ __forceinline__ float scale_f32(uint32_t e) {
   return __builtin_bit_cast(float, e == 0u ? 0x00400000u : e == 0xFFu ? 0x7FC00000u : e << 23);
 }
 
+// U tokens a wavefront, kThr / 64 apart.  Loads are unconditional (an absent
+// slot's from slot 0) so that all U tokens' leave together.
+template <int U>
 __global__ __launch_bounds__(kThr) void k_latent_read(Cache k, const int64_t* __restrict__ slots,
                                                       int64_t T, uint16_t* __restrict__ c,
                                                       int64_t ldc, uint16_t* __restrict__ k_rope,
                                                       int64_t ldr) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * (kThr / 64) + (threadIdx.x >> 6);
-  if (t >= T) return;
-  const int64_t s = slots[t];
-  uint2 v = make_uint2(0, 0);
-  uint4 r = make_uint4(0, 0, 0, 0);
-  uint32_t e = 127;
-  if (s >= 0 && s < k.slots) {
-    v = *reinterpret_cast<const uint2*>(k.codes + s * k.ldc + lane * 8);
-    e = k.scales[s * k.lds + (lane >> 2)];
-    if (lane < 8) r = *reinterpret_cast<const uint4*>(k.rope + s * k.ldr + lane * 8);
+  const int64_t t0 = (int64_t)blockIdx.x * (kThr / 64 * U) + (threadIdx.x >> 6);
+  int64_t s[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t t = t0 + u * (kThr / 64);
+    s[u] = slots[t < T ? t : T - 1];
   }
-  const float f = scale_f32(e);
-  uint4 w;
-  w.x = decode2<false>(v.x, f);
-  w.y = decode2<true>(v.x, f);
-  w.z = decode2<false>(v.y, f);
-  w.w = decode2<true>(v.y, f);
-  *reinterpret_cast<uint4*>(c + t * ldc + lane * 8) = w;
-  if (lane < 8) *reinterpret_cast<uint4*>(k_rope + t * ldr + lane * 8) = r;
+  uint2 v[U];
+  uint4 r[U];
+  uint32_t e[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const bool in = s[u] >= 0 && s[u] < k.slots;
+    const int64_t x = in ? s[u] : 0;
+    v[u] = make_uint2(0, 0);
+    r[u] = make_uint4(0, 0, 0, 0);
+    e[u] = 127;
+    if (k.slots > 0) {
+      v[u] = *reinterpret_cast<const uint2*>(k.codes + x * k.ldc + lane * 8);
+      e[u] = k.scales[x * k.lds + (lane >> 2)];
+      r[u] = *reinterpret_cast<const uint4*>(k.rope + x * k.ldr + (lane & 7) * 8);
+    }
+    if (!in) {
+      v[u] = make_uint2(0, 0);
+      r[u] = make_uint4(0, 0, 0, 0);
+      e[u] = 127;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t t = t0 + u * (kThr / 64);
+    if (t >= T) break;
+    const float f = scale_f32(e[u]);
+    uint4 w;
+    w.x = decode2<false>(v[u].x, f);
+    w.y = decode2<true>(v[u].x, f);
+    w.z = decode2<false>(v[u].y, f);
+    w.w = decode2<true>(v[u].y, f);
+    *reinterpret_cast<uint4*>(c + t * ldc + lane * 8) = w;
+    if (lane < 8) *reinterpret_cast<uint4*>(k_rope + t * ldr + lane * 8) = r[u];
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -691,8 +716,15 @@ extern "C" int mx_latent_cache_read(const mxq_latent_cache* cache, const int64_t
   MXQ_TRY(check_cache(cache, &k));
   MXQ_TRY(check_rows(c, ldc, k_rope, ldr, slots, T));
   if (T == 0) return MXQ_OK;
-  hipLaunchKernelGGL(k_latent_read, dim3((uint32_t)((T + 3) / 4)), dim3(kThr), 0, stream, k,
-                     slots, T, c, ldc, k_rope, ldr);
+  // Four tokens a wavefront where that still leaves eight workgroups to every CU
+  // (65521 tokens whose cache and outputs are in no cache: 28.2 us against 30.3 with
+  // one), else one (419 tokens: 2.2 us against 2.8).
+  if (T >= 256 * 8 * 16)
+    hipLaunchKernelGGL(k_latent_read<4>, dim3((uint32_t)((T + 15) / 16)), dim3(kThr), 0, stream, k,
+                       slots, T, c, ldc, k_rope, ldr);
+  else
+    hipLaunchKernelGGL(k_latent_read<1>, dim3((uint32_t)((T + 3) / 4)), dim3(kThr), 0, stream, k,
+                       slots, T, c, ldc, k_rope, ldr);
   return launch_status();
 }
 

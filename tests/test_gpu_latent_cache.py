@@ -316,3 +316,25 @@ def test_empty_batch_and_all_empty_requests():
         o, lse = mxq.mx_latent_decode(q, cache, torch.zeros((3, 3), dtype=torch.int32, device="cuda"),
                                       lens, 16, max_len, 0.1)
         assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("T", [32767, 32768, 40001])
+def test_read_many_tokens(T):
+    """Around the size from which a wavefront reads several tokens; the last of them
+    ends inside a workgroup, and some slots are absent."""
+    say(f"latent cache read T={T}")
+    cache = _random_cache(900, 13)
+    slots = np.random.default_rng(T).integers(-20, 920, T).astype(np.int64)
+    out = torch.full((T + 1, 576), 5.0, dtype=torch.bfloat16, device="cuda")
+    mxq.mx_latent_cache_read(_to_gpu(cache), to_dev(slots), c=out[:T, :512], k_rope=out[:T, 512:])
+    rc, rr = latent.cache_read(cache, slots)
+    _equal_bf16(host(out[:T, :512]), rc)
+    assert np.array_equal(host(out[:T, 512:]), rr)
+    assert (out[T:] == 5.0).all()
+
+
+@pytest.mark.parametrize("T", [3, 33000])
+def test_read_from_an_empty_cache(T):
+    say(f"latent cache read T={T}, no slots")
+    c, r = mxq.mx_latent_cache_read(mxq.latent_cache(0), torch.zeros(T, dtype=torch.int64, device="cuda"))
+    assert not c.any() and not r.any()

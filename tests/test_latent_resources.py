@@ -1,5 +1,5 @@
 """The latent attention kernels keep everything in registers: the compiler reports no
-scratch memory and no spilled register for any of them.  They are written for
+scratch memory and no spilled vector register for any of them.  They are written for
 that (a spilled value costs a trip to memory in the inner loop, and a spill placed
 in a block that only some lanes reach has restored a wrong address).  CPU only: it
 compiles the sources for their resource report, cached by their digest."""
