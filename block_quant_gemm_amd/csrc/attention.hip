@@ -624,18 +624,19 @@ __global__ __launch_bounds__(kThr, 2) void k_attn_fwd(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Backward.  Eight wavefronts, two a SIMD: a pair shares 32 rows of the
-// workgroup's 128.  Of each tile of 64, one of the pair forms P and dS against
+// Backward.  With PAIRS = 4, eight wavefronts, two a SIMD: a pair shares 32 rows
+// of the workgroup's 128.  Of each tile of 64, one of the pair forms P and dS against
 // the first 32 rows, the other against the last, and they hand each other the
 // operands through LDS (as they are, in lane order).  Then each takes half of
 // the result's columns over all 64.  That halves the sums a wavefront holds,
 // which is what lets two of them share a SIMD: one's exponentials run beside
-// the other's products.
+// the other's products.  With PAIRS = 2, 64 rows and a wavefront a SIMD: shorter
+// steps, for calls that leave CUs idle otherwise.
 // ---------------------------------------------------------------------------
 
-constexpr int kBwdThr = 512, kPairs = 4;
+template <int PAIRS>
 struct Exchange {
-  uint4 f[kPairs][2][4][64];                     // pair, half, P slabs and dS slabs, lane
+  uint4 f[PAIRS][2][4][64];                      // pair, half, P slabs and dS slabs, lane
 };
 
 // Backward, queries: dQ and D, which the keys' kernel reads.
@@ -646,27 +647,28 @@ struct Exchange {
 // numbers).  With dS' = P * (dP - d), the row sum r of dS' is D - d, and
 //   dQ = scale * (dS' K - r (P K)):
 // the products P K and dS' K share the reads of K.
-__global__ __launch_bounds__(kBwdThr, 2) void k_attn_dq(AttnArgs a) {
+template <int PAIRS>
+__global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTile];
-  __shared__ __attribute__((aligned(16))) Exchange ex;
-  __shared__ float s_rest[kPairs][2][32];
-  __shared__ uint32_t s_bad[kPairs][2];
-  constexpr int BM = 32 * kPairs;
+  __shared__ __attribute__((aligned(16))) Exchange<PAIRS> ex;
+  __shared__ float s_rest[PAIRS][2][32];
+  __shared__ uint32_t s_bad[PAIRS][2];
+  constexpr int BM = 32 * PAIRS;
   const int head = blockIdx.x % a.H;
   const SeqTile st = find_tile<false>(a, blockIdx.x / a.H, BM);
   if (!st.ok) return;
   const int l = threadIdx.x & 63, n = l & 31, h = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int pair = w & 3, half = w >> 2;
+  const int pair = w % PAIRS, half = w / PAIRS;
   const int wrow0 = st.row0 + pair * 32, row = wrow0 + n;
   const Head x = head_of(a, st, head);
-  const Copy cp = copy_plan<8>(lds, a.kn.ld, a.ldr, a.v.ld);
+  const Copy cp = copy_plan<2 * PAIRS>(lds, a.kn.ld, a.ldr, a.v.ld);
   Reads rp = read_plan();
   const int last = (st.row0 + BM < st.lq ? st.row0 + BM : st.lq) - 1;
   const int kend = keys_seen(a, st, last);
   const int wfirst = keys_seen(a, st, wrow0), wlast = keys_seen(a, st, wrow0 + 31);
   const int lim = keys_seen(a, st, row);
-  if (kend > 0) tile_copy<8>(cp, x.kn, x.kr, x.v, 0, st.lk, 0);
+  if (kend > 0) tile_copy<2 * PAIRS>(cp, x.kn, x.kr, x.v, 0, st.lk, 0);
 
   bf16x8 q[kSteps], g[kVSteps];
   own_rows(q, x.q, a.q.ld, x.q + kNope, a.q.ld, row, st.lq);
@@ -691,7 +693,7 @@ __global__ __launch_bounds__(kBwdThr, 2) void k_attn_dq(AttnArgs a) {
   int buf = 0;
   for (int k0 = 0; k0 < kend; k0 += kBN, buf ^= 1) {
     tile_wait();
-    if (k0 + kBN < kend) tile_copy<8>(cp, x.kn, x.kr, x.v, k0 + kBN, st.lk, buf ^ 1);
+    if (k0 + kBN < kend) tile_copy<2 * PAIRS>(cp, x.kn, x.kr, x.v, k0 + kBN, st.lk, buf ^ 1);
     const bool live = k0 < wlast;                  // the same for both of a pair
     const uint8_t* tile = lds + buf * kTile;
     // the units' addresses are formed again in every tile: kept, they cost too many registers
@@ -774,22 +776,23 @@ __global__ __launch_bounds__(kBwdThr, 2) void k_attn_dq(AttnArgs a) {
 // Backward, keys: dK, dV, walking the queries that see the workgroup's keys.  The
 // rotary part of dK is summed over the heads by k_attn_drope, from one FP32 part
 // a head, in head order.
-__global__ __launch_bounds__(kBwdThr, 2) void k_attn_dkv(AttnArgs a) {
+template <int PAIRS>
+__global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTile];
-  __shared__ __attribute__((aligned(16))) Exchange ex;
+  __shared__ __attribute__((aligned(16))) Exchange<PAIRS> ex;
   __shared__ __attribute__((aligned(16))) float stat[2][2][kBN];   // lse (powers of two), D
-  __shared__ uint32_t s_bad[kPairs][2];
-  constexpr int BM = 32 * kPairs;
+  __shared__ uint32_t s_bad[PAIRS][2];
+  constexpr int BM = 32 * PAIRS;
   const int head = blockIdx.x % a.H;
   const SeqTile st = find_tile<true>(a, blockIdx.x / a.H, BM);
   if (!st.ok) return;
   const int l = threadIdx.x & 63, n = l & 31, h = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int pair = w & 3, half = w >> 2;
+  const int pair = w % PAIRS, half = w / PAIRS;
   const int wkey = st.row0 + pair * 32, row = wkey + n;   // the pair's keys, this lane's
   const int diff = st.lk - st.lq;                  // query i sees keys j <= i + diff
   const Head x = head_of(a, st, head);
-  const Copy cp = copy_plan<8>(lds, a.q.ld, a.q.ld, a.dout.ld);
+  const Copy cp = copy_plan<2 * PAIRS>(lds, a.q.ld, a.q.ld, a.dout.ld);
   Reads rp = read_plan();
 
   // queries from lim on see this lane's key; the tile starts at the first that sees any
@@ -811,7 +814,7 @@ __global__ __launch_bounds__(kBwdThr, 2) void k_attn_dkv(AttnArgs a) {
   float z = 0.0f;
   if (q0 < st.lq) {
     z = stat_of(q0);
-    tile_copy<8>(cp, x.q, x.q + kNope, x.g, q0, st.lq, 0);
+    tile_copy<2 * PAIRS>(cp, x.q, x.q + kNope, x.g, q0, st.lq, 0);
   }
   bf16x8 k[kSteps], v[kVSteps];
   own_rows(k, x.kn, a.kn.ld, x.kr, a.ldr, row, st.lk);
@@ -831,7 +834,7 @@ __global__ __launch_bounds__(kBwdThr, 2) void k_attn_dkv(AttnArgs a) {
     tile_wait();
     if (q0 + kBN < st.lq) {
       z = stat_of(q0 + kBN);
-      tile_copy<8>(cp, x.q, x.q + kNope, x.g, q0 + kBN, st.lq, buf ^ 1);
+      tile_copy<2 * PAIRS>(cp, x.q, x.q + kNope, x.g, q0 + kBN, st.lq, buf ^ 1);
     }
     const bool live = q0 + kBN > wlim;             // some query here sees the pair's keys
     const uint8_t* tile = lds + buf * kTile;
@@ -936,6 +939,7 @@ __global__ __launch_bounds__(kThr) void k_attn_drope(AttnArgs a) {
   if (t >= a.Tk) return;
   const float* p = a.rope_part + t * kRope + c;
   f32x4 s = {};
+#pragma unroll 8
   for (int h = 0; h < a.H; ++h) s += *reinterpret_cast<const f32x4*>(p + h * a.Tk * kRope);
   uint2 w;
   w.x = bf16x2_bits(s[0] * a.scale, s[1] * a.scale);
@@ -1052,9 +1056,15 @@ extern "C" int latent_attention_backward(
   if (workspace_bytes < need) return MXQ_ERR_WORKSPACE;
   if (need > 0 && !workspace) return MXQ_ERR_NULL;
   if (!aligned16(workspace)) return MXQ_ERR_ALIGN;
+  // Workgroups of 64 rows where about that many, T / 64 and half a tile a sequence,
+  // still run at once, one a CU (one sequence of 360, 16 heads: 43 us for the three
+  // kernels against 59; 2 of 1000, 8 heads: 74 against 100); else of 128 (4 of 300, 16
+  // heads, a second turn for 64 CUs: 58 against 61; 8 of 512, 16 heads: 138 against 152).
+  const auto few = [&](int64_t T) { return (T / 64 + a.B / 2) * a.H <= 256; };
+  const bool fewq = few(a.Tq), fewk = few(a.Tk);
   uint32_t nq, nk, nr;
-  MXQ_TRY(grid_of(a.Tq, 128, a, &nq));
-  MXQ_TRY(grid_of(a.Tk, 128, a, &nk));
+  MXQ_TRY(grid_of(a.Tq, fewq ? 64 : 128, a, &nq));
+  MXQ_TRY(grid_of(a.Tk, fewk ? 64 : 128, a, &nk));
   nr = (uint32_t)((a.Tk * (kRope / 4) + kThr - 1) / kThr);     // at most 2^23
   a.o = {o, ldo, ldo_head};
   a.dout = {dout, lddo, lddo_head};
@@ -1068,11 +1078,17 @@ extern "C" int latent_attention_backward(
   a.rope_part = static_cast<float*>(workspace);
   a.delta = a.rope_part + a.H * a.Tk * kRope;
   if (a.Tq > 0) {
-    hipLaunchKernelGGL(k_attn_dq, dim3(nq), dim3(kBwdThr), 0, stream, a);
+    if (fewq)
+      hipLaunchKernelGGL(k_attn_dq<2>, dim3(nq), dim3(256), 0, stream, a);
+    else
+      hipLaunchKernelGGL(k_attn_dq<4>, dim3(nq), dim3(512), 0, stream, a);
     MXQ_TRY(launch_status());
   }
   if (a.Tk > 0) {
-    hipLaunchKernelGGL(k_attn_dkv, dim3(nk), dim3(kBwdThr), 0, stream, a);
+    if (fewk)
+      hipLaunchKernelGGL(k_attn_dkv<2>, dim3(nk), dim3(256), 0, stream, a);
+    else
+      hipLaunchKernelGGL(k_attn_dkv<4>, dim3(nk), dim3(512), 0, stream, a);
     MXQ_TRY(launch_status());
     hipLaunchKernelGGL(k_attn_drope, dim3(nr), dim3(kThr), 0, stream, a);
     MXQ_TRY(launch_status());

@@ -291,3 +291,42 @@ def test_long_rows_against_64_bit_products(H, lens):
     for name, r in zip(("o", "dq", "dk_nope", "dk_rope", "dv"), (ref.detach(), *grads)):
         e = ((got[name].double() - r).norm() / r.norm()).item()
         assert e < (2 / 3) ** 0.5 * 2 ** -8, f"{name}: {e:.3g}"
+
+
+def _with_empty(d, n=600):
+    """The same sequences and n empty ones after them: more workgroups than a small
+    call has, which decides how many rows one of them takes."""
+    return {k: np.concatenate([v, np.full(n, v[-1])]) if k in ("oq", "ok") else v for k, v in d.items()}
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_with_many_empty_sequences(case):
+    """Both workgroup sizes of the backward kernels, against the oracle and bit for bit."""
+    lq, lk, H, causal = CASES[case]
+    say(f"latent attention and 600 empty sequences, lq={lq} lk={lk} H={H} causal={causal}")
+    d = _inputs(lq, lk, H, case)
+    few, many = _run(d, causal), _run(_with_empty(d), causal)
+    ref = latent.attention_backward(codec.bf16_bits_to_f64(d["do"]), *_f64(d), d["oq"], d["ok"],
+                                    SCALE, causal)
+    _compare(many, ref)
+    for n, x in few.items():
+        assert torch.equal(x.contiguous().view(torch.int16), many[n].contiguous().view(torch.int16)), n
+
+
+@pytest.mark.parametrize("what", [0x7FC0, 0x7F80])
+def test_hidden_nan_with_many_empty_sequences(what):
+    say(f"latent attention and 600 empty sequences, rows of {what:#x}")
+    n, cut = 150, 70
+    d = _inputs([n], [n], 1, 70)
+    sound = {k: (v[:cut].copy() if k not in ("oq", "ok") else np.array([0, cut])) for k, v in d.items()}
+    _bad_rows(d, range(cut, n, 7), what)
+    got = _run(_with_empty(d), True)
+    ref = latent.attention_backward(codec.bf16_bits_to_f64(sound["do"]), *_f64(sound), sound["oq"],
+                                    sound["ok"], SCALE, True)
+    for name in ("o", "dq"):
+        _compare({name: got[name][:cut]}, {name: ref[name]})
+    few = _run(d, True)
+    for name in ("dk_nope", "dk_rope", "dv"):
+        a, b = host(few[name].contiguous()), host(got[name].contiguous())
+        nan = lambda x: ~np.isfinite(codec.bf16_bits_to_f64(x))
+        assert np.array_equal(nan(a), nan(b)) and np.array_equal(a[~nan(a)], b[~nan(b)]), name
