@@ -524,6 +524,15 @@ __device__ __forceinline__ int keys_seen(const AttnArgs& a, const SeqTile& s, in
 // Forward.  A workgroup of four wavefronts takes 128 query rows of one head, 32 a
 // wavefront; two workgroups share a CU, so that one's exponentials run beside
 // the other's products.
+//
+// Bound by the matrix unit and what has to run between its products.  4 sequences
+// of 4096, 16 heads, causal: 357 us, 0.96 PFLOP/s (a large matrix product reaches
+// 1.16 to 1.25 on the same card, and its rate on such data is set by power).  Of
+// 363 us in an early form the products alone took 297, and 326 were left without
+// LDS reads, 329 without maxima and exponentials.  64 rows a wavefront halve the
+// LDS reads but leave one wavefront a SIMD: 600 us.  Eight wavefronts that split
+// each tile's keys shorten the chain of a single long sequence (one of 2000, 4
+// heads: 46 us to 42) and cost every other case (this one: 470 us).
 // ---------------------------------------------------------------------------
 
 __global__ __launch_bounds__(kThr, 2) void k_attn_fwd(AttnArgs a) {
@@ -630,8 +639,16 @@ __global__ __launch_bounds__(kThr, 2) void k_attn_fwd(AttnArgs a) {
 // operands through LDS (as they are, in lane order).  Then each takes half of
 // the result's columns over all 64.  That halves the sums a wavefront holds,
 // which is what lets two of them share a SIMD: one's exponentials run beside
-// the other's products.  With PAIRS = 2, 64 rows and a wavefront a SIMD: shorter
-// steps, for calls that leave CUs idle otherwise.
+// the other's products.  The sums over a tile are taken beside the next tile's P
+// and dS, between one pair of barriers, which takes three tile buffers (1540 us for
+// the three kernels on the case below with two buffers, 1480 with three).  With
+// PAIRS = 2, 64 rows and a wavefront a SIMD: shorter steps, for calls that leave
+// CUs idle otherwise.
+//
+// 4 sequences of 4096, 16 heads, causal: dQ 759 us, dK and dV 805 us, 1.00 and 0.85
+// PFLOP/s of the 11 and 10 products of 64 columns that they form a pair (13 in all
+// are the least; those that both form are S and dP, and P K makes D exact).  Bound
+// as the forward is, with the exchange's barrier beside.
 // ---------------------------------------------------------------------------
 
 template <int PAIRS>
@@ -649,7 +666,7 @@ struct Exchange {
 // the products P K and dS' K share the reads of K.
 template <int PAIRS>
 __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTile];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[3 * kTile];
   __shared__ __attribute__((aligned(16))) Exchange<PAIRS> ex;
   __shared__ float s_rest[PAIRS][2][32];
   __shared__ uint32_t s_bad[PAIRS][2];
@@ -690,63 +707,78 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
   f32x16 dq[3] = {}, pk[3] = {};
   float rest = 0.0f;                               // row sum of this half's dS'
   const float c = a.scale * kLog2e;
-  int buf = 0;
-  for (int k0 = 0; k0 < kend; k0 += kBN, buf ^= 1) {
-    tile_wait();
-    if (k0 + kBN < kend) tile_copy<2 * PAIRS>(cp, x.kn, x.kr, x.v, k0 + kBN, st.lk, buf ^ 1);
-    const bool live = k0 < wlast;                  // the same for both of a pair
+  // P and dS against the tile at k0 (in buffer `buf`), this wavefront's 32 keys of it
+  auto first = [&](uint4 (&mine)[4], int k0, int buf) __attribute__((always_inline)) {
+    if (k0 >= wlast) return;                       // the same for both of a pair
     const uint8_t* tile = lds + buf * kTile;
     // the units' addresses are formed again in every tile: kept, they cost too many registers
     asm volatile("" : "+v"(rp.n), "+v"(rp.r), "+v"(rp.tn), "+v"(rp.tr));
-    if (live) {
-      f32x16 s = {}, dp = {};
-      // the two chains alternate while both last
-      pipelined<kSteps + kVSteps, 4>(
-          [&](int i) {
-            return i < 2 * kVSteps && (i & 1) ? y_frag(tile, rp, half, i >> 1)
-                                              : x_frag(tile, rp, half, i < 2 * kVSteps ? i >> 1 : i - kVSteps);
-          },
-          [&](int i, bf16x8 f) {
-            if (i < 2 * kVSteps && (i & 1))
-              dp = mfma(f, g[i >> 1], dp);
-            else
-              s = mfma(f, q[i < 2 * kVSteps ? i >> 1 : i - kVSteps], s);
-          });
+    f32x16 s = {}, dp = {};
+    // the two chains alternate while both last
+    pipelined<kSteps + kVSteps, 4>(
+        [&](int i) {
+          return i < 2 * kVSteps && (i & 1) ? y_frag(tile, rp, half, i >> 1)
+                                            : x_frag(tile, rp, half, i < 2 * kVSteps ? i >> 1 : i - kVSteps);
+        },
+        [&](int i, bf16x8 f) {
+          if (i < 2 * kVSteps && (i & 1))
+            dp = mfma(f, g[i >> 1], dp);
+          else
+            s = mfma(f, q[i < 2 * kVSteps ? i >> 1 : i - kVSteps], s);
+        });
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse2));
-        dp[i] = s[i] * (dp[i] - delta);
-      }
-      if (k0 + kBN > wfirst) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (k0 + 32 * half + reg_row(i, h) >= lim) s[i] = 0.0f, dp[i] = 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) rest += dp[i];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        ex.f[pair][half][j][l] = __builtin_bit_cast(uint4, slab(s, j));
-        ex.f[pair][half][2 + j][l] = __builtin_bit_cast(uint4, slab(dp, j));
-      }
+    for (int i = 0; i < 16; ++i) {
+      s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse2));
+      dp[i] = s[i] * (dp[i] - delta);
     }
-    __syncthreads();
-    if (live) {
-      bf16x8 p[4], ds[4];
-      pipelined<12, 3>(
-          [&](int i) {
-            const int j = i / 3, d = i % 3;
-            if (d == 0) {
-              p[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][j & 1][l]);
-              ds[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][2 + (j & 1)][l]);
-            }
-            return d < 2 ? wide_tr(tile, rp, j, 2 * half + d) : rope_tr(tile + kOffR, rp, j, half);
-          },
-          [&](int i, bf16x8 f) {
-            dq[i % 3] = mfma(f, ds[i / 3], dq[i % 3]);
-            pk[i % 3] = mfma(f, p[i / 3], pk[i % 3]);
-          });
+    if (k0 + kBN > wfirst) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (k0 + 32 * half + reg_row(i, h) >= lim) s[i] = 0.0f, dp[i] = 0.0f;
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) rest += dp[i];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      mine[j] = __builtin_bit_cast(uint4, slab(s, j));
+      mine[2 + j] = __builtin_bit_cast(uint4, slab(dp, j));
+    }
+  };
+  // the sums over the tile at k0, with the pair's P and dS
+  auto second = [&](int k0, int buf) __attribute__((always_inline)) {
+    if (k0 < 0 || k0 >= wlast) return;
+    const uint8_t* tile = lds + buf * kTile;
+    asm volatile("" : "+v"(rp.n), "+v"(rp.r), "+v"(rp.tn), "+v"(rp.tr));
+    bf16x8 p[4], ds[4];
+    pipelined<12, 3>(
+        [&](int i) {
+          const int j = i / 3, d = i % 3;
+          if (d == 0) {
+            p[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][j & 1][l]);
+            ds[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][2 + (j & 1)][l]);
+          }
+          return d < 2 ? wide_tr(tile, rp, j, 2 * half + d) : rope_tr(tile + kOffR, rp, j, half);
+        },
+        [&](int i, bf16x8 f) {
+          dq[i % 3] = mfma(f, ds[i / 3], dq[i % 3]);
+          pk[i % 3] = mfma(f, p[i / 3], pk[i % 3]);
+        });
+  };
+  int buf = 0, prev = 2;                           // of this tile and of the one before
+  for (int k0 = 0; k0 < kend + kBN; k0 += kBN) {
+    tile_wait();
+    const int next = buf == 2 ? 0 : buf + 1;
+    if (k0 + kBN < kend) tile_copy<2 * PAIRS>(cp, x.kn, x.kr, x.v, k0 + kBN, st.lk, next);
+    uint4 mine[4];                                 // this wavefront's P and dS slabs
+    second(k0 - kBN, prev);
+    if (k0 < kend) first(mine, k0, buf);
+    __syncthreads();                               // the last tile's operands are consumed
+    if (k0 < kend && k0 < wlast) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ex.f[pair][half][j][l] = mine[j];
+    }
+    prev = buf;
+    buf = next;
   }
   rest = half_sum(rest);
   if (h == 0) s_rest[pair][half][n] = rest;
@@ -778,7 +810,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
 // a head, in head order.
 template <int PAIRS>
 __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTile];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[3 * kTile];
   __shared__ __attribute__((aligned(16))) Exchange<PAIRS> ex;
   __shared__ __attribute__((aligned(16))) float stat[2][2][kBN];   // lse (powers of two), D
   __shared__ uint32_t s_bad[PAIRS][2];
@@ -825,77 +857,93 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a)
   f32x16 wide[4] = {}, rope = {};
   const uint32_t side = half ? 0 : kOffY, op = half ? 2 : 0;   // queries and dS, or dO and P
   const float c = a.scale * kLog2e;
-  int buf = 0;
-  for (; q0 < st.lq; q0 += kBN, buf ^= 1) {
-    if (w == 0)
-      stat[buf][0][l] = z == -__builtin_inff() ? __builtin_inff() : z * kLog2e - kShift;   // no keys: P = 0
-    else if (w == 1)
-      stat[buf][1][l] = z;
-    tile_wait();
-    if (q0 + kBN < st.lq) {
-      z = stat_of(q0 + kBN);
-      tile_copy<2 * PAIRS>(cp, x.q, x.q + kNope, x.g, q0 + kBN, st.lq, buf ^ 1);
-    }
-    const bool live = q0 + kBN > wlim;             // some query here sees the pair's keys
+  // P and dS against the tile at r0 (in buffer `buf`), this wavefront's 32 queries of it
+  auto first = [&](uint4 (&mine)[4], int r0, int buf, int sb) __attribute__((always_inline)) {
+    if (r0 + kBN <= wlim) return;                  // no query here sees the pair's keys
     const uint8_t* tile = lds + buf * kTile;
     // the units' addresses are formed again in every tile: kept, they cost too many registers
     asm volatile("" : "+v"(rp.n), "+v"(rp.r), "+v"(rp.tn), "+v"(rp.tr));
-    if (live) {
-      f32x16 s = {}, dp = {};
-      // the two chains alternate while both last
-      pipelined<kSteps + kVSteps, 4>(
-          [&](int i) {
-            return i < 2 * kVSteps && (i & 1) ? y_frag(tile, rp, half, i >> 1)
-                                              : x_frag(tile, rp, half, i < 2 * kVSteps ? i >> 1 : i - kVSteps);
-          },
-          [&](int i, bf16x8 f) {
-            if (i < 2 * kVSteps && (i & 1))
-              dp = mfma(f, v[i >> 1], dp);
-            else
-              s = mfma(f, k[i < 2 * kVSteps ? i >> 1 : i - kVSteps], s);
-          });
+    f32x16 s = {}, dp = {};
+    // the two chains alternate while both last
+    pipelined<kSteps + kVSteps, 4>(
+        [&](int i) {
+          return i < 2 * kVSteps && (i & 1) ? y_frag(tile, rp, half, i >> 1)
+                                            : x_frag(tile, rp, half, i < 2 * kVSteps ? i >> 1 : i - kVSteps);
+        },
+        [&](int i, bf16x8 f) {
+          if (i < 2 * kVSteps && (i & 1))
+            dp = mfma(f, v[i >> 1], dp);
+          else
+            s = mfma(f, k[i < 2 * kVSteps ? i >> 1 : i - kVSteps], s);
+        });
 #pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4) {
-        const int r4 = 32 * half + 8 * q4 + 4 * h;
-        const f32x4 ls = *reinterpret_cast<const f32x4*>(&stat[buf][0][r4]);
-        const f32x4 dl = *reinterpret_cast<const f32x4*>(&stat[buf][1][r4]);
+    for (int q4 = 0; q4 < 4; ++q4) {
+      const int r4 = 32 * half + 8 * q4 + 4 * h;
+      const f32x4 ls = *reinterpret_cast<const f32x4*>(&stat[sb][0][r4]);
+      const f32x4 dl = *reinterpret_cast<const f32x4*>(&stat[sb][1][r4]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 4 * q4 + e;
-          s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -ls[e]));
-          dp[i] = s[i] * (dp[i] - dl[e]);
-        }
-      }
-      if (q0 + kBN > st.lq || q0 < wlim + 31) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int qi = q0 + 32 * half + reg_row(i, h);
-          if (qi < lim || qi >= st.lq) s[i] = 0.0f, dp[i] = 0.0f;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        ex.f[pair][half][j][l] = __builtin_bit_cast(uint4, slab(s, j));
-        ex.f[pair][half][2 + j][l] = __builtin_bit_cast(uint4, slab(dp, j));
+      for (int e = 0; e < 4; ++e) {
+        const int i = 4 * q4 + e;
+        s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -ls[e]));
+        dp[i] = s[i] * (dp[i] - dl[e]);
       }
     }
-    __syncthreads();
-    if (live) {
-      bf16x8 f0[4], ds[4];
-      pipelined<20, 3>(
-          [&](int i) {
-            const int j = i / 5, d = i % 5;
-            if (d == 0) f0[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][op + (j & 1)][l]);
-            if (d == 4) ds[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][2 + (j & 1)][l]);
-            return d < 4 ? wide_tr(tile + side, rp, j, d) : rope_tr(tile + kOffR, rp, j, half);
-          },
-          [&](int i, bf16x8 f) {
-            if (i % 5 < 4)
-              wide[i % 5] = mfma(f, f0[i / 5], wide[i % 5]);
-            else
-              rope = mfma(f, ds[i / 5], rope);
-          });
+    if (r0 + kBN > st.lq || r0 < wlim + 31) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int qi = r0 + 32 * half + reg_row(i, h);
+        if (qi < lim || qi >= st.lq) s[i] = 0.0f, dp[i] = 0.0f;
+      }
     }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      mine[j] = __builtin_bit_cast(uint4, slab(s, j));
+      mine[2 + j] = __builtin_bit_cast(uint4, slab(dp, j));
+    }
+  };
+  // the sums over the tile at r0, with the pair's P and dS
+  const int begin = q0;
+  auto second = [&](int r0, int buf) __attribute__((always_inline)) {
+    if (r0 < begin || r0 + kBN <= wlim) return;
+    const uint8_t* tile = lds + buf * kTile;
+    asm volatile("" : "+v"(rp.n), "+v"(rp.r), "+v"(rp.tn), "+v"(rp.tr));
+    bf16x8 f0[4], ds[4];
+    pipelined<20, 3>(
+        [&](int i) {
+          const int j = i / 5, d = i % 5;
+          if (d == 0) f0[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][op + (j & 1)][l]);
+          if (d == 4) ds[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][2 + (j & 1)][l]);
+          return d < 4 ? wide_tr(tile + side, rp, j, d) : rope_tr(tile + kOffR, rp, j, half);
+        },
+        [&](int i, bf16x8 f) {
+          if (i % 5 < 4)
+            wide[i % 5] = mfma(f, f0[i / 5], wide[i % 5]);
+          else
+            rope = mfma(f, ds[i / 5], rope);
+        });
+  };
+  int buf = 0, prev = 2, sb = 0;                   // buffers of this tile and of the one before
+  for (; q0 < st.lq + kBN; q0 += kBN, sb ^= 1) {
+    if (w == 0)
+      stat[sb][0][l] = z == -__builtin_inff() ? __builtin_inff() : z * kLog2e - kShift;   // no keys: P = 0
+    else if (w == 1)
+      stat[sb][1][l] = z;
+    tile_wait();
+    const int next = buf == 2 ? 0 : buf + 1;
+    if (q0 + kBN < st.lq) {
+      z = stat_of(q0 + kBN);
+      tile_copy<2 * PAIRS>(cp, x.q, x.q + kNope, x.g, q0 + kBN, st.lq, next);
+    }
+    uint4 mine[4];                                 // this wavefront's P and dS slabs
+    second(q0 - kBN, prev);
+    if (q0 < st.lq) first(mine, q0, buf, sb);
+    __syncthreads();                               // the last tile's operands are consumed
+    if (q0 < st.lq && q0 + kBN > wlim) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ex.f[pair][half][j][l] = mine[j];
+    }
+    prev = buf;
+    buf = next;
   }
   bool nf = any_nonfinite(wide), own = false;      // own: the key itself is not finite
 #pragma unroll
@@ -931,7 +979,8 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a)
 }
 
 // dk_rope[t] = scale * sum over heads, in head order, rounded once.  Four
-// columns a lane.  Rows outside every sequence get unspecified values.
+// columns a lane.  Rows outside every sequence get unspecified values.  Reads its
+// parts once: 16384 keys, 16 heads, 67 MB in 12.5 us, 5.4 TB/s.
 __global__ __launch_bounds__(kThr) void k_attn_drope(AttnArgs a) {
   const int64_t i = (int64_t)blockIdx.x * kThr + threadIdx.x;
   const int64_t t = i / (kRope / 4);

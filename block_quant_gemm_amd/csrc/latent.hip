@@ -126,18 +126,29 @@ __global__ __launch_bounds__(kThr) void k_latent_read(Cache k, const int64_t* __
 //
 // The rows of one request are its query tokens' heads (row s * H + h).  A
 // workgroup takes 16 R G of them (G groups of four wavefronts with 16 R each) and
-// a run of one request's 64-token tiles; all
-// runs are about equally long, so ragged lengths balance, and a request with
-// more than one leaves parts (FP32 sums, maximum and total) for
-// k_decode_merge.  A tile's codes are widened to BF16 once, into LDS, exactly
-// (the scale folded in), and serve all rows as keys and again, read
-// transposed, as values:
+// a run of one request's 64-token tiles; all runs are about equally long, so
+// ragged lengths balance, and a request with more than one leaves parts (FP32
+// sums, maximum and total) for k_decode_merge.  A run stays inside a request, so
+// a workgroup loads its queries once.  A tile's codes are widened to BF16 once,
+// into LDS, exactly (the scale folded in), and serve all rows as keys and
+// again, read transposed, as values:
 //   logits  wavefront w takes tokens 16 w .. 16 w + 15 against all rows,
-//           queries in registers;
+//           queries in registers (with 64 rows, 4 of 18 steps; the rest in LDS);
 //   values  wavefront w takes 128 latent columns for all rows and 64 tokens.
 // So each group reads the tile once per product whatever R is.  Both
 // products leave the query row along the lanes, and a lane's probabilities go
-// to the same lane of the other wavefronts of its group.
+// to the same lane of the other wavefronts of its group, rounded to BF16 as the
+// matrix unit wants them; maxima, totals and sums stay FP32.
+//
+// 16 rows (77 KB of LDS, two workgroups a CU: one's loads run beside the other's
+// products) are bound by the cache's bytes when requests are long: 6 of 60 to 120
+// thousand tokens, 16 heads, 70.6 us, 5.1 TB/s, what a large copy reaches.  96
+// requests of 1 to 6000 tokens take 20 us in three tiles a run, 8 of them the chain
+// of lengths, page, slot and first tile.  32 and 64 rows take eight wavefronts,
+// one workgroup a CU.  24 requests of 300 to 4200 tokens with 128 rows: 33.6 us, 14
+// of them the setup and the parts' stores (25 MB), then 2.9 us a tile, of which
+// LDS is busy for 1.9 (the keys once a wavefront, and the queries that registers
+// do not hold; at R = 4 they do not fit in any split tried).
 // ---------------------------------------------------------------------------
 
 constexpr int kTok = MXQ_LATENT_TILE;            // tokens of a tile
@@ -608,7 +619,8 @@ __global__ __launch_bounds__(kThr * G, R * G == 1 ? 2 : G) void k_decode(DecodeA
 // Joins the parts of the requests that more than one workgroup worked on, in
 // their order: with M = max m, o = sum 2^(m - M) O / sum 2^(m - M) l.  One
 // workgroup a row, 128 lanes of 4 columns, GROUPS such groups taking every
-// GROUPS-th part.
+// GROUPS-th part.  Reads what k_decode wrote last (5 us for 96 requests of 16 rows
+// and 418 parts, 7.5 us for 6 of 84 parts each), little more than a launch takes.
 template <int GROUPS>
 __global__ __launch_bounds__(128 * GROUPS) void k_decode_merge(DecodeArgs a, uint32_t nrt, int rows_per_tile) {
   __shared__ __attribute__((aligned(16))) float s_o[GROUPS > 1 ? GROUPS - 1 : 1][kLat];
