@@ -645,10 +645,14 @@ __global__ __launch_bounds__(kThr, 2) void k_attn_fwd(AttnArgs a) {
 // PAIRS = 2, 64 rows and a wavefront a SIMD: shorter steps, for calls that leave
 // CUs idle otherwise.
 //
-// 4 sequences of 4096, 16 heads, causal: dQ 759 us, dK and dV 805 us, 1.00 and 0.85
+// 4 sequences of 4096, 16 heads, causal: dQ 727 us, dK and dV 736 us, 1.04 and 0.93
 // PFLOP/s of the 11 and 10 products of 64 columns that they form a pair (13 in all
-// are the least; those that both form are S and dP, and P K makes D exact).  Bound
-// as the forward is, with the exchange's barrier beside.
+// are the least; S and dP are formed by both, and P K makes D exact).  Bound by
+// the matrix unit and the chain before P and dS: without the sums over the tiles
+// 1080 us of 1470 are left, though they are half of the products; without the
+// copies 6 % less, without the second barrier nothing.  The two of a pair taking
+// the two parts in opposite orders are slower (1556 us), and 64 rows a wavefront do
+// not fit.
 // ---------------------------------------------------------------------------
 
 template <int PAIRS>
@@ -980,7 +984,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a)
 
 // dk_rope[t] = scale * sum over heads, in head order, rounded once.  Four
 // columns a lane.  Rows outside every sequence get unspecified values.  Reads its
-// parts once: 16384 keys, 16 heads, 67 MB in 12.5 us, 5.4 TB/s.
+// parts once: 16384 keys, 16 heads, 67 MB in 12.9 us, 5.2 TB/s.
 __global__ __launch_bounds__(kThr) void k_attn_drope(AttnArgs a) {
   const int64_t i = (int64_t)blockIdx.x * kThr + threadIdx.x;
   const int64_t t = i / (kRope / 4);
