@@ -330,3 +330,21 @@ def test_hidden_nan_with_many_empty_sequences(what):
         a, b = host(few[name].contiguous()), host(got[name].contiguous())
         nan = lambda x: ~np.isfinite(codec.bf16_bits_to_f64(x))
         assert np.array_equal(nan(a), nan(b)) and np.array_equal(a[~nan(a)], b[~nan(b)]), name
+
+
+@pytest.mark.parametrize("H,lens", [(64, [300, 0, 513, 129]), (64, [700, 90, 400]), (128, [140, 1, 128, 600]),
+                                    (256, [129, 300]), (300, [130, 65]), (51, [900])])
+def test_many_workgroups(H, lens):
+    """More than 256 workgroups, which start two to a CU: every tile is taken once, and each
+    head's rows are what a call with that head alone gives, bit for bit."""
+    say(f"latent attention H={H} lens={lens}")
+    d = _inputs(lens, lens, H, H)
+    for causal in (True, False):
+        got = _run(d, causal)
+        for h in (0, H // 2, H - 1):
+            one = {k: v if k in ("oq", "ok", "kr") else np.ascontiguousarray(v[:, h:h + 1]) for k, v in d.items()}
+            ref = _run(one, causal)
+            for n in ("o", "dq", "dk_nope", "dv"):
+                assert torch.equal(got[n][:, h:h + 1].contiguous().view(torch.int16),
+                                   ref[n].contiguous().view(torch.int16)), (n, h)
+            assert torch.equal(got["lse"][h], ref["lse"][0]), h
