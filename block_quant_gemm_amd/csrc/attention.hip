@@ -1130,10 +1130,13 @@ extern "C" int latent_attention_backward(
   if (need > 0 && !workspace) return MXQ_ERR_NULL;
   if (!aligned16(workspace)) return MXQ_ERR_ALIGN;
   // Workgroups of 64 rows where about that many, T / 64 and half a tile a sequence,
-  // still run at once, one a CU (one sequence of 360, 16 heads: 43 us for the three
-  // kernels against 59; 2 of 1000, 8 heads: 74 against 100); else of 128 (4 of 300, 16
-  // heads, a second turn for 64 CUs: 58 against 61; 8 of 512, 16 heads: 138 against 152).
-  const auto few = [&](int64_t T) { return (T / 64 + a.B / 2) * a.H <= 256; };
+  // still run at once, one a CU (one sequence of 360, 16 heads: 41 us for the three
+  // kernels against 59; 2 of 1000, 8 heads: 74 against 100), or, in one causal
+  // sequence, whose longest start first, in two turns (5000, 4 heads: 264 against 338;
+  // 2048, 16 heads: 149 against 164; 5400, 8 heads, more than that: 446 against 392).
+  // Else of 128 (4 of 300, 16 heads: 56 against 60; 8 of 512: 138 against 152).
+  const int64_t turn = a.causal && a.B == 1 ? 512 : 256;
+  const auto few = [&](int64_t T) { return (T / 64 + a.B / 2) * a.H <= turn; };
   const bool fewq = few(a.Tq), fewk = few(a.Tk);
   uint32_t nq, nk, nr;
   MXQ_TRY(grid_of(a.Tq, fewq ? 64 : 128, a, &nq));
