@@ -68,6 +68,9 @@ struct AttnArgs {
   int64_t ldl;
   float* delta;                                  // [H, Tq]
   float* rope_part;                              // [H, Tk, 64]
+  int32_t parts;                                 // at most, of a forward tile's keys
+  float* part_o;                                 // [parts, H, Tq, 128]
+  float* part_ml;                                // [parts, H, Tq, 2]
 };
 
 // ---------------------------------------------------------------------------
@@ -555,11 +558,22 @@ __device__ __forceinline__ int keys_seen(const AttnArgs& a, const SeqTile& s, in
 // heads: 46 us to 42) and cost every other case (this one: 470 us).
 // ---------------------------------------------------------------------------
 
+// With SPLIT, a call of few workgroups, several take a tile's keys between them,
+// and k_attn_join joins their sums.
+
+// Parts of a tile whose rows see `keys` keys.
+__device__ __forceinline__ int parts_of(const AttnArgs& a, int keys) {
+  const int n = keys / kPartKeys;
+  return n < 1 ? 1 : n < a.parts ? n : a.parts;
+}
+
+template <bool SPLIT>
 __global__ __launch_bounds__(kThr, 2) void k_attn_fwd(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTile];
   constexpr int BM = 128;
   const int head = blockIdx.x % a.H;
-  const SeqTile st = find_tile<false, true>(a, blockIdx.x / a.H, BM);
+  const uint32_t unit = blockIdx.x / a.H;
+  const SeqTile st = find_tile<false, !SPLIT>(a, SPLIT ? unit / a.parts : unit, BM);
   if (!st.ok) return;                              // uniform over the workgroup
   const int l = threadIdx.x & 63, n = l & 31, h = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -575,7 +589,16 @@ __global__ __launch_bounds__(kThr, 2) void k_attn_fwd(AttnArgs a) {
   const int kend = keys_seen(a, st, last);
   const int wfirst = keys_seen(a, st, wrow0), wlast = keys_seen(a, st, wrow0 + 31);
   const int lim = keys_seen(a, st, row);
-  if (kend > 0) tile_copy<4>(cp, kn, kr, v, 0, st.lk, 0);
+  int part = 0, parts = 1, kfirst = 0, kstop = kend;
+  if (SPLIT) {
+    part = (int)(unit % a.parts);
+    parts = parts_of(a, kend);
+    if (part >= parts) return;
+    const int tiles = (kend + kBN - 1) / kBN;
+    kfirst = tiles * part / parts * kBN;
+    if (part + 1 < parts) kstop = tiles * (part + 1) / parts * kBN;
+  }
+  if (kstop > kfirst) tile_copy<4>(cp, kn, kr, v, kfirst, st.lk, 0);
 
   bf16x8 q[kSteps];
   const uint16_t* qp = a.q.p + st.q0 * a.q.ld + head * a.q.ldh;
@@ -584,9 +607,9 @@ __global__ __launch_bounds__(kThr, 2) void k_attn_fwd(AttnArgs a) {
   float m = -__builtin_inff(), sum = 0.0f;         // reference (powers of two), total
   const float c = a.scale * kLog2e;
   int buf = 0;
-  for (int k0 = 0; k0 < kend; k0 += kBN, buf ^= 1) {
+  for (int k0 = kfirst; k0 < kstop; k0 += kBN, buf ^= 1) {
     tile_wait();
-    if (k0 + kBN < kend) tile_copy<4>(cp, kn, kr, v, k0 + kBN, st.lk, buf ^ 1);
+    if (k0 + kBN < kstop) tile_copy<4>(cp, kn, kr, v, k0 + kBN, st.lk, buf ^ 1);
     if (k0 >= wlast) continue;                     // nothing seen by this wavefront
     const uint8_t* tile = lds + buf * kTile;
     f32x16 s[2] = {};
@@ -632,6 +655,19 @@ __global__ __launch_bounds__(kThr, 2) void k_attn_fwd(AttnArgs a) {
       for (int d = 0; d < 4; ++d) o[d] = mfma(wide_tr(tile + kOffY, rp, j, d), p[j], o[d]);
   }
   const float total = half_sum(sum);
+  if (SPLIT && parts > 1) {
+    if (row < st.lq) {
+      const int64_t pr = ((int64_t)part * a.H + head) * a.Tq + st.q0 + row;
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<f32x4*>(a.part_o + pr * kVal + 32 * d + 8 * i + 4 * h) =
+              f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+      if (h == 0) a.part_ml[2 * pr] = m, a.part_ml[2 * pr + 1] = total;
+    }
+    return;
+  }
   // a row that sees nothing: zeros, and minus infinity
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   const uint64_t bad = __ballot(any_nonfinite(o) && row < st.lq && total == total);
@@ -649,6 +685,65 @@ __global__ __launch_bounds__(kThr, 2) void k_attn_fwd(AttnArgs a) {
     const int i = wrow0 + __builtin_ctz(redo);
     redo &= redo - 1;
     redo_output(a, st, head, i, keys_seen(a, st, i));
+  }
+}
+
+// Joins the parts of the tiles that have several, in their order: with M = max m,
+// o = sum 2^(m - M) O / sum 2^(m - M) l.  A workgroup takes 32 rows of a tile, 8
+// lanes a row.  Rows whose hidden keys left a NaN are redone here.
+__global__ __launch_bounds__(kThr) void k_attn_join(AttnArgs a) {
+  const int head = blockIdx.x % a.H;
+  const uint32_t unit = blockIdx.x / a.H;
+  const SeqTile st = find_tile<false>(a, unit / 4, 128);
+  if (!st.ok) return;
+  const int last = (st.row0 + 128 < st.lq ? st.row0 + 128 : st.lq) - 1;
+  const int parts = parts_of(a, keys_seen(a, st, last));
+  const int l = threadIdx.x & 63, w = threadIdx.x >> 6, c = l & 7;
+  const int row0 = st.row0 + (int)(unit % 4) * 32 + w * 8, row = row0 + (l >> 3);
+  if (parts == 1 || row0 >= st.lq) return;         // uniform over the wavefront
+  const bool ok = row < st.lq;
+  const int64_t pr = (int64_t)head * a.Tq + st.q0 + (ok ? row : row0), step = (int64_t)a.H * a.Tq;
+  float m = -__builtin_inff();
+  for (int p = 0; p < parts; ++p) m = __builtin_fmaxf(m, a.part_ml[2 * (pr + p * step)]);
+  const float ref = m == -__builtin_inff() ? 0.0f : m;
+  f32x4 o[4] = {};
+  float total = 0.0f;
+#pragma unroll 2
+  for (int p = 0; p < parts; ++p) {
+    const int64_t at = pr + p * step;
+    const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - ref);
+    total = __builtin_fmaf(f, a.part_ml[2 * at + 1], total);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(a.part_o + at * kVal + 32 * j + 4 * c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] = __builtin_fmaf(f, v[e], o[j][e]);
+    }
+  }
+  bool nf = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) nf |= !(__builtin_fabsf(o[j][e]) < __builtin_inff());
+  uint64_t bad = __ballot(nf && ok && a.causal && total == total);
+  if (ok && ((bad >> (l & 56)) & 0xFF) == 0) {
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    uint16_t* p = a.out.p + (st.q0 + row) * a.out.ld + head * a.out.ldh + 4 * c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint2 x;
+      x.x = bf16x2_bits(o[j][0] * inv, o[j][1] * inv);
+      x.y = bf16x2_bits(o[j][2] * inv, o[j][3] * inv);
+      *reinterpret_cast<uint2*>(p + 32 * j) = x;
+    }
+  }
+  if (ok && c == 0)
+    a.lse[head * a.ldl + st.q0 + row] =
+        total == 0.0f ? -__builtin_inff() : kLn2 * (ref + __builtin_amdgcn_logf(total));
+#pragma unroll 1
+  for (int y = 0; y < 8; ++y) {
+    if (((bad >> (8 * y)) & 0xFF) == 0) continue;
+    redo_output(a, st, head, row0 + y, keys_seen(a, st, row0 + y));
   }
 }
 
@@ -1091,20 +1186,35 @@ int grid_of(int64_t T, int64_t rows, const AttnArgs& a, uint32_t* n) {
 using namespace mxq;
 
 extern "C" int latent_attention(const mxq_latent_attn* d, uint16_t* o, int64_t ldo,
-                                int64_t ldo_head, float* lse, int64_t ldl, hipStream_t stream) {
+                                int64_t ldo_head, float* lse, int64_t ldl, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
   AttnArgs a;
   MXQ_TRY(check_attn(d, &a));
   MXQ_TRY(check_op(o, a.Tq, ldo, ldo_head, kVal));
   if (a.Tq > 0 && !lse) return MXQ_ERR_NULL;
   if (ldl < a.Tq) return MXQ_ERR_SHAPE;
   if ((uintptr_t)lse % 4 != 0) return MXQ_ERR_ALIGN;
+  a.parts = latent_forward_parts(a.Tq, a.Tk, a.H, a.B);
+  const size_t need = latent_forward_workspace(a.Tq, a.Tk, a.H, a.B);
+  if (workspace_bytes < need) return MXQ_ERR_WORKSPACE;
+  if (need > 0 && !workspace) return MXQ_ERR_NULL;
+  if (need > 0 && !aligned16(workspace)) return MXQ_ERR_ALIGN;
   if (a.Tq == 0) return MXQ_OK;
   a.out = {o, ldo, ldo_head};
   a.lse = lse;
   a.ldl = ldl;
   uint32_t n;
   MXQ_TRY(grid_of(a.Tq, 128, a, &n));
-  hipLaunchKernelGGL(k_attn_fwd, dim3(n), dim3(kThr), 0, stream, a);
+  if (a.parts == 1) {
+    hipLaunchKernelGGL(k_attn_fwd<false>, dim3(n), dim3(kThr), 0, stream, a);
+    return launch_status();
+  }
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = a.part_o + (int64_t)a.parts * a.H * a.Tq * kVal;
+  // few rows, so n times 16 is far from a launch's limit
+  hipLaunchKernelGGL(k_attn_fwd<true>, dim3(n * (uint32_t)a.parts), dim3(kThr), 0, stream, a);
+  MXQ_TRY(launch_status());
+  hipLaunchKernelGGL(k_attn_join, dim3(n * 4), dim3(kThr), 0, stream, a);
   return launch_status();
 }
 

@@ -54,6 +54,28 @@ inline LatentDecodePlan latent_decode_plan(int64_t B, int64_t S, int64_t H, int6
   return p;
 }
 
+// Parts along the keys that latent_attention gives a tile of 128 query rows: as
+// many as fill two workgroups on each of 256 CUs, of 384 keys at least for a
+// sequence of average length, and none below 1024 keys (a part's 6 tiles take about
+// 8 us, joining the parts 5).  With parts and without: 16 queries after 4080 keys, 16 heads, 29 us and
+// 103; 512 after 2488, 41 and 77; one sequence of 2000, 4 heads, 29 and 46.
+constexpr int kPartKeys = 384;
+inline int latent_forward_parts(int64_t Tq, int64_t Tk, int64_t H, int64_t B) {
+  if (Tq < 1 || Tk < 1 || H < 1 || B < 1) return 1;
+  // tiles: half of one more than full ones a sequence, one at least
+  const int64_t half = Tq / 128 + B / 2 + B % 2, tiles = half > B ? half : B;
+  const int64_t fill = 512 / sat_mul(tiles, H), keys = Tk / B < 1024 ? 1 : Tk / B / kPartKeys;
+  const int64_t n = fill < keys ? fill : keys;
+  return n < 1 ? 1 : n > 16 ? 16 : (int)n;
+}
+// One part's sums a row and head (128, with their reference and total), FP32.
+inline size_t latent_forward_workspace(int64_t Tq, int64_t Tk, int64_t H, int64_t B) {
+  const int n = latent_forward_parts(Tq, Tk, H, B);
+  if (n == 1) return 0;
+  const int64_t bytes = sat_mul(sat_mul(sat_mul(H, Tq), n), (MXQ_VALUE_DIM + 2) * (int64_t)sizeof(float));
+  return bytes == INT64_MAX ? SIZE_MAX : (size_t)bytes;
+}
+
 // Workspace of latent_attention_backward: the rotary key's gradient of each
 // head, and D of each row, both FP32.  SIZE_MAX when it does not fit.
 inline size_t latent_backward_workspace(int64_t Tq, int64_t Tk, int64_t H) {

@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libmxq.so")
 
 OUT_BF16, OUT_FP32 = 0, 1
 ACC_MFMA_FP8, ACC_FP32 = 0, 1
-WS_PER_TENSOR, WS_PER_GROUP, WS_LATENT_DECODE, WS_LATENT_BACKWARD = 0, 1, 2, 3
+WS_PER_TENSOR, WS_PER_GROUP, WS_LATENT_DECODE, WS_LATENT_BACKWARD, WS_LATENT_FORWARD = range(5)
 
 _i64, _i32, _p, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
 _f32 = ctypes.c_float
@@ -106,7 +106,7 @@ _SIGS = {
                                         _i64, _i32, _i32, _p, _i32, _i32, _i32, _i64, _f32, _p,
                                         _i64, _i64, _i64, _p, _p, _sz, _p]),
     "latent_attention": (ctypes.c_int, [_p, _p, _i64, _i64, _p, _i64,
-                                        _p]),
+                                        _p, _sz, _p]),
     "latent_attention_backward": (ctypes.c_int, [_p, _p, _i64, _i64, _p,
                                                  _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64,
                                                  _i64, _p, _i64, _p, _i64, _i64, _p, _sz, _p]),
@@ -845,7 +845,7 @@ def _attn_arg(q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal):
 
 
 def latent_attention(q, k_nope, k_rope, v, offsets_q=None, offsets_k=None, scale=None, causal=True,
-                     o=None, lse=None):
+                     o=None, lse=None, workspace=None):
     """Expanded latent attention over packed sequences.
 
     q BF16 [Tq, H, 192] (128 columns for k_nope, then 64 for k_rope); k_nope
@@ -862,7 +862,17 @@ def latent_attention(q, k_nope, k_rope, v, offsets_q=None, offsets_k=None, scale
         lse = q.new_empty((H, Tq), dtype=_F32)
     so = _rows("o", o, _BF16, (Tq, H, 128))
     sl = _rows("lse", lse, _F32, (H, Tq))
-    st = load().latent_attention(arg, o.data_ptr(), so[0], so[1], lse.data_ptr(), sl[0],
+    ws, size = 0, 0
+    if workspace is None:
+        B = 1 if offsets_q is None else offsets_q.shape[0] - 1
+        size = _latent_workspace(WS_LATENT_FORWARD, Tq, k_nope.shape[0], H, B)
+        if size:
+            workspace = q.new_empty(size, dtype=_U8)
+    if workspace is not None:
+        size = workspace.numel()
+        _rows("workspace", workspace, _U8, (size,))
+        ws = workspace.data_ptr()
+    st = load().latent_attention(arg, o.data_ptr(), so[0], so[1], lse.data_ptr(), sl[0], ws, size,
                                  _raw_stream(q))
     if st:
         _check(st)

@@ -772,10 +772,14 @@ typedef struct mxq_latent_attn {
  *   o    : device, BF16 [Tq, H, 128], strides ldo, ldo_head (% 8 == 0), 16-byte
  *          aligned.
  *   lse  : device float [H, Tq], row stride ldl >= Tq.
+ *   workspace : device scratch of at least mxq_workspace_size(
+ *          MXQ_WS_LATENT_FORWARD, Tq, Tk, H, B) bytes (B = 1 without offsets),
+ *          16-byte aligned; may be NULL where that is 0 (calls that fill the GPU).
  * Rows outside every sequence are not written.
  */
 MXQ_API int latent_attention(const mxq_latent_attn* attn, uint16_t* o, int64_t ldo, int64_t ldo_head,
-                     float* lse, int64_t ldl, hipStream_t stream);
+                     float* lse, int64_t ldl, void* workspace, size_t workspace_bytes,
+                     hipStream_t stream);
 
 /*
  * Gradient of latent_attention: with P = exp(z - lse), dP = dO V^T,
@@ -812,12 +816,13 @@ MXQ_API int latent_attention_backward(const mxq_latent_attn* attn, const uint16_
 /* Workspace kinds: per-tensor quantization (n = elements), per-group
  * quantization (n = rows, a1 = groups), absorbed latent attention (n = B,
  * a1 = S, a2 = H, a3 = max_len), expanded latent attention's gradient (n = Tq,
- * a1 = Tk, a2 = H). */
+ * a1 = Tk, a2 = H) and forward pass (n = Tq, a1 = Tk, a2 = H, a3 = B). */
 enum {
   MXQ_WS_PER_TENSOR = 0,
   MXQ_WS_PER_GROUP = 1,
   MXQ_WS_LATENT_DECODE = 2,
-  MXQ_WS_LATENT_BACKWARD = 3
+  MXQ_WS_LATENT_BACKWARD = 3,
+  MXQ_WS_LATENT_FORWARD = 4
 };
 
 /* Workspace bytes an operation needs (0 if none). */

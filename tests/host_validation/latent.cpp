@@ -75,7 +75,9 @@ struct Attn {
     d.scale = 0.07f;
     d.causal = 1;
   }
-  int fwd() const { return latent_attention(&d, o, lo, loh, lse, ll, nullptr); }
+  void* fws = x;
+  size_t fws_bytes = size_t(1) << 50;
+  int fwd() const { return latent_attention(&d, o, lo, loh, lse, ll, fws, fws_bytes, nullptr); }
   int bwd() const {
     return latent_attention_backward(&d, o, lo, loh, lse, ll, go, lg, lgh, dq, ldq, ldqh, dk, ldk,
                                      ldkh, dr, ldr, dv, ldv, ldvh, ws, ws_bytes, nullptr);
@@ -219,7 +221,8 @@ int main() {
   for (int64_t x : {INT64_C(0), INT64_C(1), BIG, HUGE_, -HUGE_})
     for (int64_t y : {INT64_C(1), INT64_C(65536), HUGE_})
       (void)mxq_workspace_size(MXQ_WS_LATENT_DECODE, x, y, y, x),
-          (void)mxq_workspace_size(MXQ_WS_LATENT_BACKWARD, x, x, y, 0);
+          (void)mxq_workspace_size(MXQ_WS_LATENT_BACKWARD, x, x, y, 0),
+          (void)mxq_workspace_size(MXQ_WS_LATENT_FORWARD, x, x, y, y);
 
   // ---- expanded attention and its gradient ----
   ATTN((void)0, HIP);
@@ -270,7 +273,7 @@ int main() {
   ATTN(t.d.v = t.x + 4, MXQ_ERR_ALIGN);
   ATTN(t.o = t.x + 4, MXQ_ERR_ALIGN);
   ATTN(t.lse = reinterpret_cast<float*>(P + 2), MXQ_ERR_ALIGN);
-  EXPECT(latent_attention(nullptr, X, 256, 128, nullptr, 100, nullptr), MXQ_ERR_NULL);
+  EXPECT(latent_attention(nullptr, X, 256, 128, nullptr, 100, nullptr, 0, nullptr), MXQ_ERR_NULL);
   {
     Attn t;
     t.d.Tq = 0; t.d.q = nullptr; t.o = nullptr; t.lse = nullptr;
@@ -279,6 +282,27 @@ int main() {
     EXPECT(t.bwd(), HIP);                                     // zeros for dk and dv
     t.d.Tk = 0;
     EXPECT(t.bwd(), MXQ_OK);
+  }
+  {
+    Attn t;                                                   // few queries, many keys
+    t.d.B = 1;
+    t.d.Tk = 8000;
+    const size_t need = mxq_workspace_size(MXQ_WS_LATENT_FORWARD, 100, 8000, 2, 1);
+    EXPECT(need > 0 && need % (4 * 2 * 100 * 130) == 0, true);
+    t.fws_bytes = need;
+    EXPECT(t.fwd(), HIP);
+    t.fws_bytes = need - 1;
+    EXPECT(t.fwd(), MXQ_ERR_WORKSPACE);
+    t.fws_bytes = need;
+    t.fws = nullptr;
+    EXPECT(t.fwd(), MXQ_ERR_NULL);
+    t.fws = P + 4;
+    EXPECT(t.fwd(), MXQ_ERR_ALIGN);
+    EXPECT(mxq_workspace_size(MXQ_WS_LATENT_FORWARD, 16384, 16384, 16, 4), 0);
+    Attn u;
+    u.fws = nullptr;
+    u.fws_bytes = 0;
+    EXPECT(u.fwd(), HIP);                                     // none is needed
   }
   BACK(t.go = nullptr, MXQ_ERR_NULL);
   BACK(t.dq = nullptr, MXQ_ERR_NULL);

@@ -348,3 +348,53 @@ def test_many_workgroups(H, lens):
                 assert torch.equal(got[n][:, h:h + 1].contiguous().view(torch.int16),
                                    ref[n].contiguous().view(torch.int16)), (n, h)
             assert torch.equal(got["lse"][h], ref["lse"][0]), h
+
+
+SPLIT = [
+    # few queries, many keys: query lengths, key lengths, heads, causal
+    ([16], [4100], 2, True),
+    ([1], [2600], 3, False),
+    ([130], [1500], 2, True),
+    ([1300], [1090], 1, True),                   # more queries than keys: rows that see nothing
+    ([40, 0, 3, 200], [2100, 1500, 2, 1700], 2, True),
+    ([64, 129], [3000, 700], 1, False),
+]
+
+
+@pytest.mark.parametrize("case", range(len(SPLIT)))
+def test_few_queries_many_keys(case):
+    """Calls whose tiles' keys several workgroups take between them."""
+    lq, lk, H, causal = SPLIT[case]
+    say(f"latent attention lq={lq} lk={lk} H={H} causal={causal}")
+    assert mxq.workspace_size(mxq.WS_LATENT_FORWARD, sum(lq), sum(lk), H, len(lq)) > 0
+    d = _inputs(lq, lk, H, 100 + case)
+    ref = latent.attention_backward(codec.bf16_bits_to_f64(d["do"]), *_f64(d), d["oq"], d["ok"],
+                                    SCALE, causal)
+    got = _run(d, causal)
+    _compare(got, ref)
+    again = _run(d, causal)
+    for n in got:
+        assert torch.equal(got[n].contiguous().view(torch.int16), again[n].contiguous().view(torch.int16)), n
+
+
+@pytest.mark.parametrize("what", [0x7FC0, 0x7F80])
+def test_hidden_nan_with_few_queries_many_keys(what):
+    """The last queries and their keys are broken: those before see sound keys only."""
+    say(f"latent attention 60 queries after 1940 keys, rows of {what:#x}")
+    lq, lk, cut = 60, 2000, 45
+    d = _inputs([lq], [lk], 2, 120)
+    sound = {k: v.copy() for k, v in d.items()}
+    sound["q"], sound["do"] = d["q"][:cut].copy(), d["do"][:cut].copy()
+    sound["kv"], sound["kr"] = d["kv"][:lk - lq + cut].copy(), d["kr"][:lk - lq + cut].copy()
+    sound["oq"], sound["ok"] = np.array([0, cut]), np.array([0, lk - lq + cut])
+    for r in range(cut, lq, 4):
+        d["q"][r, 0, 3] = what
+        d["kv"][lk - lq + r, :, 5] = what
+        d["kv"][lk - lq + r, :, 140] = what
+        d["kr"][lk - lq + r, 7] = what
+    t = _device(d)
+    o, lse = mxq.latent_attention(*t, to_dev(d["oq"]), to_dev(d["ok"]))
+    ref = latent.attention_backward(codec.bf16_bits_to_f64(sound["do"]), *_f64(sound), sound["oq"],
+                                    sound["ok"], SCALE, True)
+    _compare({"o": o[:cut].contiguous(), "lse": lse[:, :cut].contiguous()},
+             {n: ref[n] for n in ("o", "lse")})
