@@ -770,10 +770,30 @@ __global__ __launch_bounds__(kThr) void k_attn_join(AttnArgs a) {
 // not fit.
 // ---------------------------------------------------------------------------
 
-template <int PAIRS>
+// Slabs that a wavefront hands over: 2 of P, 2 of dS, and with FINE the 2 of what
+// dS's rounding to BF16 leaves, again in BF16.
+//
+// FINE: rounding dS once costs dQ and dK as much as rounding the result does; the
+// two together are 1.41 times the least error, evenly in large calls.  In small
+// ones, where few entries of dS carry the result, up to 1.95 times was seen; with
+// the second term 1.1 (one sequence of 360, 16 heads: 45 us for the three kernels
+// against 41).
+template <int PAIRS, bool FINE>
 struct Exchange {
-  uint4 f[PAIRS][2][4][64];                      // pair, half, P slabs and dS slabs, lane
+  uint4 f[PAIRS][2][FINE ? 6 : 4][64];           // pair, half, slab, lane
 };
+
+// What rounding to BF16 left of 8 values (slab j of p, rounded to w), rounded.
+__device__ __forceinline__ uint4 slab_rest(const f32x16& p, uint4 w, int j) {
+  f32x16 r;
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[8 * j + 2 * i] = p[8 * j + 2 * i] - __builtin_bit_cast(float, x[i] << 16);
+    r[8 * j + 2 * i + 1] = p[8 * j + 2 * i + 1] - __builtin_bit_cast(float, x[i] & 0xFFFF0000u);
+  }
+  return __builtin_bit_cast(uint4, slab(r, j));
+}
 
 // Backward, queries: dQ and D, which the keys' kernel reads.
 //
@@ -783,13 +803,13 @@ struct Exchange {
 // numbers).  With dS' = P * (dP - d), the row sum r of dS' is D - d, and
 //   dQ = scale * (dS' K - r (P K)):
 // the products P K and dS' K share the reads of K.
-template <int PAIRS>
+template <int PAIRS, bool FINE>
 __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[3 * kTile];
-  __shared__ __attribute__((aligned(16))) Exchange<PAIRS> ex;
+  __shared__ __attribute__((aligned(16))) Exchange<PAIRS, FINE> ex;
   __shared__ float s_rest[PAIRS][2][32];
   __shared__ uint32_t s_bad[PAIRS][2];
-  constexpr int BM = 32 * PAIRS;
+  constexpr int BM = 32 * PAIRS, kSlabs = FINE ? 6 : 4;
   const int head = blockIdx.x % a.H;
   const SeqTile st = find_tile<false>(a, blockIdx.x / a.H, BM);
   if (!st.ok) return;
@@ -827,7 +847,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
   float rest = 0.0f;                               // row sum of this half's dS'
   const float c = a.scale * kLog2e;
   // P and dS against the tile at k0 (in buffer `buf`), this wavefront's 32 keys of it
-  auto first = [&](uint4 (&mine)[4], int k0, int buf) __attribute__((always_inline)) {
+  auto first = [&](uint4 (&mine)[kSlabs], int k0, int buf) __attribute__((always_inline)) {
     if (k0 >= wlast) return;                       // the same for both of a pair
     const uint8_t* tile = lds + buf * kTile;
     // the units' addresses are formed again in every tile: kept, they cost too many registers
@@ -861,6 +881,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
     for (int j = 0; j < 2; ++j) {
       mine[j] = __builtin_bit_cast(uint4, slab(s, j));
       mine[2 + j] = __builtin_bit_cast(uint4, slab(dp, j));
+      if (FINE) mine[kSlabs - 2 + j] = slab_rest(dp, mine[2 + j], j);
     }
   };
   // the sums over the tile at k0, with the pair's P and dS
@@ -868,18 +889,20 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
     if (k0 < 0 || k0 >= wlast) return;
     const uint8_t* tile = lds + buf * kTile;
     asm volatile("" : "+v"(rp.n), "+v"(rp.r), "+v"(rp.tn), "+v"(rp.tr));
-    bf16x8 p[4], ds[4];
+    bf16x8 p[4], ds[4], rs[4];
     pipelined<12, 3>(
         [&](int i) {
           const int j = i / 3, d = i % 3;
           if (d == 0) {
             p[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][j & 1][l]);
             ds[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][2 + (j & 1)][l]);
+            if (FINE) rs[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][kSlabs - 2 + (j & 1)][l]);
           }
           return d < 2 ? wide_tr(tile, rp, j, 2 * half + d) : rope_tr(tile + kOffR, rp, j, half);
         },
         [&](int i, bf16x8 f) {
           dq[i % 3] = mfma(f, ds[i / 3], dq[i % 3]);
+          if (FINE) dq[i % 3] = mfma(f, rs[i / 3], dq[i % 3]);
           pk[i % 3] = mfma(f, p[i / 3], pk[i % 3]);
         });
   };
@@ -888,13 +911,13 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
     tile_wait();
     const int next = buf == 2 ? 0 : buf + 1;
     if (k0 + kBN < kend) tile_copy<2 * PAIRS>(cp, x.kn, x.kr, x.v, k0 + kBN, st.lk, next);
-    uint4 mine[4];                                 // this wavefront's P and dS slabs
+    uint4 mine[kSlabs];                            // this wavefront's P and dS slabs
     second(k0 - kBN, prev);
     if (k0 < kend) first(mine, k0, buf);
     __syncthreads();                               // the last tile's operands are consumed
     if (k0 < kend && k0 < wlast) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ex.f[pair][half][j][l] = mine[j];
+      for (int j = 0; j < kSlabs; ++j) ex.f[pair][half][j][l] = mine[j];
     }
     prev = buf;
     buf = next;
@@ -927,13 +950,13 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
 // Backward, keys: dK, dV, walking the queries that see the workgroup's keys.  The
 // rotary part of dK is summed over the heads by k_attn_drope, from one FP32 part
 // a head, in head order.
-template <int PAIRS>
+template <int PAIRS, bool FINE>
 __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[3 * kTile];
-  __shared__ __attribute__((aligned(16))) Exchange<PAIRS> ex;
+  __shared__ __attribute__((aligned(16))) Exchange<PAIRS, FINE> ex;
   __shared__ __attribute__((aligned(16))) float stat[2][2][kBN];   // lse (powers of two), D
   __shared__ uint32_t s_bad[PAIRS][2];
-  constexpr int BM = 32 * PAIRS;
+  constexpr int BM = 32 * PAIRS, kSlabs = FINE ? 6 : 4;
   const int head = blockIdx.x % a.H;
   const SeqTile st = find_tile<true>(a, blockIdx.x / a.H, BM);
   if (!st.ok) return;
@@ -977,7 +1000,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a)
   const uint32_t side = half ? 0 : kOffY, op = half ? 2 : 0;   // queries and dS, or dO and P
   const float c = a.scale * kLog2e;
   // P and dS against the tile at r0 (in buffer `buf`), this wavefront's 32 queries of it
-  auto first = [&](uint4 (&mine)[4], int r0, int buf, int sb) __attribute__((always_inline)) {
+  auto first = [&](uint4 (&mine)[kSlabs], int r0, int buf, int sb) __attribute__((always_inline)) {
     if (r0 + kBN <= wlim) return;                  // no query here sees the pair's keys
     const uint8_t* tile = lds + buf * kTile;
     // the units' addresses are formed again in every tile: kept, they cost too many registers
@@ -1018,6 +1041,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a)
     for (int j = 0; j < 2; ++j) {
       mine[j] = __builtin_bit_cast(uint4, slab(s, j));
       mine[2 + j] = __builtin_bit_cast(uint4, slab(dp, j));
+      if (FINE) mine[kSlabs - 2 + j] = slab_rest(dp, mine[2 + j], j);
     }
   };
   // the sums over the tile at r0, with the pair's P and dS
@@ -1026,19 +1050,23 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a)
     if (r0 < begin || r0 + kBN <= wlim) return;
     const uint8_t* tile = lds + buf * kTile;
     asm volatile("" : "+v"(rp.n), "+v"(rp.r), "+v"(rp.tn), "+v"(rp.tr));
-    bf16x8 f0[4], ds[4];
+    bf16x8 f0[4], ds[4], rs[4];
     pipelined<20, 3>(
         [&](int i) {
           const int j = i / 5, d = i % 5;
           if (d == 0) f0[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][op + (j & 1)][l]);
           if (d == 4) ds[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][2 + (j & 1)][l]);
+          if (FINE && d == 0) rs[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][kSlabs - 2 + (j & 1)][l]);
           return d < 4 ? wide_tr(tile + side, rp, j, d) : rope_tr(tile + kOffR, rp, j, half);
         },
         [&](int i, bf16x8 f) {
-          if (i % 5 < 4)
+          if (i % 5 < 4) {
             wide[i % 5] = mfma(f, f0[i / 5], wide[i % 5]);
-          else
+            if (FINE && half) wide[i % 5] = mfma(f, rs[i / 5], wide[i % 5]);
+          } else {
             rope = mfma(f, ds[i / 5], rope);
+            if (FINE) rope = mfma(f, rs[i / 5], rope);
+          }
         });
   };
   int buf = 0, prev = 2, sb = 0;                   // buffers of this tile and of the one before
@@ -1053,13 +1081,13 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a)
       z = stat_of(q0 + kBN);
       tile_copy<2 * PAIRS>(cp, x.q, x.q + kNope, x.g, q0 + kBN, st.lq, next);
     }
-    uint4 mine[4];                                 // this wavefront's P and dS slabs
+    uint4 mine[kSlabs];                            // this wavefront's P and dS slabs
     second(q0 - kBN, prev);
     if (q0 < st.lq) first(mine, q0, buf, sb);
     __syncthreads();                               // the last tile's operands are consumed
     if (q0 < st.lq && q0 + kBN > wlim) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ex.f[pair][half][j][l] = mine[j];
+      for (int j = 0; j < kSlabs; ++j) ex.f[pair][half][j][l] = mine[j];
     }
     prev = buf;
     buf = next;
@@ -1241,12 +1269,15 @@ extern "C" int latent_attention_backward(
   if (!aligned16(workspace)) return MXQ_ERR_ALIGN;
   // Workgroups of 64 rows where about that many, T / 64 and half a tile a sequence,
   // still run at once, one a CU (one sequence of 360, 16 heads: 41 us for the three
-  // kernels against 59; 2 of 1000, 8 heads: 74 against 100), or, in one causal
+  // kernels, without FINE, against 59; 2 of 1000, 8 heads: 74 against 100), or, in one causal
   // sequence, whose longest start first, in two turns (5000, 4 heads: 264 against 338;
   // 2048, 16 heads: 149 against 164; 5400, 8 heads, more than that: 446 against 392).
   // Else of 128 (4 of 300, 16 heads: 56 against 60; 8 of 512: 138 against 152).
   const int64_t turn = a.causal && a.B == 1 ? 512 : 256;
-  const auto few = [&](int64_t T) { return (T / 64 + a.B / 2) * a.H <= turn; };
+  // With 512 query rows at most dS has its second term, for which the exchange of
+  // 128 rows leaves no room.
+  const bool fine = a.Tq <= 512;
+  const auto few = [&](int64_t T) { return fine || (T / 64 + a.B / 2) * a.H <= turn; };
   const bool fewq = few(a.Tq), fewk = few(a.Tk);
   uint32_t nq, nk, nr;
   MXQ_TRY(grid_of(a.Tq, fewq ? 64 : 128, a, &nq));
@@ -1264,17 +1295,21 @@ extern "C" int latent_attention_backward(
   a.rope_part = static_cast<float*>(workspace);
   a.delta = a.rope_part + a.H * a.Tk * kRope;
   if (a.Tq > 0) {
-    if (fewq)
-      hipLaunchKernelGGL(k_attn_dq<2>, dim3(nq), dim3(256), 0, stream, a);
+    if (fine)
+      hipLaunchKernelGGL((k_attn_dq<2, true>), dim3(nq), dim3(256), 0, stream, a);
+    else if (fewq)
+      hipLaunchKernelGGL((k_attn_dq<2, false>), dim3(nq), dim3(256), 0, stream, a);
     else
-      hipLaunchKernelGGL(k_attn_dq<4>, dim3(nq), dim3(512), 0, stream, a);
+      hipLaunchKernelGGL((k_attn_dq<4, false>), dim3(nq), dim3(512), 0, stream, a);
     MXQ_TRY(launch_status());
   }
   if (a.Tk > 0) {
-    if (fewk)
-      hipLaunchKernelGGL(k_attn_dkv<2>, dim3(nk), dim3(256), 0, stream, a);
+    if (fine)
+      hipLaunchKernelGGL((k_attn_dkv<2, true>), dim3(nk), dim3(256), 0, stream, a);
+    else if (fewk)
+      hipLaunchKernelGGL((k_attn_dkv<2, false>), dim3(nk), dim3(256), 0, stream, a);
     else
-      hipLaunchKernelGGL(k_attn_dkv<4>, dim3(nk), dim3(512), 0, stream, a);
+      hipLaunchKernelGGL((k_attn_dkv<4, false>), dim3(nk), dim3(512), 0, stream, a);
     MXQ_TRY(launch_status());
     hipLaunchKernelGGL(k_attn_drope, dim3(nr), dim3(kThr), 0, stream, a);
     MXQ_TRY(launch_status());

@@ -398,3 +398,33 @@ def test_hidden_nan_with_few_queries_many_keys(what):
                                     sound["ok"], SCALE, True)
     _compare({"o": o[:cut].contiguous(), "lse": lse[:, :cut].contiguous()},
              {n: ref[n] for n in ("o", "lse")})
+
+
+@pytest.mark.parametrize("what", [0x7FC0, 0x7F80])
+def test_hidden_nan_in_large_calls(what):
+    """The forms that large calls take, with broken rows: each head's finite values are those
+    of a call with that head alone, and the same ones are not finite."""
+    say(f"latent attention 40 heads, rows of {what:#x}")
+    n, H = 1100, 40
+    d = _inputs([n], [n], H, 130)
+    for h in (0, 17, H - 1):
+        for r in (700, 955, n - 1):
+            d["q"][r, h, 3] = what
+            d["kv"][r, h, 5] = what
+            d["kv"][r, h, 140] = what
+            d["do"][r, h, 9] = what
+    got = _run(d, True)
+    for h in (0, 5, 17, H - 1):
+        one = {k: v if k in ("oq", "ok", "kr") else np.ascontiguousarray(v[:, h:h + 1]) for k, v in d.items()}
+        ref = _run(one, True)
+        for name in ("o", "dq", "dk_nope", "dv"):
+            a, b = host(got[name][:, h:h + 1].contiguous()), host(ref[name].contiguous())
+            va, vb = codec.bf16_bits_to_f64(a), codec.bf16_bits_to_f64(b)
+            assert np.array_equal(np.isfinite(va), np.isfinite(vb)), (name, h)
+            assert h == 5 or not np.isfinite(va).all(), (name, h)
+            ok = np.isfinite(va)
+            if ok.any():                                  # every key is seen by a broken query
+                assert np.abs(va[ok] - vb[ok]).max() <= 2 ** -6 * np.abs(vb[ok]).max(), (name, h)
+        clean = slice(0, 700)                             # rows before the first broken one
+        assert np.isfinite(codec.bf16_bits_to_f64(host(got["o"][clean, h].contiguous()))).all()
+        assert np.isfinite(codec.bf16_bits_to_f64(host(got["dq"][clean, h].contiguous()))).all()
