@@ -549,9 +549,9 @@ __device__ __forceinline__ int keys_seen(const AttnArgs& a, const SeqTile& s, in
 // the other's products.
 //
 // Bound by the matrix unit and what has to run between its products.  4 sequences
-// of 4096, 16 heads, causal: 357 us, 0.96 PFLOP/s (a large matrix product reaches
-// 1.16 to 1.25 on the same card, and its rate on such data is set by power).  Of
-// 363 us in an early form the products alone took 297, and 326 were left without
+// of 4096, 16 heads, causal: 357 to 378 us by machine, at best 0.96 PFLOP/s (a
+// large matrix product reaches 1.16 to 1.25 on the same card, and its rate on such
+// data is set by power).  Of 363 us in an early form the products alone took 297, and 326 were left without
 // LDS reads, 329 without maxima and exponentials.  64 rows a wavefront halve the
 // LDS reads but leave one wavefront a SIMD: 600 us.  Eight wavefronts that split
 // each tile's keys shorten the chain of a single long sequence (one of 2000, 4
@@ -760,9 +760,10 @@ __global__ __launch_bounds__(kThr) void k_attn_join(AttnArgs a) {
 // PAIRS = 2, 64 rows and a wavefront a SIMD: shorter steps, for calls that leave
 // CUs idle otherwise.
 //
-// 4 sequences of 4096, 16 heads, causal: dQ 727 us, dK and dV 736 us, 1.04 and 0.93
-// PFLOP/s of the 11 and 10 products of 64 columns that they form a pair (13 in all
-// are the least; S and dP are formed by both, and P K makes D exact).  Bound by
+// 4 sequences of 4096, 16 heads, causal: dQ 727 to 773 us and dK and dV 736 to 787
+// by machine, at best 1.04 and 0.93 PFLOP/s of the 11 and 10 products of 64 columns
+// that they form a pair (13 in all are the least; S and dP are formed by both, and
+// P K makes D exact).  Bound by
 // the matrix unit and the chain before P and dS: without the sums over the tiles
 // 1080 us of 1470 are left, though they are half of the products; without the
 // copies 6 % less, without the second barrier nothing.  The two of a pair taking
