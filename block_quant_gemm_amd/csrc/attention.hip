@@ -20,6 +20,8 @@
 // same order, with the staged tile read transposed (ds_read_b64_tr_b16) to match.
 // Probabilities and dS never pass through memory.
 
+#include <type_traits>
+
 #include "common.h"
 
 namespace mxq {
@@ -374,15 +376,42 @@ __device__ __forceinline__ bool frag_nonfinite(bf16x8 f) {
 }
 
 // ---------------------------------------------------------------------------
-// Rows redone by themselves.  A hidden key's probability is an exact 0, but the
-// matrix unit still multiplies it, and 0 * NaN or 0 * infinity would reach
-// rows that the mask keeps apart.  Such a product always leaves a NaN, so rows
-// whose result is not finite are computed again over their visible keys (or
-// queries) alone, one wavefront a row, before they are written.  Costs the plain
-// path one check of the results; a row with finite operands never comes here,
-// nor one whose own operand or visible logits are already not finite (its result
-// is not either, and redoing all of them would make a diverged model crawl).
+// Hidden values that are not finite.  A hidden key's probability is an exact 0, but
+// the matrix unit still multiplies it, and 0 * NaN or 0 * infinity would reach
+// rows that the mask keeps apart.  Such a product always leaves a NaN, so a
+// workgroup some of whose results are not finite walks its keys a second time
+// (the forward kernel): tiles that a wavefront's rows see whole go through the
+// matrix unit as before, since whatever they hold belongs in the result, and of the
+// tiles that the mask cuts each row adds the keys that it sees, one by one.  Only the
+// rows that were not finite are written again.  Costs a sound call one check of
+// the results; with a NaN among the values 2.5 to 4 times the call (one sequence of
+// 2048, 8 heads: 145 us against 50).  The backward kernels compute such rows again
+// by themselves, one wavefront a row, unless their own operands are not finite.
 // ---------------------------------------------------------------------------
+
+// o[i .. i + 3] += w times the 4 BF16 values at t, where they are seen.
+__device__ __forceinline__ void add4(f32x16& o, int i, bool seen, float w, const uint8_t* t) {
+  uint2 x = *reinterpret_cast<const uint2*>(t);
+  x.x = seen ? x.x : 0u;
+  x.y = seen ? x.y : 0u;
+  o[i] = __builtin_fmaf(w, bf16_lo(x.x), o[i]);
+  o[i + 1] = __builtin_fmaf(w, bf16_hi(x.x), o[i + 1]);
+  o[i + 2] = __builtin_fmaf(w, bf16_lo(x.y), o[i + 2]);
+  o[i + 3] = __builtin_fmaf(w, bf16_hi(x.y), o[i + 3]);
+}
+
+// Whether any of the workgroup's `waves` wavefronts has bits set, through the first words
+// of `lds`, which no wavefront needs any more once all are here.
+__device__ __forceinline__ bool any_wave(uint8_t* lds, uint32_t bits, int waves) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(lds);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = bits;
+  __syncthreads();
+  uint32_t all = 0;
+  for (int i = 0; i < waves; ++i) all |= w[i];
+  __syncthreads();
+  return all != 0;
+}
 
 __device__ __forceinline__ float bf(const uint16_t* p) {
   return __builtin_bit_cast(float, (uint32_t)*p << 16);
@@ -431,36 +460,6 @@ __device__ __forceinline__ float logit2(const AttnArgs& a, const Head& x, int i,
   const uint16_t* q = x.q + (int64_t)i * a.q.ld;
   return (dot(q, x.kn + (int64_t)j * a.kn.ld, kNope) + dot(q + kNope, x.kr + (int64_t)j * a.ldr, kRope)) *
          (a.scale * kLog2e);
-}
-
-// Output row i of a head, over its `keys` first keys.
-__device__ __forceinline__ void redo_output(const AttnArgs& a, const SeqTile& s, int head, int i, int keys) {
-  const Head x = head_of(a, s, head);
-  const int l = threadIdx.x & 63;
-  float m = -__builtin_inff(), sum = 0.0f, o0 = 0.0f, o1 = 0.0f;
-#pragma unroll 1
-  for (int j0 = 0; j0 < keys; j0 += 64) {
-    const int n = keys - j0 < 64 ? keys - j0 : 64;
-    const float z = l < n ? logit2(a, x, i, j0 + l) : -__builtin_inff();
-    const float mn = __builtin_fmaxf(m, wave_max(z));
-    const float ref = mn == -__builtin_inff() ? 0.0f : mn;
-    const float alpha = __builtin_amdgcn_exp2f(m - ref);
-    const float p = l < n ? __builtin_amdgcn_exp2f(z - ref) : 0.0f;
-    m = mn;
-    sum = sum * alpha + wave_sum(p);
-    o0 *= alpha;
-    o1 *= alpha;
-#pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-      const uint16_t* v = x.v + (int64_t)(j0 + j) * a.v.ld + 2 * l;
-      const float pj = lane_of(p, j);
-      o0 = __builtin_fmaf(pj, bf(v), o0);
-      o1 = __builtin_fmaf(pj, bf(v + 1), o1);
-    }
-  }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  *reinterpret_cast<uint32_t*>(a.out.p + (s.q0 + i) * a.out.ld + head * a.out.ldh + 2 * l) =
-      bf16x2_bits(o0 * inv, o1 * inv);
 }
 
 // Query gradient row i of a head, over its `keys` first keys: lane l has
@@ -567,6 +566,34 @@ __device__ __forceinline__ int parts_of(const AttnArgs& a, int keys) {
   return n < 1 ? 1 : n < a.parts ? n : a.parts;
 }
 
+// Adds the keys of the tile at k0 that a lane's row sees (those below `lim`) to its sums
+// one by one.  s: the probabilities, as the matrix unit left the logits.
+__device__ __forceinline__ void add_seen_keys(f32x16 (&o)[4], f32x16 (&s)[2], const uint8_t* tile, int k0, int lim) {
+  const uint32_t h = (threadIdx.x & 63) >> 5;
+#pragma unroll 1
+  for (uint32_t g = 0; g < 8; ++g) {               // keys 8 g .. 8 g + 7: registers 0..3 of both halves
+#pragma unroll
+    for (uint32_t e = 0; e < 4; ++e) {
+      const float own = s[0][e], other = __shfl_xor(own, 32, 64);
+#pragma unroll
+      for (uint32_t hh = 0; hh < 2; ++hh) {
+        const uint32_t key = 8 * g + 4 * hh + e;
+        const bool seen = k0 + (int)key < lim;
+        const float p = h == hh ? own : other;
+#pragma unroll
+        for (uint32_t x = 0; x < 16; ++x)          // columns 8 x + 4 h .. + 3
+          add4(o[x >> 2], 4 * (x & 3), seen, p, tile + kOffY + key * 256 + ((x ^ f_wide(key)) << 4) + 8 * h);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 12; ++i) s[0][i] = s[0][i + 4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[0][12 + i] = s[1][i];
+#pragma unroll
+    for (int i = 0; i < 12; ++i) s[1][i] = s[1][i + 4];
+  }
+}
+
 template <bool SPLIT>
 __global__ __launch_bounds__(kThr, 2) void k_attn_fwd(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTile];
@@ -603,60 +630,76 @@ __global__ __launch_bounds__(kThr, 2) void k_attn_fwd(AttnArgs a) {
   bf16x8 q[kSteps];
   const uint16_t* qp = a.q.p + st.q0 * a.q.ld + head * a.q.ldh;
   own_rows(q, qp, a.q.ld, qp + kNope, a.q.ld, row, st.lq);
-  f32x16 o[4] = {};
-  float m = -__builtin_inff(), sum = 0.0f;         // reference (powers of two), total
+  f32x16 o[4];
+  float m, sum, total;                             // reference (powers of two), total
   const float c = a.scale * kLog2e;
-  int buf = 0;
-  for (int k0 = kfirst; k0 < kstop; k0 += kBN, buf ^= 1) {
-    tile_wait();
-    if (k0 + kBN < kstop) tile_copy<4>(cp, kn, kr, v, k0 + kBN, st.lk, buf ^ 1);
-    if (k0 >= wlast) continue;                     // nothing seen by this wavefront
-    const uint8_t* tile = lds + buf * kTile;
-    f32x16 s[2] = {};
-    pipelined<2 * kSteps, 6>([&](int i) { return x_frag(tile, rp, i & 1, i >> 1); },
-                             [&](int i, bf16x8 f) { s[i & 1] = mfma(f, q[i >> 1], s[i & 1]); });
-    if (k0 + kBN > wfirst) {                       // some row does not see all of the tile
+  // The sums over this workgroup's keys.  CAREFUL: of a tile that not all rows of the
+  // wavefront see, keys are added one by one to the rows that see them, and the
+  // reference is the running maximum itself.
+  auto walk = [&](auto careful) __attribute__((always_inline)) {
+    constexpr bool CAREFUL = decltype(careful)::value;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) o[d] = f32x16{};
+    m = -__builtin_inff();
+    sum = 0.0f;
+    int buf = 0;
+    for (int k0 = kfirst; k0 < kstop; k0 += kBN, buf ^= 1) {
+      tile_wait();
+      if (k0 + kBN < kstop) tile_copy<4>(cp, kn, kr, v, k0 + kBN, st.lk, buf ^ 1);
+      if (k0 >= wlast) continue;                   // nothing seen by this wavefront
+      const uint8_t* tile = lds + buf * kTile;
+      f32x16 s[2] = {};
+      pipelined<2 * kSteps, 6>([&](int i) { return x_frag(tile, rp, i & 1, i >> 1); },
+                               [&](int i, bf16x8 f) { s[i & 1] = mfma(f, q[i >> 1], s[i & 1]); });
+      if (k0 + kBN > wfirst) {                     // some row does not see all of the tile
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (k0 + 32 * b + reg_row(i, h) >= lim) s[b][i] = -__builtin_inff();
+      }
+      float mx = s[0][0];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        mx = __builtin_fmaxf(mx, s[0][i]);
+        mx = __builtin_fmaxf(mx, s[1][i]);
+      }
+      mx = half_max(mx) * c;
+      if (__builtin_expect(__ballot(mx > m + (CAREFUL ? 0.0f : kSlack)) != 0, 0)) {
+        const float mn = __builtin_fmaxf(m, mx);
+        const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        sum *= alpha;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) o[d] *= alpha;
+      }
+      const float mc = m == -__builtin_inff() ? 0.0f : m;   // nothing seen yet: all zeros
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (k0 + 32 * b + reg_row(i, h) >= lim) s[b][i] = -__builtin_inff();
-    }
-    float mx = s[0][0];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      mx = __builtin_fmaxf(mx, s[0][i]);
-      mx = __builtin_fmaxf(mx, s[1][i]);
-    }
-    mx = half_max(mx) * c;
-    if (__builtin_expect(__ballot(mx > m + kSlack) != 0, 0)) {
-      const float mn = __builtin_fmaxf(m, mx);
-      const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
-      m = mn;
-      sum *= alpha;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) o[d] *= alpha;
-    }
-    const float mc = m == -__builtin_inff() ? 0.0f : m;   // nothing seen yet: all zeros
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], c, -mc));
-        s[b][i] = e;
-        sum += e;
+        for (int i = 0; i < 16; ++i) {
+          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], c, -mc));
+          s[b][i] = e;
+          sum += e;
+        }
+      if (CAREFUL && k0 + kBN > wfirst) {
+        add_seen_keys(o, s, tile, k0, lim);
+        continue;
       }
-    bf16x8 p[4];
+      bf16x8 p[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) p[j] = slab(s[j >> 1], j & 1);
+      for (int j = 0; j < 4; ++j) p[j] = slab(s[j >> 1], j & 1);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int d = 0; d < 4; ++d) o[d] = mfma(wide_tr(tile + kOffY, rp, j, d), p[j], o[d]);
-  }
-  const float total = half_sum(sum);
-  if (SPLIT && parts > 1) {
-    if (row < st.lq) {
+        for (int d = 0; d < 4; ++d) o[d] = mfma(wide_tr(tile + kOffY, rp, j, d), p[j], o[d]);
+    }
+    total = half_sum(sum);
+  };
+  // this lane's row, if `write`: the result, or its part
+  auto store = [&](bool write, bool with_lse) {
+    if (!write) return;
+    if (SPLIT && parts > 1) {
       const int64_t pr = ((int64_t)part * a.H + head) * a.Tq + st.q0 + row;
 #pragma unroll
       for (int d = 0; d < 4; ++d)
@@ -665,32 +708,33 @@ __global__ __launch_bounds__(kThr, 2) void k_attn_fwd(AttnArgs a) {
           *reinterpret_cast<f32x4*>(a.part_o + pr * kVal + 32 * d + 8 * i + 4 * h) =
               f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
       if (h == 0) a.part_ml[2 * pr] = m, a.part_ml[2 * pr + 1] = total;
+      return;
     }
-    return;
-  }
-  // a row that sees nothing: zeros, and minus infinity
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  const uint64_t bad = __ballot(any_nonfinite(o) && row < st.lq && total == total);
-  if (row < st.lq) {
+    // a row that sees nothing: zeros, and minus infinity
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     uint16_t* p = a.out.p + (st.q0 + row) * a.out.ld + head * a.out.ldh;
 #pragma unroll
     for (int d = 0; d < 4; ++d) store_block(o[d], inv, p + 32 * d);
-    if (h == 0)
+    if (with_lse && h == 0)
       a.lse[head * a.ldl + st.q0 + row] =
           total == 0.0f ? -__builtin_inff() : kLn2 * (m + __builtin_amdgcn_logf(total));
-  }
+  };
+  walk(std::false_type{});
+  store(row < st.lq, true);
   if (!a.causal) return;
-  uint32_t redo = (uint32_t)bad | (uint32_t)(bad >> 32);
-  while (redo) {
-    const int i = wrow0 + __builtin_ctz(redo);
-    redo &= redo - 1;
-    redo_output(a, st, head, i, keys_seen(a, st, i));
-  }
+  // rows that a hidden value may have reached, of a wavefront whose last tile hides some keys from some rows
+  const int walked = kstop < wlast ? kstop : (wlast + kBN - 1) / kBN * kBN;
+  const uint64_t bad = __ballot(any_nonfinite(o) && row < st.lq && total == total && walked > wfirst);
+  const uint32_t redo = (uint32_t)bad | (uint32_t)(bad >> 32);
+  if (!any_wave(lds, redo, 4)) return;             // uniform over the workgroup
+  tile_copy<4>(cp, kn, kr, v, kfirst, st.lk, 0);
+  walk(std::true_type{});
+  store(row < st.lq && ((redo >> n) & 1), false);
 }
 
 // Joins the parts of the tiles that have several, in their order: with M = max m,
 // o = sum 2^(m - M) O / sum 2^(m - M) l.  A workgroup takes 32 rows of a tile, 8
-// lanes a row.  Rows whose hidden keys left a NaN are redone here.
+// lanes a row.
 __global__ __launch_bounds__(kThr) void k_attn_join(AttnArgs a) {
   const int head = blockIdx.x % a.H;
   const uint32_t unit = blockIdx.x / a.H;
@@ -720,31 +764,19 @@ __global__ __launch_bounds__(kThr) void k_attn_join(AttnArgs a) {
       for (int e = 0; e < 4; ++e) o[j][e] = __builtin_fmaf(f, v[e], o[j][e]);
     }
   }
-  bool nf = false;
+  if (!ok) return;
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  uint16_t* p = a.out.p + (st.q0 + row) * a.out.ld + head * a.out.ldh + 4 * c;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) nf |= !(__builtin_fabsf(o[j][e]) < __builtin_inff());
-  uint64_t bad = __ballot(nf && ok && a.causal && total == total);
-  if (ok && ((bad >> (l & 56)) & 0xFF) == 0) {
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    uint16_t* p = a.out.p + (st.q0 + row) * a.out.ld + head * a.out.ldh + 4 * c;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint2 x;
-      x.x = bf16x2_bits(o[j][0] * inv, o[j][1] * inv);
-      x.y = bf16x2_bits(o[j][2] * inv, o[j][3] * inv);
-      *reinterpret_cast<uint2*>(p + 32 * j) = x;
-    }
+  for (int j = 0; j < 4; ++j) {
+    uint2 x;
+    x.x = bf16x2_bits(o[j][0] * inv, o[j][1] * inv);
+    x.y = bf16x2_bits(o[j][2] * inv, o[j][3] * inv);
+    *reinterpret_cast<uint2*>(p + 32 * j) = x;
   }
-  if (ok && c == 0)
+  if (c == 0)
     a.lse[head * a.ldl + st.q0 + row] =
         total == 0.0f ? -__builtin_inff() : kLn2 * (ref + __builtin_amdgcn_logf(total));
-#pragma unroll 1
-  for (int y = 0; y < 8; ++y) {
-    if (((bad >> (8 * y)) & 0xFF) == 0) continue;
-    redo_output(a, st, head, row0 + y, keys_seen(a, st, row0 + y));
-  }
 }
 
 // ---------------------------------------------------------------------------
