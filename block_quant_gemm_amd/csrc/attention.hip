@@ -379,14 +379,16 @@ __device__ __forceinline__ bool frag_nonfinite(bf16x8 f) {
 // Hidden values that are not finite.  A hidden key's probability is an exact 0, but
 // the matrix unit still multiplies it, and 0 * NaN or 0 * infinity would reach
 // rows that the mask keeps apart.  Such a product always leaves a NaN, so a
-// workgroup some of whose results are not finite walks its keys a second time
-// (the forward kernel): tiles that a wavefront's rows see whole go through the
-// matrix unit as before, since whatever they hold belongs in the result, and of the
-// tiles that the mask cuts each row adds the keys that it sees, one by one.  Only the
-// rows that were not finite are written again.  Costs a sound call one check of
-// the results; with a NaN among the values 2.5 to 4 times the call (one sequence of
-// 2048, 8 heads: 145 us against 50).  The backward kernels compute such rows again
-// by themselves, one wavefront a row, unless their own operands are not finite.
+// workgroup some of whose results are not finite walks the other side a second
+// time: tiles that all its rows see whole go through the matrix unit as before,
+// since whatever they hold belongs in the result.  Of the tiles that the mask
+// cuts, the forward kernel adds the keys one by one to the rows that see
+// them; the backward kernels, whose sums leave no registers for that, set what is not
+// finite in the staged tile to 0 for the second products, and note for each sum
+// which of it the row sees.  Only rows that were not finite are written again, without the
+// slack and the shift above.  Costs a sound call one check of the results; with
+// a NaN the kernels take 2.5 to 4 times as long, 6 where few rows are cut often
+// (one sequence of 2048, 8 heads: forward 145 us against 50, backward 370 against 140).
 // ---------------------------------------------------------------------------
 
 // o[i .. i + 3] += w times the 4 BF16 values at t, where they are seen.
@@ -398,6 +400,32 @@ __device__ __forceinline__ void add4(f32x16& o, int i, bool seen, float w, const
   o[i + 1] = __builtin_fmaf(w, bf16_hi(x.x), o[i + 1]);
   o[i + 2] = __builtin_fmaf(w, bf16_lo(x.y), o[i + 2]);
   o[i + 3] = __builtin_fmaf(w, bf16_hi(x.y), o[i + 3]);
+}
+
+// Which of 4 BF16 values are NaN or infinite: a bit each.
+__device__ __forceinline__ uint32_t nonfinite4(uint2 x) {
+  return ((x.x & 0x7F80u) == 0x7F80u ? 1u : 0u) | ((x.x & 0x7F800000u) == 0x7F800000u ? 2u : 0u) |
+         ((x.y & 0x7F80u) == 0x7F80u ? 4u : 0u) | ((x.y & 0x7F800000u) == 0x7F800000u ? 8u : 0u);
+}
+
+// Which of them are NaN.
+__device__ __forceinline__ uint32_t nan4(uint2 x) {
+  return ((x.x & 0x7FFFu) > 0x7F80u ? 1u : 0u) | ((x.x & 0x7FFFFFFFu) > 0x7F80FFFFu ? 2u : 0u) |
+         ((x.y & 0x7FFFu) > 0x7F80u ? 4u : 0u) | ((x.y & 0x7FFFFFFFu) > 0x7F80FFFFu ? 8u : 0u);
+}
+
+// Sets the NaN and infinities among `bytes` bytes of BF16 values in LDS to 0, by `threads` threads.
+__device__ __forceinline__ void clear_nonfinite(uint8_t* t, uint32_t bytes, uint32_t threads) {
+#pragma unroll 1
+  for (uint32_t i = threadIdx.x * 8; i < bytes; i += threads * 8) {
+    uint2 x = *reinterpret_cast<const uint2*>(t + i);
+    const uint32_t bits = nonfinite4(x);
+    if (bits & 1) x.x &= 0xFFFF0000u;
+    if (bits & 2) x.x &= 0xFFFFu;
+    if (bits & 4) x.y &= 0xFFFF0000u;
+    if (bits & 8) x.y &= 0xFFFFu;
+    *reinterpret_cast<uint2*>(t + i) = x;
+  }
 }
 
 // Whether any of the workgroup's `waves` wavefronts has bits set, through the first words
@@ -417,28 +445,6 @@ __device__ __forceinline__ float bf(const uint16_t* p) {
   return __builtin_bit_cast(float, (uint32_t)*p << 16);
 }
 
-// Sum of x[i] * y[i] over n columns, by one lane.
-__device__ __forceinline__ float dot(const uint16_t* x, const uint16_t* y, int n) {
-  float s = 0.0f;
-#pragma unroll 1
-  for (int i = 0; i < n; ++i) s = __builtin_fmaf(bf(x + i), bf(y + i), s);
-  return s;
-}
-
-__device__ __forceinline__ float lane_of(float x, int lane) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
-}
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) x = __builtin_fmaxf(x, __shfl_xor(x, s, 64));
-  return x;
-}
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) x += __shfl_xor(x, s, 64);
-  return x;
-}
-
 // A head's operands of one sequence.
 struct Head {
   const uint16_t *q, *kn, *kr, *v, *o, *g;       // g: the output's gradient
@@ -455,84 +461,6 @@ __device__ __forceinline__ Head head_of(const AttnArgs& a, const SeqTile& s, int
   x.lse = a.lse + head * a.ldl + s.q0;
   x.delta = a.delta + head * a.Tq + s.q0;
   return x;
-}
-__device__ __forceinline__ float logit2(const AttnArgs& a, const Head& x, int i, int j) {
-  const uint16_t* q = x.q + (int64_t)i * a.q.ld;
-  return (dot(q, x.kn + (int64_t)j * a.kn.ld, kNope) + dot(q + kNope, x.kr + (int64_t)j * a.ldr, kRope)) *
-         (a.scale * kLog2e);
-}
-
-// Query gradient row i of a head, over its `keys` first keys: lane l has
-// columns l, l + 64 and l + 128.
-__device__ __forceinline__ void redo_dq(const AttnArgs& a, const SeqTile& s, int head, int i, int keys) {
-  const Head x = head_of(a, s, head);
-  const int l = threadIdx.x & 63;
-  const float lse2 = x.lse[i] * kLog2e;
-  const uint16_t* gi = x.g + (int64_t)i * a.dout.ld;
-  float delta = 0.0f;
-#pragma unroll 1
-  for (int j = l; j < keys; j += 64)
-    delta = __builtin_fmaf(__builtin_amdgcn_exp2f(logit2(a, x, i, j) - lse2),
-                           dot(gi, x.v + (int64_t)j * a.v.ld, kVal), delta);
-  delta = wave_sum(delta);
-  float d0 = 0.0f, d1 = 0.0f, d2 = 0.0f;
-#pragma unroll 1
-  for (int j0 = 0; j0 < keys; j0 += 64) {
-    const int n = keys - j0 < 64 ? keys - j0 : 64;
-    float ds = 0.0f;
-    if (l < n)
-      ds = __builtin_amdgcn_exp2f(logit2(a, x, i, j0 + l) - lse2) *
-           (dot(gi, x.v + (int64_t)(j0 + l) * a.v.ld, kVal) - delta);
-#pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-      const float d = lane_of(ds, j);
-      const uint16_t* k = x.kn + (int64_t)(j0 + j) * a.kn.ld + l;
-      d0 = __builtin_fmaf(d, bf(k), d0);
-      d1 = __builtin_fmaf(d, bf(k + 64), d1);
-      d2 = __builtin_fmaf(d, bf(x.kr + (int64_t)(j0 + j) * a.ldr + l), d2);
-    }
-  }
-  uint16_t* p = a.dq.p + (s.q0 + i) * a.dq.ld + head * a.dq.ldh + l;
-  p[0] = (uint16_t)bf16x2_bits(d0 * a.scale, 0.0f);
-  p[64] = (uint16_t)bf16x2_bits(d1 * a.scale, 0.0f);
-  p[128] = (uint16_t)bf16x2_bits(d2 * a.scale, 0.0f);
-}
-
-// Gradients of key and value row j of a head, over the queries from `first` on.
-__device__ __forceinline__ void redo_dkv(const AttnArgs& a, const SeqTile& s, int head, int j, int first) {
-  const Head x = head_of(a, s, head);
-  const int l = threadIdx.x & 63;
-  const uint16_t* vj = x.v + (int64_t)j * a.v.ld;
-  float k0 = 0.0f, k1 = 0.0f, k2 = 0.0f, v0 = 0.0f, v1 = 0.0f;
-#pragma unroll 1
-  for (int i0 = first; i0 < s.lq; i0 += 64) {
-    const int n = s.lq - i0 < 64 ? s.lq - i0 : 64;
-    float p = 0.0f, ds = 0.0f;
-    if (l < n) {
-      const int i = i0 + l;
-      p = __builtin_amdgcn_exp2f(logit2(a, x, i, j) - x.lse[i] * kLog2e);
-      ds = p * (dot(x.g + (int64_t)i * a.dout.ld, vj, kVal) - x.delta[i]);
-    }
-#pragma unroll 1
-    for (int u = 0; u < n; ++u) {
-      const float pu = lane_of(p, u), du = lane_of(ds, u);
-      const uint16_t* q = x.q + (int64_t)(i0 + u) * a.q.ld + l;
-      const uint16_t* g = x.g + (int64_t)(i0 + u) * a.dout.ld + l;
-      k0 = __builtin_fmaf(du, bf(q), k0);
-      k1 = __builtin_fmaf(du, bf(q + 64), k1);
-      k2 = __builtin_fmaf(du, bf(q + 128), k2);
-      v0 = __builtin_fmaf(pu, bf(g), v0);
-      v1 = __builtin_fmaf(pu, bf(g + 64), v1);
-    }
-  }
-  const int64_t row = s.k0 + j;
-  uint16_t* dv = a.dv.p + row * a.dv.ld + head * a.dv.ldh + l;
-  uint16_t* dk = a.dkn.p + row * a.dkn.ld + head * a.dkn.ldh + l;
-  dv[0] = (uint16_t)bf16x2_bits(v0, 0.0f);
-  dv[64] = (uint16_t)bf16x2_bits(v1, 0.0f);
-  dk[0] = (uint16_t)bf16x2_bits(k0 * a.scale, 0.0f);
-  dk[64] = (uint16_t)bf16x2_bits(k1 * a.scale, 0.0f);
-  a.rope_part[(head * a.Tk + row) * kRope + l] = k2;
 }
 
 // Keys that query row i sees.
@@ -816,6 +744,14 @@ struct Exchange {
   uint4 f[PAIRS][2][FINE ? 6 : 4][64];           // pair, half, slab, lane
 };
 
+// Tile row r's entry for this lane's own row, of the slabs `slab` and `slab + 1` that were
+// handed over.
+template <int PAIRS, bool FINE>
+__device__ __forceinline__ float handed(const Exchange<PAIRS, FINE>& ex, int pair, uint32_t r, int slab) {
+  const uint32_t n = threadIdx.x & 31, lane = n + 32 * ((r >> 2) & 1), at = (r & 3) + 4 * ((r >> 3) & 1);
+  return bf(reinterpret_cast<const uint16_t*>(&ex.f[pair][r >> 5][slab + ((r >> 4) & 1)][lane]) + at);
+}
+
 // What rounding to BF16 left of 8 values (slab j of p, rounded to w), rounded.
 __device__ __forceinline__ uint4 slab_rest(const f32x16& p, uint4 w, int j) {
   f32x16 r;
@@ -877,7 +813,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
 
   // this wavefront's columns: N blocks 2 half, 2 half + 1 and R block half
   f32x16 dq[3] = {}, pk[3] = {};
-  float rest = 0.0f;                               // row sum of this half's dS'
+  float rest = 0.0f, unshift = kUnshift;           // row sum of this half's dS'
   const float c = a.scale * kLog2e;
   // P and dS against the tile at k0 (in buffer `buf`), this wavefront's 32 keys of it
   auto first = [&](uint4 (&mine)[kSlabs], int k0, int buf) __attribute__((always_inline)) {
@@ -939,45 +875,85 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
           pk[i % 3] = mfma(f, p[i / 3], pk[i % 3]);
         });
   };
-  int buf = 0, prev = 2;                           // of this tile and of the one before
-  for (int k0 = 0; k0 < kend + kBN; k0 += kBN) {
-    tile_wait();
-    const int next = buf == 2 ? 0 : buf + 1;
-    if (k0 + kBN < kend) tile_copy<2 * PAIRS>(cp, x.kn, x.kr, x.v, k0 + kBN, st.lk, next);
-    uint4 mine[kSlabs];                            // this wavefront's P and dS slabs
-    second(k0 - kBN, prev);
-    if (k0 < kend) first(mine, k0, buf);
-    __syncthreads();                               // the last tile's operands are consumed
-    if (k0 < kend && k0 < wlast) {
+  // The second walk: where this lane's row sees a key that is not finite, its gradient is not
+  // (such a key's logit makes the whole row NaN, or, at minus infinity, its P an exact 0).
+  uint64_t nan = 0;                                // a bit for each of this lane's 48 sums
+  const int cut = keys_seen(a, st, st.row0);       // tiles before it are seen whole by all
+  auto cover = [&](int k0, int buf) __attribute__((always_inline)) {
+    uint8_t* tile = lds + buf * kTile;
+#pragma unroll 1
+    for (uint32_t key = 0; key < kBN; ++key) {
+      uint64_t bits = 0;
 #pragma unroll
-      for (int j = 0; j < kSlabs; ++j) ex.f[pair][half][j][l] = mine[j];
+      for (uint32_t u = 0; u < 12; ++u) {          // columns 8 u + 4 h .. + 3 of this half's 96
+        const uint8_t* t = u < 8 ? tile + key * 256 + (((8 * half + u) ^ f_wide(key)) << 4)
+                                 : tile + kOffR + key * 128 + (((4 * half + u - 8) ^ f_rope(key)) << 4);
+        bits |= (uint64_t)nonfinite4(*reinterpret_cast<const uint2*>(t + 8 * h)) << (4 * u);
+      }
+      nan |= k0 + (int)key < lim ? bits : 0;
     }
-    prev = buf;
-    buf = next;
-  }
-  rest = half_sum(rest);
-  if (h == 0) s_rest[pair][half][n] = rest;
-  __syncthreads();
-  const float r = (s_rest[pair][0][n] + s_rest[pair][1][n]) * kUnshift;
+    __syncthreads();
+    clear_nonfinite(tile, kOffY, 128 * PAIRS);     // N and R
+    __syncthreads();
+  };
+  // The sums over the keys that the workgroup sees.
+  auto walk = [&](auto again) __attribute__((always_inline)) {
+    int buf = 0, prev = 2;                         // of this tile and of the one before
+    for (int k0 = 0; k0 < kend + kBN; k0 += kBN) {
+      tile_wait();
+      const int next = buf == 2 ? 0 : buf + 1;
+      if (k0 + kBN < kend) tile_copy<2 * PAIRS>(cp, x.kn, x.kr, x.v, k0 + kBN, st.lk, next);
+      uint4 mine[kSlabs];                          // this wavefront's P and dS slabs
+      if (decltype(again)::value && k0 > cut) cover(k0 - kBN, prev);
+      second(k0 - kBN, prev);
+      if (k0 < kend) first(mine, k0, buf);
+      __syncthreads();                             // the last tile's operands are consumed
+      if (k0 < kend && k0 < wlast) {
 #pragma unroll
-  for (int d = 0; d < 3; ++d) dq[d] -= pk[d] * r;
-  const uint64_t bad = __ballot(any_nonfinite(dq) && row < st.lq && lse2 == lse2 && delta == delta);
-  if (l == 0) s_bad[pair][half] = a.causal ? (uint32_t)bad | (uint32_t)(bad >> 32) : 0u;
-  __syncthreads();
-  uint32_t redo = s_bad[pair][0] | s_bad[pair][1];
-  if (row < st.lq && h == 0 && half == 0) a.delta[head * a.Tq + st.q0 + row] = delta + r;
-  if (row < st.lq && !((redo >> n) & 1)) {
+        for (int j = 0; j < kSlabs; ++j) ex.f[pair][half][j][l] = mine[j];
+      }
+      prev = buf;
+      buf = next;
+    }
+    rest = half_sum(rest);
+    if (h == 0) s_rest[pair][half][n] = rest;
+    __syncthreads();
+    const float r = (s_rest[pair][0][n] + s_rest[pair][1][n]) * unshift;
+#pragma unroll
+    for (int d = 0; d < 3; ++d) dq[d] -= pk[d] * r;
+    return r;
+  };
+  auto store = [&](bool write) {
+    if (!write) return;
     uint16_t* p = a.dq.p + (st.q0 + row) * a.dq.ld + head * a.dq.ldh;
 #pragma unroll
-    for (int d = 0; d < 2; ++d) store_block(dq[d], a.scale * kUnshift, p + 64 * half + 32 * d);
-    store_block(dq[2], a.scale * kUnshift, p + kNope + 32 * half);
-  }
-  if (half) return;
-  while (redo) {
-    const int i = wrow0 + __builtin_ctz(redo);
-    redo &= redo - 1;
-    redo_dq(a, st, head, i, keys_seen(a, st, i));
-  }
+    for (int d = 0; d < 2; ++d) store_block(dq[d], a.scale * unshift, p + 64 * half + 32 * d);
+    store_block(dq[2], a.scale * unshift, p + kNope + 32 * half);
+  };
+  const float r = walk(std::false_type{});
+  store(row < st.lq);
+  if (row < st.lq && h == 0 && half == 0) a.delta[head * a.Tq + st.q0 + row] = delta + r;
+  if (!a.causal) return;
+  // rows that a hidden key may have reached
+  const uint64_t bad = __ballot(any_nonfinite(dq) && row < st.lq && lse2 == lse2 && delta == delta);
+  if (l == 0) s_bad[pair][half] = (uint32_t)bad | (uint32_t)(bad >> 32);
+  __syncthreads();
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < PAIRS; ++i) any |= s_bad[i][0] | s_bad[i][1];
+  if (!any) return;                                // uniform over the workgroup
+  const uint32_t redo = s_bad[pair][0] | s_bad[pair][1];
+  if (kend > 0) tile_copy<2 * PAIRS>(cp, x.kn, x.kr, x.v, 0, st.lk, 0);
+#pragma unroll
+  for (int d = 0; d < 3; ++d) dq[d] = f32x16{}, pk[d] = f32x16{};
+  rest = 0.0f;
+  lse2 += kShift;
+  unshift = 1.0f;
+  walk(std::true_type{});
+#pragma unroll
+  for (int i = 0; i < 48; ++i)
+    if ((nan >> i) & 1) dq[i / 16][i % 16] = __builtin_nanf("");
+  store(row < st.lq && ((redo >> n) & 1));
 }
 
 // Backward, keys: dK, dV, walking the queries that see the workgroup's keys.  The
@@ -1102,29 +1078,84 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a)
           }
         });
   };
-  int buf = 0, prev = 2, sb = 0;                   // buffers of this tile and of the one before
-  for (; q0 < st.lq + kBN; q0 += kBN, sb ^= 1) {
-    if (w == 0)
-      stat[sb][0][l] = z == -__builtin_inff() ? __builtin_inff() : z * kLog2e - kShift;   // no keys: P = 0
-    else if (w == 1)
-      stat[sb][1][l] = z;
-    tile_wait();
-    const int next = buf == 2 ? 0 : buf + 1;
-    if (q0 + kBN < st.lq) {
-      z = stat_of(q0 + kBN);
-      tile_copy<2 * PAIRS>(cp, x.q, x.q + kNope, x.g, q0 + kBN, st.lq, next);
-    }
-    uint4 mine[kSlabs];                            // this wavefront's P and dS slabs
-    second(q0 - kBN, prev);
-    if (q0 < st.lq) first(mine, q0, buf, sb);
-    __syncthreads();                               // the last tile's operands are consumed
-    if (q0 < st.lq && q0 + kBN > wlim) {
+  // The second walk: what queries and gradients that are not finite add to this lane's sums: a
+  // bit each where it is plus infinity, and minus infinity, both where it is NaN.
+  uint64_t pos = 0, neg = 0;                       // wide
+  uint32_t nan = 0;                                // rope, always NaN: a query that is not finite
+  const int cut = (st.row0 + BM < st.lk ? st.row0 + BM : st.lk) - 1 - diff;   // queries from here on see all keys
+  auto cover = [&](int r0, int buf) __attribute__((always_inline)) {
+    uint8_t* tile = lds + buf * kTile;
+#pragma unroll 1
+    for (uint32_t i = 0; i < kBN; ++i) {
+      const bool seen = r0 + (int)i >= lim && r0 + (int)i < st.lq;
+      const bool zero = handed(ex, pair, i, 0) == 0.0f;   // 0 * infinity
+      uint64_t up = 0, down = 0;
+#pragma unroll 4
+      for (uint32_t u = 0; u < 16; ++u) {          // columns 8 u + 4 h .. + 3
+        const uint2 v = *reinterpret_cast<const uint2*>(tile + side + i * 256 + ((u ^ f_wide(i)) << 4) + 8 * h);
+        const uint32_t bits = nonfinite4(v), nans = half || zero ? bits : nan4(v);
+        const uint32_t minus = (v.x >> 15 & 1) | (v.x >> 30 & 2) | (v.y >> 13 & 4) | (v.y >> 28 & 8);
+        up |= (uint64_t)((bits & ~minus) | nans) << (4 * u);
+        down |= (uint64_t)((bits & minus) | nans) << (4 * u);
+      }
+      uint32_t r = 0;
 #pragma unroll
-      for (int j = 0; j < kSlabs; ++j) ex.f[pair][half][j][l] = mine[j];
+      for (uint32_t u = 0; u < 4; ++u)
+        r |= nonfinite4(*reinterpret_cast<const uint2*>(tile + kOffR + i * 128 + (((4 * half + u) ^ f_rope(i)) << 4) +
+                                                         8 * h)) << (4 * u);
+      pos |= seen ? up : 0;
+      neg |= seen ? down : 0;
+      nan |= seen ? r : 0;
     }
-    prev = buf;
-    buf = next;
-  }
+    __syncthreads();
+    clear_nonfinite(tile, kTile, 128 * PAIRS);
+    __syncthreads();
+  };
+  // The sums over the queries that see the workgroup's keys.
+  float shift = kShift, unshift = kUnshift;
+  auto walk = [&](auto again) __attribute__((always_inline)) {
+    int buf = 0, prev = 2, sb = 0;                 // buffers of this tile and of the one before
+    for (int q0 = begin; q0 < st.lq + kBN; q0 += kBN, sb ^= 1) {
+      if (w == 0)
+        stat[sb][0][l] = z == -__builtin_inff() ? __builtin_inff() : z * kLog2e - shift;   // no keys: P = 0
+      else if (w == 1)
+        stat[sb][1][l] = z;
+      tile_wait();
+      const int next = buf == 2 ? 0 : buf + 1;
+      if (q0 + kBN < st.lq) {
+        z = stat_of(q0 + kBN);
+        tile_copy<2 * PAIRS>(cp, x.q, x.q + kNope, x.g, q0 + kBN, st.lq, next);
+      }
+      uint4 mine[kSlabs];                          // this wavefront's P and dS slabs
+      if (decltype(again)::value && q0 > begin && q0 - kBN < cut) cover(q0 - kBN, prev);
+      second(q0 - kBN, prev);
+      if (q0 < st.lq) first(mine, q0, buf, sb);
+      __syncthreads();                             // the last tile's operands are consumed
+      if (q0 < st.lq && q0 + kBN > wlim) {
+#pragma unroll
+        for (int j = 0; j < kSlabs; ++j) ex.f[pair][half][j][l] = mine[j];
+      }
+      prev = buf;
+      buf = next;
+    }
+  };
+  auto store = [&](bool write) {
+    if (!write) return;
+    const int64_t kr = st.k0 + row;
+    uint16_t* p = half ? a.dkn.p + kr * a.dkn.ld + head * a.dkn.ldh : a.dv.p + kr * a.dv.ld + head * a.dv.ldh;
+    const float mul = half ? a.scale * unshift : unshift;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) store_block(wide[d], mul, p + 32 * d);
+    float* pr = a.rope_part + (head * a.Tk + kr) * kRope + 32 * half + 4 * h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<f32x4*>(pr + 8 * i) =
+          f32x4{rope[4 * i], rope[4 * i + 1], rope[4 * i + 2], rope[4 * i + 3]} * unshift;
+  };
+  walk(std::false_type{});
+  store(row < st.lk);
+  if (!a.causal) return;
+  // rows that a hidden query or gradient may have reached
   bool nf = any_nonfinite(wide), own = false;      // own: the key itself is not finite
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) own |= frag_nonfinite(k[i]);
@@ -1134,28 +1165,32 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a)
 #pragma unroll
   for (int i = 0; i < 16; ++i) nf |= !(__builtin_fabsf(rope[i]) < __builtin_inff());
   const uint64_t bad = __ballot(nf && row < st.lk && !own);
+  if (l == 0) s_bad[pair][half] = (uint32_t)bad | (uint32_t)(bad >> 32);
   __syncthreads();
-  if (l == 0) s_bad[pair][half] = a.causal ? (uint32_t)bad | (uint32_t)(bad >> 32) : 0u;
-  __syncthreads();
-  uint32_t redo = s_bad[pair][0] | s_bad[pair][1];
-  if (row < st.lk && !((redo >> n) & 1)) {
-    const int64_t kr = st.k0 + row;
-    uint16_t* p = half ? a.dkn.p + kr * a.dkn.ld + head * a.dkn.ldh : a.dv.p + kr * a.dv.ld + head * a.dv.ldh;
-    const float mul = half ? a.scale * kUnshift : kUnshift;
+  uint32_t any = 0;
 #pragma unroll
-    for (int d = 0; d < 4; ++d) store_block(wide[d], mul, p + 32 * d);
-    float* pr = a.rope_part + (head * a.Tk + kr) * kRope + 32 * half + 4 * h;
+  for (int i = 0; i < PAIRS; ++i) any |= s_bad[i][0] | s_bad[i][1];
+  if (!any || begin >= cut) return;                // uniform over the workgroup
+  const uint32_t redo = s_bad[pair][0] | s_bad[pair][1];
+  if (begin < st.lq) {
+    z = stat_of(begin);
+    tile_copy<2 * PAIRS>(cp, x.q, x.q + kNope, x.g, begin, st.lq, 0);
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<f32x4*>(pr + 8 * i) =
-          f32x4{rope[4 * i], rope[4 * i + 1], rope[4 * i + 2], rope[4 * i + 3]} * kUnshift;
+  for (int d = 0; d < 4; ++d) wide[d] = f32x16{};
+  rope = f32x16{};
+  shift = 0.0f;
+  unshift = 1.0f;
+  walk(std::true_type{});
+#pragma unroll
+  for (int i = 0; i < 64; ++i) {
+    const bool p = (pos >> i) & 1, m = (neg >> i) & 1;
+    wide[i / 16][i % 16] += p && m ? __builtin_nanf("") : p ? __builtin_inff() : m ? -__builtin_inff() : 0.0f;
   }
-  if (half) return;
-  while (redo) {
-    const int j = wkey + __builtin_ctz(redo);
-    redo &= redo - 1;
-    redo_dkv(a, st, head, j, j - diff < 0 ? 0 : j - diff);
-  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if ((nan >> i) & 1) rope[i] = __builtin_nanf("");
+  store(row < st.lk && ((redo >> n) & 1));
 }
 
 // dk_rope[t] = scale * sum over heads, in head order, rounded once.  Four

@@ -96,3 +96,92 @@ def test_forward_with_broken_values_everywhere(what):
     o, _ = _forward(d)
     assert (torch.isnan(o) if np.isnan(what) else o == what).all()
     _in_time(lambda: _forward(d), lambda: _forward(sound), f"forward with all values {what}")
+
+
+GRADS = ("dq", "dk_nope", "dk_rope", "dv")
+
+
+def _backward(d, o, lse):
+    return dict(zip(GRADS, mxq.latent_attention_backward(d["dout"], d["q"], d["k_nope"], d["k_rope"], d["v"], o, lse,
+                                                         d["off_q"], d["off_k"])))
+
+
+def _same(a, b):
+    return torch.equal(a.contiguous().view(torch.int16), b.contiguous().view(torch.int16))
+
+
+def _close(got, want):
+    """Either side is off by at most (2 / 3)^0.5 * 2^-8 of its norm: two roundings to BF16, each
+    spread evenly over half a unit in the last place."""
+    e = ((got.double() - want.double()).norm() / want.double().norm()).item()
+    assert e <= 2 * (2 / 3) ** 0.5 * 2.0 ** -8, f"off by {e:.3g}"
+
+
+@pytest.mark.parametrize("what", [NAN, INF, -INF])
+@pytest.mark.parametrize("lq,lk,H", [(2048, 2048, 8), (700, 700, 40), (300, 1500, 4)])
+def test_backward_with_a_broken_gradient(lq, lk, H, what):
+    """One value of one query's dO: that query's gradient and those of the keys that it sees are
+    broken, dv in its column alone; nothing else is."""
+    say(f"latent attention backward, {lq} queries {lk} keys {H} heads, one {what} in dO")
+    d = _inputs(lq, lk, H, 3)
+    o, lse = _forward(d)
+    i, col = 220, 41
+    d["dout"][i, :, col] = 0
+    sound = dict(d)
+    d = dict(d, dout=d["dout"].clone())
+    d["dout"][i, :, col] = what
+    got, ref = _backward(d, o, lse), _backward(sound, o, lse)
+    j = i + lk - lq                                       # the last key that query i sees
+    others = torch.arange(lq, device="cuda") != i
+    assert not torch.isfinite(got["dq"][i]).any() and _same(got["dq"][others], ref["dq"][others])
+    for n in ("dk_nope", "dk_rope"):
+        assert not torch.isfinite(got[n][:j + 1]).any(), n
+    hit = got["dv"][:j + 1, :, col].double()
+    assert (torch.isnan(hit) if np.isnan(what) else hit == what).all()
+    rest = torch.arange(128, device="cuda") != col
+    _close(got["dv"][..., rest], ref["dv"][..., rest])
+    apart = (j // 64 + 1) * 64 + 128                      # keys of no tile that query i is in
+    for n in ("dk_nope", "dk_rope", "dv"):
+        _close(got[n][j + 1:], ref[n][j + 1:])
+        assert _same(got[n][apart:], ref[n][apart:]), n
+    _in_time(lambda: _backward(d, o, lse), lambda: _backward(sound, o, lse), f"backward with one {what}")
+
+
+@pytest.mark.parametrize("what", [NAN, INF])
+def test_backward_with_broken_gradients_everywhere(what):
+    say(f"latent attention backward, dO all {what}")
+    d = _inputs(1500, 1500, 8, 4)
+    o, lse = _forward(d)
+    sound = dict(d)
+    d = dict(d, dout=torch.full_like(d["dout"], what))
+    got = _backward(d, o, lse)
+    assert not any(torch.isfinite(got[n]).any() for n in ("dq", "dk_nope", "dk_rope"))
+    assert (torch.isnan(got["dv"]) if np.isnan(what) else got["dv"] == what).all()
+    _in_time(lambda: _backward(d, o, lse), lambda: _backward(sound, o, lse), f"backward with dO all {what}")
+
+
+@pytest.mark.parametrize("where", ["k_nope", "k_rope", "v", "q"])
+def test_backward_with_a_broken_operand(where):
+    """One row's key, rotary key, value or query is NaN: queries before it have sound
+    gradients, and, of a query, keys after it."""
+    say(f"latent attention, forward and backward, a NaN in {where}")
+    n, H, at = 1600, 8, 1000
+    d = _inputs(n, n, H, 5)
+    sound = dict(d)
+    d = dict(d, **{where: d[where].clone()})
+    d[where][at, ..., 9] = NAN
+    (o, lse), (ro, rlse) = _forward(d), _forward(sound)
+    got, ref = _backward(d, o, lse), _backward(sound, ro, rlse)
+    assert (lse[:, :at] - rlse[:, :at]).abs().max() < 1e-4
+    _close(o[:at], ro[:at])
+    _close(got["dq"][:at], ref["dq"][:at])
+    if where == "q":
+        _close(got["dq"][at + 1:], ref["dq"][at + 1:])
+        for g in ("dk_nope", "dk_rope", "dv"):
+            _close(got[g][at + 1:], ref[g][at + 1:])
+            assert not torch.isfinite(got[g][:at + 1]).any(), g
+    else:
+        # every query from there on sees it, and every key is seen by the last query
+        assert not torch.isfinite(got["dq"][at:]).any()
+        assert not torch.isfinite(got["dk_nope"]).any() and not torch.isfinite(got["dk_rope"]).any()
+    _in_time(lambda: _backward(d, o, lse), lambda: _backward(sound, ro, rlse), f"backward with a NaN in {where}")
