@@ -364,17 +364,6 @@ __device__ __forceinline__ bool any_nonfinite(const f32x16 (&acc)[NT]) {
   return bad;
 }
 
-__device__ __forceinline__ bool frag_nonfinite(bf16x8 f) {
-  const uint4 w = __builtin_bit_cast(uint4, f);
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t x = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
-    bad |= (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
-  }
-  return bad;
-}
-
 // ---------------------------------------------------------------------------
 // Hidden values that are not finite.  A hidden key's probability is an exact 0, but
 // the matrix unit still multiplies it, and 0 * NaN or 0 * infinity would reach
@@ -1156,15 +1145,10 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a)
   store(row < st.lk);
   if (!a.causal) return;
   // rows that a hidden query or gradient may have reached
-  bool nf = any_nonfinite(wide), own = false;      // own: the key itself is not finite
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) own |= frag_nonfinite(k[i]);
-#pragma unroll
-  for (int i = 0; i < kVSteps; ++i) own |= frag_nonfinite(v[i]);
-  own = __shfl_xor((int)own, 32, 64) | (int)own;
+  bool nf = any_nonfinite(wide);
 #pragma unroll
   for (int i = 0; i < 16; ++i) nf |= !(__builtin_fabsf(rope[i]) < __builtin_inff());
-  const uint64_t bad = __ballot(nf && row < st.lk && !own);
+  const uint64_t bad = __ballot(nf && row < st.lk);
   if (l == 0) s_bad[pair][half] = (uint32_t)bad | (uint32_t)(bad >> 32);
   __syncthreads();
   uint32_t any = 0;

@@ -185,3 +185,22 @@ def test_backward_with_a_broken_operand(where):
         assert not torch.isfinite(got["dq"][at:]).any()
         assert not torch.isfinite(got["dk_nope"]).any() and not torch.isfinite(got["dk_rope"]).any()
     _in_time(lambda: _backward(d, o, lse), lambda: _backward(sound, ro, rlse), f"backward with a NaN in {where}")
+
+
+@pytest.mark.parametrize("n,H", [(64, 1), (200, 3), (700, 40)])
+def test_hidden_nan_does_not_reach_a_key_of_minus_infinity(n, H):
+    """A key whose logits are all minus infinity has probability 0 and gradient 0, whatever
+    the queries hold that do not see it."""
+    say(f"latent attention backward, a key of minus infinity, {n} rows {H} heads")
+    d = _inputs(n, n, H, 6)
+    j, i = 45, 40
+    d["q"][..., 3] = d["q"][..., 3].abs() + 0.1
+    d["k_nope"][j, :, 3] = -INF
+    d["q"][i, :, 7] = NAN
+    d["dout"][i, :, 7] = NAN
+    o, lse = _forward(d)
+    g = _backward(d, o, lse)
+    for name in ("dk_nope", "dk_rope", "dv"):
+        assert (g[name][j] == 0).all(), name
+        assert not torch.isfinite(g[name][:i + 1]).any() or name == "dv"
+        assert torch.isfinite(g[name][i + 1:]).all(), name
