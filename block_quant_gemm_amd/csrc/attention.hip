@@ -924,7 +924,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
   if (row < st.lq && h == 0 && half == 0) a.delta[head * a.Tq + st.q0 + row] = delta + r;
   if (!a.causal) return;
   // rows that a hidden key may have reached
-  const uint64_t bad = __ballot(any_nonfinite(dq) && row < st.lq && lse2 == lse2 && delta == delta);
+  const uint64_t bad = __ballot(any_nonfinite(dq) && row < st.lq && (lim == 0 || (lse2 == lse2 && delta == delta)));
   if (l == 0) s_bad[pair][half] = (uint32_t)bad | (uint32_t)(bad >> 32);
   __syncthreads();
   uint32_t any = 0;

@@ -204,3 +204,20 @@ def test_hidden_nan_does_not_reach_a_key_of_minus_infinity(n, H):
         assert (g[name][j] == 0).all(), name
         assert not torch.isfinite(g[name][:i + 1]).any() or name == "dv"
         assert torch.isfinite(g[name][i + 1:]).all(), name
+
+
+@pytest.mark.parametrize("lq,lk,H", [(100, 37, 2), (900, 300, 20)])
+def test_a_row_that_sees_nothing_has_no_gradient(lq, lk, H):
+    """More queries than keys: the first see none, and neither their own dO nor the keys after
+    them make a gradient."""
+    say(f"latent attention backward, rows that see nothing, {lq} queries {lk} keys {H} heads")
+    d = _inputs(lq, lk, H, 7)
+    first = lq - lk                                       # the first query that sees a key
+    d["dout"][first - 9:first - 3, :, 5] = NAN
+    d["dout"][first - 3:first, :, 5] = INF
+    d["k_nope"][3, :, 11] = NAN
+    d["k_rope"][5, 2] = -INF
+    o, lse = _forward(d)
+    g = _backward(d, o, lse)
+    assert (o[:first] == 0).all() and torch.isneginf(lse[:, :first]).all()
+    assert (g["dq"][:first] == 0).all()
