@@ -391,30 +391,10 @@ __device__ __forceinline__ void add4(f32x16& o, int i, bool seen, float w, const
   o[i + 3] = __builtin_fmaf(w, bf16_hi(x.y), o[i + 3]);
 }
 
-// Which of 4 BF16 values are NaN or infinite: a bit each.
-__device__ __forceinline__ uint32_t nonfinite4(uint2 x) {
-  return ((x.x & 0x7F80u) == 0x7F80u ? 1u : 0u) | ((x.x & 0x7F800000u) == 0x7F800000u ? 2u : 0u) |
-         ((x.y & 0x7F80u) == 0x7F80u ? 4u : 0u) | ((x.y & 0x7F800000u) == 0x7F800000u ? 8u : 0u);
-}
-
-// Which of them are NaN.
+// Which of 4 BF16 values are NaN: a bit each.
 __device__ __forceinline__ uint32_t nan4(uint2 x) {
   return ((x.x & 0x7FFFu) > 0x7F80u ? 1u : 0u) | ((x.x & 0x7FFFFFFFu) > 0x7F80FFFFu ? 2u : 0u) |
          ((x.y & 0x7FFFu) > 0x7F80u ? 4u : 0u) | ((x.y & 0x7FFFFFFFu) > 0x7F80FFFFu ? 8u : 0u);
-}
-
-// Sets the NaN and infinities among `bytes` bytes of BF16 values in LDS to 0, by `threads` threads.
-__device__ __forceinline__ void clear_nonfinite(uint8_t* t, uint32_t bytes, uint32_t threads) {
-#pragma unroll 1
-  for (uint32_t i = threadIdx.x * 8; i < bytes; i += threads * 8) {
-    uint2 x = *reinterpret_cast<const uint2*>(t + i);
-    const uint32_t bits = nonfinite4(x);
-    if (bits & 1) x.x &= 0xFFFF0000u;
-    if (bits & 2) x.x &= 0xFFFFu;
-    if (bits & 4) x.y &= 0xFFFF0000u;
-    if (bits & 8) x.y &= 0xFFFFu;
-    *reinterpret_cast<uint2*>(t + i) = x;
-  }
 }
 
 // Whether any of the workgroup's `waves` wavefronts has bits set, through the first words

@@ -227,6 +227,26 @@ __device__ __forceinline__ bf16x8 widen8_bf16(uint32_t w0, uint32_t w1, float s)
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// Which of 4 BF16 values are NaN or infinite: a bit each.
+__device__ __forceinline__ uint32_t nonfinite4(uint2 x) {
+  return ((x.x & 0x7F80u) == 0x7F80u ? 1u : 0u) | ((x.x & 0x7F800000u) == 0x7F800000u ? 2u : 0u) |
+         ((x.y & 0x7F80u) == 0x7F80u ? 4u : 0u) | ((x.y & 0x7F800000u) == 0x7F800000u ? 8u : 0u);
+}
+
+// Sets the NaN and infinities among `bytes` bytes of BF16 values in LDS to 0, by `threads` threads.
+__device__ __forceinline__ void clear_nonfinite(uint8_t* t, uint32_t bytes, uint32_t threads) {
+#pragma unroll 1
+  for (uint32_t i = threadIdx.x * 8; i < bytes; i += threads * 8) {
+    uint2 x = *reinterpret_cast<const uint2*>(t + i);
+    const uint32_t bits = nonfinite4(x);
+    if (bits & 1) x.x &= 0xFFFF0000u;
+    if (bits & 2) x.x &= 0xFFFFu;
+    if (bits & 4) x.y &= 0xFFFF0000u;
+    if (bits & 8) x.y &= 0xFFFFu;
+    *reinterpret_cast<uint2*>(t + i) = x;
+  }
+}
+
 // Buffer descriptor for gfx9: 48-bit base, stride 0, num_records bytes (range
 // checked: loads at or past it read 0), data format word 0x00020000.
 __device__ __forceinline__ i32x4 make_rsrc(const void* p, uint32_t bytes) {

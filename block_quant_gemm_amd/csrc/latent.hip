@@ -9,6 +9,8 @@
 //   o[r]    = sum_t softmax(z[r])_t c[t]
 // so one read of a slot serves every head and every query token of a request.
 
+#include <type_traits>
+
 #include "common.h"
 
 namespace mxq {
@@ -243,68 +245,6 @@ __device__ __forceinline__ int32_t slot_of(const DecodeArgs& a, const int32_t* p
   return (int32_t)((int64_t)pg * a.page + (t - p * a.page));
 }
 
-// One row's part over the tokens [t0, t1), by one wavefront and without the
-// matrix unit: hidden tokens are left out instead of multiplied by 0.  Lane l
-// returns columns 8 l .. 8 l + 7.  For rows whose plain result is not finite.
-__device__ __forceinline__ void redo_part(const DecodeArgs& a, int32_t b, int row, int len, int t0,
-                                          int t1, float (&o)[8], float& m, float& sum) {
-  const int l = threadIdx.x & 63;
-  const int sq = row / a.H, h = row - sq * a.H;
-  const uint16_t* q = a.q + (int64_t)b * a.ldq_seq + (int64_t)sq * a.ldq_tok + (int64_t)h * a.ldq_head;
-  const int32_t* pages = a.pages + (int64_t)b * a.ldp;
-  const float c = a.scale * kLog2e;
-  m = -__builtin_inff();
-  sum = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) o[e] = 0.0f;
-#pragma unroll 1
-  for (int base = t0; base < t1; base += 64) {
-    const int n = t1 - base < 64 ? t1 - base : 64;
-    const int32_t s = l < n ? slot_of(a, pages, (uint32_t)(base + l), len) : -1;
-    float z = -__builtin_inff();
-    if (l < n) {
-      z = 0.0f;
-      if (s >= 0) {
-#pragma unroll 1
-        for (int i = 0; i < kLat; ++i) {
-          const float f = __builtin_amdgcn_cvt_f32_fp8((int)a.k.codes[s * a.k.ldc + i], 0) *
-                          scale_f32(a.k.scales[s * a.k.lds + i / 32]);
-          z = __builtin_fmaf(f, bf16_lo(q[i]), z);
-        }
-#pragma unroll 1
-        for (int i = 0; i < kRope; ++i)
-          z = __builtin_fmaf(bf16_lo(a.k.rope[s * a.k.ldr + i]), bf16_lo(q[kLat + i]), z);
-      }
-      z *= c;
-    }
-    float mx = z;
-#pragma unroll
-    for (int sh = 32; sh > 0; sh >>= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, sh, 64));
-    const float mn = __builtin_fmaxf(m, mx);
-    const float ref = mn == -__builtin_inff() ? 0.0f : mn;
-    const float alpha = __builtin_amdgcn_exp2f(m - ref);
-    const float p = l < n ? __builtin_amdgcn_exp2f(z - ref) : 0.0f;
-    m = mn;
-    float ps = p;
-#pragma unroll
-    for (int sh = 32; sh > 0; sh >>= 1) ps += __shfl_xor(ps, sh, 64);
-    sum = sum * alpha + ps;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] *= alpha;
-#pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-      const int32_t sj = __builtin_amdgcn_readlane(s, j);
-      if (sj < 0) continue;
-      const float pj = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, p), j));
-      const float f = scale_f32(a.k.scales[sj * a.k.lds + l / 4]) * pj;
-      const uint2 w = *reinterpret_cast<const uint2*>(a.k.codes + sj * a.k.ldc + 8 * l);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        o[e] = __builtin_fmaf(__builtin_amdgcn_cvt_f32_fp8((int)((e < 4 ? w.x : w.y) >> (8 * (e & 3))), 0), f, o[e]);
-    }
-  }
-}
-
 // Four latent columns of a finished row.
 __device__ __forceinline__ uint2 bf16x4_bits(f32x4 v, float mul) {
   return make_uint2(bf16x2_bits(v[0] * mul, v[1] * mul), bf16x2_bits(v[2] * mul, v[3] * mul));
@@ -422,198 +362,224 @@ __global__ __launch_bounds__(kThr * G, R * G == 1 ? 2 : G) void k_decode(DecodeA
     if (KQ < kSteps)
       for (int kk = KQ + w; kk < kSteps; kk += 4) s_q[rg + r][kk - KQ][l] = step(kk);
   }
-  f32x4 o[R][8] = {};
+  f32x4 o[R][8];
   float m[R], sum[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) m[r] = -__builtin_inff(), sum[r] = 0.0f;
   const float c = a.scale * kLog2e;
-  __syncthreads();
-  if (a.k.slots > 0) load(i0);
-  for (uint32_t i = i0; i < i1; ++i) {
-    __syncthreads();                               // the last tile is consumed
-    if (__ballot(gone != 0)) {
+  // The second walk, a tile that not all query tokens see: takes what is not finite out of it,
+  // and notes which of this lane's sums would have had it from tokens that their row sees.
+  uint32_t nan[R];
+  auto cover = [&](uint32_t i) __attribute__((always_inline)) {
+#pragma unroll 1
+    for (uint32_t t = 0; t < kTok; ++t) {
+      uint32_t bits = 0;
 #pragma unroll
-      for (int j = 0; j < kCl; ++j)
-        if ((gone >> j) & 1) sc[j] = make_uint4(0, 0, 0, 0), se[j] = 127;
+      for (int d = 0; d < 8; ++d) {
+        const uint32_t slot = 16 * w + 2 * d + (g >> 1);
+        bits |= nonfinite4(*reinterpret_cast<const uint2*>(tile + t * kRowB + ((slot ^ fd(t)) << 4) + 8 * (g & 1)))
+                << (4 * d);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) nan[r] |= (int)(i * kTok + t) < lim[r] ? bits : 0u;
+    }
+    __syncthreads();
+    clear_nonfinite(tile, kTok * kRowB, kThr * G);
+    __syncthreads();
+  };
+  // The sums over the run's tokens.
+  auto walk = [&](auto again) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = -__builtin_inff();
+      sum[r] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[r][d] = f32x4{};
+    }
+    __syncthreads();
+    if (a.k.slots > 0) load(i0);
+    for (uint32_t i = i0; i < i1; ++i) {
+      __syncthreads();                               // the last tile is consumed
+      if (__ballot(gone != 0)) {
+#pragma unroll
+        for (int j = 0; j < kCl; ++j)
+          if ((gone >> j) & 1) sc[j] = make_uint4(0, 0, 0, 0), se[j] = 127;
+#pragma unroll
+        for (int j = 0; j < kRl; ++j)
+          if ((gone >> (8 + j)) & 1) sr[j] = make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < kCl; ++j) {
+        const float f = e8m0_f32(se[j]);
+        uint8_t* p = tile + (G == 1 ? wr ^ ((j & 1) << 4) : wr) + j * (8 * G * kRowB);
+        *reinterpret_cast<bf16x8*>(p) = widen8_bf16(sc[j].x, sc[j].y, f);
+        *reinterpret_cast<bf16x8*>(p + 512) = widen8_bf16(sc[j].z, sc[j].w, f);
+      }
 #pragma unroll
       for (int j = 0; j < kRl; ++j)
-        if ((gone >> (8 + j)) & 1) sr[j] = make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int j = 0; j < kCl; ++j) {
-      const float f = e8m0_f32(se[j]);
-      uint8_t* p = tile + (G == 1 ? wr ^ ((j & 1) << 4) : wr) + j * (8 * G * kRowB);
-      *reinterpret_cast<bf16x8*>(p) = widen8_bf16(sc[j].x, sc[j].y, f);
-      *reinterpret_cast<bf16x8*>(p + 512) = widen8_bf16(sc[j].z, sc[j].w, f);
-    }
-#pragma unroll
-    for (int j = 0; j < kRl; ++j)
-      *reinterpret_cast<uint4*>(tile + wrr + j * (32 * G * kRowB)) = sr[j];
-    __syncthreads();
-    if (i + 1 < i1 && a.k.slots > 0) load(i + 1);
+        *reinterpret_cast<uint4*>(tile + wrr + j * (32 * G * kRowB)) = sr[j];
+      __syncthreads();
+      if (i + 1 < i1 && a.k.slots > 0) load(i + 1);
 
-    f32x4 s[R] = {}, s2[R] = {};                   // two chains a row group
-    struct Step {
-      bf16x8 k, q[R];
-    };
-    pipelined<kSteps, (R == 1 ? 4 : 3)>(
-        [&](int kk) {
-          Step x;
-          x.k = *reinterpret_cast<const bf16x8*>(tile + (rk ^ ((kk & 1) << 6)) + (kk >> 1) * 128);
-          if (kk >= KQ) {
+      f32x4 s[R] = {}, s2[R] = {};                   // two chains a row group
+      struct Step {
+        bf16x8 k, q[R];
+      };
+      pipelined<kSteps, (R == 1 ? 4 : 3)>(
+          [&](int kk) {
+            Step x;
+            x.k = *reinterpret_cast<const bf16x8*>(tile + (rk ^ ((kk & 1) << 6)) + (kk >> 1) * 128);
+            if (kk >= KQ) {
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-              x.q[r] = __builtin_bit_cast(bf16x8, s_q[rg + r][kk < KQ ? 0 : kk - KQ][l]);
-          }
-          return x;
-        },
-        [&](int kk, const Step& x) {
+              for (int r = 0; r < R; ++r)
+                x.q[r] = __builtin_bit_cast(bf16x8, s_q[rg + r][kk < KQ ? 0 : kk - KQ][l]);
+            }
+            return x;
+          },
+          [&](int kk, const Step& x) {
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const bf16x8 qf = kk < KQ ? q[r][kk < KQ ? kk : 0] : x.q[r];
-            if (kk & 1)
-              s2[r] = mfma16(x.k, qf, s2[r]);
-            else
-              s[r] = mfma16(x.k, qf, s[r]);
-          }
-        });
+            for (int r = 0; r < R; ++r) {
+              const bf16x8 qf = kk < KQ ? q[r][kk < KQ ? kk : 0] : x.q[r];
+              if (kk & 1)
+                s2[r] = mfma16(x.k, qf, s2[r]);
+              else
+                s[r] = mfma16(x.k, qf, s[r]);
+            }
+          });
 #pragma unroll
-    for (int r = 0; r < R; ++r) s[r] += s2[r];
-    const int tok0 = (int)(i * kTok) + 16 * w + 4 * g;   // this lane's 4 tokens
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (tok0 + e >= lim[r]) s[r][e] = -__builtin_inff();
-      const float mx = groups_max(__builtin_fmaxf(__builtin_fmaxf(s[r][0], s[r][1]),
-                                                  __builtin_fmaxf(s[r][2], s[r][3])));
-      if (g == 0) s_max[w][(rg + r) * 16 + n] = mx;
-    }
-    __syncthreads();
-    put_slot(i + 2);                               // its loads are a whole tile away
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float mn = m[r];
-#pragma unroll
-      for (int x = 0; x < kWaves; ++x) mn = __builtin_fmaxf(mn, s_max[x][(rg + r) * 16 + n] * c);
-      if (__ballot(mn != m[r])) {
-        const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mn);
-        m[r] = mn;
-        sum[r] *= alpha;
-#pragma unroll
-        for (int d = 0; d < 8; ++d) o[r][d] *= alpha;
-      }
-      const float mc = mn == -__builtin_inff() ? 0.0f : mn;
-      float p[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][e], c, -mc));
-        sum[r] += p[e];
-      }
-      s_p[w][rg + r][l] = make_uint2(bf16x2_bits(p[0], p[1]), bf16x2_bits(p[2], p[3]));
-    }
-    __syncthreads();
-    // values: tokens 4 g + 0..3 of two wavefronts' 16 a step of 32
-    bf16x8 pf[2][R];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
+      for (int r = 0; r < R; ++r) s[r] += s2[r];
+      const int tok0 = (int)(i * kTok) + 16 * w + 4 * g;   // this lane's 4 tokens
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const uint2 x = s_p[2 * j][rg + r][l], y = s_p[2 * j + 1][rg + r][l];
-        pf[j][r] = __builtin_bit_cast(bf16x8, make_uint4(x.x, x.y, y.x, y.y));
-      }
-    pipelined<16, (R == 1 ? 4 : 3)>(
-        [&](int i2) {
-          const int j = i2 >> 3, d = i2 & 7;
-          const uint8_t* p = tile + (rv ^ ((d & 3) << 5)) + (d >> 2) * 128 + j * (32 * kRowB);
-          const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
-          const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 16 * kRowB));
-          return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-        },
-        [&](int i2, bf16x8 vf) {
 #pragma unroll
-          for (int r = 0; r < R; ++r) o[r][i2 & 7] = mfma16(vf, pf[i2 >> 3][r], o[r][i2 & 7]);
-        });
-  }
-
-  // totals of all wavefronts' tokens; rows to redo
-  __syncthreads();
+        for (int e = 0; e < 4; ++e)
+          if (tok0 + e >= lim[r]) s[r][e] = -__builtin_inff();
+        const float mx = groups_max(__builtin_fmaxf(__builtin_fmaxf(s[r][0], s[r][1]),
+                                                    __builtin_fmaxf(s[r][2], s[r][3])));
+        if (g == 0) s_max[w][(rg + r) * 16 + n] = mx;
+      }
+      __syncthreads();
+      put_slot(i + 2);                               // its loads are a whole tile away
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float mn = m[r];
+#pragma unroll
+        for (int x = 0; x < kWaves; ++x) mn = __builtin_fmaxf(mn, s_max[x][(rg + r) * 16 + n] * c);
+        if (__ballot(mn != m[r])) {
+          const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mn);
+          m[r] = mn;
+          sum[r] *= alpha;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) o[r][d] *= alpha;
+        }
+        const float mc = mn == -__builtin_inff() ? 0.0f : mn;
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][e], c, -mc));
+          sum[r] += p[e];
+        }
+        s_p[w][rg + r][l] = make_uint2(bf16x2_bits(p[0], p[1]), bf16x2_bits(p[2], p[3]));
+      }
+      __syncthreads();
+      if (decltype(again)::value && (int)(i + 1) * kTok > len - (a.S - 1)) cover(i);
+      // values: tokens 4 g + 0..3 of two wavefronts' 16 a step of 32
+      bf16x8 pf[2][R];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint2 x = s_p[2 * j][rg + r][l], y = s_p[2 * j + 1][rg + r][l];
+          pf[j][r] = __builtin_bit_cast(bf16x8, make_uint4(x.x, x.y, y.x, y.y));
+        }
+      pipelined<16, (R == 1 ? 4 : 3)>(
+          [&](int i2) {
+            const int j = i2 >> 3, d = i2 & 7;
+            const uint8_t* p = tile + (rv ^ ((d & 3) << 5)) + (d >> 2) * 128 + j * (32 * kRowB);
+            const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
+            const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 16 * kRowB));
+            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+          },
+          [&](int i2, bf16x8 vf) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) o[r][i2 & 7] = mfma16(vf, pf[i2 >> 3][r], o[r][i2 & 7]);
+          });
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {                  // totals of all wavefronts' tokens
+      const float x = groups_sum(sum[r]);
+      if (g == 0) s_max[w][(rg + r) * 16 + n] = x;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      sum[r] = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kWaves; ++x) sum[r] += s_max[x][(rg + r) * 16 + n];
+    }
+  };
+  const int64_t part = ((int64_t)blockIdx.x * gridDim.y + rt) * kRows;
+  // this lane's rows, `all` or those marked: the results, or their parts
+  auto store = [&](bool all) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int row = rt * kRows + (rg + r) * 16 + n;
+      const float total = sum[r];
+      const bool mine = row < a.rows && (all || s_redo[(rg + r) * 16 + n] != 0);
+      if (nrun == 1) {
+        const int sq = row / a.H, h = row - sq * a.H;
+        uint16_t* op = a.o + (int64_t)b * a.ldo_seq + (int64_t)sq * a.ldo_tok + (int64_t)h * a.ldo_head;
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+        if (mine) {
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+            *reinterpret_cast<uint2*>(op + slot_unit(16 * w + 2 * d + (g >> 1)) * 8 + 4 * (g & 1)) =
+                bf16x4_bits(o[r][d], inv);
+        }
+        if (mine && w == 0 && g == 0)
+          a.lse[(int64_t)b * a.rows + row] =
+              total == 0.0f ? -__builtin_inff() : kLn2 * (m[r] + __builtin_amdgcn_logf(total));
+      } else {
+        const int64_t pr = part + (rg + r) * 16 + n;
+        if (mine) {
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+            *reinterpret_cast<f32x4*>(a.part_o + pr * kLat + slot_unit(16 * w + 2 * d + (g >> 1)) * 8 +
+                                      4 * (g & 1)) = o[r][d];
+        }
+        if (mine && w == 0 && g == 0) {
+          a.part_ml[2 * pr] = m[r];
+          a.part_ml[2 * pr + 1] = total;
+        }
+      }
+    }
+  };
+  walk(std::false_type{});
+  store(true);
+  // Query tokens that do not see a tile's last tokens still multiply them, by 0, and a NaN
+  // there leaves a NaN.  A workgroup with such rows walks its run again.
+  if (a.S == 1 || (int)i1 * kTok <= len - (a.S - 1)) return;   // all of the run is seen by all
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const float x = groups_sum(sum[r]);
-    if (g == 0) s_max[w][(rg + r) * 16 + n] = x;
-    // Query tokens that do not see a tile's last tokens still multiply them, by
-    // 0; a NaN or infinity there leaves a NaN, and the row is redone.
     bool bad = false;
 #pragma unroll
     for (int d = 0; d < 8; ++d)
 #pragma unroll
       for (int e = 0; e < 4; ++e) bad |= !(__builtin_fabsf(o[r][d][e]) < __builtin_inff());
-    if (bad && a.S > 1) s_redo[(rg + r) * 16 + n] = 1;
+    if (bad && sum[r] == sum[r]) s_redo[(rg + r) * 16 + n] = 1;   // a row that sees a NaN has a NaN total
   }
   __syncthreads();
-  const int64_t part = ((int64_t)blockIdx.x * gridDim.y + rt) * kRows;
+  if (!__ballot(s_redo[l % kRows] != 0)) return;   // uniform over the workgroup
+  put_slot(i0);
+  put_slot(i0 + 1);
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    float total = 0.0f;
+  for (int r = 0; r < R; ++r) nan[r] = 0;
+  walk(std::true_type{});
 #pragma unroll
-    for (int x = 0; x < kWaves; ++x) total += s_max[x][(rg + r) * 16 + n];
-    const int row = rt * kRows + (rg + r) * 16 + n;
-    const bool mine = row < a.rows && s_redo[(rg + r) * 16 + n] == 0;
-    if (nrun == 1) {
-      const int sq = row / a.H, h = row - sq * a.H;
-      uint16_t* op = a.o + (int64_t)b * a.ldo_seq + (int64_t)sq * a.ldo_tok + (int64_t)h * a.ldo_head;
-      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-      if (mine) {
+  for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int d = 0; d < 8; ++d)
-          *reinterpret_cast<uint2*>(op + slot_unit(16 * w + 2 * d + (g >> 1)) * 8 + 4 * (g & 1)) =
-              bf16x4_bits(o[r][d], inv);
-      }
-      if (mine && w == 0 && g == 0)
-        a.lse[(int64_t)b * a.rows + row] =
-            total == 0.0f ? -__builtin_inff() : kLn2 * (m[r] + __builtin_amdgcn_logf(total));
-    } else {
-      const int64_t pr = part + (rg + r) * 16 + n;
-      if (mine) {
-#pragma unroll
-        for (int d = 0; d < 8; ++d)
-          *reinterpret_cast<f32x4*>(a.part_o + pr * kLat + slot_unit(16 * w + 2 * d + (g >> 1)) * 8 +
-                                    4 * (g & 1)) = o[r][d];
-      }
-      if (mine && w == 0 && g == 0) {
-        a.part_ml[2 * pr] = m[r];
-        a.part_ml[2 * pr + 1] = total;
-      }
-    }
-  }
-  if (a.S == 1) return;
-#pragma unroll 1
-  for (int y = wave; y < kRows; y += kWaves * G) {
-    if (s_redo[y] == 0) continue;                  // uniform over the wavefront
-    const int row = rt * kRows + y, sq = row / a.H, h = row - sq * a.H;
-    if (row >= a.rows) continue;
-    const int seen = len - (a.S - 1 - sq), end = (int)(i1 * kTok);
-    float v[8], mm, total;
-    redo_part(a, b, row, len, (int)(i0 * kTok), seen < end ? seen : end, v, mm, total);
-    if (nrun == 1) {
-      uint16_t* op = a.o + (int64_t)b * a.ldo_seq + (int64_t)sq * a.ldo_tok + (int64_t)h * a.ldo_head;
-      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-#pragma unroll
-      for (int e = 0; e < 8; e += 4)
-        *reinterpret_cast<uint2*>(op + 8 * l + e) = bf16x4_bits(f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]}, inv);
-      if (l == 0)
-        a.lse[(int64_t)b * a.rows + row] =
-            total == 0.0f ? -__builtin_inff() : kLn2 * (mm + __builtin_amdgcn_logf(total));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) a.part_o[(part + y) * kLat + 8 * l + e] = v[e];
-      if (l == 0) {
-        a.part_ml[2 * (part + y)] = mm;
-        a.part_ml[2 * (part + y) + 1] = total;
-      }
-    }
-  }
+    for (int e = 0; e < 32; ++e)
+      if ((nan[r] >> e) & 1) o[r][e / 4][e % 4] = __builtin_nanf("");
+  store(false);
 }
 
 // Joins the parts of the requests that more than one workgroup worked on, in

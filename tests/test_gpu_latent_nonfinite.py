@@ -221,3 +221,53 @@ def test_a_row_that_sees_nothing_has_no_gradient(lq, lk, H):
     g = _backward(d, o, lse)
     assert (o[:first] == 0).all() and torch.isneginf(lse[:, :first]).all()
     assert (g["dq"][:first] == 0).all()
+
+
+def _decode_inputs(lens, S, H, seed):
+    r, page = _rnd(seed), 32
+    need = -(-max(lens) // page)
+    cache = mxq.latent_cache(len(lens) * need * page)
+    pages = torch.randperm(len(lens) * need, device="cuda", generator=torch.Generator("cuda").manual_seed(seed))
+    pages = pages.view(len(lens), need).to(torch.int32)
+    n = cache[0].shape[0]
+    mxq.mx_latent_cache_write(r(n, 512), r(n, 64), torch.arange(n, device="cuda"), cache)
+    return {"q": r(len(lens), S, H, 576, sigma=0.7), "cache": cache, "pages": pages, "page_size": page,
+            "lens": torch.tensor(lens, device="cuda"), "max_len": max(lens), "scale": 192 ** -0.5}
+
+
+def _slot(d, b, t):
+    return int(d["pages"][b, t // d["page_size"]]) * d["page_size"] + t % d["page_size"]
+
+
+@pytest.mark.parametrize("S,H,lens", [(2, 64, [5000, 700, 64]), (3, 5, [4000, 90]), (2, 16, [3000] * 8), (2, 8, [1200, 1])])
+@pytest.mark.parametrize("where", ["seen", "last", "both"])
+def test_decode_with_a_broken_token(S, H, lens, where):
+    """A NaN block in a token that all query tokens of the first request see makes its rows NaN; in
+    its last token, the last query token's rows alone.  Other requests do not notice."""
+    say(f"latent decode, {len(lens)} requests, {S} tokens, {H} heads, a NaN token ({where})")
+    d = _decode_inputs(lens, S, H, 8)
+    ro, rlse = mxq.mx_latent_decode(**d)
+    sound = dict(d, cache=tuple(t.clone() for t in d["cache"]))
+    for t in {"seen": [lens[0] - 70], "last": [lens[0] - 1], "both": [lens[0] - 70, lens[0] - 1]}[where]:
+        s = _slot(d, 0, t)
+        d["cache"][0][s, 64:96] = 0x7F
+        d["cache"][1][s, 2] = 0xFF
+    o, lse = mxq.mx_latent_decode(**d)
+    assert _same(o[1:], ro[1:]) and torch.equal(lse[1:], rlse[1:])
+    assert torch.isnan(o[0, -1]).all() and torch.isnan(lse[0, -1]).all()
+    if where == "last":
+        assert (lse[0, :-1] - rlse[0, :-1]).abs().max() < 1e-4
+        _near(o[0, :-1], ro[0, :-1], 6.0)                 # 6: the largest of the normal latents, nearly
+    else:
+        assert torch.isnan(o[0]).all() and torch.isnan(lse[0]).all()
+    _in_time(lambda: mxq.mx_latent_decode(**d), lambda: mxq.mx_latent_decode(**sound), "decode with a NaN token")
+
+
+def test_decode_with_nan_everywhere():
+    say("latent decode, all tokens NaN")
+    d = _decode_inputs([4000] * 6, 2, 64, 9)
+    sound = dict(d, cache=tuple(t.clone() for t in d["cache"]))
+    d["cache"][1].fill_(0xFF)
+    o, lse = mxq.mx_latent_decode(**d)
+    assert torch.isnan(o).all() and torch.isnan(lse).all()
+    _in_time(lambda: mxq.mx_latent_decode(**d), lambda: mxq.mx_latent_decode(**sound), "decode with NaN everywhere")
