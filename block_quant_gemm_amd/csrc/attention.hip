@@ -414,6 +414,8 @@ __device__ __forceinline__ float bf(const uint16_t* p) {
   return __builtin_bit_cast(float, (uint32_t)*p << 16);
 }
 
+__device__ __forceinline__ int lane_id() { return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)); }
+
 // A head's operands of one sequence.
 struct Head {
   const uint16_t *q, *kn, *kr, *v, *o, *g;       // g: the output's gradient
@@ -700,23 +702,33 @@ __global__ __launch_bounds__(kThr) void k_attn_join(AttnArgs a) {
 // not fit.
 // ---------------------------------------------------------------------------
 
-// Slabs that a wavefront hands over: 2 of P, 2 of dS, and with FINE the 2 of what
-// dS's rounding to BF16 leaves, again in BF16.
-//
-// FINE: rounding dS once costs dQ and dK as much as rounding the result does; the
-// two together are 1.41 times the least error, evenly in large calls.  In small
-// ones, where few entries of dS carry the result, up to 1.95 times was seen; with
-// the second term 1.1 (one sequence of 360, 16 heads: 45 us for the three kernels
-// against 41).
-template <int PAIRS, bool FINE>
+// Slabs that a wavefront hands over: 2 of P and 2 of dS.
+template <int PAIRS>
 struct Exchange {
-  uint4 f[PAIRS][2][FINE ? 6 : 4][64];           // pair, half, slab, lane
+  uint4 f[PAIRS][2][4][64];                      // pair, half, slab, lane
 };
+
+// Rounding dS once costs dQ and dK as much as rounding the result does; the two
+// together are 1.41 times the least error, evenly where many entries of dS make a
+// result.  Where few do it varies, up to 1.7 times (one sequence of 18, 2 heads).  So where
+// queries see at most kFew keys, what the rounding left of dS is handed on as a second
+// BF16 term and multiplied in a run of its own: 1.0 times the least.  It lies in the tile
+// buffer that is free until the next tile but one is copied, whose copy then starts
+// after it is read.  Whether a group of 32 query rows (dQ) or a tile of 64 (dK) has it goes by
+// what its first row sees, so a sequence's gradient does not depend on what shares the
+// call, and it costs a sequence's first tiles alone.  The second walk does without.
+constexpr int kFew = 64;
+struct Rests {
+  uint4 f[2][2][64];                             // half, slab, lane, of one pair
+};
+__device__ __forceinline__ Rests& rests_of(uint8_t* lds, int buf, int pair) {
+  return reinterpret_cast<Rests*>(lds + buf * kTile)[pair];
+}
 
 // Tile row r's entry for this lane's own row, of the slabs `slab` and `slab + 1` that were
 // handed over.
-template <int PAIRS, bool FINE>
-__device__ __forceinline__ float handed(const Exchange<PAIRS, FINE>& ex, int pair, uint32_t r, int slab) {
+template <int PAIRS>
+__device__ __forceinline__ float handed(const Exchange<PAIRS>& ex, int pair, uint32_t r, int slab) {
   const uint32_t n = threadIdx.x & 31, lane = n + 32 * ((r >> 2) & 1), at = (r & 3) + 4 * ((r >> 3) & 1);
   return bf(reinterpret_cast<const uint16_t*>(&ex.f[pair][r >> 5][slab + ((r >> 4) & 1)][lane]) + at);
 }
@@ -741,13 +753,13 @@ __device__ __forceinline__ uint4 slab_rest(const f32x16& p, uint4 w, int j) {
 // numbers).  With dS' = P * (dP - d), the row sum r of dS' is D - d, and
 //   dQ = scale * (dS' K - r (P K)):
 // the products P K and dS' K share the reads of K.
-template <int PAIRS, bool FINE>
+template <int PAIRS>
 __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[3 * kTile];
-  __shared__ __attribute__((aligned(16))) Exchange<PAIRS, FINE> ex;
+  __shared__ __attribute__((aligned(16))) Exchange<PAIRS> ex;
   __shared__ float s_rest[PAIRS][2][32];
   __shared__ uint32_t s_bad[PAIRS][2];
-  constexpr int BM = 32 * PAIRS, kSlabs = FINE ? 6 : 4;
+  constexpr int BM = 32 * PAIRS;
   const int head = blockIdx.x % a.H;
   const SeqTile st = find_tile<false>(a, blockIdx.x / a.H, BM);
   if (!st.ok) return;
@@ -784,8 +796,11 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
   f32x16 dq[3] = {}, pk[3] = {};
   float rest = 0.0f, unshift = kUnshift;           // row sum of this half's dS'
   const float c = a.scale * kLog2e;
+  const int cut = keys_seen(a, st, st.row0);       // tiles before it are seen whole by all
+  // tiles before these have a second term of dS: in the pair's rows, and in any of the workgroup's
+  const int few = wfirst <= kFew ? wlast : 0, few_any = cut <= kFew ? kFew + 32 : 0;
   // P and dS against the tile at k0 (in buffer `buf`), this wavefront's 32 keys of it
-  auto first = [&](uint4 (&mine)[kSlabs], int k0, int buf) __attribute__((always_inline)) {
+  auto first = [&](auto again, uint4 (&mine)[4], int k0, int buf, int spare) __attribute__((always_inline)) {
     if (k0 >= wlast) return;                       // the same for both of a pair
     const uint8_t* tile = lds + buf * kTile;
     // the units' addresses are formed again in every tile: kept, they cost too many registers
@@ -819,35 +834,41 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
     for (int j = 0; j < 2; ++j) {
       mine[j] = __builtin_bit_cast(uint4, slab(s, j));
       mine[2 + j] = __builtin_bit_cast(uint4, slab(dp, j));
-      if (FINE) mine[kSlabs - 2 + j] = slab_rest(dp, mine[2 + j], j);
+      if (!decltype(again)::value && k0 < few) rests_of(lds, spare, pair).f[half][j][l] = slab_rest(dp, mine[2 + j], j);
     }
   };
   // the sums over the tile at k0, with the pair's P and dS
-  auto second = [&](int k0, int buf) __attribute__((always_inline)) {
+  auto second = [&](auto again, int k0, int buf, int spare) __attribute__((always_inline)) {
     if (k0 < 0 || k0 >= wlast) return;
     const uint8_t* tile = lds + buf * kTile;
     asm volatile("" : "+v"(rp.n), "+v"(rp.r), "+v"(rp.tn), "+v"(rp.tr));
-    bf16x8 p[4], ds[4], rs[4];
+    bf16x8 p[4], ds[4];
     pipelined<12, 3>(
         [&](int i) {
           const int j = i / 3, d = i % 3;
           if (d == 0) {
             p[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][j & 1][l]);
             ds[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][2 + (j & 1)][l]);
-            if (FINE) rs[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][kSlabs - 2 + (j & 1)][l]);
           }
           return d < 2 ? wide_tr(tile, rp, j, 2 * half + d) : rope_tr(tile + kOffR, rp, j, half);
         },
         [&](int i, bf16x8 f) {
           dq[i % 3] = mfma(f, ds[i / 3], dq[i % 3]);
-          if (FINE) dq[i % 3] = mfma(f, rs[i / 3], dq[i % 3]);
           pk[i % 3] = mfma(f, p[i / 3], pk[i % 3]);
         });
+    if (!decltype(again)::value && k0 < few) {
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        const bf16x8 rs = __builtin_bit_cast(bf16x8, rests_of(lds, spare, pair).f[j >> 1][j & 1][l]);
+        dq[0] = mfma(wide_tr(tile, rp, j, 2 * half), rs, dq[0]);
+        dq[1] = mfma(wide_tr(tile, rp, j, 2 * half + 1), rs, dq[1]);
+        dq[2] = mfma(rope_tr(tile + kOffR, rp, j, half), rs, dq[2]);
+      }
+    }
   };
   // The second walk: where this lane's row sees a key that is not finite, its gradient is not
   // (such a key's logit makes the whole row NaN, or, at minus infinity, its P an exact 0).
   uint64_t nan = 0;                                // a bit for each of this lane's 48 sums
-  const int cut = keys_seen(a, st, st.row0);       // tiles before it are seen whole by all
   auto cover = [&](int k0, int buf) __attribute__((always_inline)) {
     uint8_t* tile = lds + buf * kTile;
 #pragma unroll 1
@@ -871,47 +892,52 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
     for (int k0 = 0; k0 < kend + kBN; k0 += kBN) {
       tile_wait();
       const int next = buf == 2 ? 0 : buf + 1;
-      if (k0 + kBN < kend) tile_copy<2 * PAIRS>(cp, x.kn, x.kr, x.v, k0 + kBN, st.lk, next);
-      uint4 mine[kSlabs];                          // this wavefront's P and dS slabs
+      const bool late = !decltype(again)::value && k0 > 0 && k0 - kBN < few_any;   // the last tile's rests are in the way
+      if (!late && k0 + kBN < kend) tile_copy<2 * PAIRS>(cp, x.kn, x.kr, x.v, k0 + kBN, st.lk, next);
+      uint4 mine[4];                               // this wavefront's P and dS slabs
       if (decltype(again)::value && k0 > cut) cover(k0 - kBN, prev);
-      second(k0 - kBN, prev);
-      if (k0 < kend) first(mine, k0, buf);
+      second(again, k0 - kBN, prev, next);
+      if (late || (!decltype(again)::value && k0 < few_any)) __syncthreads();   // the rests, and the last tile, are consumed
+      if (late && k0 + kBN < kend) tile_copy<2 * PAIRS>(cp, x.kn, x.kr, x.v, k0 + kBN, st.lk, next);
+      if (k0 < kend) first(again, mine, k0, buf, prev);
       __syncthreads();                             // the last tile's operands are consumed
       if (k0 < kend && k0 < wlast) {
 #pragma unroll
-        for (int j = 0; j < kSlabs; ++j) ex.f[pair][half][j][l] = mine[j];
+        for (int j = 0; j < 4; ++j) ex.f[pair][half][j][l] = mine[j];
       }
       prev = buf;
       buf = next;
     }
     rest = half_sum(rest);
-    if (h == 0) s_rest[pair][half][n] = rest;
+    const int lane = lane_id();                    // formed again: kept through the loop, it costs a register
+    if (lane < 32) s_rest[pair][half][lane] = rest;
     __syncthreads();
-    const float r = (s_rest[pair][0][n] + s_rest[pair][1][n]) * unshift;
+    const float r = (s_rest[pair][0][lane & 31] + s_rest[pair][1][lane & 31]) * unshift;
 #pragma unroll
     for (int d = 0; d < 3; ++d) dq[d] -= pk[d] * r;
     return r;
   };
   auto store = [&](bool write) {
-    if (!write) return;
+    const int row = wrow0 + (lane_id() & 31);
+    if (row >= st.lq || !write) return;
     uint16_t* p = a.dq.p + (st.q0 + row) * a.dq.ld + head * a.dq.ldh;
 #pragma unroll
     for (int d = 0; d < 2; ++d) store_block(dq[d], a.scale * unshift, p + 64 * half + 32 * d);
     store_block(dq[2], a.scale * unshift, p + kNope + 32 * half);
   };
   const float r = walk(std::false_type{});
-  store(row < st.lq);
-  if (row < st.lq && h == 0 && half == 0) a.delta[head * a.Tq + st.q0 + row] = delta + r;
+  store(true);
+  const int after = wrow0 + (lane_id() & 31);      // this lane's row
+  if (after < st.lq && lane_id() < 32 && half == 0) a.delta[head * a.Tq + st.q0 + after] = delta + r;
   if (!a.causal) return;
   // rows that a hidden key may have reached
-  const uint64_t bad = __ballot(any_nonfinite(dq) && row < st.lq && (lim == 0 || (lse2 == lse2 && delta == delta)));
-  if (l == 0) s_bad[pair][half] = (uint32_t)bad | (uint32_t)(bad >> 32);
+  const uint64_t bad = __ballot(any_nonfinite(dq) && after < st.lq && (lim == 0 || (lse2 == lse2 && delta == delta)));
+  if (lane_id() == 0) s_bad[pair][half] = (uint32_t)bad | (uint32_t)(bad >> 32);
   __syncthreads();
   uint32_t any = 0;
 #pragma unroll
   for (int i = 0; i < PAIRS; ++i) any |= s_bad[i][0] | s_bad[i][1];
   if (!any) return;                                // uniform over the workgroup
-  const uint32_t redo = s_bad[pair][0] | s_bad[pair][1];
   if (kend > 0) tile_copy<2 * PAIRS>(cp, x.kn, x.kr, x.v, 0, st.lk, 0);
 #pragma unroll
   for (int d = 0; d < 3; ++d) dq[d] = f32x16{}, pk[d] = f32x16{};
@@ -922,19 +948,19 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
 #pragma unroll
   for (int i = 0; i < 48; ++i)
     if ((nan >> i) & 1) dq[i / 16][i % 16] = __builtin_nanf("");
-  store(row < st.lq && ((redo >> n) & 1));
+  store(((s_bad[pair][0] | s_bad[pair][1]) >> (lane_id() & 31)) & 1);
 }
 
 // Backward, keys: dK, dV, walking the queries that see the workgroup's keys.  The
 // rotary part of dK is summed over the heads by k_attn_drope, from one FP32 part
 // a head, in head order.
-template <int PAIRS, bool FINE>
+template <int PAIRS>
 __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[3 * kTile];
-  __shared__ __attribute__((aligned(16))) Exchange<PAIRS, FINE> ex;
+  __shared__ __attribute__((aligned(16))) Exchange<PAIRS> ex;
   __shared__ __attribute__((aligned(16))) float stat[2][2][kBN];   // lse (powers of two), D
   __shared__ uint32_t s_bad[PAIRS][2];
-  constexpr int BM = 32 * PAIRS, kSlabs = FINE ? 6 : 4;
+  constexpr int BM = 32 * PAIRS;
   const int head = blockIdx.x % a.H;
   const SeqTile st = find_tile<true>(a, blockIdx.x / a.H, BM);
   if (!st.ok) return;
@@ -977,8 +1003,11 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a)
   f32x16 wide[4] = {}, rope = {};
   const uint32_t side = half ? 0 : kOffY, op = half ? 2 : 0;   // queries and dS, or dO and P
   const float c = a.scale * kLog2e;
+  // Tiles before it have a second term of dS: their first query sees at most kFew keys.
+  // Without a mask all queries see as many, and the first two tiles are taken.
+  const int few = a.causal ? kFew - diff : st.lk <= kFew ? 2 * kBN : 0;
   // P and dS against the tile at r0 (in buffer `buf`), this wavefront's 32 queries of it
-  auto first = [&](uint4 (&mine)[kSlabs], int r0, int buf, int sb) __attribute__((always_inline)) {
+  auto first = [&](auto fine, uint4 (&mine)[4], int r0, int buf, int spare, int sb) __attribute__((always_inline)) {
     if (r0 + kBN <= wlim) return;                  // no query here sees the pair's keys
     const uint8_t* tile = lds + buf * kTile;
     // the units' addresses are formed again in every tile: kept, they cost too many registers
@@ -1019,33 +1048,41 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a)
     for (int j = 0; j < 2; ++j) {
       mine[j] = __builtin_bit_cast(uint4, slab(s, j));
       mine[2 + j] = __builtin_bit_cast(uint4, slab(dp, j));
-      if (FINE) mine[kSlabs - 2 + j] = slab_rest(dp, mine[2 + j], j);
+      if (decltype(fine)::value && r0 < few) rests_of(lds, spare, pair).f[half][j][l] = slab_rest(dp, mine[2 + j], j);
     }
   };
   // the sums over the tile at r0, with the pair's P and dS
   const int begin = q0;
-  auto second = [&](int r0, int buf) __attribute__((always_inline)) {
+  auto second = [&](auto fine, int r0, int buf, int spare) __attribute__((always_inline)) {
     if (r0 < begin || r0 + kBN <= wlim) return;
     const uint8_t* tile = lds + buf * kTile;
     asm volatile("" : "+v"(rp.n), "+v"(rp.r), "+v"(rp.tn), "+v"(rp.tr));
-    bf16x8 f0[4], ds[4], rs[4];
+    bf16x8 f0[4], ds[4];
     pipelined<20, 3>(
         [&](int i) {
           const int j = i / 5, d = i % 5;
           if (d == 0) f0[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][op + (j & 1)][l]);
           if (d == 4) ds[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][2 + (j & 1)][l]);
-          if (FINE && d == 0) rs[j] = __builtin_bit_cast(bf16x8, ex.f[pair][j >> 1][kSlabs - 2 + (j & 1)][l]);
           return d < 4 ? wide_tr(tile + side, rp, j, d) : rope_tr(tile + kOffR, rp, j, half);
         },
         [&](int i, bf16x8 f) {
           if (i % 5 < 4) {
             wide[i % 5] = mfma(f, f0[i / 5], wide[i % 5]);
-            if (FINE && half) wide[i % 5] = mfma(f, rs[i / 5], wide[i % 5]);
           } else {
             rope = mfma(f, ds[i / 5], rope);
-            if (FINE) rope = mfma(f, rs[i / 5], rope);
           }
         });
+    if (decltype(fine)::value && r0 < few) {
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        const bf16x8 rs = __builtin_bit_cast(bf16x8, rests_of(lds, spare, pair).f[j >> 1][j & 1][l]);
+        if (half) {
+#pragma unroll
+          for (int d = 0; d < 4; ++d) wide[d] = mfma(wide_tr(tile, rp, j, d), rs, wide[d]);
+        }
+        rope = mfma(rope_tr(tile + kOffR, rp, j, half), rs, rope);
+      }
+    }
   };
   // The second walk: what queries and gradients that are not finite add to this lane's sums: a
   // bit each where it is plus infinity, and minus infinity, both where it is NaN.
@@ -1083,30 +1120,40 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dkv(AttnArgs a)
   // The sums over the queries that see the workgroup's keys.
   float shift = kShift, unshift = kUnshift;
   auto walk = [&](auto again) __attribute__((always_inline)) {
-    int buf = 0, prev = 2, sb = 0;                 // buffers of this tile and of the one before
-    for (int q0 = begin; q0 < st.lq + kBN; q0 += kBN, sb ^= 1) {
+    int q0 = begin, buf = 0, prev = 2, sb = 0;     // this tile, its buffer and the last tile's
+    // FINE: there may be second terms, of this tile or of the last, which are in the next copy's way
+    auto step = [&](auto fine) __attribute__((always_inline)) {
+      constexpr bool FINE = decltype(fine)::value;
       if (w == 0)
         stat[sb][0][l] = z == -__builtin_inff() ? __builtin_inff() : z * kLog2e - shift;   // no keys: P = 0
       else if (w == 1)
         stat[sb][1][l] = z;
       tile_wait();
       const int next = buf == 2 ? 0 : buf + 1;
+      const bool late = FINE && q0 > begin;
       if (q0 + kBN < st.lq) {
         z = stat_of(q0 + kBN);
-        tile_copy<2 * PAIRS>(cp, x.q, x.q + kNope, x.g, q0 + kBN, st.lq, next);
+        if (!late) tile_copy<2 * PAIRS>(cp, x.q, x.q + kNope, x.g, q0 + kBN, st.lq, next);
       }
-      uint4 mine[kSlabs];                          // this wavefront's P and dS slabs
+      uint4 mine[4];                               // this wavefront's P and dS slabs
       if (decltype(again)::value && q0 > begin && q0 - kBN < cut) cover(q0 - kBN, prev);
-      second(q0 - kBN, prev);
-      if (q0 < st.lq) first(mine, q0, buf, sb);
+      second(fine, q0 - kBN, prev, next);
+      if (FINE) __syncthreads();                   // the last tile and its rests are consumed
+      if (late && q0 + kBN < st.lq) tile_copy<2 * PAIRS>(cp, x.q, x.q + kNope, x.g, q0 + kBN, st.lq, next);
+      if (q0 < st.lq) first(fine, mine, q0, buf, prev, sb);
       __syncthreads();                             // the last tile's operands are consumed
       if (q0 < st.lq && q0 + kBN > wlim) {
 #pragma unroll
-        for (int j = 0; j < kSlabs; ++j) ex.f[pair][half][j][l] = mine[j];
+        for (int j = 0; j < 4; ++j) ex.f[pair][half][j][l] = mine[j];
       }
       prev = buf;
       buf = next;
-    }
+      q0 += kBN;
+      sb ^= 1;
+    };
+    if (!decltype(again)::value && begin < few)
+      while (q0 < st.lq + kBN && q0 < few + kBN) step(std::true_type{});
+    while (q0 < st.lq + kBN) step(std::false_type{});
   };
   auto store = [&](bool write) {
     if (!write) return;
@@ -1301,15 +1348,12 @@ extern "C" int latent_attention_backward(
   if (!aligned16(workspace)) return MXQ_ERR_ALIGN;
   // Workgroups of 64 rows where about that many, T / 64 and half a tile a sequence,
   // still run at once, one a CU (one sequence of 360, 16 heads: 41 us for the three
-  // kernels, without FINE, against 59; 2 of 1000, 8 heads: 74 against 100), or, in one causal
+  // kernels against 59; 2 of 1000, 8 heads: 74 against 100), or, in one causal
   // sequence, whose longest start first, in two turns (5000, 4 heads: 264 against 338;
   // 2048, 16 heads: 149 against 164; 5400, 8 heads, more than that: 446 against 392).
   // Else of 128 (4 of 300, 16 heads: 56 against 60; 8 of 512: 138 against 152).
   const int64_t turn = a.causal && a.B == 1 ? 512 : 256;
-  // With 512 query rows at most dS has its second term, for which the exchange of
-  // 128 rows leaves no room.
-  const bool fine = a.Tq <= 512;
-  const auto few = [&](int64_t T) { return fine || (T / 64 + a.B / 2) * a.H <= turn; };
+  const auto few = [&](int64_t T) { return (T / 64 + a.B / 2) * a.H <= turn; };
   const bool fewq = few(a.Tq), fewk = few(a.Tk);
   uint32_t nq, nk, nr;
   MXQ_TRY(grid_of(a.Tq, fewq ? 64 : 128, a, &nq));
@@ -1327,21 +1371,17 @@ extern "C" int latent_attention_backward(
   a.rope_part = static_cast<float*>(workspace);
   a.delta = a.rope_part + a.H * a.Tk * kRope;
   if (a.Tq > 0) {
-    if (fine)
-      hipLaunchKernelGGL((k_attn_dq<2, true>), dim3(nq), dim3(256), 0, stream, a);
-    else if (fewq)
-      hipLaunchKernelGGL((k_attn_dq<2, false>), dim3(nq), dim3(256), 0, stream, a);
+    if (fewq)
+      hipLaunchKernelGGL(k_attn_dq<2>, dim3(nq), dim3(256), 0, stream, a);
     else
-      hipLaunchKernelGGL((k_attn_dq<4, false>), dim3(nq), dim3(512), 0, stream, a);
+      hipLaunchKernelGGL(k_attn_dq<4>, dim3(nq), dim3(512), 0, stream, a);
     MXQ_TRY(launch_status());
   }
   if (a.Tk > 0) {
-    if (fine)
-      hipLaunchKernelGGL((k_attn_dkv<2, true>), dim3(nk), dim3(256), 0, stream, a);
-    else if (fewk)
-      hipLaunchKernelGGL((k_attn_dkv<2, false>), dim3(nk), dim3(256), 0, stream, a);
+    if (fewk)
+      hipLaunchKernelGGL(k_attn_dkv<2>, dim3(nk), dim3(256), 0, stream, a);
     else
-      hipLaunchKernelGGL((k_attn_dkv<4, false>), dim3(nk), dim3(512), 0, stream, a);
+      hipLaunchKernelGGL(k_attn_dkv<4>, dim3(nk), dim3(512), 0, stream, a);
     MXQ_TRY(launch_status());
     hipLaunchKernelGGL(k_attn_drope, dim3(nr), dim3(kThr), 0, stream, a);
     MXQ_TRY(launch_status());

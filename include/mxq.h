@@ -787,8 +787,9 @@ MXQ_API int latent_attention(const mxq_latent_attn* attn, uint16_t* o, int64_t l
  *   dq = scale * dS K,  dk = scale * dS^T Q,  dv = P^T dO,
  * the rotary key's gradient summed over the heads.  D does not inherit the
  * rounding of o (which only starts it).  FP32 sums; P and dS are
- * rounded to BF16 for the products (dS to two BF16 terms where Tq <= 512);
- * results do not depend on timing (no atomics).  Every row of a sequence is
+ * rounded to BF16 for the products (dS to two BF16 terms where a query sees at
+ * most 64 keys: whole groups of 32 rows for dq and 64 for dk, by their first).  A sequence's
+ * gradient does not depend on what shares the call, or on timing (no atomics).  Every row of a sequence is
  * written, with zeros where nothing reaches it.
  *   attn     : as for latent_attention, with the same values.
  *   o, lse   : latent_attention's results.
