@@ -1346,14 +1346,7 @@ extern "C" int latent_attention_backward(
   if (workspace_bytes < need) return MXQ_ERR_WORKSPACE;
   if (need > 0 && !workspace) return MXQ_ERR_NULL;
   if (!aligned16(workspace)) return MXQ_ERR_ALIGN;
-  // Workgroups of 64 rows where about that many, T / 64 and half a tile a sequence,
-  // still run at once, one a CU (one sequence of 360, 16 heads: 41 us for the three
-  // kernels against 59; 2 of 1000, 8 heads: 74 against 100), or, in one causal
-  // sequence, whose longest start first, in two turns (5000, 4 heads: 264 against 338;
-  // 2048, 16 heads: 149 against 164; 5400, 8 heads, more than that: 446 against 392).
-  // Else of 128 (4 of 300, 16 heads: 56 against 60; 8 of 512: 138 against 152).
-  const int64_t turn = a.causal && a.B == 1 ? 512 : 256;
-  const auto few = [&](int64_t T) { return (T / 64 + a.B / 2) * a.H <= turn; };
+  const auto few = [&](int64_t T) { return latent_backward_rows(T, a.H, a.B, a.causal) == 64; };
   const bool fewq = few(a.Tq), fewk = few(a.Tk);
   uint32_t nq, nk, nr;
   MXQ_TRY(grid_of(a.Tq, fewq ? 64 : 128, a, &nq));
@@ -1387,4 +1380,8 @@ extern "C" int latent_attention_backward(
     MXQ_TRY(launch_status());
   }
   return MXQ_OK;
+}
+
+extern "C" int mxq_latent_backward_rows(int64_t T, int32_t H, int32_t B, int causal) {
+  return T < 0 || H < 1 || B < 1 ? 0 : latent_backward_rows(T, H, B, causal);
 }

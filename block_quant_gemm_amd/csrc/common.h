@@ -76,6 +76,21 @@ inline size_t latent_forward_workspace(int64_t Tq, int64_t Tk, int64_t H, int64_
   return bytes == INT64_MAX ? SIZE_MAX : (size_t)bytes;
 }
 
+// Rows that a workgroup of latent_attention_backward takes, of T query rows or of T key rows
+// in B sequences: 64 where about that many workgroups, T / 64 and half a tile a
+// sequence, still run at once, one a CU (one sequence of 360, 16 heads: 41 us for the three
+// kernels against 59; 2 of 1000, 8 heads: 74 against 100), or, in one causal
+// sequence, whose longest start first, in two turns (5000, 4 heads: 264 against 338;
+// 2048, 16 heads: 149 against 164; 5400, 8 heads, more than that: 446 against 392).
+// Else 128 (4 of 300, 16 heads: 56 against 60; 8 of 512: 138 against 152).  In calls of at
+// most 512 rows and 64 sequences the half tiles are not counted: a second turn of short ones
+// costs less than wavefronts past a sequence's end (forward and backward, 4 of 128, 32
+// heads: 41 against 54; 64 of 8, 16 heads: 74 against 82).
+inline int latent_backward_rows(int64_t T, int64_t H, int64_t B, bool causal) {
+  const int64_t turn = causal && B == 1 ? 512 : 256;
+  return sat_mul(T / 64 + (T > 512 || B > 64 ? B / 2 : 0), H) <= turn ? 64 : 128;
+}
+
 // Workspace of latent_attention_backward: the rotary key's gradient of each
 // head, and D of each row, both FP32.  SIZE_MAX when it does not fit.
 inline size_t latent_backward_workspace(int64_t Tq, int64_t Tk, int64_t H) {

@@ -111,6 +111,7 @@ _SIGS = {
                                                  _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64,
                                                  _i64, _p, _i64, _p, _i64, _i64, _p, _sz, _p]),
     "mxq_workspace_size": (_sz, [ctypes.c_int, _i64, _i64, _i64, _i64]),
+    "mxq_latent_backward_rows": (ctypes.c_int, [_i64, _i32, _i32, ctypes.c_int]),
     "mxq_validate_offsets": (ctypes.c_int, [_p, _i32, _i64, _p]),
 }
 
@@ -303,6 +304,12 @@ def mx_quantize_dual_batch(items):
 
 def workspace_size(op, n, a1=0, a2=0, a3=0):
     return int(load().mxq_workspace_size(op, n, a1, a2, a3))
+
+
+def latent_backward_rows(T, H, B=1, causal=True):
+    """Rows that a workgroup of latent_attention_backward takes, 64 or 128, of T query
+    rows (for dq) or T key rows (for dk and dv) in B sequences."""
+    return int(load().mxq_latent_backward_rows(T, H, B, int(causal)))
 
 
 def fp8_quantize_per_tensor(x, q=None, scale=None, workspace=None):

@@ -829,6 +829,11 @@ enum {
 /* Workspace bytes an operation needs (0 if none). */
 MXQ_API size_t mxq_workspace_size(int op, int64_t n, int64_t a1, int64_t a2, int64_t a3);
 
+/* Rows that one workgroup of latent_attention_backward takes, 64 or 128, of T query rows
+ * (for dq) or T key rows (for dk and dv) in B sequences (1 without offsets): for
+ * tests and profiles.  Results do not depend on it.  0 for sizes that no call has. */
+MXQ_API int mxq_latent_backward_rows(int64_t T, int32_t H, int32_t B, int causal);
+
 /*
  * Debug check of device-side group offsets: copies them to the host (this
  * call synchronizes the stream) and verifies offsets[0] == 0, non-decreasing,
