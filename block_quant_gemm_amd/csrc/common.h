@@ -230,7 +230,8 @@ __device__ __forceinline__ float e8m0_f32(uint32_t c) { return __builtin_bit_cas
 
 // Eight E4M3 codes (bytes of w0, then w1) times 2^(c - 127) as BF16, element
 // i from byte i.  Exact while the product is a normal or subnormal BF16
-// value with its bits intact: scale codes 3..246.
+// value with its bits intact: scale codes 3..246.  Under the others the product is
+// rounded to nearest even, as the same product formed in FP32 is (all codes under all scales compared).
 __device__ __forceinline__ bf16x8 widen8_bf16(uint32_t w0, uint32_t w1, float s) {
   typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
   const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, false);

@@ -693,7 +693,8 @@ MXQ_API int mx_latent_cache_read(const mxq_latent_cache* cache, const int64_t* s
  * over the tokens t < n - (S - 1 - s): the S query tokens are the request's
  * last S tokens, already in the cache, and each sees itself and what precedes
  * it.  A row that sees nothing gets zeros and minus infinity.
- * c[t] is the cached block's value, widened exactly; the products are exact,
+ * c[t] is what mx_latent_cache_read gives for the slot (the block's value, exact
+ * in BF16 but for the smallest scale codes, 0 to 2); the products are exact,
  * sums, maxima and totals are FP32, and the probabilities are rounded to BF16 for
  * the second product.  Results do not depend on timing (no atomics).
  *   q          : device, BF16 [B, S, H, 576], strides ldq_seq, ldq_tok,
