@@ -154,13 +154,13 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _raw_stream(t):
-    """The handle of the current stream, which has to be on t's GPU, without the
-    stream object around it."""
-    dev = torch._C._cuda_getDevice()
-    if t.get_device() != dev:
-        raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{dev}")
-    return torch._C._cuda_getCurrentRawStream(dev)
+def _current_gpu():
+    return torch._C._cuda_getDevice()
+
+
+def _raw_stream(gpu):
+    """The handle of that GPU's current stream, without the stream object around it."""
+    return torch._C._cuda_getCurrentRawStream(gpu)
 
 
 def _bf16_bits(x):
@@ -722,12 +722,12 @@ _ATTN_STRUCT = struct.Struct("PqqPqqPqPqqPPqqiifi")       # mxq_latent_attn of m
 _BF16, _U8, _I64, _F32 = torch.bfloat16, torch.uint8, torch.int64, torch.float32
 
 
-def _rows(name, t, dtype, shape):
-    """The strides of t.  Raises unless t is in GPU memory, has this dtype and shape,
+def _rows(gpu, name, t, dtype, shape):
+    """The strides of t.  Raises unless t is on GPU number `gpu`, has this dtype and shape,
     and adjacent values along its last dimension: the C calls take addresses and
-    strides and can see neither a host address nor a tensor that is too small."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a tensor on the GPU, got {t.device}")
+    strides and can see neither whose address it is nor a tensor that is too small."""
+    if t.get_device() != gpu:
+        raise ValueError(f"{name}: expected a tensor on the current GPU, cuda:{gpu}, got {t.device}")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -751,12 +751,12 @@ def latent_cache(slots, device="cuda"):
             torch.zeros((slots, ROPE_DIM), dtype=torch.bfloat16, device=device))
 
 
-def _cache_arg(cache):
+def _cache_arg(gpu, cache):
     codes, scales, k_rope = cache
     n = codes.shape[0]
-    sc = _rows("cache codes", codes, _U8, (n, 512))
-    ss = _rows("cache scales", scales, _U8, (n, 16))
-    sr = _rows("cache k_rope", k_rope, _BF16, (n, 64))
+    sc = _rows(gpu, "cache codes", codes, _U8, (n, 512))
+    ss = _rows(gpu, "cache scales", scales, _U8, (n, 16))
+    sr = _rows(gpu, "cache k_rope", k_rope, _BF16, (n, 64))
     return _CACHE_STRUCT.pack(codes.data_ptr(), sc[0], scales.data_ptr(), ss[0],
                               k_rope.data_ptr(), sr[0], n)
 
@@ -765,12 +765,13 @@ def mx_latent_cache_write(c, k_rope, slots, cache):
     """Quantizes T tokens into the cache: slot slots[t] (int64, device; outside
     the cache: skipped) gets c[t] (BF16 [T, 512]) as MX codes and scales, and
     k_rope[t] (BF16 [T, 64]).  Returns the cache."""
-    T = c.shape[0]
-    sc = _rows("c", c, _BF16, (T, 512))
-    sr = _rows("k_rope", k_rope, _BF16, (T, 64))
-    _rows("slots", slots, _I64, (T,))
+    T, gpu = c.shape[0], _current_gpu()
+    sc = _rows(gpu, "c", c, _BF16, (T, 512))
+    sr = _rows(gpu, "k_rope", k_rope, _BF16, (T, 64))
+    _rows(gpu, "slots", slots, _I64, (T,))
+    arg = _cache_arg(gpu, cache)
     st = load().mx_latent_cache_write(c.data_ptr(), sc[0], k_rope.data_ptr(), sr[0],
-                                      slots.data_ptr(), T, _cache_arg(cache), _raw_stream(c))
+                                      slots.data_ptr(), T, arg, _raw_stream(gpu))
     if st:
         _check(st)
     return cache
@@ -779,16 +780,17 @@ def mx_latent_cache_write(c, k_rope, slots, cache):
 def mx_latent_cache_read(cache, slots, c=None, k_rope=None):
     """The tokens in the slots `slots` (int64 [T], device; outside the cache:
     zeros).  Returns (c BF16 [T, 512], k_rope BF16 [T, 64])."""
-    T = slots.shape[0]
-    _rows("slots", slots, _I64, (T,))
+    T, gpu = slots.shape[0], _current_gpu()
+    _rows(gpu, "slots", slots, _I64, (T,))
     if c is None:
         c = cache[2].new_empty((T, 512))
     if k_rope is None:
         k_rope = cache[2].new_empty((T, 64))
-    sc = _rows("c", c, _BF16, (T, 512))
-    sr = _rows("k_rope", k_rope, _BF16, (T, 64))
-    st = load().mx_latent_cache_read(_cache_arg(cache), slots.data_ptr(), T, c.data_ptr(), sc[0],
-                                     k_rope.data_ptr(), sr[0], _raw_stream(slots))
+    sc = _rows(gpu, "c", c, _BF16, (T, 512))
+    sr = _rows(gpu, "k_rope", k_rope, _BF16, (T, 64))
+    arg = _cache_arg(gpu, cache)
+    st = load().mx_latent_cache_read(arg, slots.data_ptr(), T, c.data_ptr(), sc[0],
+                                     k_rope.data_ptr(), sr[0], _raw_stream(gpu))
     if st:
         _check(st)
     return c, k_rope
@@ -803,46 +805,48 @@ def mx_latent_decode(q, cache, pages, lens, page_size, max_len, scale, o=None, l
     [B] cached tokens, the S query tokens among them (the last); max_len: host
     bound of lens.  Returns (o BF16 [B, S, H, 512], lse float32 [B, S, H])."""
     B, S, H, _ = q.shape
-    sq = _rows("q", q, _BF16, (B, S, H, 576))
+    gpu = _current_gpu()
+    sq = _rows(gpu, "q", q, _BF16, (B, S, H, 576))
     width = pages.shape[-1]
-    sp = _rows("pages", pages, torch.int32, (B, width))
-    _rows("lens", lens, _I64, (B,))
+    sp = _rows(gpu, "pages", pages, torch.int32, (B, width))
+    _rows(gpu, "lens", lens, _I64, (B,))
     if o is None:
         o = q.new_empty((B, S, H, 512))
     if lse is None:
         lse = q.new_empty((B, S, H), dtype=_F32)
-    so = _rows("o", o, _BF16, (B, S, H, 512))
-    _rows("lse", lse, _F32, (B, S, H))
+    so = _rows(gpu, "o", o, _BF16, (B, S, H, 512))
+    _rows(gpu, "lse", lse, _F32, (B, S, H))
     if not lse.is_contiguous():
         raise ValueError("lse: has to be contiguous")
     if workspace is None:
         workspace = q.new_empty(_latent_workspace(WS_LATENT_DECODE, B, S, H, max_len), dtype=_U8)
-    _rows("workspace", workspace, _U8, (workspace.numel(),))
+    _rows(gpu, "workspace", workspace, _U8, (workspace.numel(),))
+    arg = _cache_arg(gpu, cache)
     st = load().mx_latent_decode(
-        q.data_ptr(), sq[0], sq[1], sq[2], _cache_arg(cache), pages.data_ptr(), sp[0], width,
+        q.data_ptr(), sq[0], sq[1], sq[2], arg, pages.data_ptr(), sp[0], width,
         page_size, lens.data_ptr(), B, S, H, max_len, scale, o.data_ptr(), so[0], so[1], so[2],
-        lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(q))
+        lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(gpu))
     if st:
         _check(st)
     return o, lse
 
 
-def _attn_arg(q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal):
+def _attn_arg(gpu, q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal):
     Tq, H, _ = q.shape
     Tk = k_nope.shape[0]
-    sq = _rows("q", q, _BF16, (Tq, H, 192))
-    sk = _rows("k_nope", k_nope, _BF16, (Tk, H, 128))
-    sr = _rows("k_rope", k_rope, _BF16, (Tk, 64))
-    sv = _rows("v", v, _BF16, (Tk, H, 128))
+    sq = _rows(gpu, "q", q, _BF16, (Tq, H, 192))
+    sk = _rows(gpu, "k_nope", k_nope, _BF16, (Tk, H, 128))
+    sr = _rows(gpu, "k_rope", k_rope, _BF16, (Tk, 64))
+    sv = _rows(gpu, "v", v, _BF16, (Tk, H, 128))
     if offsets_k is None:
         offsets_k = offsets_q
     B = oq = ok = 0
     if offsets_q is not None:
         B = offsets_q.shape[0] - 1
-        _rows("offsets_q", offsets_q, _I64, (B + 1,))
+        _rows(gpu, "offsets_q", offsets_q, _I64, (B + 1,))
         oq = offsets_q.data_ptr()
     if offsets_k is not None:
-        _rows("offsets_k", offsets_k, _I64, (B + 1,))
+        _rows(gpu, "offsets_k", offsets_k, _I64, (B + 1,))
         ok = offsets_k.data_ptr()
     if scale is None:
         scale = (NOPE_DIM + ROPE_DIM) ** -0.5
@@ -862,13 +866,14 @@ def latent_attention(q, k_nope, k_rope, v, offsets_q=None, offsets_k=None, scale
     offsets_q; both None: one sequence); scale defaults to 192 ** -0.5.
     Returns (o BF16 [Tq, H, 128], lse float32 [H, Tq])."""
     Tq, H, _ = q.shape
-    arg = _attn_arg(q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal)
+    gpu = _current_gpu()
+    arg = _attn_arg(gpu, q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal)
     if o is None:
         o = q.new_empty((Tq, H, 128))
     if lse is None:
         lse = q.new_empty((H, Tq), dtype=_F32)
-    so = _rows("o", o, _BF16, (Tq, H, 128))
-    sl = _rows("lse", lse, _F32, (H, Tq))
+    so = _rows(gpu, "o", o, _BF16, (Tq, H, 128))
+    sl = _rows(gpu, "lse", lse, _F32, (H, Tq))
     ws, size = 0, 0
     if workspace is None:
         B = 1 if offsets_q is None else offsets_q.shape[0] - 1
@@ -877,10 +882,10 @@ def latent_attention(q, k_nope, k_rope, v, offsets_q=None, offsets_k=None, scale
             workspace = q.new_empty(size, dtype=_U8)
     if workspace is not None:
         size = workspace.numel()
-        _rows("workspace", workspace, _U8, (size,))
+        _rows(gpu, "workspace", workspace, _U8, (size,))
         ws = workspace.data_ptr()
     st = load().latent_attention(arg, o.data_ptr(), so[0], so[1], lse.data_ptr(), sl[0], ws, size,
-                                 _raw_stream(q))
+                                 _raw_stream(gpu))
     if st:
         _check(st)
     return o, lse
@@ -895,11 +900,11 @@ def latent_attention_backward(dout, q, k_nope, k_rope, v, o, lse, offsets_q=None
     Returns (dq, dk_nope, dk_rope, dv), shaped as their operands; dk_nope and dv
     are the halves of one [Tk, H, 256] buffer unless they are given."""
     Tq, H, _ = q.shape
-    Tk = k_nope.shape[0]
-    arg = _attn_arg(q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal)
-    sg = _rows("dout", dout, _BF16, (Tq, H, 128))
-    so = _rows("o", o, _BF16, (Tq, H, 128))
-    sl = _rows("lse", lse, _F32, (H, Tq))
+    Tk, gpu = k_nope.shape[0], _current_gpu()
+    arg = _attn_arg(gpu, q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal)
+    sg = _rows(gpu, "dout", dout, _BF16, (Tq, H, 128))
+    so = _rows(gpu, "o", o, _BF16, (Tq, H, 128))
+    sl = _rows(gpu, "lse", lse, _F32, (H, Tq))
     if dq is None:
         dq = q.new_empty((Tq, H, 192))
     if dk_nope is None or dv is None:
@@ -908,18 +913,18 @@ def latent_attention_backward(dout, q, k_nope, k_rope, v, o, lse, offsets_q=None
         dv = dkv[..., 128:] if dv is None else dv
     if dk_rope is None:
         dk_rope = q.new_empty((Tk, 64))
-    sdq = _rows("dq", dq, _BF16, (Tq, H, 192))
-    sdk = _rows("dk_nope", dk_nope, _BF16, (Tk, H, 128))
-    sdr = _rows("dk_rope", dk_rope, _BF16, (Tk, 64))
-    sdv = _rows("dv", dv, _BF16, (Tk, H, 128))
+    sdq = _rows(gpu, "dq", dq, _BF16, (Tq, H, 192))
+    sdk = _rows(gpu, "dk_nope", dk_nope, _BF16, (Tk, H, 128))
+    sdr = _rows(gpu, "dk_rope", dk_rope, _BF16, (Tk, 64))
+    sdv = _rows(gpu, "dv", dv, _BF16, (Tk, H, 128))
     if workspace is None:
         workspace = q.new_empty(_latent_workspace(WS_LATENT_BACKWARD, Tq, Tk, H, 0), dtype=_U8)
-    _rows("workspace", workspace, _U8, (workspace.numel(),))
+    _rows(gpu, "workspace", workspace, _U8, (workspace.numel(),))
     st = load().latent_attention_backward(
         arg, o.data_ptr(), so[0], so[1], lse.data_ptr(), sl[0], dout.data_ptr(), sg[0], sg[1],
         dq.data_ptr(), sdq[0], sdq[1], dk_nope.data_ptr(), sdk[0], sdk[1], dk_rope.data_ptr(),
         sdr[0], dv.data_ptr(), sdv[0], sdv[1], workspace.data_ptr(), workspace.numel(),
-        _raw_stream(q))
+        _raw_stream(gpu))
     if st:
         _check(st)
     return dq, dk_nope, dk_rope, dv
