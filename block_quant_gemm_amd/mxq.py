@@ -738,6 +738,10 @@ def _rows(gpu, name, t, dtype, shape):
     return s
 
 
+# A dimension of one may have any stride, which the C calls, that check strides alone, could
+# refuse: where the callers below pass one on, they pass the row's length in its place.
+
+
 @functools.lru_cache(maxsize=1024)
 def _latent_workspace(op, n, a1, a2, a3):
     return workspace_size(op, n, a1, a2, a3)
@@ -757,6 +761,8 @@ def _cache_arg(gpu, cache):
     sc = _rows(gpu, "cache codes", codes, _U8, (n, 512))
     ss = _rows(gpu, "cache scales", scales, _U8, (n, 16))
     sr = _rows(gpu, "cache k_rope", k_rope, _BF16, (n, 64))
+    if n < 2:
+        sc, ss, sr = (512,), (16,), (64,)
     return _CACHE_STRUCT.pack(codes.data_ptr(), sc[0], scales.data_ptr(), ss[0],
                               k_rope.data_ptr(), sr[0], n)
 
@@ -769,6 +775,8 @@ def mx_latent_cache_write(c, k_rope, slots, cache):
     sc = _rows(gpu, "c", c, _BF16, (T, 512))
     sr = _rows(gpu, "k_rope", k_rope, _BF16, (T, 64))
     _rows(gpu, "slots", slots, _I64, (T,))
+    if T < 2:
+        sc, sr = (512,), (64,)
     arg = _cache_arg(gpu, cache)
     st = load().mx_latent_cache_write(c.data_ptr(), sc[0], k_rope.data_ptr(), sr[0],
                                       slots.data_ptr(), T, arg, _raw_stream(gpu))
@@ -788,6 +796,8 @@ def mx_latent_cache_read(cache, slots, c=None, k_rope=None):
         k_rope = cache[2].new_empty((T, 64))
     sc = _rows(gpu, "c", c, _BF16, (T, 512))
     sr = _rows(gpu, "k_rope", k_rope, _BF16, (T, 64))
+    if T < 2:
+        sc, sr = (512,), (64,)
     arg = _cache_arg(gpu, cache)
     st = load().mx_latent_cache_read(arg, slots.data_ptr(), T, c.data_ptr(), sc[0],
                                      k_rope.data_ptr(), sr[0], _raw_stream(gpu))
@@ -823,12 +833,19 @@ def mx_latent_decode(q, cache, pages, lens, page_size, max_len, scale, o=None, l
     _rows(gpu, "workspace", workspace, _U8, (workspace.numel(),))
     arg = _cache_arg(gpu, cache)
     st = load().mx_latent_decode(
-        q.data_ptr(), sq[0], sq[1], sq[2], arg, pages.data_ptr(), sp[0], width,
-        page_size, lens.data_ptr(), B, S, H, max_len, scale, o.data_ptr(), so[0], so[1], so[2],
+        q.data_ptr(), sq[0] if B > 1 else 576, sq[1] if S > 1 else 576, sq[2] if H > 1 else 576, arg,
+        pages.data_ptr(), sp[0] if B > 1 else width, width,
+        page_size, lens.data_ptr(), B, S, H, max_len, scale, o.data_ptr(),
+        so[0] if B > 1 else 512, so[1] if S > 1 else 512, so[2] if H > 1 else 512,
         lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(gpu))
     if st:
         _check(st)
     return o, lse
+
+
+def _steps(s, rows, heads, width):
+    """Row and head strides to pass on."""
+    return s[0] if rows > 1 else width, s[1] if heads > 1 else width
 
 
 def _attn_arg(gpu, q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal):
@@ -850,6 +867,8 @@ def _attn_arg(gpu, q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal):
         ok = offsets_k.data_ptr()
     if scale is None:
         scale = (NOPE_DIM + ROPE_DIM) ** -0.5
+    if Tq == 1 or Tk == 1 or H == 1:
+        sq, sk, sr, sv = _steps(sq, Tq, H, 192), _steps(sk, Tk, H, 128), _steps(sr, Tk, 2, 64), _steps(sv, Tk, H, 128)
     return _ATTN_STRUCT.pack(q.data_ptr(), sq[0], sq[1], k_nope.data_ptr(), sk[0], sk[1],
                              k_rope.data_ptr(), sr[0], v.data_ptr(), sv[0], sv[1], oq, ok, Tq, Tk,
                              B, H, scale, int(causal))
@@ -874,6 +893,8 @@ def latent_attention(q, k_nope, k_rope, v, offsets_q=None, offsets_k=None, scale
         lse = q.new_empty((H, Tq), dtype=_F32)
     so = _rows(gpu, "o", o, _BF16, (Tq, H, 128))
     sl = _rows(gpu, "lse", lse, _F32, (H, Tq))
+    if Tq == 1 or H == 1:
+        so, sl = _steps(so, Tq, H, 128), _steps(sl, H, 2, Tq)
     ws, size = 0, 0
     if workspace is None:
         B = 1 if offsets_q is None else offsets_q.shape[0] - 1
@@ -917,6 +938,9 @@ def latent_attention_backward(dout, q, k_nope, k_rope, v, o, lse, offsets_q=None
     sdk = _rows(gpu, "dk_nope", dk_nope, _BF16, (Tk, H, 128))
     sdr = _rows(gpu, "dk_rope", dk_rope, _BF16, (Tk, 64))
     sdv = _rows(gpu, "dv", dv, _BF16, (Tk, H, 128))
+    if Tq == 1 or Tk == 1 or H == 1:
+        so, sl, sg, sdq = _steps(so, Tq, H, 128), _steps(sl, H, 2, Tq), _steps(sg, Tq, H, 128), _steps(sdq, Tq, H, 192)
+        sdk, sdr, sdv = _steps(sdk, Tk, H, 128), _steps(sdr, Tk, 2, 64), _steps(sdv, Tk, H, 128)
     if workspace is None:
         workspace = q.new_empty(_latent_workspace(WS_LATENT_BACKWARD, Tq, Tk, H, 0), dtype=_U8)
     _rows(gpu, "workspace", workspace, _U8, (workspace.numel(),))
