@@ -10,6 +10,9 @@ ROOT = os.path.dirname(PKG)
 SOURCES = ["csrc/quant.hip", "csrc/gemm.hip", "csrc/latent.hip", "csrc/attention.hip",
            "csrc/api.hip"]
 LIB = os.path.join(PKG, "libmxq.so")
+FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+         # keep FP32 arithmetic off the packed-FP32 instructions
+         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 # Loop-carried accumulators stay whole vectors: split into scalars, they are
 # copied between the two halves of the register file in every iteration.
 EXTRA_FLAGS = {s: ["-mllvm", "-amdgpu-codegenprepare-break-large-phis=0"]
@@ -17,9 +20,9 @@ EXTRA_FLAGS = {s: ["-mllvm", "-amdgpu-codegenprepare-break-large-phis=0"]
 
 
 def source_digest():
-    """SHA-256 of the kernel sources and the C header (identifies a build)."""
+    """SHA-256 of the kernel sources, the C header and the compiler's flags (identifies a build)."""
     import hashlib
-    h = hashlib.sha256()
+    h = hashlib.sha256(repr((FLAGS, sorted(EXTRA_FLAGS.items()))).encode())
     for rel in SOURCES + ["csrc/common.h"]:
         with open(os.path.join(PKG, rel), "rb") as f:
             h.update(f.read())
@@ -38,10 +41,7 @@ def hipcc():
 def build(verbose=False):
     """Compile every source for gfx950 into block_quant_gemm_amd/libmxq.so."""
     tmp = LIB + ".tmp"
-    common = [hipcc(), "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",
-              "-I" + os.path.join(ROOT, "include"),
-              # keep FP32 arithmetic off the packed-FP32 instructions
-              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
+    common = [hipcc(), *FLAGS, "-I" + os.path.join(ROOT, "include")]
     with tempfile.TemporaryDirectory() as d:
         objs = [os.path.join(d, os.path.basename(s) + ".o") for s in SOURCES]
         cmds = [common + EXTRA_FLAGS.get(s, []) + ["-c", os.path.join(PKG, s), "-o", o]
