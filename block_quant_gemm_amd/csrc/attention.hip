@@ -1253,7 +1253,7 @@ int check_attn(const mxq_latent_attn* d, AttnArgs* a) {
   if (d->H < 1 || d->H > 65536 || d->Tq < 0 || d->Tk < 0 || d->Tq > kMaxRows || d->Tk > kMaxRows)
     return MXQ_ERR_SHAPE;
   if (d->causal != 0 && d->causal != 1) return MXQ_ERR_ARG;
-  if (!(d->scale > 0.0f) || d->scale > 3.4e38f) return MXQ_ERR_ARG;
+  if (!(d->scale > 0.0f && d->scale <= kMaxScale)) return MXQ_ERR_ARG;
   if ((d->offsets_q == nullptr) != (d->offsets_k == nullptr)) return MXQ_ERR_NULL;
   if (d->offsets_q && (d->B < 1 || d->B > 65536)) return MXQ_ERR_SHAPE;
   MXQ_TRY(check_op(d->q, d->Tq, d->ldq, d->ldq_head, kQk));

@@ -20,6 +20,9 @@ inline int64_t sat_add(int64_t a, int64_t b) {
   return __builtin_add_overflow(a, b, &r) ? INT64_MAX : r;
 }
 
+// Largest scale of the logits: with it, scale * log2(e), the exponents' factor, is finite.
+constexpr float kMaxScale = 2e38f;
+
 // Tokens of a tile of the latent cache's absorbed attention.
 #define MXQ_LATENT_TILE 64
 

@@ -720,7 +720,7 @@ extern "C" int mx_latent_decode(const uint16_t* q, int64_t ldq_seq, int64_t ldq_
   if (sat_mul(S, H) > 65536 || sat_mul(B, sat_mul(S, H)) >= (INT64_C(1) << 24)) return MXQ_ERR_SHAPE;
   // tokens are counted in 32 bits, and every sequence's pages must be in the table
   if (max_len > (INT64_C(1) << 30) || max_len > sat_mul(max_pages, page_size)) return MXQ_ERR_SHAPE;
-  if (!(scale > 0.0f) || scale > 3.4e38f) return MXQ_ERR_ARG;
+  if (!(scale > 0.0f && scale <= kMaxScale)) return MXQ_ERR_ARG;
   if (B == 0) return MXQ_OK;
   if (ldq_head < kLat + kRope || ldq_tok < kLat + kRope || ldq_seq < kLat + kRope ||
       ldo_head < kLat || ldo_tok < kLat || ldo_seq < kLat || ld_pages < max_pages)

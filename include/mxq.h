@@ -708,7 +708,7 @@ MXQ_API int mx_latent_cache_read(const mxq_latent_cache* cache, const int64_t* s
  *   lens       : device int64 [B].
  *   max_len    : host bound of the lengths, <= max_pages * page_size and 2^30;
  *                it sets the split of the work, longer requests are cut to it.
- *   scale      : > 0, finite.
+ *   scale      : > 0, at most 2e38.
  *   o          : device, BF16 [B, S, H, 512], strides ldo_* elements (each
  *                >= 512, % 4 == 0), 8-byte aligned.
  *   lse        : device float [B, S, H], contiguous.
@@ -739,7 +739,7 @@ MXQ_API int mx_latent_decode(const uint16_t* q, int64_t ldq_seq, int64_t ldq_tok
  *             buffers.
  *   H       : 1 .. 65536.  B: 1 .. 65536.  Tq, Tk: at most 2^27, and
  *             (Tq / 128 + B) * H and (Tk / 128 + B) * H less than 2^23.
- *   scale   : > 0, finite.
+ *   scale   : > 0, at most 2e38.
  *   causal  : 0, or 1: query i of a sequence with lq queries and lk keys sees
  *             keys j <= i + lk - lq (the queries are the last lq tokens).
  * Strides are multiples of 8 and pointers 16-byte aligned.

@@ -29,3 +29,15 @@ def test_documented_sizes_are_taken(host_only_lib, Tq, Tk, B, H):  # noqa: F811
 @pytest.mark.parametrize("Tq,Tk,B,H", [(100, 1 << 27, 1, 8), (1 << 27, 100, 1, 8), (100, 100, 8192, 1024)])
 def test_larger_ones_are_refused(host_only_lib, Tq, Tk, B, H):  # noqa: F811
     assert _backward(host_only_lib, Tq, Tk, B, H) == SHAPE
+
+
+@pytest.mark.parametrize("scale,want", [(2e38, HIP), (2.4e38, 4), (3.4e38, 4), (1e-44, HIP)])
+def test_scales_whose_power_of_two_form_overflows_are_refused(host_only_lib, scale, want):  # noqa: F811
+    """The exponentials are taken of scale * log2(e) times the products."""
+    attn = mxq._ATTN_STRUCT.pack(P, 384, 192, P, 256, 128, P, 64, P, 256, 128, P, P, 10, 10, 1, 2, scale, 1)
+    assert host_only_lib.latent_attention(attn, P, 256, 128, P, 10, P, BIG, None) == want
+    assert host_only_lib.latent_attention_backward(attn, P, 256, 128, P, 10, P, 256, 128, P, 384, 192, P, 256, 128, P, 64,
+                                                   P, 256, 128, P, BIG, None) == want
+    cache = mxq._CACHE_STRUCT.pack(P, 512, P, 16, P, 64, 64)
+    assert host_only_lib.mx_latent_decode(P, 1152, 1152, 576, cache, P, 4, 4, 8, P, 2, 1, 2, 32, scale, P, 1024, 1024, 512,
+                                          P, P, BIG, None) == want
