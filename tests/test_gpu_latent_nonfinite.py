@@ -11,7 +11,10 @@ import pytest
 import torch
 
 from block_quant_gemm_amd import mxq
-from tests.gpu_helpers import say
+from oracle import codec, latent
+from tests.gpu_helpers import host, say
+from tests.test_gpu_latent_attention import SCALE, _f64, _run, _with_empty
+from tests.test_gpu_latent_attention import _inputs as oracle_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -271,3 +274,41 @@ def test_decode_with_nan_everywhere():
     o, lse = mxq.mx_latent_decode(**d)
     assert torch.isnan(o).all() and torch.isnan(lse).all()
     _in_time(lambda: mxq.mx_latent_decode(**d), lambda: mxq.mx_latent_decode(**sound), "decode with NaN everywhere")
+
+
+@pytest.mark.parametrize("rows", [64, 128])
+@pytest.mark.parametrize("seed", range(16))
+def test_scattered_broken_values_against_the_oracle(seed, rows):
+    """NaN and infinities at a few places of all operands, odd lengths: exactly the outputs that the
+    definition makes not finite are not, of o and dv in kind, and the others are within the bounds."""
+    rng = np.random.default_rng(seed)
+    lq, lk, H = [int(n) for n in rng.integers(2, 230, 3)], [int(n) for n in rng.integers(2, 230, 3)], 2
+    say(f"latent attention, scattered broken values, lq={lq} lk={lk}, {rows}-row workgroups")
+    d = oracle_inputs(lq, lk, H, 300 + seed)
+    for b in range(3):
+        for name, n in (("q", lq[b]), ("do", lq[b]), ("kv", lk[b]), ("kr", lk[b])):
+            first = int(d["oq" if name in ("q", "do") else "ok"][b])
+            for _ in range(rng.integers(0, 3)):
+                what = (0x7FC0, 0x7F80, 0xFF80)[rng.integers(0, 3)]
+                # a sequence's first key stays sound, so that no row's logits are all minus infinity
+                r = first + int(rng.integers(n // 2 if n > 1 else 0, n)) if name in ("q", "do") else \
+                    first + int(rng.integers(max(1, n // 2), n))
+                if name == "kr":
+                    d[name][r, rng.integers(0, 64)] = what
+                else:
+                    d[name][r, rng.integers(0, H), rng.integers(0, d[name].shape[2])] = what
+    with np.errstate(all="ignore"):
+        ref = latent.attention_backward(codec.bf16_bits_to_f64(d["do"]), *_f64(d), d["oq"], d["ok"], SCALE, True)
+    run = d if rows == 64 else _with_empty(d)
+    for n in ("q", "kr"):
+        assert mxq.latent_backward_rows(d[n].shape[0], H, len(run["oq"]) - 1) == rows
+    got = _run(run, True)
+    for name, (val, err) in ref.items():
+        g = host(got[name].contiguous())
+        g = g.astype(np.float64) if name == "lse" else codec.bf16_bits_to_f64(g)
+        ok = np.isfinite(val)
+        if name in ("o", "dv", "lse"):
+            assert np.array_equal(g[~ok], val[~ok], equal_nan=True), name
+        assert np.array_equal(np.isfinite(g), ok), (name, int((np.isfinite(g) != ok).sum()))
+        tol = np.where(np.isnan(err), np.inf, err)[ok]
+        assert (np.abs(g[ok] - val[ok]) <= tol).all(), name
