@@ -691,8 +691,8 @@ __global__ __launch_bounds__(kThr) void k_attn_join(AttnArgs a) {
 // PAIRS = 2, 64 rows and a wavefront a SIMD: shorter steps, for calls that leave
 // CUs idle otherwise.
 //
-// 4 sequences of 4096, 16 heads, causal: dQ 727 to 773 us and dK and dV 736 to 787
-// by machine, at best 1.04 and 0.93 PFLOP/s of the 11 and 10 products of 64 columns
+// 4 sequences of 4096, 16 heads, causal: dQ 720 to 759 us and dK and dV 709 to 750
+// by machine, at best 1.05 and 0.97 PFLOP/s of the 11 and 10 products of 64 columns
 // that they form a pair (13 in all are the least; S and dP are formed by both, and
 // P K makes D exact).  Bound by
 // the matrix unit and the chain before P and dS: without the sums over the tiles

@@ -144,10 +144,11 @@ __global__ __launch_bounds__(kThr) void k_latent_read(Cache k, const int64_t* __
 //
 // 16 rows (77 KB of LDS, two workgroups a CU: one's loads run beside the other's
 // products) are bound by the cache's bytes when requests are long: 6 of 60 to 120
-// thousand tokens, 16 heads, 71 us, 5.0 TB/s, what a large copy reaches.  96
+// thousand tokens, 16 heads, 73 to 76 us by machine (71 at best), 4.7 to 4.9 TB/s; a large copy
+// reaches 5.0.  96
 // requests of 1 to 6000 tokens take 20 us in three tiles a run, 8 of them the chain
 // of lengths, page, slot and first tile.  32 and 64 rows take eight wavefronts,
-// one workgroup a CU.  24 requests of 300 to 4200 tokens with 128 rows: 33.6 us, 14
+// one workgroup a CU.  24 requests of 300 to 4200 tokens with 128 rows: 32 us, 14
 // of them the setup and the parts' stores (25 MB), then 2.9 us a tile, of which
 // LDS is busy for 1.9 (the keys once a wavefront, and the queries that registers
 // do not hold; at R = 4 they do not fit in any split tried).

@@ -883,7 +883,9 @@ def latent_attention(q, k_nope, k_rope, v, offsets_q=None, offsets_k=None, scale
     [Tk, H, 256] projection); k_rope BF16 [Tk, 64], shared by the heads;
     offsets_q, offsets_k int64 [B+1] on the device (offsets_k defaults to
     offsets_q; both None: one sequence); scale defaults to 192 ** -0.5.
-    Returns (o BF16 [Tq, H, 128], lse float32 [H, Tq])."""
+    Returns (o BF16 [Tq, H, 128], lse float32 [H, Tq]).  Rows outside every
+    sequence (before the first offset or after the last) are left as they are, which
+    in buffers that this call allocates is undefined."""
     Tq, H, _ = q.shape
     gpu = _current_gpu()
     arg = _attn_arg(gpu, q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal)
@@ -919,7 +921,8 @@ def latent_attention_backward(dout, q, k_nope, k_rope, v, o, lse, offsets_q=None
 
     The other arguments are the forward call's and its results o and lse.
     Returns (dq, dk_nope, dk_rope, dv), shaped as their operands; dk_nope and dv
-    are the halves of one [Tk, H, 256] buffer unless they are given."""
+    are the halves of one [Tk, H, 256] buffer unless they are given.  Rows outside every
+    sequence are undefined in dk_rope and left as they are in the others."""
     Tq, H, _ = q.shape
     Tk, gpu = k_nope.shape[0], _current_gpu()
     arg = _attn_arg(gpu, q, k_nope, k_rope, v, offsets_q, offsets_k, scale, causal)
