@@ -797,7 +797,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
   float rest = 0.0f, unshift = kUnshift;           // row sum of this half's dS'
   const float c = a.scale * kLog2e;
   const int cut = keys_seen(a, st, st.row0);       // tiles before it are seen whole by all
-  // tiles before these have a second term of dS: in the pair's rows, and in any of the workgroup's
+  // tiles before these have a second term of dS: for the pair's rows, and for any of the workgroup's
   const int few = wfirst <= kFew ? wlast : 0, few_any = cut <= kFew ? kFew + 32 : 0;
   // P and dS against the tile at k0 (in buffer `buf`), this wavefront's 32 keys of it
   auto first = [&](auto again, uint4 (&mine)[4], int k0, int buf, int spare) __attribute__((always_inline)) {
@@ -888,16 +888,18 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS / 2) void k_attn_dq(AttnArgs a) 
   };
   // The sums over the keys that the workgroup sees.
   auto walk = [&](auto again) __attribute__((always_inline)) {
+    constexpr bool FIRST = !decltype(again)::value;
     int buf = 0, prev = 2;                         // of this tile and of the one before
     for (int k0 = 0; k0 < kend + kBN; k0 += kBN) {
       tile_wait();
       const int next = buf == 2 ? 0 : buf + 1;
-      const bool late = !decltype(again)::value && k0 > 0 && k0 - kBN < few_any;   // the last tile's rests are in the way
+      // whether the last tile's rests lie where the next copy goes
+      const bool late = FIRST && k0 > 0 && k0 - kBN < few_any;
       if (!late && k0 + kBN < kend) tile_copy<2 * PAIRS>(cp, x.kn, x.kr, x.v, k0 + kBN, st.lk, next);
       uint4 mine[4];                               // this wavefront's P and dS slabs
-      if (decltype(again)::value && k0 > cut) cover(k0 - kBN, prev);
+      if (!FIRST && k0 > cut) cover(k0 - kBN, prev);
       second(again, k0 - kBN, prev, next);
-      if (late || (!decltype(again)::value && k0 < few_any)) __syncthreads();   // the rests, and the last tile, are consumed
+      if (late || (FIRST && k0 < few_any)) __syncthreads();   // the last tile and its rests are consumed
       if (late && k0 + kBN < kend) tile_copy<2 * PAIRS>(cp, x.kn, x.kr, x.v, k0 + kBN, st.lk, next);
       if (k0 < kend) first(again, mine, k0, buf, prev);
       __syncthreads();                             // the last tile's operands are consumed
