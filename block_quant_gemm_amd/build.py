@@ -8,7 +8,7 @@ import tempfile
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = ["csrc/quant.hip", "csrc/gemm.hip", "csrc/latent.hip", "csrc/attention.hip",
-           "csrc/api.hip"]
+           "csrc/norm.hip", "csrc/ffn.hip", "csrc/api.hip"]
 LIB = os.path.join(PKG, "libmxq.so")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",
          # keep FP32 arithmetic off the packed-FP32 instructions

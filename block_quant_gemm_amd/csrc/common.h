@@ -102,6 +102,22 @@ inline size_t latent_backward_workspace(int64_t Tq, int64_t Tk, int64_t H) {
   return words > INT64_MAX / (int64_t)sizeof(float) ? SIZE_MAX : (size_t)words * sizeof(float);
 }
 
+// Workgroups of mx_rms_norm_backward, each with a sum a column of dw.
+inline uint32_t norm_backward_parts(int64_t M, int64_t K) {
+  const int64_t per = K <= 512 ? 4 : 1, groups = (M + per - 1) / per;
+  return (uint32_t)(groups < 512 ? groups : 512);
+}
+inline size_t norm_backward_workspace(int64_t M, int64_t K) {
+  if (M < 1 || K < 1 || M > MXQ_NORM_MAX_ROWS || K > MXQ_NORM_MAX_COLS) return 0;
+  return (size_t)norm_backward_parts(M, K) * (size_t)K * sizeof(float);
+}
+
+// Workspace of mx_gated_ffn_decode: h's codes and scales.
+inline size_t ffn_decode_workspace(int64_t M, int64_t F) {
+  if (M < 1 || F < 1 || M > MXQ_FFN_DECODE_MAX_ROWS || F > MXQ_FFN_DECODE_MAX_DIM) return 0;
+  return (size_t)M * (size_t)(F + F / 32);
+}
+
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));

@@ -130,6 +130,9 @@ struct GemmArgs {
   // per-group-scaled SwiGLU product: h in BF16 and each group's max |h|
   uint16_t* h; int64_t ldh;
   uint32_t* hamax;                                  // [E] FP32 bit patterns (atomic max)
+  // SwiGLU gradient epilogue: the forward's gate/up product [M, 2F]; c takes
+  // the gradient in BF16 (or null), hq .. hsT its MX copies [M, 2F], [2F, hcap]
+  const uint16_t* gu; int64_t ldgu;
 };
 
 // One operand of a workgroup: codes and scales as buffer resources whose
@@ -290,6 +293,25 @@ __device__ __forceinline__ uint32_t mx_block_f32(const float (&v)[32], uint32_t 
   return code;
 }
 
+// 32 BF16 values (64 bytes, 16-byte aligned).
+__device__ __forceinline__ void load32_bf16(const uint16_t* p, float (&v)[32]) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p + 8 * d);
+    v[8 * d] = bf16_lo(x.x); v[8 * d + 1] = bf16_hi(x.x);
+    v[8 * d + 2] = bf16_lo(x.y); v[8 * d + 3] = bf16_hi(x.y);
+    v[8 * d + 4] = bf16_lo(x.z); v[8 * d + 5] = bf16_hi(x.z);
+    v[8 * d + 6] = bf16_lo(x.w); v[8 * d + 7] = bf16_hi(x.w);
+  }
+}
+__device__ __forceinline__ void store32_bf16(uint16_t* p, const float (&v)[32]) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+    *reinterpret_cast<uint4*>(p + 8 * d) =
+        make_uint4(bf16x2_bits(v[8 * d], v[8 * d + 1]), bf16x2_bits(v[8 * d + 2], v[8 * d + 3]),
+                   bf16x2_bits(v[8 * d + 4], v[8 * d + 5]), bf16x2_bits(v[8 * d + 6], v[8 * d + 7]));
+}
+
 // The MFMA operand of tile row r for one k-step: 16-byte chunks c0 and c1.
 __device__ __forceinline__ i32x8 read_frag(const uint8_t* l, int r, int c0, int c1) {
   const uint4 x = *reinterpret_cast<const uint4*>(l + lds_off(r, c0));
@@ -380,6 +402,19 @@ __device__ void group_table(const int64_t* offsets, int E, int64_t M, int64_t* s
     }
   }
   __syncthreads();
+}
+
+// Rows of the first n groups after each is padded to whole blocks of 32: a
+// group's first column in the column copy.  Every lane gets it.
+__device__ __forceinline__ int64_t padded_rows(const int64_t* s_off, int n) {
+  int64_t p = 0;
+  for (int gi = threadIdx.x & 63; gi < n; gi += 64) {
+    const int64_t d = s_off[gi + 1] - s_off[gi];
+    p += d > 0 ? (d + 31) & ~31LL : 0;
+  }
+#pragma unroll
+  for (int sh = 32; sh >= 1; sh >>= 1) p += __shfl_xor(p, sh, 64);
+  return p;
 }
 
 // Weight-gradient tile order: the experts by padded token count, largest
@@ -502,9 +537,14 @@ constexpr int kBlkScaleWords = 320;
 // every finite BF16 block yields unless its largest magnitude is below
 // 2^-116), and multiplied on the BF16 matrix instruction, whose products are
 // exact and whose sums are FP32-accurate.
-template <int KIND, bool PT, int OUT, bool SW, bool SWI, bool BLK, bool XA = false, int MI = 4>
+// SWB: the SwiGLU gradient (variable M, MX): the product is the gradient of h
+// (dY times the down weights), and the epilogue turns it into that of the
+// gate/up product and writes its MX copies.
+template <int KIND, bool PT, int OUT, bool SW, bool SWI, bool BLK, bool XA = false, int MI = 4,
+          bool SWB = false>
 __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
   static_assert(MI == 4 || (MI == 2 && !SWI && !BLK), "row tiles per wavefront");
+  static_assert(!SWB || (KIND == kVarM && !PT && !SWI && MI == 4), "SwiGLU gradient kind");
   constexpr int TMR = MI * 64;                      // tile rows (256, or 128)
   constexpr int RW = MI * 32;                       // rows per wavefront
   constexpr int DPM = 4 / MI;                       // stage loads issued per MFMA
@@ -553,7 +593,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
     B = op_tile(g.b, g.bs, g.ldb, g.ldsb, n0, 0, g.N - n0, kdim, !PT && !BLK, SW);
   } else if (KIND == kVarM) {
     group_table(g.offsets, g.E, g.M, s_off, s_start);
-    if (SWI && blockIdx.x == 0 && wave == 0 && g.poff) {
+    if ((SWI || SWB) && blockIdx.x == 0 && wave == 0 && g.poff) {
       // padded offsets of the column copy: each group rounded up to 32 rows
       int64_t carry = 0;
       if (lane == 0) g.poff[0] = 0;
@@ -571,6 +611,15 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
         }
         if (gi < g.E) g.poff[gi + 1] = carry + v;
         carry += __shfl(v, 63, 64);
+      }
+    }
+    if (SWB) {
+      // columns of the column copy past the padded total: zeros, a row a workgroup in turn
+      const int64_t total = padded_rows(s_off, g.E);
+      for (int64_t r = blockIdx.x; r < 2 * g.F; r += g.nblocks) {
+        for (int64_t c = total + 16 * t; c < g.hcap; c += 16 * kThreads)
+          *reinterpret_cast<uint4*>(g.hqT + r * g.ldhqT + c) = make_uint4(0, 0, 0, 0);
+        for (int64_t c = total / 32 + t; c < g.hcap / 32; c += kThreads) g.hsT[r * g.ldhsT + c] = 0;
       }
     }
     const uint32_t tiles_m = (uint32_t)s_start[g.E];  // data-dependent M-tile count
@@ -1134,6 +1183,114 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
     }
   }
 
+  if constexpr (SWB) {
+    // ---- SwiGLU gradient epilogue.  With sg = 1 / (1 + e^-g):
+    //   d gate = dh u sg (1 + g (1 - sg)),   d up = dh g sg.
+    // In two rounds of 128 columns (each wavefront's j-th 32): dh staged in FP32
+    // as [256 rows][128], then (row, 32-column block) items, two a lane, read
+    // g and u, write both row copies and put d gate, then d up, in dh's
+    // place, from which (column, 32-row block) items make the column copy.
+    // Rows past the group are zero: the column copy's padding.
+    const int64_t F = g.F;
+    const int rows_t = c_rows < TM ? (int)c_rows : TM;
+    const int rows_p = (rows_t + 31) & ~31;
+    const int64_t pbase = padded_rows(s_off, group) + (m0 - s_off[group]);
+    float* hst = reinterpret_cast<float*>(smem);
+    constexpr int LD = kCStride / 4;
+    // column copy of the staged 128 columns, rows `first` + column of qT
+    auto columns = [&](int j, int64_t first) {
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        const int item = t + kThreads * k;
+        const int col = item & 127, blk = item >> 7;
+        float v[32];
+#pragma unroll
+        for (int r = 0; r < 32; ++r) v[r] = hst[(blk * 32 + r) * LD + col];
+        uint32_t w[8];
+        const uint32_t code = mx_block_f32(v, w);
+        const int64_t hc = n0 + (col >> 5) * 64 + j * 32 + (col & 31), pcol = pbase + blk * 32;
+        if (blk * 32 < rows_p && hc < F && pcol + 32 <= g.hcap) {
+          uint8_t* d = g.hqT + (first + hc) * g.ldhqT + pcol;
+          *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(d + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+          g.hsT[(first + hc) * g.ldhsT + (pcol >> 5)] = (uint8_t)code;
+        }
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      barrier();                                    // the LDS reads before are done
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int ml = wm * 128 + i * 32 + r32;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16& v = acc[i][j];
+          *reinterpret_cast<f32x4*>(&hst[ml * LD + (bn >> 1) + q * 8 + half * 4]) =
+              f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        }
+      }
+      barrier();
+      float up[2][32];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int item = t + kThreads * k;
+        const int row = item >> 2, blk = item & 3;
+        const int64_t hc = n0 + blk * 64 + j * 32, m = m0 + row;
+        const bool ok = row < rows_t && hc < F;
+        float gv[32], dg[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) gv[e] = up[k][e] = 0.0f;
+        if (ok) {
+          load32_bf16(g.gu + m * g.ldgu + hc, gv);
+          load32_bf16(g.gu + m * g.ldgu + F + hc, up[k]);
+        }
+        float* p = &hst[row * LD + blk * 32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float dh = ok ? p[e] : 0.0f;
+          const float sg = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-gv[e] * 1.4426950408889634f));
+          dg[e] = dh * up[k][e] * sg * __builtin_fmaf(gv[e], 1.0f - sg, 1.0f);
+          up[k][e] = dh * gv[e] * sg;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<f32x4*>(p + e) = f32x4{dg[e], dg[e + 1], dg[e + 2], dg[e + 3]};
+        uint32_t w0[8], w1[8];
+        const uint32_t c0 = mx_block_f32(dg, w0), c1 = mx_block_f32(up[k], w1);
+        if (ok) {
+          uint8_t* d = g.hq + m * g.ldhq + hc;
+          *reinterpret_cast<uint4*>(d) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+          *reinterpret_cast<uint4*>(d + 16) = make_uint4(w0[4], w0[5], w0[6], w0[7]);
+          *reinterpret_cast<uint4*>(d + F) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+          *reinterpret_cast<uint4*>(d + F + 16) = make_uint4(w1[4], w1[5], w1[6], w1[7]);
+          g.hs[m * g.ldhs + (hc >> 5)] = (uint8_t)c0;
+          g.hs[m * g.ldhs + ((F + hc) >> 5)] = (uint8_t)c1;
+          if (cbase) {
+            uint16_t* o = static_cast<uint16_t*>(cbase) + m * g.ldc + hc;
+            store32_bf16(o, dg);
+            store32_bf16(o + F, up[k]);
+          }
+        }
+      }
+      barrier();
+      columns(j, 0);
+      barrier();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int item = t + kThreads * k;
+        float* p = &hst[(item >> 2) * LD + (item & 3) * 32];
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<f32x4*>(p + e) =
+              f32x4{up[k][e], up[k][e + 1], up[k][e + 2], up[k][e + 3]};
+      }
+      barrier();
+      columns(j, F);
+    }
+    return;
+  }
+
   // ---- epilogue: acc[i][j] holds C[m = wm*128 + i*32 + lane%32]
   //                [n = bn + j*32 + 8*(v/4) + 4*(lane/32) + v%4]
   float mul = 1.0f;
@@ -1277,6 +1434,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_swiglu(GemmArgs g) {
 
 __global__ __launch_bounds__(kThreads, 1) void k_gemm_swiglu_pg(GemmArgs g) {
   gemm_body<kVarM, true, MXQ_OUT_BF16, false, true, false>(g);
+}
+
+template <bool SW, bool XA>
+__global__ __launch_bounds__(kThreads, 1) void k_gemm_swiglu_grad(GemmArgs g) {
+  gemm_body<kVarM, false, MXQ_OUT_BF16, SW, false, false, XA, 4, true>(g);
 }
 
 template <int OUT>
@@ -1578,6 +1740,63 @@ extern "C" int mx_grouped_gemm_swiglu(const uint8_t* a, const uint8_t* a_scale, 
   else
     hipLaunchKernelGGL((k_gemm_swiglu<false>), dim3((uint32_t)blocks), dim3(kThreads), 0,
                        stream, g);
+  return hipGetLastError() == hipSuccess ? MXQ_OK : MXQ_ERR_HIP;
+}
+
+extern "C" int mx_grouped_gemm_swiglu_backward(
+    const uint8_t* dy, const uint8_t* dy_scale, int64_t ldd, int64_t ldsd, const uint8_t* wT,
+    const uint8_t* wT_scale, int64_t ldw, int64_t ldsw, int64_t w_estride, int64_t ws_estride,
+    const int64_t* offsets, int32_t E, int64_t M, int64_t F, int64_t K, const uint16_t* gu,
+    int64_t ldgu, void* dgu, int64_t lddgu, uint8_t* q, int64_t ldq, uint8_t* scale, int64_t lds,
+    uint8_t* qT, int64_t ldqT, uint8_t* scaleT, int64_t ldsT, int64_t M_cap,
+    int64_t* offsets_padded, int accum, hipStream_t stream) {
+  if (M < 0 || F < 0 || K < 0 || M_cap < 0) return MXQ_ERR_SHAPE;
+  if (M > kMaxDim || F > kMaxDim || K > kMaxDim || M_cap > kMaxDim) return MXQ_ERR_SHAPE;
+  if (accum != MXQ_ACC_MFMA_FP8 && accum != MXQ_ACC_FP32) return MXQ_ERR_ARG;
+  if (E < 1 || E > kMaxGroups) return MXQ_ERR_SHAPE;
+  if (!offsets) return MXQ_ERR_NULL;
+  if (F % 32 != 0 || K % 32 != 0 || M_cap % 32 != 0) return MXQ_ERR_SHAPE;
+  if (M > 0 && M_cap < M + 31LL * E) return MXQ_ERR_SHAPE;
+  if (F == 0) return MXQ_OK;
+  if (M > 0 && (!gu || !q || !scale)) return MXQ_ERR_NULL;
+  if (M_cap > 0 && (!qT || !scaleT)) return MXQ_ERR_NULL;
+  if (ldqT < M_cap || ldsT < M_cap / 32 || ldqT > kMaxDim || ldsT > kMaxDim) return MXQ_ERR_SHAPE;
+  if (M > 0 && (ldgu < 2 * F || ldq < 2 * F || lds < 2 * F / 32 || ldgu > kMaxDim || ldq > kMaxDim ||
+                lds > kMaxDim || (dgu && (lddgu < 2 * F || lddgu > kMaxDim))))
+    return MXQ_ERR_SHAPE;
+  int st;
+  if (K > 0 && M > 0) {
+    if ((st = check_operand(dy, dy_scale, ldd, ldsd, K, true))) return st;
+    if ((st = check_operand(wT, wT_scale, ldw, ldsw, K, true))) return st;
+  }
+  if (w_estride < 0 || ws_estride < 0 || w_estride > kMaxDim || ws_estride > kMaxDim)
+    return MXQ_ERR_SHAPE;
+  if (w_estride % 16 != 0 || ldqT % 16 != 0 || !aligned(qT, 16)) return MXQ_ERR_ALIGN;
+  if (M > 0 && (ldq % 16 != 0 || !aligned(q, 16) || ldgu % 8 != 0 || !aligned(gu, 16) ||
+                (dgu && (lddgu % 8 != 0 || !aligned(dgu, 16)))))
+    return MXQ_ERR_ALIGN;
+  GemmArgs g = make_args(dy, dy_scale, ldd, ldsd, wT, wT_scale, ldw, ldsw, M, F, K, dgu, lddgu);
+  g.b_estride = w_estride; g.bs_estride = ws_estride;
+  g.offsets = offsets; g.E = E;
+  g.F = F;
+  g.hq = q; g.hs = scale; g.ldhq = ldq; g.ldhs = lds;
+  g.hqT = qT; g.hsT = scaleT; g.ldhqT = ldqT; g.ldhsT = ldsT;
+  g.hcap = M_cap;
+  g.poff = offsets_padded;
+  g.gu = gu; g.ldgu = ldgu;
+  // Workgroups past the group tiles only clear their share past the padded total.
+  const int64_t blocks = sat_mul(tiles_of(M, TM) + E, g.tiles_n);
+  if (blocks > 0x7FFFFFFF) return MXQ_ERR_SHAPE;
+  g.nblocks = (uint32_t)blocks;
+  const dim3 grid((uint32_t)blocks), block(kThreads);
+  const bool windows = ldsd % 16 == 0 && ldsw % 16 == 0;
+  if (accum == MXQ_ACC_FP32) {
+    if (windows) hipLaunchKernelGGL((k_gemm_swiglu_grad<true, true>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_gemm_swiglu_grad<false, true>), grid, block, 0, stream, g);
+  } else {
+    if (windows) hipLaunchKernelGGL((k_gemm_swiglu_grad<true, false>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_gemm_swiglu_grad<false, false>), grid, block, 0, stream, g);
+  }
   return hipGetLastError() == hipSuccess ? MXQ_OK : MXQ_ERR_HIP;
 }
 

@@ -1,0 +1,460 @@
+// Root-mean-square norm with the residual's addition and MX output, its
+// gradient, and their C-ABI launchers.
+//
+//   s = BF16(x + r),  rstd = 1 / sqrt(mean_k s^2 + eps),  y = s rstd w
+//   dx = rstd (dy w - s rstd c) + ds,  c = mean_k(dy w s rstd),  dw = sum_m dy s rstd
+//
+// Both are streams: every element is read and written once (the column copy
+// reads s again), so bytes bound them.
+
+#include "common.h"
+
+namespace mxq {
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+struct NormArgs {
+  const uint16_t* x; int64_t ldx;
+  const uint16_t* r; int64_t ldr;                   // residual, or null
+  const uint16_t* w;
+  uint16_t* s; int64_t lds_;                        // the sum, or null without a residual
+  float* rstd;
+  uint16_t* y; int64_t ldy;                         // BF16 output, or null
+  uint8_t* q; int64_t ldq; uint8_t* sc; int64_t ldsc;
+  uint8_t* qT; int64_t ldqT, cap; uint8_t* scT; int64_t ldscT;   // column copy, or null
+  int64_t M;
+  uint32_t K;
+  float eps;
+};
+
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+  f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
+  f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]), bf16x2_bits(f[4], f[5]),
+                    bf16x2_bits(f[6], f[7]));
+}
+
+// MX scale code of a block from the FP32 pattern of its largest magnitude
+// (sign cleared; NaN above Inf above finite values).
+__device__ __forceinline__ uint32_t mx_scale_code_f32(uint32_t am) {
+  const uint32_t E = am >> 23;
+  return am >= 0x7F800000u ? 0xFFu : (E > 8u ? E - 8u : 0u);
+}
+
+// One MX block of 32 FP32 values held by a DPP quad, 8 a lane.
+__device__ __forceinline__ uint2 quant8_f32(const float (&v)[8], uint32_t& code) {
+  uint32_t am = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t m = __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu;
+    am = am > m ? am : m;
+  }
+  uint32_t o = dpp_u32(am, kQuadXor1);
+  am = am > o ? am : o;
+  o = dpp_u32(am, kQuadXor2);
+  am = am > o ? am : o;
+  code = mx_scale_code_f32(am);
+  if (code == 0xFFu) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  const float inv = mx_inv_scale(code);
+  uint32_t lo = cvt2_e4m3_sat<false>(v[0] * inv, v[1] * inv, 0u);
+  lo = cvt2_e4m3_sat<true>(v[2] * inv, v[3] * inv, lo);
+  uint32_t hi = cvt2_e4m3_sat<false>(v[4] * inv, v[5] * inv, 0u);
+  hi = cvt2_e4m3_sat<true>(v[6] * inv, v[7] * inv, hi);
+  return make_uint2(lo, hi);
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int sh = 32; sh >= 1; sh >>= 1) v += __shfl_xor(v, sh, 64);
+  return v;
+}
+
+// rstd of a row from its sum of squares.  The squares are summed in FP64, in
+// which those of BF16 values are exact and neither overflow nor vanish.
+__device__ __forceinline__ float rstd_of(double ss, uint32_t K, float eps) {
+  return (float)(1.0 / __builtin_sqrt(ss / (double)K + (double)eps));
+}
+
+// y of 8 elements: two FP32 roundings, the same wherever it is formed.
+__device__ __forceinline__ void normed8(uint4 s, float rstd, uint4 w, float (&y)[8]) {
+  float a[8], b[8];
+  unpack8(s, a);
+  unpack8(w, b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = a[i] * rstd * b[i];
+}
+
+// A row is held by W wavefronts, CH chunks of 8 elements a lane, so it is read
+// once.  Lane l of wavefront v holds elements 8 (64 (W c + v) + l) .. + 8 of
+// chunk c.
+template <int W, int CH>
+__global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_rows(NormArgs g) {
+  constexpr int ROWS = W >= 4 ? 1 : 4 / W;          // rows a workgroup
+  __shared__ double s_part[W > 1 ? W : 1];
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+  const uint32_t v = W > 1 ? wave : 0u;
+  const int64_t row = (int64_t)blockIdx.x * ROWS + (W > 1 ? 0 : wave);
+  if (W == 1 && row >= g.M) return;
+  uint32_t col[CH];
+  uint4 s[CH];
+  double ss = 0;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    col[c] = 8u * (64u * (W * c + v) + lane);
+    s[c] = col[c] < g.K ? *reinterpret_cast<const uint4*>(g.x + row * g.ldx + col[c])
+                        : make_uint4(0, 0, 0, 0);
+  }
+  if (g.r) {
+    uint4 r[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      r[c] = col[c] < g.K ? *reinterpret_cast<const uint4*>(g.r + row * g.ldr + col[c])
+                          : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float a[8], b[8];
+      unpack8(s[c], a);
+      unpack8(r[c], b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] += b[i];
+      s[c] = pack8(a);
+      if (col[c] < g.K) *reinterpret_cast<uint4*>(g.s + row * g.lds_ + col[c]) = s[c];
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    float a[8];
+    unpack8(s[c], a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)a[i], (double)a[i], ss);
+  }
+  ss = wave_sum(ss);
+  if (W > 1) {
+    if (lane == 0) s_part[wave] = ss;
+    __syncthreads();
+    ss = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) ss += s_part[i];
+  }
+  const float rstd = rstd_of(ss, g.K, g.eps);
+  if (lane == 0 && v == 0) g.rstd[row] = rstd;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const bool ok = col[c] < g.K;
+    const uint4 w = ok ? *reinterpret_cast<const uint4*>(g.w + col[c]) : make_uint4(0, 0, 0, 0);
+    float y[8];
+    normed8(s[c], rstd, w, y);
+    uint32_t code;
+    const uint2 q = quant8_f32(y, code);            // all four lanes of a quad take part
+    if (ok) {
+      *reinterpret_cast<uint2*>(g.q + row * g.ldq + col[c]) = q;
+      if ((lane & 3u) == 0u) g.sc[row * g.ldsc + (col[c] >> 5)] = (uint8_t)code;
+      if (g.y) *reinterpret_cast<uint4*>(g.y + row * g.ldy + col[c]) = pack8(y);
+    }
+  }
+}
+
+// The column copy: 128 rows x 64 columns of y, formed again from s and rstd, in
+// LDS; each wavefront quantizes one block of 32 rows, a column a lane, and the
+// codes leave as 128-byte rows of the transpose.
+constexpr int kNcRows = 128, kNcCols = 64, kNcLd = kNcCols + 1;
+
+__global__ __launch_bounds__(256) void k_norm_columns(NormArgs g) {
+  __shared__ float tile[kNcRows * kNcLd];
+  __shared__ __attribute__((aligned(16))) uint8_t outq[kNcCols * (kNcRows + 16)];
+  __shared__ uint8_t outs[kNcCols * 4];
+  const uint32_t nk = (g.K + kNcCols - 1) / kNcCols;
+  const int64_t p0 = (int64_t)(blockIdx.x / nk) * kNcRows;
+  const uint32_t k0 = blockIdx.x % nk * kNcCols;
+  const uint16_t* s = g.r ? g.s : g.x;
+  const int64_t ld = g.r ? g.lds_ : g.ldx;
+  const int tid = threadIdx.x, chunk = tid & 7;
+  const uint32_t k = k0 + chunk * 8;
+  const uint4 w = k < g.K ? *reinterpret_cast<const uint4*>(g.w + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int i = u * 32 + (tid >> 3);
+    const int64_t row = p0 + i;
+    float y[8] = {};
+    if (row < g.M && k < g.K)
+      normed8(*reinterpret_cast<const uint4*>(s + row * ld + k), g.rstd[row], w, y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) tile[i * kNcLd + chunk * 8 + e] = y[e];
+  }
+  __syncthreads();
+  const int c = tid & 63, b = tid >> 6;
+  float v[32];
+  uint32_t am = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    v[i] = tile[(b * 32 + i) * kNcLd + c];
+    const uint32_t m = __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu;
+    am = am > m ? am : m;
+  }
+  const uint32_t code = mx_scale_code_f32(am);
+  const float inv = mx_inv_scale(code == 0xFFu ? 127u : code);
+#pragma unroll
+  for (int d = 0; d < 8; ++d) {
+    uint32_t o = cvt2_e4m3_sat<false>(v[4 * d] * inv, v[4 * d + 1] * inv, 0u);
+    o = cvt2_e4m3_sat<true>(v[4 * d + 2] * inv, v[4 * d + 3] * inv, o);
+    *reinterpret_cast<uint32_t*>(&outq[c * (kNcRows + 16) + b * 32 + d * 4]) =
+        code == 0xFFu ? 0x7F7F7F7Fu : o;
+  }
+  outs[c * 4 + b] = (uint8_t)code;
+  __syncthreads();
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    const int cc = it * 32 + (tid >> 3), c16 = tid & 7;
+    const int64_t p = p0 + c16 * 16;
+    if (k0 + cc < g.K && p < g.cap)
+      *reinterpret_cast<uint4*>(g.qT + (int64_t)(k0 + cc) * g.ldqT + p) =
+          *reinterpret_cast<const uint4*>(&outq[cc * (kNcRows + 16) + c16 * 16]);
+  }
+  const int cc = tid >> 2, bb = tid & 3;
+  if (k0 + cc < g.K && p0 + bb * 32 < g.cap)
+    g.scT[(int64_t)(k0 + cc) * g.ldscT + (p0 >> 5) + bb] = outs[cc * 4 + bb];
+}
+
+struct NormGradArgs {
+  const uint16_t* dy; int64_t lddy;
+  const uint16_t* s; int64_t lds_;
+  const float* rstd;
+  const uint16_t* w;
+  const uint16_t* ds; int64_t ldds;                 // gradient of the sum, or null
+  uint16_t* dx; int64_t lddx;
+  float* dw;                                        // or null
+  float* part;                                      // [parts, K] sums over a workgroup's rows
+  int64_t M;
+  uint32_t K, parts;
+};
+
+// Workgroup b takes rows b, b + grid, ...; a row is held as in k_norm_rows.
+// dw's sums stay in registers over a wavefront's rows; the workgroup's wavefronts
+// add theirs in order, and k_norm_join the workgroups', so the result
+// does not depend on timing.
+template <int W, int CH>
+__global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_grad(NormGradArgs g) {
+  constexpr int ROWS = W >= 4 ? 1 : 4 / W;
+  __shared__ float s_part[2][W > 1 ? W : 1];
+  __shared__ float s_dw[W > 1 ? 1 : 512 * CH];
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+  const uint32_t v = W > 1 ? wave : 0u;
+  uint32_t col[CH];
+  uint4 w[CH];
+  float acc[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    col[c] = 8u * (64u * (W * c + v) + lane);
+    w[c] = col[c] < g.K ? *reinterpret_cast<const uint4*>(g.w + col[c]) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[c][i] = 0.0f;
+  }
+  int flip = 0;
+  for (int64_t row = (int64_t)blockIdx.x * ROWS + (W > 1 ? 0 : wave); row < g.M;
+       row += (int64_t)gridDim.x * ROWS) {
+    uint4 dy[CH], s[CH], ds[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const bool ok = col[c] < g.K;
+      dy[c] = ok ? *reinterpret_cast<const uint4*>(g.dy + row * g.lddy + col[c]) : make_uint4(0, 0, 0, 0);
+      s[c] = ok ? *reinterpret_cast<const uint4*>(g.s + row * g.lds_ + col[c]) : make_uint4(0, 0, 0, 0);
+      ds[c] = ok && g.ds ? *reinterpret_cast<const uint4*>(g.ds + row * g.ldds + col[c])
+                         : make_uint4(0, 0, 0, 0);
+    }
+    const float rstd = g.rstd[row];
+    float along = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float a[8], b[8], h[8];
+      unpack8(dy[c], a);
+      unpack8(s[c], b);
+      unpack8(w[c], h);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float xh = b[i] * rstd;
+        acc[c][i] = __builtin_fmaf(a[i], xh, acc[c][i]);
+        along = __builtin_fmaf(a[i] * h[i], xh, along);
+      }
+    }
+#pragma unroll
+    for (int sh = 32; sh >= 1; sh >>= 1) along += __shfl_xor(along, sh, 64);
+    if (W > 1) {
+      // two buffers in turn: a wavefront writes a row's only after all have read the one before
+      if (lane == 0) s_part[flip][wave] = along;
+      __syncthreads();
+      along = 0.0f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) along += s_part[flip][i];
+      flip ^= 1;
+    }
+    const float m = along / (float)g.K;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float a[8], b[8], h[8], e[8];
+      unpack8(dy[c], a);
+      unpack8(s[c], b);
+      unpack8(w[c], h);
+      unpack8(ds[c], e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        a[i] = __builtin_fmaf(rstd, __builtin_fmaf(-(b[i] * rstd), m, a[i] * h[i]), e[i]);
+      if (col[c] < g.K) *reinterpret_cast<uint4*>(g.dx + row * g.lddx + col[c]) = pack8(a);
+    }
+  }
+  if (!g.dw) return;
+  float* out = g.part + (int64_t)blockIdx.x * g.K;
+  if (W > 1) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (col[c] < g.K) {
+        *reinterpret_cast<float4*>(out + col[c]) = make_float4(acc[c][0], acc[c][1], acc[c][2], acc[c][3]);
+        *reinterpret_cast<float4*>(out + col[c] + 4) = make_float4(acc[c][4], acc[c][5], acc[c][6], acc[c][7]);
+      }
+  } else {
+    for (uint32_t k = 0; k < 4; ++k) {
+      if (wave == k) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float* p = &s_dw[col[c] + i];
+            *p = k ? *p + acc[c][i] : acc[c][i];
+          }
+      }
+      __syncthreads();
+    }
+    for (uint32_t k = threadIdx.x; k < g.K; k += blockDim.x) out[k] = s_dw[k];
+  }
+}
+
+// dw from the workgroups' sums: 16 columns a workgroup, 16 threads a column.
+__global__ __launch_bounds__(256) void k_norm_join(const float* part, uint32_t parts, uint32_t K,
+                                                   float* dw) {
+  __shared__ float s[16][17];
+  const uint32_t c = threadIdx.x & 15, t = threadIdx.x >> 4, k = blockIdx.x * 16 + c;
+  float a = 0.0f;
+  if (k < K)
+    for (uint32_t p = t; p < parts; p += 16) a += part[(int64_t)p * K + k];
+  s[t][c] = a;
+  __syncthreads();
+  if (t == 0 && k < K) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) a += s[i][c];
+    dw[k] = a;
+  }
+}
+
+}  // namespace mxq
+
+using namespace mxq;
+
+static inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// A row operand of K BF16 values: NULL, stride and alignment.
+static int check_rows(const void* p, int64_t ld, int64_t K) {
+  if (!p) return MXQ_ERR_NULL;
+  if (ld < K || ld > (INT64_C(1) << 39)) return MXQ_ERR_SHAPE;
+  return ld % 8 == 0 && aligned(p, 16) ? MXQ_OK : MXQ_ERR_ALIGN;
+}
+
+static int check_norm_size(int64_t M, int64_t K) {
+  if (M < 0 || K < 0 || M > MXQ_NORM_MAX_ROWS || K > MXQ_NORM_MAX_COLS || K % 32 != 0)
+    return MXQ_ERR_SHAPE;
+  return MXQ_OK;
+}
+
+extern "C" int mx_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr,
+                           const uint16_t* weight, int64_t M, int64_t K, float eps,
+                           uint16_t* total, int64_t ldt, float* rstd, uint16_t* y, int64_t ldy,
+                           uint8_t* q, int64_t ldq, uint8_t* scale, int64_t lds, uint8_t* qT,
+                           int64_t ldqT, int64_t M_cap, uint8_t* scaleT, int64_t ldsT,
+                           hipStream_t stream) {
+  int st = check_norm_size(M, K);
+  if (st) return st;
+  if (!(eps > 0.0f) || !(eps <= 3.4028235e38f)) return MXQ_ERR_ARG;
+  if (qT) {
+    if (M_cap < 0 || M_cap % 32 != 0 || M_cap < (M + 31) / 32 * 32 || M_cap > 2 * MXQ_NORM_MAX_ROWS ||
+        ldqT < M_cap || ldsT < M_cap / 32)
+      return MXQ_ERR_SHAPE;
+    if (!scaleT) return MXQ_ERR_NULL;
+    if (ldqT % 16 != 0 || !aligned(qT, 16)) return MXQ_ERR_ALIGN;
+  }
+  if (K == 0 || (M == 0 && (!qT || M_cap == 0))) return MXQ_OK;
+  if (M > 0) {
+    if ((st = check_rows(x, ldx, K))) return st;
+    if (residual && (st = check_rows(residual, ldr, K))) return st;
+    if (residual && (st = check_rows(total, ldt, K))) return st;
+    if (y && (st = check_rows(y, ldy, K))) return st;
+    if (!weight || !rstd || !q || !scale) return MXQ_ERR_NULL;
+    if (ldq < K || lds < K / 32) return MXQ_ERR_SHAPE;
+    if (!aligned(weight, 16) || !aligned(rstd, 4) || ldq % 16 != 0 || !aligned(q, 16))
+      return MXQ_ERR_ALIGN;
+  }
+  NormArgs g{x, ldx, residual, ldr, weight, total, ldt, rstd, y, ldy, q, ldq, scale, lds,
+             qT, ldqT, M_cap, scaleT, ldsT, M, (uint32_t)K, eps};
+#define MXQ_ROWS(W, CH)                                                                        \
+  hipLaunchKernelGGL((k_norm_rows<W, CH>), dim3((uint32_t)(W >= 4 ? M : (M + 3) / 4)),         \
+                     dim3(W == 16 ? 1024 : 256), 0, stream, g)
+  if (M > 0) {
+    if (K <= 512) MXQ_ROWS(1, 1);
+    else if (K <= 2048 && M >= 1024) MXQ_ROWS(1, 4);
+    else if (K <= 2048) MXQ_ROWS(4, 1);
+    else if (K <= 4096) MXQ_ROWS(4, 2);
+    else if (K <= 8192) MXQ_ROWS(4, 4);
+    else MXQ_ROWS(16, 2);
+    if (hipGetLastError() != hipSuccess) return MXQ_ERR_HIP;
+  }
+#undef MXQ_ROWS
+  if (qT && M_cap > 0) {
+    const int64_t blocks = (M_cap + kNcRows - 1) / kNcRows * ((K + kNcCols - 1) / kNcCols);
+    hipLaunchKernelGGL(k_norm_columns, dim3((uint32_t)blocks), dim3(256), 0, stream, g);
+    if (hipGetLastError() != hipSuccess) return MXQ_ERR_HIP;
+  }
+  return MXQ_OK;
+}
+
+extern "C" int mx_rms_norm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* total,
+                                    int64_t ldt, const float* rstd, const uint16_t* weight,
+                                    const uint16_t* dtotal, int64_t lddt, int64_t M, int64_t K,
+                                    uint16_t* dx, int64_t lddx, float* dw, void* workspace,
+                                    size_t workspace_bytes, hipStream_t stream) {
+  int st = check_norm_size(M, K);
+  if (st) return st;
+  if (K == 0 || (M == 0 && !dw)) return MXQ_OK;
+  if (M > 0) {
+    if ((st = check_rows(dy, lddy, K))) return st;
+    if ((st = check_rows(total, ldt, K))) return st;
+    if (dtotal && (st = check_rows(dtotal, lddt, K))) return st;
+    if ((st = check_rows(dx, lddx, K))) return st;
+    if (!rstd || !weight) return MXQ_ERR_NULL;
+    if (!aligned(rstd, 4) || !aligned(weight, 16)) return MXQ_ERR_ALIGN;
+  }
+  const uint32_t parts = norm_backward_parts(M, K);
+  if (dw) {
+    if (!aligned(dw, 4) || !aligned(workspace, 16)) return MXQ_ERR_ALIGN;
+    if (M > 0 && !workspace) return MXQ_ERR_NULL;
+    if (workspace_bytes < norm_backward_workspace(M, K)) return MXQ_ERR_WORKSPACE;
+  }
+  NormGradArgs g{dy, lddy, total, ldt, rstd, weight, dtotal, lddt, dx, lddx, dw,
+                 static_cast<float*>(workspace), M, (uint32_t)K, parts};
+#define MXQ_GRAD(W, CH)                                                                        \
+  hipLaunchKernelGGL((k_norm_grad<W, CH>), dim3(parts), dim3(W == 16 ? 1024 : 256), 0, stream, g)
+  if (M > 0) {
+    if (K <= 512) MXQ_GRAD(1, 1);
+    else if (K <= 2048) MXQ_GRAD(4, 1);
+    else if (K <= 4096) MXQ_GRAD(4, 2);
+    else if (K <= 8192) MXQ_GRAD(16, 1);
+    else MXQ_GRAD(16, 2);
+    if (hipGetLastError() != hipSuccess) return MXQ_ERR_HIP;
+  }
+#undef MXQ_GRAD
+  if (dw) {
+    hipLaunchKernelGGL(k_norm_join, dim3((uint32_t)((K + 15) / 16)), dim3(256), 0, stream, g.part,
+                       M > 0 ? parts : 0u, (uint32_t)K, dw);
+    if (hipGetLastError() != hipSuccess) return MXQ_ERR_HIP;
+  }
+  return MXQ_OK;
+}

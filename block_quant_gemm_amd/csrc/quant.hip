@@ -1067,6 +1067,8 @@ extern "C" size_t mxq_workspace_size(int op, int64_t n, int64_t a1, int64_t a2, 
   if (op == MXQ_WS_LATENT_DECODE) return latent_decode_plan(n, a1, a2, a3).bytes;
   if (op == MXQ_WS_LATENT_BACKWARD) return latent_backward_workspace(n, a1, a2);
   if (op == MXQ_WS_LATENT_FORWARD) return latent_forward_workspace(n, a1, a2, a3);
+  if (op == MXQ_WS_NORM_BACKWARD) return norm_backward_workspace(n, a1);
+  if (op == MXQ_WS_FFN_DECODE) return ffn_decode_workspace(n, a1);
   return 0;
 }
 

@@ -1,7 +1,8 @@
 """ctypes binding of libmxq.so.
 
 Argument marshalling only: every function below checks nothing itself (the
-latent-attention calls, which take many related tensors, check their shapes),
+latent-attention, norm and feed-forward calls, which take many related tensors,
+check their shapes),
 allocates its outputs with torch (device memory is the caller's), passes raw
 device pointers and the current HIP stream to the C function of the same
 name, and raises if the library returns an error.  All arithmetic happens in
@@ -21,6 +22,7 @@ LIB_PATH = os.path.join(_HERE, "libmxq.so")
 OUT_BF16, OUT_FP32 = 0, 1
 ACC_MFMA_FP8, ACC_FP32 = 0, 1
 WS_PER_TENSOR, WS_PER_GROUP, WS_LATENT_DECODE, WS_LATENT_BACKWARD, WS_LATENT_FORWARD = range(5)
+WS_NORM_BACKWARD, WS_FFN_DECODE = 5, 6
 
 _i64, _i32, _p, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
 _f32 = ctypes.c_float
@@ -110,6 +112,17 @@ _SIGS = {
     "latent_attention_backward": (ctypes.c_int, [_p, _p, _i64, _i64, _p,
                                                  _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64,
                                                  _i64, _p, _i64, _p, _i64, _i64, _p, _sz, _p]),
+    "mx_grouped_gemm_swiglu_backward": (ctypes.c_int, [
+        _p, _p, _i64, _i64, _p, _p, _i64, _i64, _i64, _i64, _p, _i32, _i64, _i64, _i64, _p, _i64,
+        _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i64, _p, ctypes.c_int, _p]),
+    "mx_gated_ffn_decode": (ctypes.c_int, [
+        _p, _p, _i64, _i64, _p, _p, _i64, _i64, _i64, _i64, _p, _p, _i64, _i64, _i64, _i64, _p,
+        _i32, _i64, _i64, _i64, _i64, _p, _i64, _p, _sz, _p]),
+    "mx_rms_norm": (ctypes.c_int, [
+        _p, _i64, _p, _i64, _p, _i64, _i64, _f32, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _p,
+        _i64, _i64, _p, _i64, _p]),
+    "mx_rms_norm_backward": (ctypes.c_int, [
+        _p, _i64, _p, _i64, _p, _p, _p, _i64, _i64, _i64, _p, _i64, _p, _p, _sz, _p]),
     "mxq_workspace_size": (_sz, [ctypes.c_int, _i64, _i64, _i64, _i64]),
     "mxq_latent_backward_rows": (ctypes.c_int, [_i64, _i32, _i32, ctypes.c_int]),
     "mxq_validate_offsets": (ctypes.c_int, [_p, _i32, _i64, _p]),
@@ -955,6 +968,214 @@ def latent_attention_backward(dout, q, k_nope, k_rope, v, o, lse, offsets_q=None
     if st:
         _check(st)
     return dq, dk_nope, dk_rope, dv
+
+
+# ---------------------------------------------------------------------------
+# norm and gated feed-forward
+# ---------------------------------------------------------------------------
+
+def _stride(s, rows, width):
+    """The row stride to pass on."""
+    return s[0] if rows > 1 else width
+
+
+def _up16(n):
+    return (n + 15) // 16 * 16
+
+
+def mx_rms_norm(x, weight, residual=None, eps=1e-6, y=False, columns=False, M_cap=None, total=None,
+                rstd=None, q=None, scale=None, qT=None, scaleT=None):
+    """Root-mean-square norm with the residual's addition and the MX operand of the next
+    product: s = x + residual (BF16), y = s / sqrt(mean s^2 + eps) * weight, quantized.
+
+    x, residual BF16 [M, K] (residual or None), weight BF16 [K].  ``y``: True allocates
+    y in BF16 as well, a tensor receives it.  ``columns``: the column copy too (for
+    the weight gradient), which qT or scaleT imply.  ``total`` may be x or residual.  Returns (total,
+    rstd float32 [M], y or None, q [M, K], scale [M, K/32], qT [K, M_cap] or None,
+    scaleT [K, M_cap/32] or None); total is x itself without a residual."""
+    (M, K), gpu = x.shape, _current_gpu()
+    sx = _rows(gpu, "x", x, _BF16, (M, K))
+    _rows(gpu, "weight", weight, _BF16, (K,))
+    sr = st = sy = sqT = ssT = (0,)
+    if residual is not None:
+        sr = _rows(gpu, "residual", residual, _BF16, (M, K))
+        if total is None:
+            total = x.new_empty((M, K))
+        st = _rows(gpu, "total", total, _BF16, (M, K))
+    elif total is not None and total is not x:
+        raise ValueError("total: there is none without a residual (the sum is x)")
+    if rstd is None:
+        rstd = x.new_empty(M, dtype=_F32)
+    _rows(gpu, "rstd", rstd, _F32, (M,))
+    if y is True:
+        y = x.new_empty((M, K))
+    elif y is False:
+        y = None
+    if y is not None:
+        sy = _rows(gpu, "y", y, _BF16, (M, K))
+    if q is None:
+        q = x.new_empty((M, K), dtype=_U8)
+    sq = _rows(gpu, "q", q, _U8, (M, K))
+    if scale is None:
+        scale = x.new_empty((M, _up16(K // 32)), dtype=_U8)[:, :K // 32]
+    ss = _rows(gpu, "scale", scale, _U8, (M, K // 32))
+    cap = 0
+    if columns or qT is not None or scaleT is not None:
+        cap = M_cap
+        if cap is None:
+            cap = qT.shape[1] if qT is not None else colwise_capacity(M)
+        if qT is None:
+            qT = x.new_empty((K, cap), dtype=_U8)
+        if scaleT is None:
+            scaleT = x.new_empty((K, _up16(cap // 32)), dtype=_U8)[:, :cap // 32]
+        sqT = _rows(gpu, "qT", qT, _U8, (K, cap))
+        ssT = _rows(gpu, "scaleT", scaleT, _U8, (K, cap // 32))
+    status = load().mx_rms_norm(
+        x.data_ptr(), _stride(sx, M, K), 0 if residual is None else residual.data_ptr(),
+        _stride(sr, M, K), weight.data_ptr(), M, K, eps,
+        0 if residual is None else total.data_ptr(), _stride(st, M, K), rstd.data_ptr(),
+        0 if y is None else y.data_ptr(), _stride(sy, M, K), q.data_ptr(), _stride(sq, M, K),
+        scale.data_ptr(), _stride(ss, M, K // 32), 0 if qT is None else qT.data_ptr(),
+        _stride(sqT, K, cap), cap, 0 if scaleT is None else scaleT.data_ptr(),
+        _stride(ssT, K, cap // 32), _raw_stream(gpu))
+    if status:
+        _check(status)
+    return x if residual is None else total, rstd, y, q, scale, qT, scaleT
+
+
+def mx_rms_norm_backward(dy, total, rstd, weight, dtotal=None, dx=None, dw=True, workspace=None):
+    """Gradients of mx_rms_norm from that of y (BF16 [M, K]): (dx, dw).
+
+    total, rstd: the forward call's; dtotal: the gradient of total that comes past the
+    norm, or None.  dx BF16 [M, K], of x and of residual alike, may be dy or dtotal; dw
+    float32 [K] (True allocates it, a tensor receives it; None or False skips it)."""
+    (M, K), gpu = dy.shape, _current_gpu()
+    sy = _rows(gpu, "dy", dy, _BF16, (M, K))
+    st = _rows(gpu, "total", total, _BF16, (M, K))
+    _rows(gpu, "rstd", rstd, _F32, (M,))
+    _rows(gpu, "weight", weight, _BF16, (K,))
+    sd = (0,) if dtotal is None else _rows(gpu, "dtotal", dtotal, _BF16, (M, K))
+    if dx is None:
+        dx = dy.new_empty((M, K))
+    sx = _rows(gpu, "dx", dx, _BF16, (M, K))
+    ws = size = 0
+    if dw is True:
+        dw = dy.new_empty(K, dtype=_F32)
+    elif dw is False:
+        dw = None
+    if dw is not None:
+        _rows(gpu, "dw", dw, _F32, (K,))
+        if workspace is None:
+            workspace = dy.new_empty(_latent_workspace(WS_NORM_BACKWARD, M, K, 0, 0), dtype=_U8)
+        size = workspace.numel()
+        _rows(gpu, "workspace", workspace, _U8, (size,))
+        ws = workspace.data_ptr()
+    status = load().mx_rms_norm_backward(
+        dy.data_ptr(), _stride(sy, M, K), total.data_ptr(), _stride(st, M, K), rstd.data_ptr(),
+        weight.data_ptr(), 0 if dtotal is None else dtotal.data_ptr(), _stride(sd, M, K), M, K,
+        dx.data_ptr(), _stride(sx, M, K), 0 if dw is None else dw.data_ptr(), ws, size,
+        _raw_stream(gpu))
+    if status:
+        _check(status)
+    return dx, dw
+
+
+def _stack(gpu, name, w, scale, groups, rows, cols):
+    """(row, scale row, expert, scale expert) strides of codes [E, rows, cols] and their scales."""
+    sw = _rows(gpu, name, w, _U8, (groups, rows, cols))
+    ss = _rows(gpu, name + " scales", scale, _U8, (groups, rows, cols // 32))
+    return (sw[1] if rows > 1 else _up16(cols), ss[1] if rows > 1 else cols // 32,
+            sw[0] if groups > 1 else 0, ss[0] if groups > 1 else 0)
+
+
+def mx_grouped_gemm_swiglu_backward(dy, dy_scale, wT, wT_scale, gu, offsets, dgu=False,
+                                    accum=ACC_MFMA_FP8, M_cap=None, q=None, scale=None, qT=None,
+                                    scaleT=None, offsets_padded=None):
+    """Gradient of mx_grouped_gemm_swiglu's gate/up product from the experts' output's.
+
+    dy [M, K] codes with scales [M, K/32] (row copy of the output's gradient); wT
+    [E, F, K] codes with scales [E, F, K/32]: the transposed down weights, e.g.
+    expert_view of their column copies; gu BF16 [M, 2F] from the forward pass; offsets int64
+    [E+1] on the device.  ``dgu``: True allocates the gradient in BF16 as well, a tensor
+    receives it.  Returns (dgu or None, q [M, 2F], scale [M, 2F/32], qT [2F, M_cap], scaleT
+    [2F, M_cap/32], offsets_padded [E+1])."""
+    M, K = dy.shape
+    E, F, _ = wT.shape
+    gpu = _current_gpu()
+    sd = _rows(gpu, "dy", dy, _U8, (M, K))
+    ssd = _rows(gpu, "dy scales", dy_scale, _U8, (M, K // 32))
+    w = _stack(gpu, "wT", wT, wT_scale, E, F, K)
+    sg = _rows(gpu, "gu", gu, _BF16, (M, 2 * F))
+    _rows(gpu, "offsets", offsets, _I64, (E + 1,))
+    if M_cap is None:
+        M_cap = qT.shape[1] if qT is not None else colwise_capacity(M, E)
+    so = (0,)
+    if dgu is True:
+        dgu = gu.new_empty((M, 2 * F))
+    elif dgu is False:
+        dgu = None
+    if dgu is not None:
+        so = _rows(gpu, "dgu", dgu, _BF16, (M, 2 * F))
+    if q is None:
+        q = gu.new_empty((M, 2 * F), dtype=_U8)
+    if scale is None:
+        scale = gu.new_empty((M, _up16(F // 16)), dtype=_U8)[:, :F // 16]
+    if qT is None:
+        qT = gu.new_empty((2 * F, M_cap), dtype=_U8)
+    if scaleT is None:
+        scaleT = gu.new_empty((2 * F, _up16(M_cap // 32)), dtype=_U8)[:, :M_cap // 32]
+    if offsets_padded is None:
+        offsets_padded = offsets.new_empty(E + 1)
+    sq = _rows(gpu, "q", q, _U8, (M, 2 * F))
+    ss = _rows(gpu, "scale", scale, _U8, (M, F // 16))
+    sqT = _rows(gpu, "qT", qT, _U8, (2 * F, M_cap))
+    ssT = _rows(gpu, "scaleT", scaleT, _U8, (2 * F, M_cap // 32))
+    _rows(gpu, "offsets_padded", offsets_padded, _I64, (E + 1,))
+    status = load().mx_grouped_gemm_swiglu_backward(
+        dy.data_ptr(), dy_scale.data_ptr(), _stride(sd, M, _up16(K)), _stride(ssd, M, K // 32),
+        wT.data_ptr(), wT_scale.data_ptr(), *w, offsets.data_ptr(), E, M, F, K, gu.data_ptr(),
+        _stride(sg, M, 2 * F), 0 if dgu is None else dgu.data_ptr(), _stride(so, M, 2 * F),
+        q.data_ptr(), _stride(sq, M, 2 * F), scale.data_ptr(), _stride(ss, M, F // 16),
+        qT.data_ptr(), sqT[0], scaleT.data_ptr(), ssT[0], M_cap, offsets_padded.data_ptr(), accum,
+        _raw_stream(gpu))
+    if status:
+        _check(status)
+    return dgu, q, scale, qT, scaleT, offsets_padded
+
+
+def mx_gated_ffn_decode(x, x_scale, w_gu, w_gu_scale, w_down, w_down_scale, offsets=None, y=None,
+                        workspace=None):
+    """The gated feed-forward block of few tokens: y = MX(silu(g) u) W_down^T, g and u the
+    halves of the gate/up product.
+
+    x [M, K] codes with scales [M, K/32]; w_gu [E, 2F, K] (gate rows first) and w_down
+    [E, N, F] codes with their scales, any row and expert strides; offsets int64 [E+1]
+    on the device (None: E = 1, all rows).  Returns y BF16 [M, N]; rows outside every
+    group are left as they are."""
+    M, K = x.shape
+    E, F2, _ = w_gu.shape
+    N, F = w_down.shape[1], F2 // 2
+    gpu = _current_gpu()
+    sx = _rows(gpu, "x", x, _U8, (M, K))
+    ss = _rows(gpu, "x scales", x_scale, _U8, (M, K // 32))
+    gu = _stack(gpu, "w_gu", w_gu, w_gu_scale, E, 2 * F, K)
+    down = _stack(gpu, "w_down", w_down, w_down_scale, E, N, F)
+    if offsets is not None:
+        _rows(gpu, "offsets", offsets, _I64, (E + 1,))
+    if y is None:
+        y = x.new_empty((M, N), dtype=_BF16)
+    sy = _rows(gpu, "y", y, _BF16, (M, N))
+    if workspace is None:
+        workspace = x.new_empty(_latent_workspace(WS_FFN_DECODE, M, F, 0, 0), dtype=_U8)
+    _rows(gpu, "workspace", workspace, _U8, (workspace.numel(),))
+    status = load().mx_gated_ffn_decode(
+        x.data_ptr(), x_scale.data_ptr(), _stride(sx, M, _up16(K)), _stride(ss, M, K // 32),
+        w_gu.data_ptr(), w_gu_scale.data_ptr(), *gu, w_down.data_ptr(), w_down_scale.data_ptr(),
+        *down, 0 if offsets is None else offsets.data_ptr(), E, M, K, F, N, y.data_ptr(),
+        _stride(sy, M, N), workspace.data_ptr(), workspace.numel(), _raw_stream(gpu))
+    if status:
+        _check(status)
+    return y
 
 
 def validate_offsets(offsets, M):

@@ -1,6 +1,6 @@
 /*
- * mxq.h — MX-FP8 block quantization, (grouped) GEMM and latent attention on
- * AMD MI355X (gfx950).
+ * mxq.h — MX-FP8 block quantization, (grouped) GEMM, latent attention and the
+ * norms and gated feed-forward steps between them on AMD MI355X (gfx950).
  *
  * C ABI of libmxq.so.  Every pointer argument marked "device" is an address in
  * GPU memory; the library never allocates, frees or keeps any caller buffer.
@@ -523,6 +523,84 @@ MXQ_API int mx_grouped_gemm_swiglu(const uint8_t* a, const uint8_t* a_scale, int
                            hipStream_t stream);
 
 /*
+ * Gradient of the routed experts' gate/up product from that of the experts'
+ * output: the down product's data gradient with SwiGLU's gradient and the MX
+ * quantization in the epilogue (the backward pass of mx_grouped_gemm_swiglu; the
+ * producer of the operands of the gate/up weight gradient and of the
+ * data gradient below it).
+ *   For each group e with rows [offsets[e], offsets[e+1]), g = gu[:, :F], u = gu[:, F:]:
+ *     dh = dY[rows, :] . W_e  (FP32 sums),  sg = 1 / (1 + e^-g),
+ *     dgu = [dh * u * sg * (1 + g * (1 - sg)) | dh * g * sg],  in FP32,
+ *   MX-quantized as mx_quantize_dual would quantize it, from the FP32 values.
+ *   dy, dy_scale : device, [M, K] codes / [M, K/32] scales of the output's
+ *                 gradient (row copy), strides ldd, ldsd.
+ *   wT, wT_scale : device, per expert e the [F, K] codes of the transposed down
+ *                 weight, blocked along K, at wT + e*w_estride, row stride ldw,
+ *                 and its scales at wT_scale + e*ws_estride, row stride ldsw (the
+ *                 column copy of the [E*K, F] weights, one group per expert:
+ *                 w_estride = K, ws_estride = K/32).
+ *   offsets     : device int64 [E+1] expert row ranges, as for mx_quantize_colwise.
+ *   gu          : device, BF16 [M, 2F], row stride ldgu: the forward pass's
+ *                 gate/up product.
+ *   dgu         : device BF16 [M, 2F] (row stride lddgu) receiving the gradient
+ *                 rounded to BF16, or NULL.
+ *   q, scale    : device, its row copy: codes [M, 2F] (ldq), scales [M, 2F/32] (lds).
+ *   qT, scaleT  : device, its grouped column copy: codes [2F, M_cap] (ldqT), scales
+ *                 [2F, M_cap/32] (ldsT), each group zero-padded to a multiple of
+ *                 32 rows; columns in [padded total, M_cap) are zero-filled;
+ *                 M_cap >= M + 31*E when M > 0 (else MXQ_ERR_SHAPE).
+ *   offsets_padded : device int64 [E+1] receiving the padded offsets, or NULL.
+ *   accum       : as for mx_grouped_gemm.
+ * Requires F % 32 == 0, K % 32 == 0, M_cap % 32 == 0; ldq and ldqT multiples of 16
+ * and ldgu, lddgu of 8, with 16-byte aligned q, qT, gu and dgu; the operand
+ * requirements of mx_grouped_gemm.  Rows outside every group are not written in
+ * q, scale and dgu.  F == 0 is a no-op; with M == 0 only offsets_padded and the
+ * column copy's zeros are written.
+ */
+MXQ_API int mx_grouped_gemm_swiglu_backward(
+    const uint8_t* dy, const uint8_t* dy_scale, int64_t ldd, int64_t ldsd, const uint8_t* wT,
+    const uint8_t* wT_scale, int64_t ldw, int64_t ldsw, int64_t w_estride, int64_t ws_estride,
+    const int64_t* offsets, int32_t E, int64_t M, int64_t F, int64_t K, const uint16_t* gu,
+    int64_t ldgu, void* dgu, int64_t lddgu, uint8_t* q, int64_t ldq, uint8_t* scale, int64_t lds,
+    uint8_t* qT, int64_t ldqT, uint8_t* scaleT, int64_t ldsT, int64_t M_cap,
+    int64_t* offsets_padded, int accum, hipStream_t stream);
+
+/*
+ * The whole gated feed-forward block of few tokens (decoding): per group e with rows
+ * [offsets[e], offsets[e+1])
+ *   h = silu(g) * u of the gate/up product (FP32), MX-quantized row-wise,
+ *   y[rows, :] = h . W_down,eT,
+ * as mx_grouped_gemm_swiglu and mx_grouped_gemm with MXQ_ACC_FP32 would form them:
+ * products exact, sums FP32, y rounded to BF16 once.  For any number of rows, but
+ * made for a few per group: each 64 rows of a group read its weights again.
+ *   x, x_scale  : device, [M, K] codes / [M, K/32] scales, strides ldx, ldsx.
+ *   w_gu, w_gu_scale : device, per expert the [2F, K] gate/up codes (gate rows
+ *                 [0, F)) at w_gu + e*gu_estride, row stride ldgu, and their scales
+ *                 at w_gu_scale + e*gus_estride, row stride ldsgu.
+ *   w_down, w_down_scale : device, per expert the [N, F] down codes at w_down +
+ *                 e*d_estride, row stride ldd, scales likewise (ds_estride, ldsd).
+ *   offsets     : device int64 [E+1], non-decreasing within [0, M], E at most
+ *                 256; or NULL: one group of all rows (E = 1).
+ *   y           : device, BF16 [M, N], row stride ldy.
+ *   workspace   : device scratch of at least mxq_workspace_size(MXQ_WS_FFN_DECODE,
+ *                 M, F, 0, 0) bytes, 16-byte aligned.
+ * Requires K % 32 == 0, F % 32 == 0; code row and expert strides multiples of 16
+ * with 16-byte aligned codes; scales have no alignment rule.  M <=
+ * MXQ_FFN_DECODE_MAX_ROWS; K, F, N <= MXQ_FFN_DECODE_MAX_DIM.  Rows outside every
+ * group are not written.  M == 0 or N == 0 is a no-op; K == 0 or F == 0 writes zeros.
+ */
+#define MXQ_FFN_DECODE_MAX_ROWS (1 << 20)
+#define MXQ_FFN_DECODE_MAX_DIM (1 << 20)
+MXQ_API int mx_gated_ffn_decode(const uint8_t* x, const uint8_t* x_scale, int64_t ldx,
+                        int64_t ldsx, const uint8_t* w_gu, const uint8_t* w_gu_scale,
+                        int64_t ldgu, int64_t ldsgu, int64_t gu_estride, int64_t gus_estride,
+                        const uint8_t* w_down, const uint8_t* w_down_scale, int64_t ldd,
+                        int64_t ldsd, int64_t d_estride, int64_t ds_estride,
+                        const int64_t* offsets, int32_t E, int64_t M, int64_t K, int64_t F,
+                        int64_t N, uint16_t* y, int64_t ldy, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+
+/*
  * Grouped MX GEMM with variable K (MoE weight gradient, contraction over the
  * tokens of each expert; [HP329] §8 wgrad row, [TTNPU] grouped MX quant for
  * wgrad).  Operands come from mx_quantize_colwise with the same offsets:
@@ -608,6 +686,66 @@ MXQ_API int fp8_grouped_gemm_wgrad_per_group(const uint8_t* at, const float* a_s
                                      int64_t N, int64_t K,
                                      void* c, int64_t ldc, int out_dtype, int accum,
                                      hipStream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * Root-mean-square norm                                                     *
+ * ------------------------------------------------------------------------ */
+
+/*
+ * The norm before a product, with the residual's addition before it and the
+ * product's MX operand after it, from one read:
+ *   s = x + residual, rounded to BF16 (x itself without a residual),
+ *   rstd = 1 / sqrt(mean_k s^2 + eps),   y = s * rstd * weight  (FP32),
+ * and y MX-quantized as mx_quantize_dual (rows, or rows and columns) would
+ * quantize it, from the FP32 values.  The squares are summed in FP64.
+ *   x        : device, BF16 [M, K], row stride ldx elements (a column range of a
+ *              wider matrix, for one).
+ *   residual : device, BF16 [M, K], row stride ldr, or NULL.
+ *   weight   : device, BF16 [K].
+ *   eps      : > 0, finite.
+ *   total    : device, BF16 [M, K], row stride ldt, receiving s; may be x or
+ *              residual, with its stride.  Not used (may be NULL) without a residual.
+ *   rstd     : device float [M].
+ *   y        : device, BF16 [M, K], row stride ldy, receiving y rounded to BF16,
+ *              or NULL.
+ *   q, scale : device, y's row copy: codes [M, K] (ldq), scales [M, K/32] (lds).
+ *   qT, scaleT : device, y's column copy as one group: codes [K, M_cap] (ldqT),
+ *              scales [K, M_cap/32] (ldsT), columns in [M, M_cap) zero-filled; M_cap a
+ *              multiple of 32, at least M.  qT NULL: no column copy.
+ * Requires K % 32 == 0; ldx, ldr, ldt, ldy multiples of 8, ldq and ldqT of 16; all
+ * pointers but rstd, scale and scaleT 16-byte aligned.  M <= MXQ_NORM_MAX_ROWS, K <=
+ * MXQ_NORM_MAX_COLS.  Outputs other than total must not overlap inputs.  K == 0
+ * is a no-op, M == 0 writes only the column copy's zeros.
+ */
+#define MXQ_NORM_MAX_ROWS (1 << 25)
+#define MXQ_NORM_MAX_COLS 16384
+MXQ_API int mx_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr,
+                const uint16_t* weight, int64_t M, int64_t K, float eps, uint16_t* total,
+                int64_t ldt, float* rstd, uint16_t* y, int64_t ldy, uint8_t* q, int64_t ldq,
+                uint8_t* scale, int64_t lds, uint8_t* qT, int64_t ldqT, int64_t M_cap,
+                uint8_t* scaleT, int64_t ldsT, hipStream_t stream);
+
+/*
+ * Gradient of mx_rms_norm (its roundings passed over):
+ *   dx = rstd * (dy * w - s * rstd * c) + dtotal,  c = mean_k(dy * w * s * rstd),
+ *   dw = sum over the rows of dy * s * rstd.
+ * dx is the gradient of x and of residual alike.
+ *   dy       : device, BF16 [M, K], row stride lddy: the gradient of y.
+ *   total, rstd : the forward call's s (x, without a residual) and rstd.
+ *   dtotal   : device, BF16 [M, K], row stride lddt: the gradient of s that comes
+ *              past the norm, or NULL.
+ *   dx       : device, BF16 [M, K], row stride lddx; may be dy or dtotal, with its stride.
+ *   dw       : device float [K], or NULL for a weight that does not learn.
+ *   workspace : device scratch of at least mxq_workspace_size(MXQ_WS_NORM_BACKWARD,
+ *              M, K, 0, 0) bytes, 16-byte aligned; not used without dw.
+ * Sums are FP32, in an order that does not depend on timing (no atomics).  Sizes,
+ * strides and alignment as for mx_rms_norm.  M == 0 writes only dw's zeros.
+ */
+MXQ_API int mx_rms_norm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* total,
+                         int64_t ldt, const float* rstd, const uint16_t* weight,
+                         const uint16_t* dtotal, int64_t lddt, int64_t M, int64_t K,
+                         uint16_t* dx, int64_t lddx, float* dw, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------ *
  * Latent attention                                                          *
@@ -818,13 +956,16 @@ MXQ_API int latent_attention_backward(const mxq_latent_attn* attn, const uint16_
 /* Workspace kinds: per-tensor quantization (n = elements), per-group
  * quantization (n = rows, a1 = groups), absorbed latent attention (n = B,
  * a1 = S, a2 = H, a3 = max_len), expanded latent attention's gradient (n = Tq,
- * a1 = Tk, a2 = H) and forward pass (n = Tq, a1 = Tk, a2 = H, a3 = B). */
+ * a1 = Tk, a2 = H) and forward pass (n = Tq, a1 = Tk, a2 = H, a3 = B), the norm's
+ * gradient (n = M, a1 = K), the feed-forward block of few tokens (n = M, a1 = F). */
 enum {
   MXQ_WS_PER_TENSOR = 0,
   MXQ_WS_PER_GROUP = 1,
   MXQ_WS_LATENT_DECODE = 2,
   MXQ_WS_LATENT_BACKWARD = 3,
-  MXQ_WS_LATENT_FORWARD = 4
+  MXQ_WS_LATENT_FORWARD = 4,
+  MXQ_WS_NORM_BACKWARD = 5,
+  MXQ_WS_FFN_DECODE = 6
 };
 
 /* Workspace bytes an operation needs (0 if none). */
