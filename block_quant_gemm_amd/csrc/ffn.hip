@@ -219,42 +219,36 @@ static int check_codes(const uint8_t* q, const uint8_t* s, int64_t ld, int64_t l
   return ld % 16 == 0 && aligned(q, 16) ? MXQ_OK : MXQ_ERR_ALIGN;
 }
 
-extern "C" int mx_gated_ffn_decode(const uint8_t* x, const uint8_t* x_scale, int64_t ldx,
-                                   int64_t ldsx, const uint8_t* w_gu, const uint8_t* w_gu_scale,
-                                   int64_t ldgu, int64_t ldsgu, int64_t gu_estride,
-                                   int64_t gus_estride, const uint8_t* w_down,
-                                   const uint8_t* w_down_scale, int64_t ldd, int64_t ldsd,
-                                   int64_t d_estride, int64_t ds_estride, const int64_t* offsets,
-                                   int32_t E, int64_t M, int64_t K, int64_t F, int64_t N,
-                                   uint16_t* y, int64_t ldy, void* workspace,
-                                   size_t workspace_bytes, hipStream_t stream) {
+extern "C" int mx_gated_ffn_decode(const mxq_ffn_decode* ffn, hipStream_t stream) {
+  if (!ffn) return MXQ_ERR_NULL;
+  const mxq_ffn_decode& f = *ffn;
+  const int64_t M = f.M, K = f.K, F = f.F, N = f.N;
+  const int32_t E = f.E;
   if (M < 0 || K < 0 || F < 0 || N < 0 || M > MXQ_FFN_DECODE_MAX_ROWS ||
       K > MXQ_FFN_DECODE_MAX_DIM || F > MXQ_FFN_DECODE_MAX_DIM || N > MXQ_FFN_DECODE_MAX_DIM)
     return MXQ_ERR_SHAPE;
-  if (offsets ? E < 1 || E > 256 : E != 1) return MXQ_ERR_SHAPE;
+  if (f.offsets ? E < 1 || E > 256 : E != 1) return MXQ_ERR_SHAPE;
   if (K % 32 != 0 || F % 32 != 0) return MXQ_ERR_SHAPE;
   if (M == 0 || N == 0) return MXQ_OK;
   int st;
   if (K > 0 && F > 0) {
-    if ((st = check_codes(x, x_scale, ldx, ldsx, K))) return st;
-    if ((st = check_codes(w_gu, w_gu_scale, ldgu, ldsgu, K))) return st;
+    if ((st = check_codes(f.x, f.x_scale, f.ldx, f.ldsx, K))) return st;
+    if ((st = check_codes(f.w_gu, f.w_gu_scale, f.ldgu, f.ldsgu, K))) return st;
   }
-  if (F > 0 && (st = check_codes(w_down, w_down_scale, ldd, ldsd, F))) return st;
-  if (!y) return MXQ_ERR_NULL;
-  if (ldy < N || ldy > kMaxStride) return MXQ_ERR_SHAPE;
-  if (!aligned(y, 2)) return MXQ_ERR_ALIGN;
-  if (gu_estride < 0 || gus_estride < 0 || d_estride < 0 || ds_estride < 0 ||
-      gu_estride > kMaxStride || gus_estride > kMaxStride || d_estride > kMaxStride ||
-      ds_estride > kMaxStride)
-    return MXQ_ERR_SHAPE;
-  if (gu_estride % 16 != 0 || d_estride % 16 != 0) return MXQ_ERR_ALIGN;
-  if (F > 0 && !workspace) return MXQ_ERR_NULL;
-  if (!aligned(workspace, 16)) return MXQ_ERR_ALIGN;
-  if (workspace_bytes < ffn_decode_workspace(M, F)) return MXQ_ERR_WORKSPACE;
-  uint8_t* hq = static_cast<uint8_t*>(workspace);
-  uint8_t* hs = hq + M * F;
-  FfnArgs a{x, x_scale, ldx, ldsx, w_gu, w_gu_scale, ldgu, ldsgu, gu_estride, gus_estride,
-            offsets, M, (uint32_t)(K / 32), F, hq, hs, F, F / 32, y, ldy, N};
+  if (F > 0 && (st = check_codes(f.w_down, f.w_down_scale, f.ldd, f.ldsd, F))) return st;
+  if (!f.y) return MXQ_ERR_NULL;
+  if (f.ldy < N || f.ldy > kMaxStride) return MXQ_ERR_SHAPE;
+  if (!aligned(f.y, 2)) return MXQ_ERR_ALIGN;
+  for (const int64_t s : {f.gu_estride, f.gus_estride, f.d_estride, f.ds_estride})
+    if (s < 0 || s > kMaxStride) return MXQ_ERR_SHAPE;
+  if (f.gu_estride % 16 != 0 || f.d_estride % 16 != 0) return MXQ_ERR_ALIGN;
+  if (F > 0 && !f.workspace) return MXQ_ERR_NULL;
+  if (!aligned(f.workspace, 16)) return MXQ_ERR_ALIGN;
+  if (f.workspace_bytes < ffn_decode_workspace(M, F)) return MXQ_ERR_WORKSPACE;
+  uint8_t* hq = static_cast<uint8_t*>(f.workspace);
+  FfnArgs a{f.x, f.x_scale, f.ldx, f.ldsx, f.w_gu, f.w_gu_scale, f.ldgu, f.ldsgu, f.gu_estride,
+            f.gus_estride, f.offsets, M, (uint32_t)(K / 32), F, hq, hq + M * F, F, F / 32, f.y,
+            f.ldy, N};
   const int64_t per = M / E;
   const int T = E == 1 ? (M <= 16 ? 1 : M <= 32 ? 2 : 4) : (per <= 8 ? 1 : per <= 16 ? 2 : 4);
   if (F > 0) {
@@ -264,8 +258,8 @@ extern "C" int mx_gated_ffn_decode(const uint8_t* x, const uint8_t* x_scale, int
     else hipLaunchKernelGGL(k_ffn_gate<4>, grid, block, 0, stream, a);
     if (hipGetLastError() != hipSuccess) return MXQ_ERR_HIP;
   }
-  a.w = w_down; a.ws = w_down_scale; a.ldw = ldd; a.ldws = ldsd;
-  a.w_estride = d_estride; a.ws_estride = ds_estride;
+  a.w = f.w_down; a.ws = f.w_down_scale; a.ldw = f.ldd; a.ldws = f.ldsd;
+  a.w_estride = f.d_estride; a.ws_estride = f.ds_estride;
   a.nblk = (uint32_t)(F / 32);
   const dim3 grid((uint32_t)((N + 15) / 16), (uint32_t)E);
 #define MXQ_DOWN(T, NW) hipLaunchKernelGGL((k_ffn_down<T, NW>), grid, dim3(NW * 64), 0, stream, a)

@@ -14,20 +14,6 @@ namespace mxq {
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
-struct NormArgs {
-  const uint16_t* x; int64_t ldx;
-  const uint16_t* r; int64_t ldr;                   // residual, or null
-  const uint16_t* w;
-  uint16_t* s; int64_t lds_;                        // the sum, or null without a residual
-  float* rstd;
-  uint16_t* y; int64_t ldy;                         // BF16 output, or null
-  uint8_t* q; int64_t ldq; uint8_t* sc; int64_t ldsc;
-  uint8_t* qT; int64_t ldqT, cap; uint8_t* scT; int64_t ldscT;   // column copy, or null
-  int64_t M;
-  uint32_t K;
-  float eps;
-};
-
 __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
   f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
   f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
@@ -91,7 +77,7 @@ __device__ __forceinline__ void normed8(uint4 s, float rstd, uint4 w, float (&y)
 // once.  Lane l of wavefront v holds elements 8 (64 (W c + v) + l) .. + 8 of
 // chunk c.
 template <int W, int CH>
-__global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_rows(NormArgs g) {
+__global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_rows(mxq_norm g) {
   constexpr int ROWS = W >= 4 ? 1 : 4 / W;          // rows a workgroup
   __shared__ double s_part[W > 1 ? W : 1];
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
@@ -107,11 +93,11 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_rows(NormArgs g) 
     s[c] = col[c] < g.K ? *reinterpret_cast<const uint4*>(g.x + row * g.ldx + col[c])
                         : make_uint4(0, 0, 0, 0);
   }
-  if (g.r) {
+  if (g.residual) {
     uint4 r[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      r[c] = col[c] < g.K ? *reinterpret_cast<const uint4*>(g.r + row * g.ldr + col[c])
+      r[c] = col[c] < g.K ? *reinterpret_cast<const uint4*>(g.residual + row * g.ldr + col[c])
                           : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -121,7 +107,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_rows(NormArgs g) 
 #pragma unroll
       for (int i = 0; i < 8; ++i) a[i] += b[i];
       s[c] = pack8(a);
-      if (col[c] < g.K) *reinterpret_cast<uint4*>(g.s + row * g.lds_ + col[c]) = s[c];
+      if (col[c] < g.K) *reinterpret_cast<uint4*>(g.total + row * g.ldt + col[c]) = s[c];
     }
   }
 #pragma unroll
@@ -139,19 +125,19 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_rows(NormArgs g) 
 #pragma unroll
     for (int i = 0; i < W; ++i) ss += s_part[i];
   }
-  const float rstd = rstd_of(ss, g.K, g.eps);
+  const float rstd = rstd_of(ss, (uint32_t)g.K, g.eps);
   if (lane == 0 && v == 0) g.rstd[row] = rstd;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const bool ok = col[c] < g.K;
-    const uint4 w = ok ? *reinterpret_cast<const uint4*>(g.w + col[c]) : make_uint4(0, 0, 0, 0);
+    const uint4 w = ok ? *reinterpret_cast<const uint4*>(g.weight + col[c]) : make_uint4(0, 0, 0, 0);
     float y[8];
     normed8(s[c], rstd, w, y);
     uint32_t code;
     const uint2 q = quant8_f32(y, code);            // all four lanes of a quad take part
     if (ok) {
       *reinterpret_cast<uint2*>(g.q + row * g.ldq + col[c]) = q;
-      if ((lane & 3u) == 0u) g.sc[row * g.ldsc + (col[c] >> 5)] = (uint8_t)code;
+      if ((lane & 3u) == 0u) g.scale[row * g.lds + (col[c] >> 5)] = (uint8_t)code;
       if (g.y) *reinterpret_cast<uint4*>(g.y + row * g.ldy + col[c]) = pack8(y);
     }
   }
@@ -162,18 +148,18 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_rows(NormArgs g) 
 // codes leave as 128-byte rows of the transpose.
 constexpr int kNcRows = 128, kNcCols = 64, kNcLd = kNcCols + 1;
 
-__global__ __launch_bounds__(256) void k_norm_columns(NormArgs g) {
+__global__ __launch_bounds__(256) void k_norm_columns(mxq_norm g) {
   __shared__ float tile[kNcRows * kNcLd];
   __shared__ __attribute__((aligned(16))) uint8_t outq[kNcCols * (kNcRows + 16)];
   __shared__ uint8_t outs[kNcCols * 4];
-  const uint32_t nk = (g.K + kNcCols - 1) / kNcCols;
+  const uint32_t nk = ((uint32_t)g.K + kNcCols - 1) / kNcCols;
   const int64_t p0 = (int64_t)(blockIdx.x / nk) * kNcRows;
   const uint32_t k0 = blockIdx.x % nk * kNcCols;
-  const uint16_t* s = g.r ? g.s : g.x;
-  const int64_t ld = g.r ? g.lds_ : g.ldx;
+  const uint16_t* s = g.residual ? g.total : g.x;
+  const int64_t ld = g.residual ? g.ldt : g.ldx;
   const int tid = threadIdx.x, chunk = tid & 7;
   const uint32_t k = k0 + chunk * 8;
-  const uint4 w = k < g.K ? *reinterpret_cast<const uint4*>(g.w + k) : make_uint4(0, 0, 0, 0);
+  const uint4 w = k < g.K ? *reinterpret_cast<const uint4*>(g.weight + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int i = u * 32 + (tid >> 3);
@@ -209,34 +195,21 @@ __global__ __launch_bounds__(256) void k_norm_columns(NormArgs g) {
   for (int it = 0; it < 2; ++it) {
     const int cc = it * 32 + (tid >> 3), c16 = tid & 7;
     const int64_t p = p0 + c16 * 16;
-    if (k0 + cc < g.K && p < g.cap)
+    if (k0 + cc < g.K && p < g.M_cap)
       *reinterpret_cast<uint4*>(g.qT + (int64_t)(k0 + cc) * g.ldqT + p) =
           *reinterpret_cast<const uint4*>(&outq[cc * (kNcRows + 16) + c16 * 16]);
   }
   const int cc = tid >> 2, bb = tid & 3;
-  if (k0 + cc < g.K && p0 + bb * 32 < g.cap)
-    g.scT[(int64_t)(k0 + cc) * g.ldscT + (p0 >> 5) + bb] = outs[cc * 4 + bb];
+  if (k0 + cc < g.K && p0 + bb * 32 < g.M_cap)
+    g.scaleT[(int64_t)(k0 + cc) * g.ldsT + (p0 >> 5) + bb] = outs[cc * 4 + bb];
 }
-
-struct NormGradArgs {
-  const uint16_t* dy; int64_t lddy;
-  const uint16_t* s; int64_t lds_;
-  const float* rstd;
-  const uint16_t* w;
-  const uint16_t* ds; int64_t ldds;                 // gradient of the sum, or null
-  uint16_t* dx; int64_t lddx;
-  float* dw;                                        // or null
-  float* part;                                      // [parts, K] sums over a workgroup's rows
-  int64_t M;
-  uint32_t K, parts;
-};
 
 // Workgroup b takes rows b, b + grid, ...; a row is held as in k_norm_rows.
 // dw's sums stay in registers over a wavefront's rows; the workgroup's wavefronts
 // add theirs in order, and k_norm_join the workgroups', so the result
 // does not depend on timing.
 template <int W, int CH>
-__global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_grad(NormGradArgs g) {
+__global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_grad(mxq_norm_grad g) {
   constexpr int ROWS = W >= 4 ? 1 : 4 / W;
   __shared__ float s_part[2][W > 1 ? W : 1];
   __shared__ float s_dw[W > 1 ? 1 : 512 * CH];
@@ -248,7 +221,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_grad(NormGradArgs
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     col[c] = 8u * (64u * (W * c + v) + lane);
-    w[c] = col[c] < g.K ? *reinterpret_cast<const uint4*>(g.w + col[c]) : make_uint4(0, 0, 0, 0);
+    w[c] = col[c] < g.K ? *reinterpret_cast<const uint4*>(g.weight + col[c]) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[c][i] = 0.0f;
   }
@@ -260,8 +233,8 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_grad(NormGradArgs
     for (int c = 0; c < CH; ++c) {
       const bool ok = col[c] < g.K;
       dy[c] = ok ? *reinterpret_cast<const uint4*>(g.dy + row * g.lddy + col[c]) : make_uint4(0, 0, 0, 0);
-      s[c] = ok ? *reinterpret_cast<const uint4*>(g.s + row * g.lds_ + col[c]) : make_uint4(0, 0, 0, 0);
-      ds[c] = ok && g.ds ? *reinterpret_cast<const uint4*>(g.ds + row * g.ldds + col[c])
+      s[c] = ok ? *reinterpret_cast<const uint4*>(g.total + row * g.ldt + col[c]) : make_uint4(0, 0, 0, 0);
+      ds[c] = ok && g.dtotal ? *reinterpret_cast<const uint4*>(g.dtotal + row * g.lddt + col[c])
                          : make_uint4(0, 0, 0, 0);
     }
     const float rstd = g.rstd[row];
@@ -305,7 +278,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_grad(NormGradArgs
     }
   }
   if (!g.dw) return;
-  float* out = g.part + (int64_t)blockIdx.x * g.K;
+  float* out = static_cast<float*>(g.workspace) + (int64_t)blockIdx.x * g.K;
   if (W > 1) {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
@@ -330,14 +303,24 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_grad(NormGradArgs
   }
 }
 
-// dw from the workgroups' sums: 16 columns a workgroup, 16 threads a column.
+// dw from the workgroups' sums: 16 columns a workgroup, 16 threads a column,
+// eight loads in flight each.
 __global__ __launch_bounds__(256) void k_norm_join(const float* part, uint32_t parts, uint32_t K,
                                                    float* dw) {
   __shared__ float s[16][17];
   const uint32_t c = threadIdx.x & 15, t = threadIdx.x >> 4, k = blockIdx.x * 16 + c;
   float a = 0.0f;
   if (k < K)
-    for (uint32_t p = t; p < parts; p += 16) a += part[(int64_t)p * K + k];
+    for (uint32_t p0 = t; p0 < parts; p0 += 128) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t p = p0 + 16 * i;
+        v[i] = p < parts ? part[(int64_t)p * K + k] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a += v[i];
+    }
   s[t][c] = a;
   __syncthreads();
   if (t == 0 && k < K) {
@@ -353,10 +336,12 @@ using namespace mxq;
 
 static inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+constexpr int64_t kMaxStride = INT64_C(1) << 39;
+
 // A row operand of K BF16 values: NULL, stride and alignment.
 static int check_rows(const void* p, int64_t ld, int64_t K) {
   if (!p) return MXQ_ERR_NULL;
-  if (ld < K || ld > (INT64_C(1) << 39)) return MXQ_ERR_SHAPE;
+  if (ld < K || ld > kMaxStride) return MXQ_ERR_SHAPE;
   return ld % 8 == 0 && aligned(p, 16) ? MXQ_OK : MXQ_ERR_ALIGN;
 }
 
@@ -366,35 +351,31 @@ static int check_norm_size(int64_t M, int64_t K) {
   return MXQ_OK;
 }
 
-extern "C" int mx_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr,
-                           const uint16_t* weight, int64_t M, int64_t K, float eps,
-                           uint16_t* total, int64_t ldt, float* rstd, uint16_t* y, int64_t ldy,
-                           uint8_t* q, int64_t ldq, uint8_t* scale, int64_t lds, uint8_t* qT,
-                           int64_t ldqT, int64_t M_cap, uint8_t* scaleT, int64_t ldsT,
-                           hipStream_t stream) {
+extern "C" int mx_rms_norm(const mxq_norm* norm, hipStream_t stream) {
+  if (!norm) return MXQ_ERR_NULL;
+  const mxq_norm& g = *norm;
+  const int64_t M = g.M, K = g.K;
   int st = check_norm_size(M, K);
   if (st) return st;
-  if (!(eps > 0.0f) || !(eps <= 3.4028235e38f)) return MXQ_ERR_ARG;
-  if (qT) {
-    if (M_cap < 0 || M_cap % 32 != 0 || M_cap < (M + 31) / 32 * 32 || M_cap > 2 * MXQ_NORM_MAX_ROWS ||
-        ldqT < M_cap || ldsT < M_cap / 32)
+  if (!(g.eps > 0.0f) || !(g.eps <= 3.4028235e38f)) return MXQ_ERR_ARG;
+  if (g.qT) {
+    if (g.M_cap < 0 || g.M_cap % 32 != 0 || g.M_cap < M || g.M_cap > 2 * (int64_t)MXQ_NORM_MAX_ROWS ||
+        g.ldqT < g.M_cap || g.ldsT < g.M_cap / 32 || g.ldqT > kMaxStride || g.ldsT > kMaxStride)
       return MXQ_ERR_SHAPE;
-    if (!scaleT) return MXQ_ERR_NULL;
-    if (ldqT % 16 != 0 || !aligned(qT, 16)) return MXQ_ERR_ALIGN;
+    if (!g.scaleT) return MXQ_ERR_NULL;
+    if (g.ldqT % 16 != 0 || !aligned(g.qT, 16)) return MXQ_ERR_ALIGN;
   }
-  if (K == 0 || (M == 0 && (!qT || M_cap == 0))) return MXQ_OK;
+  if (K == 0 || (M == 0 && (!g.qT || g.M_cap == 0))) return MXQ_OK;
   if (M > 0) {
-    if ((st = check_rows(x, ldx, K))) return st;
-    if (residual && (st = check_rows(residual, ldr, K))) return st;
-    if (residual && (st = check_rows(total, ldt, K))) return st;
-    if (y && (st = check_rows(y, ldy, K))) return st;
-    if (!weight || !rstd || !q || !scale) return MXQ_ERR_NULL;
-    if (ldq < K || lds < K / 32) return MXQ_ERR_SHAPE;
-    if (!aligned(weight, 16) || !aligned(rstd, 4) || ldq % 16 != 0 || !aligned(q, 16))
+    if ((st = check_rows(g.x, g.ldx, K))) return st;
+    if (g.residual && (st = check_rows(g.residual, g.ldr, K))) return st;
+    if (g.residual && (st = check_rows(g.total, g.ldt, K))) return st;
+    if (g.y && (st = check_rows(g.y, g.ldy, K))) return st;
+    if (!g.weight || !g.rstd || !g.q || !g.scale) return MXQ_ERR_NULL;
+    if (g.ldq < K || g.lds < K / 32 || g.ldq > kMaxStride || g.lds > kMaxStride) return MXQ_ERR_SHAPE;
+    if (!aligned(g.weight, 16) || !aligned(g.rstd, 4) || g.ldq % 16 != 0 || !aligned(g.q, 16))
       return MXQ_ERR_ALIGN;
   }
-  NormArgs g{x, ldx, residual, ldr, weight, total, ldt, rstd, y, ldy, q, ldq, scale, lds,
-             qT, ldqT, M_cap, scaleT, ldsT, M, (uint32_t)K, eps};
 #define MXQ_ROWS(W, CH)                                                                        \
   hipLaunchKernelGGL((k_norm_rows<W, CH>), dim3((uint32_t)(W >= 4 ? M : (M + 3) / 4)),         \
                      dim3(W == 16 ? 1024 : 256), 0, stream, g)
@@ -408,38 +389,35 @@ extern "C" int mx_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* resid
     if (hipGetLastError() != hipSuccess) return MXQ_ERR_HIP;
   }
 #undef MXQ_ROWS
-  if (qT && M_cap > 0) {
-    const int64_t blocks = (M_cap + kNcRows - 1) / kNcRows * ((K + kNcCols - 1) / kNcCols);
+  if (g.qT && g.M_cap > 0) {
+    const int64_t blocks = (g.M_cap + kNcRows - 1) / kNcRows * ((K + kNcCols - 1) / kNcCols);
     hipLaunchKernelGGL(k_norm_columns, dim3((uint32_t)blocks), dim3(256), 0, stream, g);
     if (hipGetLastError() != hipSuccess) return MXQ_ERR_HIP;
   }
   return MXQ_OK;
 }
 
-extern "C" int mx_rms_norm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* total,
-                                    int64_t ldt, const float* rstd, const uint16_t* weight,
-                                    const uint16_t* dtotal, int64_t lddt, int64_t M, int64_t K,
-                                    uint16_t* dx, int64_t lddx, float* dw, void* workspace,
-                                    size_t workspace_bytes, hipStream_t stream) {
+extern "C" int mx_rms_norm_backward(const mxq_norm_grad* grad, hipStream_t stream) {
+  if (!grad) return MXQ_ERR_NULL;
+  const mxq_norm_grad& g = *grad;
+  const int64_t M = g.M, K = g.K;
   int st = check_norm_size(M, K);
   if (st) return st;
-  if (K == 0 || (M == 0 && !dw)) return MXQ_OK;
+  if (K == 0 || (M == 0 && !g.dw)) return MXQ_OK;
   if (M > 0) {
-    if ((st = check_rows(dy, lddy, K))) return st;
-    if ((st = check_rows(total, ldt, K))) return st;
-    if (dtotal && (st = check_rows(dtotal, lddt, K))) return st;
-    if ((st = check_rows(dx, lddx, K))) return st;
-    if (!rstd || !weight) return MXQ_ERR_NULL;
-    if (!aligned(rstd, 4) || !aligned(weight, 16)) return MXQ_ERR_ALIGN;
+    if ((st = check_rows(g.dy, g.lddy, K))) return st;
+    if ((st = check_rows(g.total, g.ldt, K))) return st;
+    if (g.dtotal && (st = check_rows(g.dtotal, g.lddt, K))) return st;
+    if ((st = check_rows(g.dx, g.lddx, K))) return st;
+    if (!g.rstd || !g.weight) return MXQ_ERR_NULL;
+    if (!aligned(g.rstd, 4) || !aligned(g.weight, 16)) return MXQ_ERR_ALIGN;
   }
   const uint32_t parts = norm_backward_parts(M, K);
-  if (dw) {
-    if (!aligned(dw, 4) || !aligned(workspace, 16)) return MXQ_ERR_ALIGN;
-    if (M > 0 && !workspace) return MXQ_ERR_NULL;
-    if (workspace_bytes < norm_backward_workspace(M, K)) return MXQ_ERR_WORKSPACE;
+  if (g.dw) {
+    if (M > 0 && !g.workspace) return MXQ_ERR_NULL;
+    if (!aligned(g.dw, 4) || !aligned(g.workspace, 16)) return MXQ_ERR_ALIGN;
+    if (g.workspace_bytes < norm_backward_workspace(M, K)) return MXQ_ERR_WORKSPACE;
   }
-  NormGradArgs g{dy, lddy, total, ldt, rstd, weight, dtotal, lddt, dx, lddx, dw,
-                 static_cast<float*>(workspace), M, (uint32_t)K, parts};
 #define MXQ_GRAD(W, CH)                                                                        \
   hipLaunchKernelGGL((k_norm_grad<W, CH>), dim3(parts), dim3(W == 16 ? 1024 : 256), 0, stream, g)
   if (M > 0) {
@@ -451,9 +429,9 @@ extern "C" int mx_rms_norm_backward(const uint16_t* dy, int64_t lddy, const uint
     if (hipGetLastError() != hipSuccess) return MXQ_ERR_HIP;
   }
 #undef MXQ_GRAD
-  if (dw) {
-    hipLaunchKernelGGL(k_norm_join, dim3((uint32_t)((K + 15) / 16)), dim3(256), 0, stream, g.part,
-                       M > 0 ? parts : 0u, (uint32_t)K, dw);
+  if (g.dw) {
+    hipLaunchKernelGGL(k_norm_join, dim3((uint32_t)((K + 15) / 16)), dim3(256), 0, stream,
+                       static_cast<const float*>(g.workspace), M > 0 ? parts : 0u, (uint32_t)K, g.dw);
     if (hipGetLastError() != hipSuccess) return MXQ_ERR_HIP;
   }
   return MXQ_OK;

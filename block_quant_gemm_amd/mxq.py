@@ -115,14 +115,9 @@ _SIGS = {
     "mx_grouped_gemm_swiglu_backward": (ctypes.c_int, [
         _p, _p, _i64, _i64, _p, _p, _i64, _i64, _i64, _i64, _p, _i32, _i64, _i64, _i64, _p, _i64,
         _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i64, _p, ctypes.c_int, _p]),
-    "mx_gated_ffn_decode": (ctypes.c_int, [
-        _p, _p, _i64, _i64, _p, _p, _i64, _i64, _i64, _i64, _p, _p, _i64, _i64, _i64, _i64, _p,
-        _i32, _i64, _i64, _i64, _i64, _p, _i64, _p, _sz, _p]),
-    "mx_rms_norm": (ctypes.c_int, [
-        _p, _i64, _p, _i64, _p, _i64, _i64, _f32, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _p,
-        _i64, _i64, _p, _i64, _p]),
-    "mx_rms_norm_backward": (ctypes.c_int, [
-        _p, _i64, _p, _i64, _p, _p, _p, _i64, _i64, _i64, _p, _i64, _p, _p, _sz, _p]),
+    "mx_gated_ffn_decode": (ctypes.c_int, [_p, _p]),
+    "mx_rms_norm": (ctypes.c_int, [_p, _p]),
+    "mx_rms_norm_backward": (ctypes.c_int, [_p, _p]),
     "mxq_workspace_size": (_sz, [ctypes.c_int, _i64, _i64, _i64, _i64]),
     "mxq_latent_backward_rows": (ctypes.c_int, [_i64, _i32, _i32, ctypes.c_int]),
     "mxq_validate_offsets": (ctypes.c_int, [_p, _i32, _i64, _p]),
@@ -974,6 +969,12 @@ def latent_attention_backward(dout, q, k_nope, k_rope, v, o, lse, offsets_q=None
 # norm and gated feed-forward
 # ---------------------------------------------------------------------------
 
+# As above, the marshalling is lean: buffers that a call allocates itself need no check.
+_NORM_STRUCT = struct.Struct("PqPqPPqPPqPqPqPqPqqqqf4x")  # mxq_norm of mxq.h
+_NORM_GRAD_STRUCT = struct.Struct("PqPqPPPqPqPPNqq")       # mxq_norm_grad
+_FFN_STRUCT = struct.Struct("PPqqPPqqqqPPqqqqPPqPNqqqqi4x")  # mxq_ffn_decode
+
+
 def _stride(s, rows, width):
     """The row stride to pass on."""
     return s[0] if rows > 1 else width
@@ -983,61 +984,78 @@ def _up16(n):
     return (n + 15) // 16 * 16
 
 
+def _scales_like(t, rows, cols):
+    """_scale_buffer on t's GPU, and its row stride."""
+    ld = (cols + 15) // 16 * 16
+    s = t.new_empty((rows, ld), dtype=_U8)
+    return (s if ld == cols else s[:, :cols]), ld
+
+
 def mx_rms_norm(x, weight, residual=None, eps=1e-6, y=False, columns=False, M_cap=None, total=None,
                 rstd=None, q=None, scale=None, qT=None, scaleT=None):
     """Root-mean-square norm with the residual's addition and the MX operand of the next
     product: s = x + residual (BF16), y = s / sqrt(mean s^2 + eps) * weight, quantized.
 
     x, residual BF16 [M, K] (residual or None), weight BF16 [K].  ``y``: True allocates
-    y in BF16 as well, a tensor receives it.  ``columns``: the column copy too (for
-    the weight gradient), which qT or scaleT imply.  ``total`` may be x or residual.  Returns (total,
-    rstd float32 [M], y or None, q [M, K], scale [M, K/32], qT [K, M_cap] or None,
+    y in BF16 as well, a tensor receives it.  ``columns``: the column copy too (for the
+    weight gradient), which qT or scaleT imply.  ``total`` may be x or residual.  Returns
+    (total, rstd float32 [M], y or None, q [M, K], scale [M, K/32], qT [K, M_cap] or None,
     scaleT [K, M_cap/32] or None); total is x itself without a residual."""
     (M, K), gpu = x.shape, _current_gpu()
-    sx = _rows(gpu, "x", x, _BF16, (M, K))
+    shape, blocks = (M, K), K // 32
+    ldx = _stride(_rows(gpu, "x", x, _BF16, shape), M, K)
     _rows(gpu, "weight", weight, _BF16, (K,))
-    sr = st = sy = sqT = ssT = (0,)
+    r = t = yp = qTp = sTp = cap = 0
+    ldr = ldt = ldy = ldq = K
+    lds = blocks
+    ldqT = ldsT = 0
     if residual is not None:
-        sr = _rows(gpu, "residual", residual, _BF16, (M, K))
+        ldr, r = _stride(_rows(gpu, "residual", residual, _BF16, shape), M, K), residual.data_ptr()
         if total is None:
-            total = x.new_empty((M, K))
-        st = _rows(gpu, "total", total, _BF16, (M, K))
+            total = x.new_empty(shape)
+        else:
+            ldt = _stride(_rows(gpu, "total", total, _BF16, shape), M, K)
+        t = total.data_ptr()
     elif total is not None and total is not x:
         raise ValueError("total: there is none without a residual (the sum is x)")
     if rstd is None:
         rstd = x.new_empty(M, dtype=_F32)
-    _rows(gpu, "rstd", rstd, _F32, (M,))
+    else:
+        _rows(gpu, "rstd", rstd, _F32, (M,))
     if y is True:
-        y = x.new_empty((M, K))
+        y = x.new_empty(shape)
     elif y is False:
         y = None
+    elif y is not None:
+        ldy = _stride(_rows(gpu, "y", y, _BF16, shape), M, K)
     if y is not None:
-        sy = _rows(gpu, "y", y, _BF16, (M, K))
+        yp = y.data_ptr()
     if q is None:
-        q = x.new_empty((M, K), dtype=_U8)
-    sq = _rows(gpu, "q", q, _U8, (M, K))
+        q = x.new_empty(shape, dtype=_U8)
+    else:
+        ldq = _stride(_rows(gpu, "q", q, _U8, shape), M, K)
     if scale is None:
-        scale = x.new_empty((M, _up16(K // 32)), dtype=_U8)[:, :K // 32]
-    ss = _rows(gpu, "scale", scale, _U8, (M, K // 32))
-    cap = 0
+        scale, lds = _scales_like(x, M, blocks)
+    else:
+        lds = _stride(_rows(gpu, "scale", scale, _U8, (M, blocks)), M, blocks)
     if columns or qT is not None or scaleT is not None:
         cap = M_cap
         if cap is None:
             cap = qT.shape[1] if qT is not None else colwise_capacity(M)
+        ldqT = cap
         if qT is None:
             qT = x.new_empty((K, cap), dtype=_U8)
+        else:
+            ldqT = _stride(_rows(gpu, "qT", qT, _U8, (K, cap)), K, cap)
         if scaleT is None:
-            scaleT = x.new_empty((K, _up16(cap // 32)), dtype=_U8)[:, :cap // 32]
-        sqT = _rows(gpu, "qT", qT, _U8, (K, cap))
-        ssT = _rows(gpu, "scaleT", scaleT, _U8, (K, cap // 32))
+            scaleT, ldsT = _scales_like(x, K, cap // 32)
+        else:
+            ldsT = _stride(_rows(gpu, "scaleT", scaleT, _U8, (K, cap // 32)), K, cap // 32)
+        qTp, sTp = qT.data_ptr(), scaleT.data_ptr()
     status = load().mx_rms_norm(
-        x.data_ptr(), _stride(sx, M, K), 0 if residual is None else residual.data_ptr(),
-        _stride(sr, M, K), weight.data_ptr(), M, K, eps,
-        0 if residual is None else total.data_ptr(), _stride(st, M, K), rstd.data_ptr(),
-        0 if y is None else y.data_ptr(), _stride(sy, M, K), q.data_ptr(), _stride(sq, M, K),
-        scale.data_ptr(), _stride(ss, M, K // 32), 0 if qT is None else qT.data_ptr(),
-        _stride(sqT, K, cap), cap, 0 if scaleT is None else scaleT.data_ptr(),
-        _stride(ssT, K, cap // 32), _raw_stream(gpu))
+        _NORM_STRUCT.pack(x.data_ptr(), ldx, r, ldr, weight.data_ptr(), t, ldt, rstd.data_ptr(), yp, ldy,
+                          q.data_ptr(), ldq, scale.data_ptr(), lds, qTp, ldqT, sTp, ldsT, M, K, cap, eps),
+        _raw_stream(gpu))
     if status:
         _check(status)
     return x if residual is None else total, rstd, y, q, scale, qT, scaleT
@@ -1050,30 +1068,37 @@ def mx_rms_norm_backward(dy, total, rstd, weight, dtotal=None, dx=None, dw=True,
     norm, or None.  dx BF16 [M, K], of x and of residual alike, may be dy or dtotal; dw
     float32 [K] (True allocates it, a tensor receives it; None or False skips it)."""
     (M, K), gpu = dy.shape, _current_gpu()
-    sy = _rows(gpu, "dy", dy, _BF16, (M, K))
-    st = _rows(gpu, "total", total, _BF16, (M, K))
+    shape = (M, K)
+    ldy = _stride(_rows(gpu, "dy", dy, _BF16, shape), M, K)
+    ldt = _stride(_rows(gpu, "total", total, _BF16, shape), M, K)
     _rows(gpu, "rstd", rstd, _F32, (M,))
     _rows(gpu, "weight", weight, _BF16, (K,))
-    sd = (0,) if dtotal is None else _rows(gpu, "dtotal", dtotal, _BF16, (M, K))
+    ds = ws = size = dwp = 0
+    ldd = ldx = K
+    if dtotal is not None:
+        ldd, ds = _stride(_rows(gpu, "dtotal", dtotal, _BF16, shape), M, K), dtotal.data_ptr()
     if dx is None:
-        dx = dy.new_empty((M, K))
-    sx = _rows(gpu, "dx", dx, _BF16, (M, K))
-    ws = size = 0
+        dx = dy.new_empty(shape)
+    else:
+        ldx = _stride(_rows(gpu, "dx", dx, _BF16, shape), M, K)
     if dw is True:
         dw = dy.new_empty(K, dtype=_F32)
     elif dw is False:
         dw = None
-    if dw is not None:
+    elif dw is not None:
         _rows(gpu, "dw", dw, _F32, (K,))
+    if dw is not None:
+        dwp = dw.data_ptr()
         if workspace is None:
-            workspace = dy.new_empty(_latent_workspace(WS_NORM_BACKWARD, M, K, 0, 0), dtype=_U8)
-        size = workspace.numel()
-        _rows(gpu, "workspace", workspace, _U8, (size,))
+            size = _latent_workspace(WS_NORM_BACKWARD, M, K, 0, 0)
+            workspace = dy.new_empty(size, dtype=_U8)
+        else:
+            size = workspace.numel()
+            _rows(gpu, "workspace", workspace, _U8, (size,))
         ws = workspace.data_ptr()
     status = load().mx_rms_norm_backward(
-        dy.data_ptr(), _stride(sy, M, K), total.data_ptr(), _stride(st, M, K), rstd.data_ptr(),
-        weight.data_ptr(), 0 if dtotal is None else dtotal.data_ptr(), _stride(sd, M, K), M, K,
-        dx.data_ptr(), _stride(sx, M, K), 0 if dw is None else dw.data_ptr(), ws, size,
+        _NORM_GRAD_STRUCT.pack(dy.data_ptr(), ldy, total.data_ptr(), ldt, rstd.data_ptr(),
+                               weight.data_ptr(), ds, ldd, dx.data_ptr(), ldx, dwp, ws, size, M, K),
         _raw_stream(gpu))
     if status:
         _check(status)
@@ -1083,7 +1108,7 @@ def mx_rms_norm_backward(dy, total, rstd, weight, dtotal=None, dx=None, dw=True,
 def _stack(gpu, name, w, scale, groups, rows, cols):
     """(row, scale row, expert, scale expert) strides of codes [E, rows, cols] and their scales."""
     sw = _rows(gpu, name, w, _U8, (groups, rows, cols))
-    ss = _rows(gpu, name + " scales", scale, _U8, (groups, rows, cols // 32))
+    ss = _rows(gpu, "its scales", scale, _U8, (groups, rows, cols // 32))
     return (sw[1] if rows > 1 else _up16(cols), ss[1] if rows > 1 else cols // 32,
             sw[0] if groups > 1 else 0, ss[0] if groups > 1 else 0)
 
@@ -1109,34 +1134,41 @@ def mx_grouped_gemm_swiglu_backward(dy, dy_scale, wT, wT_scale, gu, offsets, dgu
     _rows(gpu, "offsets", offsets, _I64, (E + 1,))
     if M_cap is None:
         M_cap = qT.shape[1] if qT is not None else colwise_capacity(M, E)
-    so = (0,)
+    ldo = ldq = 2 * F
+    ldqT, out = M_cap, 0
     if dgu is True:
         dgu = gu.new_empty((M, 2 * F))
     elif dgu is False:
         dgu = None
+    elif dgu is not None:
+        ldo = _stride(_rows(gpu, "dgu", dgu, _BF16, (M, 2 * F)), M, 2 * F)
     if dgu is not None:
-        so = _rows(gpu, "dgu", dgu, _BF16, (M, 2 * F))
+        out = dgu.data_ptr()
     if q is None:
         q = gu.new_empty((M, 2 * F), dtype=_U8)
+    else:
+        ldq = _stride(_rows(gpu, "q", q, _U8, (M, 2 * F)), M, 2 * F)
     if scale is None:
-        scale = gu.new_empty((M, _up16(F // 16)), dtype=_U8)[:, :F // 16]
+        scale, lds = _scales_like(gu, M, F // 16)
+    else:
+        lds = _stride(_rows(gpu, "scale", scale, _U8, (M, F // 16)), M, F // 16)
     if qT is None:
         qT = gu.new_empty((2 * F, M_cap), dtype=_U8)
+    else:
+        ldqT = _rows(gpu, "qT", qT, _U8, (2 * F, M_cap))[0]
     if scaleT is None:
-        scaleT = gu.new_empty((2 * F, _up16(M_cap // 32)), dtype=_U8)[:, :M_cap // 32]
+        scaleT, ldsT = _scales_like(gu, 2 * F, M_cap // 32)
+    else:
+        ldsT = _rows(gpu, "scaleT", scaleT, _U8, (2 * F, M_cap // 32))[0]
     if offsets_padded is None:
         offsets_padded = offsets.new_empty(E + 1)
-    sq = _rows(gpu, "q", q, _U8, (M, 2 * F))
-    ss = _rows(gpu, "scale", scale, _U8, (M, F // 16))
-    sqT = _rows(gpu, "qT", qT, _U8, (2 * F, M_cap))
-    ssT = _rows(gpu, "scaleT", scaleT, _U8, (2 * F, M_cap // 32))
-    _rows(gpu, "offsets_padded", offsets_padded, _I64, (E + 1,))
+    else:
+        _rows(gpu, "offsets_padded", offsets_padded, _I64, (E + 1,))
     status = load().mx_grouped_gemm_swiglu_backward(
         dy.data_ptr(), dy_scale.data_ptr(), _stride(sd, M, _up16(K)), _stride(ssd, M, K // 32),
         wT.data_ptr(), wT_scale.data_ptr(), *w, offsets.data_ptr(), E, M, F, K, gu.data_ptr(),
-        _stride(sg, M, 2 * F), 0 if dgu is None else dgu.data_ptr(), _stride(so, M, 2 * F),
-        q.data_ptr(), _stride(sq, M, 2 * F), scale.data_ptr(), _stride(ss, M, F // 16),
-        qT.data_ptr(), sqT[0], scaleT.data_ptr(), ssT[0], M_cap, offsets_padded.data_ptr(), accum,
+        _stride(sg, M, 2 * F), out, ldo, q.data_ptr(), ldq, scale.data_ptr(), lds, qT.data_ptr(), ldqT,
+        scaleT.data_ptr(), ldsT, M_cap, offsets_padded.data_ptr(), accum,
         _raw_stream(gpu))
     if status:
         _check(status)
@@ -1160,19 +1192,25 @@ def mx_gated_ffn_decode(x, x_scale, w_gu, w_gu_scale, w_down, w_down_scale, offs
     ss = _rows(gpu, "x scales", x_scale, _U8, (M, K // 32))
     gu = _stack(gpu, "w_gu", w_gu, w_gu_scale, E, 2 * F, K)
     down = _stack(gpu, "w_down", w_down, w_down_scale, E, N, F)
+    at, ldy = 0, N
     if offsets is not None:
         _rows(gpu, "offsets", offsets, _I64, (E + 1,))
+        at = offsets.data_ptr()
     if y is None:
         y = x.new_empty((M, N), dtype=_BF16)
-    sy = _rows(gpu, "y", y, _BF16, (M, N))
+    else:
+        ldy = _stride(_rows(gpu, "y", y, _BF16, (M, N)), M, N)
     if workspace is None:
-        workspace = x.new_empty(_latent_workspace(WS_FFN_DECODE, M, F, 0, 0), dtype=_U8)
-    _rows(gpu, "workspace", workspace, _U8, (workspace.numel(),))
+        size = _latent_workspace(WS_FFN_DECODE, M, F, 0, 0)
+        workspace = x.new_empty(size, dtype=_U8)
+    else:
+        size = workspace.numel()
+        _rows(gpu, "workspace", workspace, _U8, (size,))
     status = load().mx_gated_ffn_decode(
-        x.data_ptr(), x_scale.data_ptr(), _stride(sx, M, _up16(K)), _stride(ss, M, K // 32),
-        w_gu.data_ptr(), w_gu_scale.data_ptr(), *gu, w_down.data_ptr(), w_down_scale.data_ptr(),
-        *down, 0 if offsets is None else offsets.data_ptr(), E, M, K, F, N, y.data_ptr(),
-        _stride(sy, M, N), workspace.data_ptr(), workspace.numel(), _raw_stream(gpu))
+        _FFN_STRUCT.pack(x.data_ptr(), x_scale.data_ptr(), _stride(sx, M, _up16(K)),
+                         _stride(ss, M, K // 32), w_gu.data_ptr(), w_gu_scale.data_ptr(), *gu,
+                         w_down.data_ptr(), w_down_scale.data_ptr(), *down, at, y.data_ptr(), ldy,
+                         workspace.data_ptr(), size, M, K, F, N, E), _raw_stream(gpu))
     if status:
         _check(status)
     return y

@@ -573,6 +573,7 @@ MXQ_API int mx_grouped_gemm_swiglu_backward(
  * as mx_grouped_gemm_swiglu and mx_grouped_gemm with MXQ_ACC_FP32 would form them:
  * products exact, sums FP32, y rounded to BF16 once.  For any number of rows, but
  * made for a few per group: each 64 rows of a group read its weights again.
+ *   ffn         : host struct, read during the call only:
  *   x, x_scale  : device, [M, K] codes / [M, K/32] scales, strides ldx, ldsx.
  *   w_gu, w_gu_scale : device, per expert the [2F, K] gate/up codes (gate rows
  *                 [0, F)) at w_gu + e*gu_estride, row stride ldgu, and their scales
@@ -591,14 +592,25 @@ MXQ_API int mx_grouped_gemm_swiglu_backward(
  */
 #define MXQ_FFN_DECODE_MAX_ROWS (1 << 20)
 #define MXQ_FFN_DECODE_MAX_DIM (1 << 20)
-MXQ_API int mx_gated_ffn_decode(const uint8_t* x, const uint8_t* x_scale, int64_t ldx,
-                        int64_t ldsx, const uint8_t* w_gu, const uint8_t* w_gu_scale,
-                        int64_t ldgu, int64_t ldsgu, int64_t gu_estride, int64_t gus_estride,
-                        const uint8_t* w_down, const uint8_t* w_down_scale, int64_t ldd,
-                        int64_t ldsd, int64_t d_estride, int64_t ds_estride,
-                        const int64_t* offsets, int32_t E, int64_t M, int64_t K, int64_t F,
-                        int64_t N, uint16_t* y, int64_t ldy, void* workspace,
-                        size_t workspace_bytes, hipStream_t stream);
+typedef struct mxq_ffn_decode {
+  const uint8_t* x;
+  const uint8_t* x_scale;
+  int64_t ldx, ldsx;
+  const uint8_t* w_gu;
+  const uint8_t* w_gu_scale;
+  int64_t ldgu, ldsgu, gu_estride, gus_estride;
+  const uint8_t* w_down;
+  const uint8_t* w_down_scale;
+  int64_t ldd, ldsd, d_estride, ds_estride;
+  const int64_t* offsets;
+  uint16_t* y;
+  int64_t ldy;
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t M, K, F, N;
+  int32_t E;
+} mxq_ffn_decode;
+MXQ_API int mx_gated_ffn_decode(const mxq_ffn_decode* ffn, hipStream_t stream);
 
 /*
  * Grouped MX GEMM with variable K (MoE weight gradient, contraction over the
@@ -698,11 +710,11 @@ MXQ_API int fp8_grouped_gemm_wgrad_per_group(const uint8_t* at, const float* a_s
  *   rstd = 1 / sqrt(mean_k s^2 + eps),   y = s * rstd * weight  (FP32),
  * and y MX-quantized as mx_quantize_dual (rows, or rows and columns) would
  * quantize it, from the FP32 values.  The squares are summed in FP64.
+ *   norm : host struct, read during the call only:
  *   x        : device, BF16 [M, K], row stride ldx elements (a column range of a
  *              wider matrix, for one).
  *   residual : device, BF16 [M, K], row stride ldr, or NULL.
  *   weight   : device, BF16 [K].
- *   eps      : > 0, finite.
  *   total    : device, BF16 [M, K], row stride ldt, receiving s; may be x or
  *              residual, with its stride.  Not used (may be NULL) without a residual.
  *   rstd     : device float [M].
@@ -712,6 +724,7 @@ MXQ_API int fp8_grouped_gemm_wgrad_per_group(const uint8_t* at, const float* a_s
  *   qT, scaleT : device, y's column copy as one group: codes [K, M_cap] (ldqT),
  *              scales [K, M_cap/32] (ldsT), columns in [M, M_cap) zero-filled; M_cap a
  *              multiple of 32, at least M.  qT NULL: no column copy.
+ *   eps      : > 0, finite.
  * Requires K % 32 == 0; ldx, ldr, ldt, ldy multiples of 8, ldq and ldqT of 16; all
  * pointers but rstd, scale and scaleT 16-byte aligned.  M <= MXQ_NORM_MAX_ROWS, K <=
  * MXQ_NORM_MAX_COLS.  Outputs other than total must not overlap inputs.  K == 0
@@ -719,17 +732,36 @@ MXQ_API int fp8_grouped_gemm_wgrad_per_group(const uint8_t* at, const float* a_s
  */
 #define MXQ_NORM_MAX_ROWS (1 << 25)
 #define MXQ_NORM_MAX_COLS 16384
-MXQ_API int mx_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr,
-                const uint16_t* weight, int64_t M, int64_t K, float eps, uint16_t* total,
-                int64_t ldt, float* rstd, uint16_t* y, int64_t ldy, uint8_t* q, int64_t ldq,
-                uint8_t* scale, int64_t lds, uint8_t* qT, int64_t ldqT, int64_t M_cap,
-                uint8_t* scaleT, int64_t ldsT, hipStream_t stream);
+typedef struct mxq_norm {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* residual;
+  int64_t ldr;
+  const uint16_t* weight;
+  uint16_t* total;
+  int64_t ldt;
+  float* rstd;
+  uint16_t* y;
+  int64_t ldy;
+  uint8_t* q;
+  int64_t ldq;
+  uint8_t* scale;
+  int64_t lds;
+  uint8_t* qT;
+  int64_t ldqT;
+  uint8_t* scaleT;
+  int64_t ldsT;
+  int64_t M, K, M_cap;
+  float eps;
+} mxq_norm;
+MXQ_API int mx_rms_norm(const mxq_norm* norm, hipStream_t stream);
 
 /*
  * Gradient of mx_rms_norm (its roundings passed over):
  *   dx = rstd * (dy * w - s * rstd * c) + dtotal,  c = mean_k(dy * w * s * rstd),
  *   dw = sum over the rows of dy * s * rstd.
  * dx is the gradient of x and of residual alike.
+ *   grad : host struct, read during the call only:
  *   dy       : device, BF16 [M, K], row stride lddy: the gradient of y.
  *   total, rstd : the forward call's s (x, without a residual) and rstd.
  *   dtotal   : device, BF16 [M, K], row stride lddt: the gradient of s that comes
@@ -741,11 +773,23 @@ MXQ_API int mx_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* residual
  * Sums are FP32, in an order that does not depend on timing (no atomics).  Sizes,
  * strides and alignment as for mx_rms_norm.  M == 0 writes only dw's zeros.
  */
-MXQ_API int mx_rms_norm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* total,
-                         int64_t ldt, const float* rstd, const uint16_t* weight,
-                         const uint16_t* dtotal, int64_t lddt, int64_t M, int64_t K,
-                         uint16_t* dx, int64_t lddx, float* dw, void* workspace,
-                         size_t workspace_bytes, hipStream_t stream);
+typedef struct mxq_norm_grad {
+  const uint16_t* dy;
+  int64_t lddy;
+  const uint16_t* total;
+  int64_t ldt;
+  const float* rstd;
+  const uint16_t* weight;
+  const uint16_t* dtotal;
+  int64_t lddt;
+  uint16_t* dx;
+  int64_t lddx;
+  float* dw;
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t M, K;
+} mxq_norm_grad;
+MXQ_API int mx_rms_norm_backward(const mxq_norm_grad* grad, hipStream_t stream);
 
 /* ------------------------------------------------------------------------ *
  * Latent attention                                                          *

@@ -14,19 +14,22 @@ def _call(lib, name, good, **change):
     args = dict(good)
     assert set(change) <= set(args)
     args.update(change)
-    return getattr(lib, name)(*args.values())
+    values = [v or 0 for v in args.values()]
+    pack = STRUCTS.get(name)
+    return getattr(lib, name)(*((pack.pack(*values), None) if pack else args.values()))
 
 
-NORM = dict(x=P, ldx=64, r=P, ldr=64, w=P, M=4, K=64, eps=1e-6, total=P, ldt=64, rstd=P, y=P, ldy=64, q=P,
-            ldq=64, scale=P, lds=2, qT=P, ldqT=32, M_cap=32, scaleT=P, ldsT=1, stream=None)
-GRAD = dict(dy=P, lddy=64, total=P, ldt=64, rstd=P, w=P, dtotal=P, lddt=64, M=4, K=64, dx=P, lddx=64, dw=P,
-            ws=P, ws_bytes=1 << 20, stream=None)
+STRUCTS = {"mx_rms_norm": mxq._NORM_STRUCT, "mx_rms_norm_backward": mxq._NORM_GRAD_STRUCT,
+           "mx_gated_ffn_decode": mxq._FFN_STRUCT}
+NORM = dict(x=P, ldx=64, r=P, ldr=64, w=P, total=P, ldt=64, rstd=P, y=P, ldy=64, q=P, ldq=64, scale=P, lds=2,
+            qT=P, ldqT=32, scaleT=P, ldsT=1, M=4, K=64, M_cap=32, eps=1e-6)
+GRAD = dict(dy=P, lddy=64, total=P, ldt=64, rstd=P, w=P, dtotal=P, lddt=64, dx=P, lddx=64, dw=P, ws=P,
+            ws_bytes=1 << 20, M=4, K=64)
 SWIGLU = dict(dy=P, dys=P, ldd=64, ldsd=2, wT=P, wTs=P, ldw=64, ldsw=2, we=64 * 32, wse=64, offsets=P, E=2, M=40,
               F=32, K=64, gu=P, ldgu=64, dgu=P, lddgu=64, q=P, ldq=64, scale=P, lds=2, qT=P, ldqT=128, scaleT=P,
               ldsT=4, M_cap=128, poff=P, accum=0, stream=None)
 FFN = dict(x=P, xs=P, ldx=64, ldsx=2, gu=P, gus=P, ldgu=64, ldsgu=2, gue=64 * 64, guse=128, d=P, dsc=P, ldd=32,
-           ldsd=1, de=32 * 40, dse=40, offsets=P, E=2, M=4, K=64, F=32, N=40, y=P, ldy=40, ws=P, ws_bytes=1 << 20,
-           stream=None)
+           ldsd=1, de=32 * 40, dse=40, offsets=P, y=P, ldy=40, ws=P, ws_bytes=1 << 20, M=4, K=64, F=32, N=40, E=2)
 
 
 @pytest.mark.parametrize("change,status", [
@@ -70,6 +73,11 @@ def test_swiglu_gradient(host_only_lib, change, status):  # noqa: F811
     ({"x": P + 8}, 3), ({"d": P + 8}, 3), ({"M": 0}, 0), ({"N": 0}, 0)])
 def test_ffn_decode(host_only_lib, change, status):  # noqa: F811
     assert _call(host_only_lib, "mx_gated_ffn_decode", FFN, **change) == status
+
+
+def test_no_struct(host_only_lib):  # noqa: F811
+    for name in STRUCTS:
+        assert getattr(host_only_lib, name)(None, None) == 1
 
 
 def test_workspaces():
