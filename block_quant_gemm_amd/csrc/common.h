@@ -247,6 +247,40 @@ __device__ __forceinline__ void quant8(uint4 v, uint32_t& lo, uint32_t& hi, uint
 // converted value into NaN.
 __device__ __forceinline__ float e8m0_f32(uint32_t c) { return __builtin_bit_cast(float, c << 23); }
 
+// E8M0 code of an MX block from its largest FP32 magnitude (NaN if it holds one).
+__device__ __forceinline__ uint32_t mx_code_of(float top) {
+  const uint32_t am = __builtin_bit_cast(uint32_t, top), E = am >> 23;
+  return (am & 0x7FFFFFFFu) >= 0x7F800000u ? 0xFFu : (E > 8u ? E - 8u : 0u);
+}
+
+// An MX block of 32 FP32 values: its E8M0 code and the 32 E4M3 codes.  The largest
+// magnitude by v_maximum3, two values an instruction, NaN kept; the scaled
+// conversion divides by 2^e and rounds to nearest even (all binades compared with
+// multiplying and converting), values past 448 * 2^e clamped before it.
+__device__ __forceinline__ uint32_t mx_block(const float (&v)[32], uint32_t (&out)[8]) {
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) top = __builtin_elementwise_maximum(top, __builtin_fabsf(v[i]));
+  const uint32_t code = mx_code_of(top);
+  const float s = e8m0_f32(code);
+  const float lim = 448.0f * (code ? s : __builtin_bit_cast(float, 1u << 22));   // 2^-127 is subnormal
+#pragma unroll
+  for (int d = 0; d < 8; ++d) {
+    i16x2 w;
+    w = __builtin_nondeterministic_value(w);        // both halves are written below
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, __builtin_amdgcn_fmed3f(v[4 * d], -lim, lim),
+                                                 __builtin_amdgcn_fmed3f(v[4 * d + 1], -lim, lim), s, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, __builtin_amdgcn_fmed3f(v[4 * d + 2], -lim, lim),
+                                                 __builtin_amdgcn_fmed3f(v[4 * d + 3], -lim, lim), s, true);
+    out[d] = __builtin_bit_cast(uint32_t, w);
+  }
+  if (__builtin_expect(__ballot(code == 0xFFu) != 0, 0)) {      // a branch, not a select a dword
+#pragma unroll
+    for (int d = 0; d < 8; ++d) out[d] = code == 0xFFu ? 0x7F7F7F7Fu : out[d];
+  }
+  return code;
+}
+
 // Eight E4M3 codes (bytes of w0, then w1) times 2^(c - 127) as BF16, element
 // i from byte i.  Exact while the product is a normal or subnormal BF16
 // value with its bits intact: scale codes 3..246.  Under the others the product is
@@ -292,6 +326,19 @@ __device__ __forceinline__ i32x4 make_rsrc(const void* p, uint32_t bytes) {
   r[2] = (int)bytes;
   r[3] = 0x00020000;
   return r;
+}
+
+// The same range checked descriptor for the buffer load and store builtins: accesses
+// past `bytes` read zeros and write nothing.
+typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+__device__ __forceinline__ uint4 buffer_load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+}
+__device__ __forceinline__ void buffer_store(__amdgpu_buffer_rsrc_t r, uint32_t off, uint4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, v), r, (int)off, 0, 0);
 }
 
 }  // namespace mxq

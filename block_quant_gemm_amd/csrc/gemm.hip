@@ -108,6 +108,14 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 __device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int lds_off(int r, int c) { return r * TS + ((c ^ swz(r)) << 4); }
 
+// The SwiGLU gradient reads rows r, r + 1, r + 2, r + 3, r + 32 .. r + 35 of B by consecutive
+// lanes (see `brow` below); with bit 5 of the row in the chunk's top bit those are free of
+// conflicts too.
+template <bool B5>
+__device__ __forceinline__ int lds_off5(int r, int c) {
+  return r * TS + ((c ^ swz(r) ^ (B5 ? (r >> 5 & 1) << 2 : 0)) << 4);
+}
+
 struct GemmArgs {
   const uint8_t* a; const uint8_t* as; int64_t lda, ldsa;
   const uint8_t* b; const uint8_t* bs; int64_t ldb, ldsb;
@@ -192,11 +200,13 @@ struct LaneOffsets {
   uint32_t sblk;            // blk (0 or 1) of the lane's scale entry
 };
 
+template <bool B5 = false>
 __device__ __forceinline__ LaneOffsets lane_offsets(const OpTile& t) {
   LaneOffsets o;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int rsub = lane >> 3, slot = lane & 7;
   o.kc0 = (uint32_t)((slot ^ (rsub >> 1)) * 16);
+  if (B5) o.kc0 ^= (w & 1) * 64;                    // bit 5 of rows 32 w .. 32 w + 31
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int row = (w * 4 + j) * 8 + rsub;
@@ -293,29 +303,33 @@ __device__ __forceinline__ uint32_t mx_block_f32(const float (&v)[32], uint32_t 
   return code;
 }
 
-// 32 BF16 values (64 bytes, 16-byte aligned).
-__device__ __forceinline__ void load32_bf16(const uint16_t* p, float (&v)[32]) {
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    const uint4 x = *reinterpret_cast<const uint4*>(p + 8 * d);
-    v[8 * d] = bf16_lo(x.x); v[8 * d + 1] = bf16_hi(x.x);
-    v[8 * d + 2] = bf16_lo(x.y); v[8 * d + 3] = bf16_hi(x.y);
-    v[8 * d + 4] = bf16_lo(x.z); v[8 * d + 5] = bf16_hi(x.z);
-    v[8 * d + 6] = bf16_lo(x.w); v[8 * d + 7] = bf16_hi(x.w);
-  }
+__device__ __forceinline__ uint32_t dword(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
-__device__ __forceinline__ void store32_bf16(uint16_t* p, const float (&v)[32]) {
-#pragma unroll
-  for (int d = 0; d < 4; ++d)
-    *reinterpret_cast<uint4*>(p + 8 * d) =
-        make_uint4(bf16x2_bits(v[8 * d], v[8 * d + 1]), bf16x2_bits(v[8 * d + 2], v[8 * d + 3]),
-                   bf16x2_bits(v[8 * d + 4], v[8 * d + 5]), bf16x2_bits(v[8 * d + 6], v[8 * d + 7]));
+// Exchange between two registers and 16 lanes: the odd 16-lane rows of a with the even
+// ones of b; or 32 lanes: the upper half of a with the lower half of b.
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap16(uint4& a, uint4& b) {
+  swap16(a.x, b.x); swap16(a.y, b.y); swap16(a.z, b.z); swap16(a.w, b.w);
+}
+__device__ __forceinline__ void swap32(uint4& a, uint4& b) {
+  swap32(a.x, b.x); swap32(a.y, b.y); swap32(a.z, b.z); swap32(a.w, b.w);
 }
 
 // The MFMA operand of tile row r for one k-step: 16-byte chunks c0 and c1.
+template <bool B5 = false>
 __device__ __forceinline__ i32x8 read_frag(const uint8_t* l, int r, int c0, int c1) {
-  const uint4 x = *reinterpret_cast<const uint4*>(l + lds_off(r, c0));
-  const uint4 y = *reinterpret_cast<const uint4*>(l + lds_off(r, c1));
+  const uint4 x = *reinterpret_cast<const uint4*>(l + lds_off5<B5>(r, c0));
+  const uint4 y = *reinterpret_cast<const uint4*>(l + lds_off5<B5>(r, c1));
   i32x8 f;
   f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
   f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
@@ -544,7 +558,7 @@ template <int KIND, bool PT, int OUT, bool SW, bool SWI, bool BLK, bool XA = fal
           bool SWB = false>
 __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
   static_assert(MI == 4 || (MI == 2 && !SWI && !BLK), "row tiles per wavefront");
-  static_assert(!SWB || (KIND == kVarM && !PT && !SWI && MI == 4), "SwiGLU gradient kind");
+  static_assert(!SWB || (KIND == kVarM && !PT && !SWI), "SwiGLU gradient kind");
   constexpr int TMR = MI * 64;                      // tile rows (256, or 128)
   constexpr int RW = MI * 32;                       // rows per wavefront
   constexpr int DPM = 4 / MI;                       // stage loads issued per MFMA
@@ -696,8 +710,15 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
   // kdim < 2^31 (the launchers check that a tile's byte offsets fit in 32 bits)
   const uint32_t kdim32 = (uint32_t)kdim;
   const int32_t nsteps = (int32_t)((kdim + TK - 1) / TK);
-  const LaneOffsets oA = lane_offsets(A);
-  const LaneOffsets oB = SWI ? lane_offsets_gu(B, n0 / 2, g.F) : lane_offsets(B);
+  const LaneOffsets oA = lane_offsets<SWB>(A);
+  const LaneOffsets oB = SWI ? lane_offsets_gu(B, n0 / 2, g.F) : lane_offsets<SWB>(B);
+  // Row of B that this lane gives the instruction for column tile j.  The SwiGLU
+  // gradient deals them so that a lane's 32 accumulators of a row are 32 consecutive
+  // columns, an MX block: row m = 8q + 4h + e of the instruction, which becomes
+  // accumulator 4q + e of half h, takes column 32 h + 16 j + 4 q + e.
+  auto brow = [&](int j) {
+    return SWB ? bn + 32 * (r32 >> 2 & 1) + 16 * j + 4 * (r32 >> 3) + (r32 & 3) : bn + j * 32 + r32;
+  };
   const i32x4 none = make_rsrc(g.c, 0);              // zero range: loads read 0
   const uint32_t lds_codes = lds_addr(smem), lds_scales = lds_addr(ssc);
 
@@ -793,9 +814,9 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
     const uint8_t* lB = lA + kStage;
     const int c0 = ks * 4 + half, c1 = c0 + 2;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) f.a[i] = read_frag(lA, wm * RW + i * 32 + r32, c0, c1);
+    for (int i = 0; i < MI; ++i) f.a[i] = read_frag<SWB>(lA, wm * RW + i * 32 + r32, c0, c1);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) f.b[j] = read_frag(lB, bn + j * 32 + r32, c0, c1);
+    for (int j = 0; j < 2; ++j) f.b[j] = read_frag<SWB>(lB, brow(j), c0, c1);
     if (BLK) {
       const uint32_t* sc = ssc + slot * kBlkScaleWords;
 #pragma unroll
@@ -812,12 +833,12 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
 #pragma unroll
       for (int i = 0; i < MI; ++i) f.sa[i] = sc[(wm * RW + i * 32 + r32) * 2 + h0];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) f.sb[j] = sc[2 * TM + (bn + j * 32 + r32) * 2 + h0];
+      for (int j = 0; j < 2; ++j) f.sb[j] = sc[2 * TM + brow(j) * 2 + h0];
       if (XA) {
 #pragma unroll
         for (int i = 0; i < MI; ++i) f.sa1[i] = sc[(wm * RW + i * 32 + r32) * 2 + 1];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) f.sb1[j] = sc[2 * TM + (bn + j * 32 + r32) * 2 + 1];
+        for (int j = 0; j < 2; ++j) f.sb1[j] = sc[2 * TM + brow(j) * 2 + 1];
       }
     } else {
       // block 2s + half of row r: window (smis + 2s + half) / 16 relative to
@@ -833,12 +854,12 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
                             (ta >> 4 ? ps1 : ps0) * kWinBytes + (ta & 15) + (wm * RW + r32) * 16;
         const uint8_t* wB = reinterpret_cast<const uint8_t*>(ssc) +
                             (tb >> 4 ? ps1 : ps0) * kWinBytes + kWinBytes / 2 + (tb & 15) +
-                            (bn + r32) * 16;
+                            brow(0) * 16;
         const uint32_t keep = valid ? 0xFFu : 0u;   // a mask, so the loads stay unconditional
 #pragma unroll
         for (int i = 0; i < MI; ++i) sa[i] = (uint32_t)wA[i * 32 * 16] & keep;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) sb[j] = (uint32_t)wB[j * 32 * 16] & keep;
+        for (int j = 0; j < 2; ++j) sb[j] = (uint32_t)wB[j * (SWB ? 16 : 32) * 16] & keep;
       };
       window_codes(XA ? 0 : half, f.sa, f.sb);
       if (XA) window_codes(1, f.sa1, f.sb1);
@@ -1186,107 +1207,184 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
   if constexpr (SWB) {
     // ---- SwiGLU gradient epilogue.  With sg = 1 / (1 + e^-g):
     //   d gate = dh u sg (1 + g (1 - sg)),   d up = dh g sg.
-    // In two rounds of 128 columns (each wavefront's j-th 32): dh staged in FP32
-    // as [256 rows][128], then (row, 32-column block) items, two a lane, read
-    // g and u, write both row copies and put d gate, then d up, in dh's
-    // place, from which (column, 32-row block) items make the column copy.
-    // Rows past the group are zero: the column copy's padding.
+    // In rounds of 32 rows a wavefront: a lane holds 32 consecutive columns of dh in one row
+    // (see brow), reads their gates and ups, and has an MX block of either row copy
+    // to itself.  Both go to LDS in FP32 ([64 rows][256 columns] each, rows
+    // padded), from which (column, 32-row block) items, one a lane, make the
+    // column copy.  Rows past the group are zero: the column copy's padding.
+    constexpr int LD = TN + 4;
+    static_assert(2 * 64 * LD * 4 <= kSmem && 512 * TMR <= kSmem, "staged gradients");
     const int64_t F = g.F;
-    const int rows_t = c_rows < TM ? (int)c_rows : TM;
+    const int rows_t = c_rows < TMR ? (int)c_rows : TMR;
     const int rows_p = (rows_t + 31) & ~31;
     const int64_t pbase = padded_rows(s_off, group) + (m0 - s_off[group]);
     float* hst = reinterpret_cast<float*>(smem);
-    constexpr int LD = kCStride / 4;
-    // column copy of the staged 128 columns, rows `first` + column of qT
-    auto columns = [&](int j, int64_t first) {
-#pragma unroll 1
-      for (int k = 0; k < 2; ++k) {
-        const int item = t + kThreads * k;
-        const int col = item & 127, blk = item >> 7;
-        float v[32];
+    // Tile-relative offsets through range-checked descriptors: rows past the group
+    // read zeros and are not written; columns past F get an offset past every range.
+    const uint32_t left = (uint32_t)(F - n0);       // columns from the tile's first to F
+    auto tile_of = [&](const void* base, int64_t ld, int64_t first, int size) {
+      return buffer_of(static_cast<const uint8_t*>(base) + (m0 * ld + first + n0) * size,
+                       (uint32_t)(((rows_t - 1) * ld + left) * size));
+    };
+    const auto dgu_g = tile_of(g.gu, g.ldgu, 0, 2), dgu_u = tile_of(g.gu, g.ldgu, F, 2);
+    const auto dq_g = tile_of(g.hq, g.ldhq, 0, 1), dq_u = tile_of(g.hq, g.ldhq, F, 1);
+    const uint32_t ldgu = (uint32_t)g.ldgu * 2, ldhq = (uint32_t)g.ldhq;
+    const uint32_t r16 = wm * RW + (lane & 15), q16 = lane >> 4;
+    // Gates and ups of a round: the lane's 64 bytes of each.  Loaded as 64-byte runs of 16
+    // rows an instruction (instruction k: rows 16 (k % 2) .., chunks 4 (k / 2) + lane / 16 of a
+    // row's 8 chunks of 16 bytes), and dealt to their lanes by exchanges of 16
+    // and 32 lanes: instruction's and lane's bits of the row and of the chunk change places.
+    const uint32_t gu_off[2] = {bn + 8 * q16 < left ? r16 * ldgu + (bn + 8 * q16) * 2 : 0x80000000u,
+                                bn + 32 + 8 * q16 < left ? r16 * ldgu + (bn + 32 + 8 * q16) * 2 : 0x80000000u};
+    auto load_gu = [&](int i, uint4 (&v)[8]) {
 #pragma unroll
-        for (int r = 0; r < 32; ++r) v[r] = hst[(blk * 32 + r) * LD + col];
-        uint32_t w[8];
-        const uint32_t code = mx_block_f32(v, w);
-        const int64_t hc = n0 + (col >> 5) * 64 + j * 32 + (col & 31), pcol = pbase + blk * 32;
-        if (blk * 32 < rows_p && hc < F && pcol + 32 <= g.hcap) {
-          uint8_t* d = g.hqT + (first + hc) * g.ldhqT + pcol;
-          *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(d + 16) = make_uint4(w[4], w[5], w[6], w[7]);
-          g.hsT[(first + hc) * g.ldhsT + (pcol >> 5)] = (uint8_t)code;
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t o = gu_off[k >> 1] + (uint32_t)(i * 32 + 16 * (k & 1)) * ldgu;
+        v[k] = buffer_load(dgu_g, o);
+        v[4 + k] = buffer_load(dgu_u, o);
+      }
+    };
+    auto deal_gu = [&](uint4 (&v)[8]) {
+#pragma unroll
+      for (int x = 0; x < 8; x += 4) {
+        swap16(v[x], v[x + 1]);
+        swap16(v[x + 2], v[x + 3]);
+        swap32(v[x], v[x + 2]);
+        swap32(v[x + 1], v[x + 3]);
+      }
+    };
+    // Scales wait in LDS for the end: [256 rows][8 blocks of d gate, 8 of d up], then
+    // [512 columns][8 blocks].
+    uint8_t* srow = reinterpret_cast<uint8_t*>(ssc);
+    uint8_t* scol = srow + TM * 16;
+    static_assert(sizeof(ssc) >= TM * 16 + 2 * TN * 8, "staged scales");
+    // The lane's 32 codes of a row copy: stored as 64-byte runs of 16 rows.
+    const uint32_t q_off = bn + 16 * q16 < left ? r16 * ldhq + bn + 16 * q16 : 0x80000000u;
+    auto row_copy = [&](const float (&v)[32], int i, int up) {
+      uint32_t w[8];
+      const uint32_t code = mx_block(v, w);
+      uint4 x = make_uint4(w[0], w[1], w[2], w[3]), y = make_uint4(w[4], w[5], w[6], w[7]);
+      swap16(x, y);
+      const auto d = up ? dq_u : dq_g;
+      buffer_store(d, q_off + (uint32_t)(i * 32) * ldhq, x);
+      buffer_store(d, q_off + (uint32_t)(i * 32 + 16) * ldhq, y);
+      srow[(wm * RW + i * 32 + r32) * 16 + up * 8 + (bn >> 5) + half] = (uint8_t)code;
+      if (cbase) {
+        const int row = wm * RW + i * 32 + r32;
+        if (row < rows_t && bn + 32 * half < (int)left) {
+          uint16_t* o = static_cast<uint16_t*>(cbase) + (m0 + row) * g.ldc + up * F + n0 + bn + 32 * half;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(o + 8 * k) =
+                make_uint4(bf16x2_bits(v[8 * k], v[8 * k + 1]), bf16x2_bits(v[8 * k + 2], v[8 * k + 3]),
+                           bf16x2_bits(v[8 * k + 4], v[8 * k + 5]), bf16x2_bits(v[8 * k + 6], v[8 * k + 7]));
         }
       }
     };
+    const int col = t & 255, wb = t >> 8;           // column items: the wavefronts' half wm = wb
+    uint32_t cq[2][MI][8];                          // their codes, d gate and d up
+    uint4 gu[8];
+    load_gu(0, gu);
+    barrier();                                      // the k loop's LDS reads are done
+    if (rows_t < TMR) {
+      // whatever the weights hold, rows past the group are zero
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      barrier();                                    // the LDS reads before are done
+      for (int i = 0; i < MI; ++i) {
+        const bool live = wm * RW + i * 32 + r32 < rows_t;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int ml = wm * 128 + i * 32 + r32;
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x16& v = acc[i][j];
-          *reinterpret_cast<f32x4*>(&hst[ml * LD + (bn >> 1) + q * 8 + half * 4]) =
-              f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-        }
+          for (int v = 0; v < 16; ++v) acc[i][j][v] = live ? acc[i][j][v] : 0.0f;
       }
-      barrier();
-      float up[2][32];
+    }
+    static_for<MI>([&](auto ic) {
+      constexpr int i = decltype(ic)::value;
+      float dg[32], du[32];
+      deal_gu(gu);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int item = t + kThreads * k;
-        const int row = item >> 2, blk = item & 3;
-        const int64_t hc = n0 + blk * 64 + j * 32, m = m0 + row;
-        const bool ok = row < rows_t && hc < F;
-        float gv[32], dg[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) gv[e] = up[k][e] = 0.0f;
-        if (ok) {
-          load32_bf16(g.gu + m * g.ldgu + hc, gv);
-          load32_bf16(g.gu + m * g.ldgu + F + hc, up[k]);
-        }
-        float* p = &hst[row * LD + blk * 32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float dh = ok ? p[e] : 0.0f;
-          const float sg = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-gv[e] * 1.4426950408889634f));
-          dg[e] = dh * up[k][e] * sg * __builtin_fmaf(gv[e], 1.0f - sg, 1.0f);
-          up[k][e] = dh * gv[e] * sg;
-        }
-#pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<f32x4*>(p + e) = f32x4{dg[e], dg[e + 1], dg[e + 2], dg[e + 3]};
-        uint32_t w0[8], w1[8];
-        const uint32_t c0 = mx_block_f32(dg, w0), c1 = mx_block_f32(up[k], w1);
-        if (ok) {
-          uint8_t* d = g.hq + m * g.ldhq + hc;
-          *reinterpret_cast<uint4*>(d) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-          *reinterpret_cast<uint4*>(d + 16) = make_uint4(w0[4], w0[5], w0[6], w0[7]);
-          *reinterpret_cast<uint4*>(d + F) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-          *reinterpret_cast<uint4*>(d + F + 16) = make_uint4(w1[4], w1[5], w1[6], w1[7]);
-          g.hs[m * g.ldhs + (hc >> 5)] = (uint8_t)c0;
-          g.hs[m * g.ldhs + ((F + hc) >> 5)] = (uint8_t)c1;
-          if (cbase) {
-            uint16_t* o = static_cast<uint16_t*>(cbase) + m * g.ldc + hc;
-            store32_bf16(o, dg);
-            store32_bf16(o + F, up[k]);
-          }
-        }
+      for (int e = 0; e < 32; ++e) {
+        const uint32_t gw = dword(gu[e >> 3], e >> 1 & 3), uw = dword(gu[4 + (e >> 3)], e >> 1 & 3);
+        const float x = e & 1 ? bf16_hi(gw) : bf16_lo(gw), u = e & 1 ? bf16_hi(uw) : bf16_lo(uw);
+        const float sg = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.4426950408889634f));
+        const float s = acc[i][e >> 4][e & 15] * sg;
+        du[e] = s * x;
+        dg[e] = u * __builtin_fmaf(du[e], 1.0f - sg, s);
+        if ((e & 7) == 7) __builtin_amdgcn_sched_barrier(0);   // few values in flight: registers
       }
-      barrier();
-      columns(j, 0);
+      float* p = hst + (wm * 32 + r32) * LD + bn + 32 * half;
+#pragma unroll
+      for (int e = 0; e < 32; e += 4) {
+        *reinterpret_cast<f32x4*>(p + e) = f32x4{dg[e], dg[e + 1], dg[e + 2], dg[e + 3]};
+        *reinterpret_cast<f32x4*>(p + 64 * LD + e) = f32x4{du[e], du[e + 1], du[e + 2], du[e + 3]};
+      }
+      row_copy(dg, i, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      row_copy(du, i, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (i + 1 < MI) load_gu(i + 1, gu);
       barrier();
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int item = t + kThreads * k;
-        float* p = &hst[(item >> 2) * LD + (item & 3) * 32];
+        float v[32];
 #pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<f32x4*>(p + e) =
-              f32x4{up[k][e], up[k][e + 1], up[k][e + 2], up[k][e + 3]};
+        for (int r = 0; r < 32; ++r) v[r] = hst[((k * 2 + wb) * 32 + r) * LD + col];
+        scol[(k * 256 + col) * 8 + wb * MI + i] = (uint8_t)mx_block(v, cq[k][i]);
+        __builtin_amdgcn_sched_barrier(0);
       }
       barrier();
-      columns(j, F);
+    });
+    // The column copy leaves as runs of the tile's rows: [512 columns][TMR] bytes
+    // in LDS, 16-byte chunks exchanged with the column's low bits.
+    constexpr int CH = TMR / 16;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const int chunk = (wb * (RW / 16) + 2 * i + d) ^ (col & (CH - 1));
+          *reinterpret_cast<uint4*>(smem + (k * 256 + col) * TMR + chunk * 16) =
+              make_uint4(cq[k][i][4 * d], cq[k][i][4 * d + 1], cq[k][i][4 * d + 2], cq[k][i][4 * d + 3]);
+        }
+    barrier();
+    // chunk t % CH of columns t / CH, + 512 / CH, ... (whole columns of d gate, then of d up)
+    const int chunk = t % CH;
+    if (chunk * 16 < rows_p && pbase + chunk * 16 + 16 <= g.hcap) {
+      const uint32_t ldqT = (uint32_t)g.ldhqT;
+      uint8_t* qT = g.hqT + n0 * g.ldhqT + pbase;   // uniform
+      uint8_t* qTu = qT + F * g.ldhqT;
+#pragma unroll
+      for (int it = 0; it < CH; ++it) {
+        const uint32_t c = it * (kThreads / CH) + t / CH, cl = c & 255;
+        const uint4 v = *reinterpret_cast<const uint4*>(smem + c * TMR + ((chunk ^ (cl & (CH - 1))) << 4));
+        if (cl < left)
+          *reinterpret_cast<uint4*>((it * (kThreads / CH) < 256 ? qT : qTu) + (uint64_t)cl * ldqT + chunk * 16) = v;
+      }
+    }
+    // a column's scales by one thread; a row's blocks of d gate or d up by another
+    auto store_scales = [](uint8_t* d, const uint8_t* s, int n) {
+      if (n >= 2 * MI) {
+        uint64_t v = *reinterpret_cast<const uint64_t*>(s);
+        __builtin_memcpy(d, &v, 2 * MI);            // any alignment
+      } else {
+        for (int k = 0; k < n; ++k) d[k] = s[k];
+      }
+    };
+    if ((uint32_t)col < left) {
+      const int64_t room = (g.hcap - pbase) >> 5;
+      const int n = rows_p / 32 < room ? rows_p / 32 : (int)room;
+      store_scales(g.hsT + (wb * F + n0 + col) * g.ldhsT + (pbase >> 5), scol + t * 8, n);
+    }
+    if (t < 2 * TMR && (t >> 1) < rows_t) {
+      const int n = left < TN ? (int)left / 32 : 8;
+      uint8_t* d = g.hs + (m0 + (t >> 1)) * g.ldhs + (((t & 1) * F + n0) >> 5);
+      const uint8_t* s = srow + (t >> 1) * 16 + (t & 1) * 8;
+      if (n == 8) {
+        const uint64_t v = *reinterpret_cast<const uint64_t*>(s);
+        __builtin_memcpy(d, &v, 8);
+      } else {
+        for (int k = 0; k < n; ++k) d[k] = s[k];
+      }
     }
     return;
   }
@@ -1771,6 +1869,9 @@ extern "C" int mx_grouped_gemm_swiglu_backward(
   }
   if (w_estride < 0 || ws_estride < 0 || w_estride > kMaxDim || ws_estride > kMaxDim)
     return MXQ_ERR_SHAPE;
+  // a tile's rows of gu and q have 32-bit byte offsets
+  if (M > 0 && (!fits32(sat_mul(ldgu, 2), 0) || !fits32(ldq, 0))) return MXQ_ERR_SHAPE;
+  if (ldqT > 0xFFFFFFFFLL) return MXQ_ERR_SHAPE;
   if (w_estride % 16 != 0 || ldqT % 16 != 0 || !aligned(qT, 16)) return MXQ_ERR_ALIGN;
   if (M > 0 && (ldq % 16 != 0 || !aligned(q, 16) || ldgu % 8 != 0 || !aligned(gu, 16) ||
                 (dgu && (lddgu % 8 != 0 || !aligned(dgu, 16)))))

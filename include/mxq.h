@@ -553,8 +553,8 @@ MXQ_API int mx_grouped_gemm_swiglu(const uint8_t* a, const uint8_t* a_scale, int
  *   accum       : as for mx_grouped_gemm.
  * Requires F % 32 == 0, K % 32 == 0, M_cap % 32 == 0; ldq and ldqT multiples of 16
  * and ldgu, lddgu of 8, with 16-byte aligned q, qT, gu and dgu; the operand
- * requirements of mx_grouped_gemm.  Rows outside every group are not written in
- * q, scale and dgu.  F == 0 is a no-op; with M == 0 only offsets_padded and the
+ * requirements of mx_grouped_gemm; 257 rows of gu and of q within 2^31 bytes, ldqT
+ * less than 2^32.  Rows outside every group are not written in q, scale and dgu.  F == 0 is a no-op; with M == 0 only offsets_padded and the
  * column copy's zeros are written.
  */
 MXQ_API int mx_grouped_gemm_swiglu_backward(

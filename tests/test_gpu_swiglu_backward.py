@@ -9,9 +9,10 @@ good to a unit in the last place (2 u24):
            of the value, and 2 u24 of 2^x: (3 |g| + 2) u24
   sg       that times 1 - sg <= 1, 1 + e rounded, 1/x: dl = (3 |g| + 5) u24 of sg
   1 - sg   sg dl + u24 absolute
-  P = 1 + g (1 - sg)   one FMA: |g| (sg dl + u24) + u24 |P|
-  d gate = dh u sg P   three products: |dh u| (sg eP + |P| sg dl) + 4 u24 |d gate|
-  d up = dh g sg       two products: |dh g| sg dl + 3 u24 |d up|
+  s = dh sg, d up = s g    two products: |dh g| sg dl + 3 u24 |d up|
+  d gate = u (d up (1 - sg) + s) = u s P, P = 1 + g (1 - sg)    the FMA's product is off by
+    |s| |g| (sg dl + u24 + u24 (1 - sg)) and it rounds once: with eP = |g| (sg dl + 2 u24) +
+    u24 |P|, |dh u| (sg eP + |P| sg dl) + 4 u24 |d gate|
 and both with dh's own error times |u sg P| and |g sg|; underflow to 2^-126 (1 + |g|)|u dh|
 where a factor is subnormal, and for g < -87, where e^-g is infinite in FP32, sg is 0:
 the whole term, |dh u g| e^g.  Codes are checked against these intervals
@@ -43,7 +44,7 @@ def grad_bounds(dh, ddh, g, u):
     ag, au, ah = np.abs(g), np.abs(u), np.abs(dh) + ddh
     dl = (3 * ag + 5) * U
     P = 1 + g * (1 - sg)
-    eP = ag * (sg * dl + U) + U * np.abs(P)
+    eP = ag * (sg * dl + 2 * U) + U * np.abs(P)
     tiny = 2.0 ** -126 * (1 + ag) * (1 + au * ah)
     lost = np.where(g < -87, ag * np.exp(np.minimum(g, 0.0)) * 1.01, 0.0)
     eg = ddh * np.abs(u * sg * P) + ah * au * (sg * eP + np.abs(P) * sg * dl + lost) + 4 * U * np.abs(dg) + tiny
