@@ -253,25 +253,29 @@ __device__ __forceinline__ uint32_t mx_code_of(float top) {
   return (am & 0x7FFFFFFFu) >= 0x7F800000u ? 0xFFu : (E > 8u ? E - 8u : 0u);
 }
 
+// Conversions of this wavefront to E4M3 saturate from here on, instead of giving NaN
+// from 464 on (MODE.FP16_OVFL).
+__device__ __forceinline__ void saturate_conversions() {
+  __builtin_amdgcn_s_setreg(1 | 23 << 6, 1);        // hwreg(MODE), bit 23, one bit
+}
+
 // An MX block of 32 FP32 values: its E8M0 code and the 32 E4M3 codes.  The largest
 // magnitude by v_maximum3, two values an instruction, NaN kept; the scaled
-// conversion divides by 2^e and rounds to nearest even (all binades compared with
-// multiplying and converting), values past 448 * 2^e clamped before it.
+// conversion divides by 2^e, rounds to nearest even and, after
+// saturate_conversions, saturates (all binades compared with clamping,
+// multiplying and converting).
 __device__ __forceinline__ uint32_t mx_block(const float (&v)[32], uint32_t (&out)[8]) {
   float top = 0.0f;
 #pragma unroll
   for (int i = 0; i < 32; ++i) top = __builtin_elementwise_maximum(top, __builtin_fabsf(v[i]));
   const uint32_t code = mx_code_of(top);
   const float s = e8m0_f32(code);
-  const float lim = 448.0f * (code ? s : __builtin_bit_cast(float, 1u << 22));   // 2^-127 is subnormal
 #pragma unroll
   for (int d = 0; d < 8; ++d) {
-    i16x2 w;
-    w = __builtin_nondeterministic_value(w);        // both halves are written below
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, __builtin_amdgcn_fmed3f(v[4 * d], -lim, lim),
-                                                 __builtin_amdgcn_fmed3f(v[4 * d + 1], -lim, lim), s, false);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, __builtin_amdgcn_fmed3f(v[4 * d + 2], -lim, lim),
-                                                 __builtin_amdgcn_fmed3f(v[4 * d + 3], -lim, lim), s, true);
+    // both halves are written: any dead register will do to start from
+    i16x2 w = __builtin_bit_cast(i16x2, d ? v[4 * d - 4] : top);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, v[4 * d], v[4 * d + 1], s, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, v[4 * d + 2], v[4 * d + 3], s, true);
     out[d] = __builtin_bit_cast(uint32_t, w);
   }
   if (__builtin_expect(__ballot(code == 0xFFu) != 0, 0)) {      // a branch, not a select a dword

@@ -1212,6 +1212,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
     // to itself.  Both go to LDS in FP32 ([64 rows][256 columns] each, rows
     // padded), from which (column, 32-row block) items, one a lane, make the
     // column copy.  Rows past the group are zero: the column copy's padding.
+    saturate_conversions();
     constexpr int LD = TN + 4;
     static_assert(2 * 64 * LD * 4 <= kSmem && 512 * TMR <= kSmem, "staged gradients");
     const int64_t F = g.F;
