@@ -52,6 +52,7 @@ constexpr int kSmem = kSlots * 2 * kStage > TM * kCStride ? kSlots * 2 * kStage 
 constexpr int kGroupMDense = 8;
 constexpr int kGroupMVarM = 4;
 constexpr int kMaxGroups = 256;
+constexpr uint32_t kCUs = 256;                    // of an MI355X
 
 // Compile-time loops: f(std::integral_constant<int, I>) for I in [B, E).
 template <int B, class F, int... I>
@@ -637,7 +638,20 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
       }
     }
     const uint32_t tiles_m = (uint32_t)s_start[g.E];  // data-dependent M-tile count
-    const uint32_t tile = blockIdx.x;
+    uint32_t tile = blockIdx.x;
+    int part_rows = TM, part = 0;
+    if (SWB) {
+      // What does not fill a turn of the CUs goes in half or quarter tiles where those fit one.
+      const uint32_t tiles = tiles_m * g.tiles_n, over = tiles % kCUs;
+      const uint32_t split = over == 0 || over > kCUs / 2 ? 1 : over > kCUs / 4 ? 2 : 4;
+      const uint32_t whole = split == 1 ? tiles : tiles - over;
+      if (tile >= whole) {
+        if (tile - whole >= over * split || split == 1) return;
+        part_rows = TM / (int)split;
+        part = (int)((tile - whole) / over);
+        tile = whole + (tile - whole) % over;
+      }
+    }
     if (tile >= tiles_m * g.tiles_n) return;          // surplus workgroup
     uint32_t tm, tn;
     raster<kGroupMVarM>(tile, tiles_m, g.tiles_n, tm, tn);
@@ -651,6 +665,12 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
     m0 = s_off[e] + (int64_t)(tm - s_start[e]) * TM;
     n0 = (int64_t)tn * TN;
     c_rows = s_off[e + 1] - m0;
+    if (SWB) {
+      m0 += part * part_rows;
+      c_rows -= part * part_rows;
+      if (c_rows <= 0) return;
+      if (c_rows > part_rows) c_rows = part_rows;
+    }
     A = op_tile(g.a, g.as, g.lda, g.ldsa, m0, 0, c_rows, kdim, !PT, SW);
     if (SWI)
       B = op_expert(g.b + (int64_t)e * g.b_estride,
@@ -716,6 +736,11 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
   // gradient deals them so that a lane's 32 accumulators of a row are 32 consecutive
   // columns, an MX block: row m = 8q + 4h + e of the instruction, which becomes
   // accumulator 4q + e of half h, takes column 32 h + 16 j + 4 q + e.
+  // Its wavefronts take 32-row blocks in turn (row 64 i + 32 wm), so that a tile of 64 or 128
+  // rows is one or two blocks of each: `live` of MI.  The others' products are skipped in the
+  // exact mode; in FP8 the branches cost more (49152 rows, 64 experts: 354 us with them, 333).
+  auto arow = [&](int i) { return SWB ? i * 64 + wm * 32 + r32 : wm * RW + i * 32 + r32; };
+  const int live = SWB ? __builtin_amdgcn_readfirstlane(((c_rows < TMR ? (int)c_rows : TMR) + 63) / 64) : MI;
   auto brow = [&](int j) {
     return SWB ? bn + 32 * (r32 >> 2 & 1) + 16 * j + 4 * (r32 >> 3) + (r32 & 3) : bn + j * 32 + r32;
   };
@@ -814,7 +839,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
     const uint8_t* lB = lA + kStage;
     const int c0 = ks * 4 + half, c1 = c0 + 2;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) f.a[i] = read_frag<SWB>(lA, wm * RW + i * 32 + r32, c0, c1);
+    for (int i = 0; i < MI; ++i) f.a[i] = read_frag<SWB>(lA, arow(i), c0, c1);
 #pragma unroll
     for (int j = 0; j < 2; ++j) f.b[j] = read_frag<SWB>(lB, brow(j), c0, c1);
     if (BLK) {
@@ -831,12 +856,12 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
       const uint32_t* sc = ssc + (slot * 2 + ks) * 2 * 2 * TM;
       const int h0 = XA ? 0 : half;
 #pragma unroll
-      for (int i = 0; i < MI; ++i) f.sa[i] = sc[(wm * RW + i * 32 + r32) * 2 + h0];
+      for (int i = 0; i < MI; ++i) f.sa[i] = sc[arow(i) * 2 + h0];
 #pragma unroll
       for (int j = 0; j < 2; ++j) f.sb[j] = sc[2 * TM + brow(j) * 2 + h0];
       if (XA) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i) f.sa1[i] = sc[(wm * RW + i * 32 + r32) * 2 + 1];
+        for (int i = 0; i < MI; ++i) f.sa1[i] = sc[arow(i) * 2 + 1];
 #pragma unroll
         for (int j = 0; j < 2; ++j) f.sb1[j] = sc[2 * TM + brow(j) * 2 + 1];
       }
@@ -851,13 +876,13 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
         const bool valid = 2 * (uint32_t)s + hb < nblk;
         const uint32_t ta = A.smis + u, tb = B.smis + u;
         const uint8_t* wA = reinterpret_cast<const uint8_t*>(ssc) +
-                            (ta >> 4 ? ps1 : ps0) * kWinBytes + (ta & 15) + (wm * RW + r32) * 16;
+                            (ta >> 4 ? ps1 : ps0) * kWinBytes + (ta & 15) + arow(0) * 16;
         const uint8_t* wB = reinterpret_cast<const uint8_t*>(ssc) +
                             (tb >> 4 ? ps1 : ps0) * kWinBytes + kWinBytes / 2 + (tb & 15) +
                             brow(0) * 16;
         const uint32_t keep = valid ? 0xFFu : 0u;   // a mask, so the loads stay unconditional
 #pragma unroll
-        for (int i = 0; i < MI; ++i) sa[i] = (uint32_t)wA[i * 32 * 16] & keep;
+        for (int i = 0; i < MI; ++i) sa[i] = (uint32_t)wA[i * (SWB ? 64 : 32) * 16] & keep;
 #pragma unroll
         for (int j = 0; j < 2; ++j) sb[j] = (uint32_t)wB[j * (SWB ? 16 : 32) * 16] & keep;
       };
@@ -926,13 +951,15 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
         }
         static_for<MI>([&](auto ic) {
           constexpr int I = decltype(ic)::value;
-          const float sc = e8m0_f32(HB ? f.sa1[I] : f.sa[I]);
-          const bf16x8 a0 = widen8_bf16(f.a[I][4 * HB], f.a[I][4 * HB + 1], sc);
-          const bf16x8 a1 = widen8_bf16(f.a[I][4 * HB + 2], f.a[I][4 * HB + 3], sc);
+          if (!SWB || I < live) {
+            const float sc = e8m0_f32(HB ? f.sa1[I] : f.sa[I]);
+            const bf16x8 a0 = widen8_bf16(f.a[I][4 * HB], f.a[I][4 * HB + 1], sc);
+            const bf16x8 a1 = widen8_bf16(f.a[I][4 * HB + 2], f.a[I][4 * HB + 3], sc);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            acc[I][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bw[j][0], a0, acc[I][j], 0, 0, 0);
-            acc[I][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bw[j][1], a1, acc[I][j], 0, 0, 0);
+            for (int j = 0; j < 2; ++j) {
+              acc[I][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bw[j][0], a0, acc[I][j], 0, 0, 0);
+              acc[I][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bw[j][1], a1, acc[I][j], 0, 0, 0);
+            }
           }
           if constexpr (ISSUE)
             static_for<DPM>([&](auto dd) { stage_dma(u, HB * 4 + I * DPM + decltype(dd)::value); });
@@ -1230,7 +1257,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
     const auto dgu_g = tile_of(g.gu, g.ldgu, 0, 2), dgu_u = tile_of(g.gu, g.ldgu, F, 2);
     const auto dq_g = tile_of(g.hq, g.ldhq, 0, 1), dq_u = tile_of(g.hq, g.ldhq, F, 1);
     const uint32_t ldgu = (uint32_t)g.ldgu * 2, ldhq = (uint32_t)g.ldhq;
-    const uint32_t r16 = wm * RW + (lane & 15), q16 = lane >> 4;
+    const uint32_t r16 = wm * 32 + (lane & 15), q16 = lane >> 4;
     // Gates and ups of a round: the lane's 64 bytes of each.  Loaded as 64-byte runs of 16
     // rows an instruction (instruction k: rows 16 (k % 2) .., chunks 4 (k / 2) + lane / 16 of a
     // row's 8 chunks of 16 bytes), and dealt to their lanes by exchanges of 16
@@ -1240,7 +1267,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
     auto load_gu = [&](int i, uint4 (&v)[8]) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t o = gu_off[k >> 1] + (uint32_t)(i * 32 + 16 * (k & 1)) * ldgu;
+        const uint32_t o = gu_off[k >> 1] + (uint32_t)(i * 64 + 16 * (k & 1)) * ldgu;
         v[k] = buffer_load(dgu_g, o);
         v[4 + k] = buffer_load(dgu_u, o);
       }
@@ -1267,11 +1294,11 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
       uint4 x = make_uint4(w[0], w[1], w[2], w[3]), y = make_uint4(w[4], w[5], w[6], w[7]);
       swap16(x, y);
       const auto d = up ? dq_u : dq_g;
-      buffer_store(d, q_off + (uint32_t)(i * 32) * ldhq, x);
-      buffer_store(d, q_off + (uint32_t)(i * 32 + 16) * ldhq, y);
-      srow[(wm * RW + i * 32 + r32) * 16 + up * 8 + (bn >> 5) + half] = (uint8_t)code;
+      buffer_store(d, q_off + (uint32_t)(i * 64) * ldhq, x);
+      buffer_store(d, q_off + (uint32_t)(i * 64 + 16) * ldhq, y);
+      srow[arow(i) * 16 + up * 8 + (bn >> 5) + half] = (uint8_t)code;
       if (cbase) {
-        const int row = wm * RW + i * 32 + r32;
+        const int row = arow(i);
         if (row < rows_t && bn + 32 * half < (int)left) {
           uint16_t* o = static_cast<uint16_t*>(cbase) + (m0 + row) * g.ldc + up * F + n0 + bn + 32 * half;
 #pragma unroll
@@ -1282,7 +1309,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
         }
       }
     };
-    const int col = t & 255, wb = t >> 8;           // column items: the wavefronts' half wm = wb
+    const int col = t & 255, wb = t >> 8;           // column items: the 32-row blocks with wm = wb
     uint32_t cq[2][MI][8];                          // their codes, d gate and d up
     uint4 gu[8];
     load_gu(0, gu);
@@ -1291,15 +1318,16 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
       // whatever the weights hold, rows past the group are zero
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
-        const bool live = wm * RW + i * 32 + r32 < rows_t;
+        const bool in = arow(i) < rows_t;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int v = 0; v < 16; ++v) acc[i][j][v] = live ? acc[i][j][v] : 0.0f;
+          for (int v = 0; v < 16; ++v) acc[i][j][v] = in ? acc[i][j][v] : 0.0f;
       }
     }
     static_for<MI>([&](auto ic) {
       constexpr int i = decltype(ic)::value;
+      if (i >= live) return;                        // uniform: no rows there
       float dg[32], du[32];
       deal_gu(gu);
 #pragma unroll
@@ -1329,7 +1357,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
         float v[32];
 #pragma unroll
         for (int r = 0; r < 32; ++r) v[r] = hst[((k * 2 + wb) * 32 + r) * LD + col];
-        scol[(k * 256 + col) * 8 + wb * MI + i] = (uint8_t)mx_block(v, cq[k][i]);
+        scol[(k * 256 + col) * 8 + 2 * i + wb] = (uint8_t)mx_block(v, cq[k][i]);
         __builtin_amdgcn_sched_barrier(0);
       }
       barrier();
@@ -1343,7 +1371,8 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
       for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int d = 0; d < 2; ++d) {
-          const int chunk = (wb * (RW / 16) + 2 * i + d) ^ (col & (CH - 1));
+          if (i >= live) continue;
+          const int chunk = (4 * i + 2 * wb + d) ^ (col & (CH - 1));
           *reinterpret_cast<uint4*>(smem + (k * 256 + col) * TMR + chunk * 16) =
               make_uint4(cq[k][i][4 * d], cq[k][i][4 * d + 1], cq[k][i][4 * d + 2], cq[k][i][4 * d + 3]);
         }
@@ -1364,9 +1393,9 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
     }
     // a column's scales by one thread; a row's blocks of d gate or d up by another
     auto store_scales = [](uint8_t* d, const uint8_t* s, int n) {
-      if (n >= 2 * MI) {
-        uint64_t v = *reinterpret_cast<const uint64_t*>(s);
-        __builtin_memcpy(d, &v, 2 * MI);            // any alignment
+      if (n == 8) {
+        const uint64_t v = *reinterpret_cast<const uint64_t*>(s);
+        __builtin_memcpy(d, &v, 8);                 // any alignment
       } else {
         for (int k = 0; k < n; ++k) d[k] = s[k];
       }
@@ -1378,14 +1407,8 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
     }
     if (t < 2 * TMR && (t >> 1) < rows_t) {
       const int n = left < TN ? (int)left / 32 : 8;
-      uint8_t* d = g.hs + (m0 + (t >> 1)) * g.ldhs + (((t & 1) * F + n0) >> 5);
-      const uint8_t* s = srow + (t >> 1) * 16 + (t & 1) * 8;
-      if (n == 8) {
-        const uint64_t v = *reinterpret_cast<const uint64_t*>(s);
-        __builtin_memcpy(d, &v, 8);
-      } else {
-        for (int k = 0; k < n; ++k) d[k] = s[k];
-      }
+      store_scales(g.hs + (m0 + (t >> 1)) * g.ldhs + (((t & 1) * F + n0) >> 5),
+                   srow + (t >> 1) * 16 + (t & 1) * 8, n);
     }
     return;
   }
@@ -1886,8 +1909,9 @@ extern "C" int mx_grouped_gemm_swiglu_backward(
   g.hcap = M_cap;
   g.poff = offsets_padded;
   g.gu = gu; g.ldgu = ldgu;
-  // Workgroups past the group tiles only clear their share past the padded total.
-  const int64_t blocks = sat_mul(tiles_of(M, TM) + E, g.tiles_n);
+  // Workgroups past the group tiles only clear their share past the padded total; the last
+  // tiles may go in parts, up to 3 more workgroups each for at most a quarter of the CUs.
+  const int64_t blocks = sat_add(sat_mul(tiles_of(M, TM) + E, g.tiles_n), 3 * (kCUs / 4));
   if (blocks > 0x7FFFFFFF) return MXQ_ERR_SHAPE;
   g.nblocks = (uint32_t)blocks;
   const dim3 grid((uint32_t)blocks), block(kThreads);
