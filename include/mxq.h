@@ -587,11 +587,13 @@ MXQ_API int mx_grouped_gemm_swiglu_backward(
  *                 M, F, 0, 0) bytes, 16-byte aligned.
  * Requires K % 32 == 0, F % 32 == 0; code row and expert strides multiples of 16
  * with 16-byte aligned codes; scales have no alignment rule.  M <=
- * MXQ_FFN_DECODE_MAX_ROWS; K, F, N <= MXQ_FFN_DECODE_MAX_DIM.  Rows outside every
+ * MXQ_FFN_DECODE_MAX_ROWS; K, F, N <= MXQ_FFN_DECODE_MAX_DIM; row strides of codes
+ * and scales <= MXQ_FFN_DECODE_MAX_STRIDE.  Rows outside every
  * group are not written.  M == 0 or N == 0 is a no-op; K == 0 or F == 0 writes zeros.
  */
 #define MXQ_FFN_DECODE_MAX_ROWS (1 << 20)
 #define MXQ_FFN_DECODE_MAX_DIM (1 << 20)
+#define MXQ_FFN_DECODE_MAX_STRIDE (1 << 26)
 typedef struct mxq_ffn_decode {
   const uint8_t* x;
   const uint8_t* x_scale;

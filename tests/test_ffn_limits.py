@@ -60,6 +60,7 @@ def test_norm_gradient(host_only_lib, change, status):  # noqa: F811
     ({"ldd": 72}, 3), ({"ldw": 72}, 3), ({"we": 8}, 3), ({"we": -16}, 2), ({"ldgu": 32}, 2), ({"ldgu": 68}, 3),
     ({"lddgu": 60}, 2), ({"dgu": P + 2}, 3), ({"gu": P + 8}, 3), ({"ldq": 72}, 3), ({"lds": 1}, 2), ({"ldqT": 136}, 3),
     ({"ldqT": 64}, 2), ({"ldsT": 3}, 2), ({"q": P + 8}, 3), ({"qT": P + 8}, 3), ({"F": 0}, 0),
+    ({"ldgu": 1 << 23}, 2), ({"ldq": 1 << 24}, 2), ({"ldqT": 1 << 32}, 2),
     ({"M": 1 << 39, "M_cap": 1 << 39, "ldqT": 1 << 39, "ldsT": 1 << 39, "E": 1}, 2)])
 def test_swiglu_gradient(host_only_lib, change, status):  # noqa: F811
     assert _call(host_only_lib, "mx_grouped_gemm_swiglu_backward", SWIGLU, **change) == status
@@ -67,7 +68,7 @@ def test_swiglu_gradient(host_only_lib, change, status):  # noqa: F811
 
 @pytest.mark.parametrize("change,status", [
     ({"M": -1}, 2), ({"K": 40}, 2), ({"F": 40}, 2), ({"E": 0}, 2), ({"E": 257}, 2), ({"offsets": None}, 2),
-    ({"M": 1 << 21}, 2), ({"N": 1 << 21}, 2), ({"x": None}, 1), ({"gus": None}, 1), ({"d": None}, 1), ({"y": None}, 1),
+    ({"M": 1 << 21}, 2), ({"N": 1 << 21}, 2), ({"ldgu": (1 << 26) + 16}, 2), ({"x": None}, 1), ({"gus": None}, 1), ({"d": None}, 1), ({"y": None}, 1),
     ({"ws": None}, 1), ({"ws_bytes": 4 * 33 - 1}, 5), ({"ws": P + 8}, 3), ({"ldx": 32}, 2), ({"ldx": 72}, 3),
     ({"ldsgu": 1}, 2), ({"ldd": 40}, 3), ({"gue": 8}, 3), ({"de": -16}, 2), ({"ldy": 39}, 2), ({"y": P + 1}, 3),
     ({"x": P + 8}, 3), ({"d": P + 8}, 3), ({"M": 0}, 0), ({"N": 0}, 0)])
