@@ -84,7 +84,11 @@ def _call(x, w_gu, w_down, offs=None, **kw):
 # M, K, F, N: one token, partial token tiles, one and many blocks, odd N, both splits of F
 DENSE = [(1, 32, 32, 1), (1, 2048, 352, 256), (2, 96, 64, 17), (7, 288, 2080, 40), (16, 512, 96, 64),
          (17, 640, 128, 33), (31, 2080, 32, 16), (33, 544, 160, 100), (64, 256, 2112, 48),
-         (65, 256, 64, 31), (130, 128, 96, 8), (3, 4128, 64, 5)]
+         (65, 256, 64, 31), (130, 128, 96, 8), (3, 4128, 64, 5),
+         # a wavefront's whole share of the contraction in one iteration
+         (9, 64, 1408, 20), (1, 64, 10944, 24), (8, 32, 9216, 16), (2, 64, 1408, 9), (12, 64, 1536, 16),
+         # two and four token tiles a workgroup; more token tiles than workgroups along them
+         (20, 64, 8256, 24), (64, 64, 10944, 16), (50, 96, 64, 4112), (1100, 32, 32, 16)]
 
 
 @pytest.mark.parametrize("M,K,F,N", DENSE)
@@ -96,7 +100,7 @@ def test_dense(M, K, F, N):
 
 @pytest.mark.parametrize("counts,K,F,N", [
     ([1, 0, 3, 2], 256, 96, 48), ([0, 0, 9], 160, 64, 33), ([17, 1, 0, 40, 70], 288, 128, 64),
-    ([2] * 40, 512, 32, 16), ([0, 300, 1, 0], 64, 64, 40)])
+    ([2] * 40, 512, 32, 16), ([0, 300, 1, 0], 64, 64, 40), ([3, 0, 2, 1, 7, 9], 64, 1408, 24)])
 def test_experts(counts, K, F, N):
     say(f"gated ffn experts {counts} K={K} F={F} N={N}")
     offs = workloads.offsets_from_counts(np.array(counts, np.int64))

@@ -74,7 +74,8 @@ def _check_norm(s, w, out, cap=None):
 
 
 ROWS = [(1, 32), (3, 64), (33, 96), (5, 512), (129, 544), (40, 2048), (1030, 2048), (1025, 1056),
-        (37, 2080), (7, 4096), (9, 4128), (4, 8192), (3, 8224), (2, 16384), (2, 12000 // 32 * 32)]
+        (37, 2080), (7, 4096), (9, 4128), (4, 8192), (3, 8224), (2, 16384), (2, 12000),
+        (300, 1024), (4100, 2048)]
 
 
 @pytest.mark.parametrize("M,K", ROWS)

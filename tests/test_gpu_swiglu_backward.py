@@ -189,6 +189,34 @@ def test_gradient_against_differences():
         assert abs((dgu * d).sum() - num) <= (2.0 ** -8 + 1e-4) * np.abs(dgu * d).sum() + 1e-6
 
 
+@pytest.mark.parametrize("rows,split", [(256 * 14 + 40, 2), (256 * 30, 1), (256 * 45 + 7, 4)])
+def test_tiles_in_parts(rows, split):
+    """Whole tiles, and the last ones in halves or quarters: how a call's tiles are dealt does
+    not change a row's or a block's result.  Columns 1408: 6 tiles across, so 90, 180 and 276
+    tiles; against calls of one group's 640 rows, whose 18 tiles go in quarters."""
+    say(f"SwiGLU gradient {rows} rows, the last tiles in {split}")
+    F, K, step = 1408, 64, 640
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    draw = lambda *s, sigma=1.0: (torch.randn(*s, generator=gen, device="cuda") * sigma).to(torch.bfloat16)
+    dq, ds = mxq.mx_quantize_rowwise(draw(rows, K))
+    wq, ws = mxq.mx_quantize_rowwise(draw(F, K, sigma=0.02))
+    w = wq.view(1, F, K), ws.view(1, F, K // 32)
+    gu = draw(rows, 2 * F)
+    off = lambda n: torch.tensor([0, n], device="cuda")
+    for accum in (mxq.ACC_MFMA_FP8, mxq.ACC_FP32):
+        every = mxq.mx_grouped_gemm_swiglu_backward(dq, ds, *w, gu, off(rows), dgu=True, accum=accum)
+        for a in range(0, rows, step):
+            n = min(step, rows - a)
+            part = mxq.mx_grouped_gemm_swiglu_backward(dq[a:a + n], ds[a:a + n], *w, gu[a:a + n], off(n),
+                                                       dgu=True, accum=accum)
+            for u, v in zip(every[:3], part[:3]):
+                assert torch.equal(u[a:a + n], v)
+            p = -(-n // 32) * 32
+            assert torch.equal(every[3][:, a:a + p], part[3][:, :p])
+            assert torch.equal(every[4][:, a // 32:(a + p) // 32], part[4][:, :p // 32])
+        assert (every[3][:, -(-rows // 32) * 32:] == 0).all()
+
+
 def test_rows_outside_the_groups_are_left():
     """Offsets that start after row 0 and end before row M."""
     ops = _operands([40, 90, 50], 96, 64, seed=6)
