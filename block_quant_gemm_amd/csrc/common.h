@@ -254,9 +254,19 @@ __device__ __forceinline__ uint32_t mx_code_of(float top) {
 }
 
 // Conversions of this wavefront to E4M3 saturate from here on, instead of giving NaN
-// from 464 on (MODE.FP16_OVFL).
+// from 464 on (MODE.FP16_OVFL).  The mode reaches conversions to BF16 too: what FP32 still holds
+// and BF16 does not would become BF16's largest value instead of infinity, so they are made
+// before, or after plain_conversions.
 __device__ __forceinline__ void saturate_conversions() {
   __builtin_amdgcn_s_setreg(1 | 23 << 6, 1);        // hwreg(MODE), bit 23, one bit
+}
+__device__ __forceinline__ void plain_conversions() { __builtin_amdgcn_s_setreg(1 | 23 << 6, 0); }
+
+// Holds a conversion's operand or result on its side of a change of the mode: neither it nor the
+// change moves past this.
+template <class T>
+__device__ __forceinline__ void pin(T& v) {
+  asm volatile("" : "+v"(v));
 }
 
 // An MX block of 32 FP32 values: its E8M0 code and the 32 E4M3 codes.  The largest

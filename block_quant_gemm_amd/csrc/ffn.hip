@@ -8,6 +8,13 @@
 // each holding its weights in registers as they come from memory, and add their
 // sums in LDS in a fixed order.
 //
+// Bound: the bytes where there are many (64 experts of 2048 x 1408, 64 rows: gate/up 80 us for
+// 389 MB, 4.9 TB/s; down 35 us for 193 MB, 5.5 TB/s), else the chain of offsets, weights and sums
+// (one token, 2048 x 10944: gate/up 16 us for 46 MB, down 6 us for 23 MB; a workgroup alone takes
+// 7.6 us) and the rate at which a CU takes load instructions, some 50 cycles each.  Weights through
+// LDS, their scales through LDS or as dwords, 16 wavefronts for gate/up, and loads past the caches were
+// all slower.
+//
 // Products are exact: codes are widened to BF16 with the block's scale folded in
 // and multiplied on v_mfma_f32_16x16x32_bf16, which takes, per lane l, 8 values of row
 // (token) l % 16.  Which k each lane's values are is free as long as both
@@ -133,7 +140,8 @@ __device__ __forceinline__ void gate_store(const FfnArgs& g, float a, float u, i
   }
 }
 
-// Workgroups along z take a group's token tiles in turn.
+// Workgroups along z take a group's token tiles in turn.  T tiles of 16 tokens share a weight read;
+// two runs of loads ahead (STEPS) as far as the registers go.
 template <int T, int NW, int STEPS>
 __global__ __launch_bounds__(NW * 64, T == 1 ? 4 : 2) void k_ffn_gate(FfnArgs g) {
   constexpr int LD = 68;                            // 64 rows and padding
@@ -245,12 +253,10 @@ static inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) 
 
 constexpr int64_t kMaxStride = int64_t(1) << 39;
 
-// Codes [rows, K] and their scales.  16 rows have 32-bit offsets.
+// Codes [rows, K] and their scales.
 static int check_codes(const uint8_t* q, const uint8_t* s, int64_t ld, int64_t lds, int64_t K) {
   if (!q || !s) return MXQ_ERR_NULL;
-  if (ld < K || lds < K / 32 || ld > MXQ_FFN_DECODE_MAX_STRIDE ||
-      lds > MXQ_FFN_DECODE_MAX_STRIDE)
-    return MXQ_ERR_SHAPE;
+  if (ld < K || lds < K / 32 || ld > kMaxStride || lds > kMaxStride) return MXQ_ERR_SHAPE;
   return ld % 16 == 0 && aligned(q, 16) ? MXQ_OK : MXQ_ERR_ALIGN;
 }
 
@@ -311,12 +317,15 @@ extern "C" int mx_gated_ffn_decode(const mxq_ffn_decode* ffn, hipStream_t stream
   const int64_t units = (N + 15) / 16 * E;
   const int T = tiles(units);
   // eight columns a workgroup where sixteen would leave CUs without one (one token, 2048 x 10944:
-  // 6.2 us and 8.8)
+  // 6.0 us and 9.4)
   const bool narrow = M <= 8 && units <= 256;
   const dim3 grid((uint32_t)(narrow ? (N + 7) / 8 : (N + 15) / 16), (uint32_t)E, along_z(T));
 #define MXQ_DOWN(T, SPAN, NW)                                                                  \
   hipLaunchKernelGGL((k_ffn_down<T, SPAN, NW>), grid, dim3(NW * 64), 0, stream, a)
-  if (F > 2048) {
+  // sixteen wavefronts for long rows only, where four would take many turns each (one token, F =
+  // 10944: 6.1 us and 7.3, F = 8192: 7.0 and 6.7, F = 4096: 6.9 and 5.1; 48 tokens, F = 10944: 19.5 and
+  // 21.6; 64 experts, F = 1408: 107 and 41)
+  if (F > 8192) {
     if (narrow) MXQ_DOWN(1, 2, 16);
     else if (T == 1) MXQ_DOWN(1, 1, 16);
     else if (T == 2) MXQ_DOWN(2, 1, 16);

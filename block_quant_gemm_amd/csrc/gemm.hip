@@ -1239,6 +1239,10 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
     // to itself.  Both go to LDS in FP32 ([64 rows][256 columns] each, rows
     // padded), from which (column, 32-row block) items, one a lane, make the
     // column copy.  Rows past the group are zero: the column copy's padding.
+    // Bound: the product's loop, then the epilogue's vector instructions, some 16 us a tile (49152
+    // rows, 64 experts, 1408 x 2048: 326 us, the product alone 191; 2048 x 10944 x 2048: 107 and 65;
+    // one expert of 1501 rows in FP32 mode 52 and 43).  A lane to a block instead of 4 columns of 8
+    // rows halved it: no exchanges for the largest magnitude, codes four a dword.
     saturate_conversions();
     constexpr int LD = TN + 4;
     static_assert(2 * 64 * LD * 4 <= kSmem && 512 * TMR <= kSmem, "staged gradients");
@@ -1298,15 +1302,24 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
       buffer_store(d, q_off + (uint32_t)(i * 64 + 16) * ldhq, y);
       srow[arow(i) * 16 + up * 8 + (bn >> 5) + half] = (uint8_t)code;
       if (cbase) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) pin(w[k]);
+        plain_conversions();
         const int row = arow(i);
         if (row < rows_t && bn + 32 * half < (int)left) {
           uint16_t* o = static_cast<uint16_t*>(cbase) + (m0 + row) * g.ldc + up * F + n0 + bn + 32 * half;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(o + 8 * k) =
-                make_uint4(bf16x2_bits(v[8 * k], v[8 * k + 1]), bf16x2_bits(v[8 * k + 2], v[8 * k + 3]),
-                           bf16x2_bits(v[8 * k + 4], v[8 * k + 5]), bf16x2_bits(v[8 * k + 6], v[8 * k + 7]));
+          for (int k = 0; k < 4; ++k) {
+            float a[8];
+            uint32_t b[4];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) pin(a[e] = v[8 * k + e]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pin(b[e] = bf16x2_bits(a[2 * e], a[2 * e + 1]));
+            *reinterpret_cast<uint4*>(o + 8 * k) = make_uint4(b[0], b[1], b[2], b[3]);
+          }
         }
+        saturate_conversions();
       }
     };
     const int col = t & 255, wb = t >> 8;           // column items: the 32-row blocks with wm = wb

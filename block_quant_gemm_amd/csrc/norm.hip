@@ -5,7 +5,8 @@
 //   dx = rstd (dy w - s rstd c) + ds,  c = mean_k(dy w s rstd),  dw = sum_m dy s rstd
 //
 // Both are streams: every element is read and written once (the column copy
-// reads s again), so bytes bound them.
+// of wide rows reads s again), so bytes bound them; under a few thousand rows the latency of one
+// row's chain does (7 rows of 2048: 3.4 us), and below that the host's time of the call.
 
 #include "common.h"
 
@@ -75,7 +76,7 @@ __device__ __forceinline__ void normed8(uint4 s, float rstd, uint4 w, float (&y)
 
 // A row is held by W wavefronts, CH chunks of 8 elements a lane, so it is read
 // once.  Lane l of wavefront v holds elements 8 (64 (W c + v) + l) .. + 8 of
-// chunk c.
+// chunk c.  Measured, 16384 x 2048 with a residual: 41.7 us for 235 MB (5.6 TB/s).
 template <int W, int CH>
 __global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_rows(mxq_norm g) {
   constexpr int ROWS = W >= 4 ? 1 : 4 / W;          // rows a workgroup
@@ -153,7 +154,6 @@ template <int CH>
 __global__ __launch_bounds__(512, 4) void k_norm_dual(mxq_norm g) {
   constexpr int RW = 4, LD = 512 + 4;               // rows a wavefront; LDS row of floats
   __shared__ __attribute__((aligned(16))) float tile[32 * LD];
-  saturate_conversions();
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
   uint32_t rb = blockIdx.x;
   if ((rb | 31u) < gridDim.x) rb = (rb & ~31u) | ((rb & 7u) << 2) | ((rb >> 3) & 3u);
@@ -212,8 +212,12 @@ __global__ __launch_bounds__(512, 4) void k_norm_dual(mxq_norm g) {
     if (512u * c >= K) break;                       // uniform
     const uint32_t col = 512 * c + 8 * lane;
     const bool in = col < K;
-    const uint4 w = in ? *reinterpret_cast<const uint4*>(g.weight + col) : make_uint4(0, 0, 0, 0);
-    if (c) __syncthreads();                         // the columns before have been read
+    uint4 w = in ? *reinterpret_cast<const uint4*>(g.weight + col) : make_uint4(0, 0, 0, 0);
+    if (c) {
+      plain_conversions();
+      pin(w.x), pin(w.y), pin(w.z), pin(w.w);       // y is formed after it
+      __syncthreads();                              // the columns before have been read
+    }
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
       float y[8];
@@ -231,6 +235,7 @@ __global__ __launch_bounds__(512, 4) void k_norm_dual(mxq_norm g) {
       *reinterpret_cast<f32x4*>(t + 4) = ok ? f32x4{y[4], y[5], y[6], y[7]} : f32x4{0, 0, 0, 0};
     }
     __syncthreads();
+    saturate_conversions();                         // not over total and y
     const uint32_t kc = 512 * c + threadIdx.x;
     if (kc < K) {
       float v[32];
@@ -238,6 +243,8 @@ __global__ __launch_bounds__(512, 4) void k_norm_dual(mxq_norm g) {
       for (int i = 0; i < 32; ++i) v[i] = tile[i * LD + threadIdx.x];
       uint32_t o[8];
       const uint32_t code = mx_block(v, o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) pin(o[i]);
       uint8_t* d = g.qT + kc * g.ldqT + (int64_t)rb * 32;
       *reinterpret_cast<uint4*>(d) = make_uint4(o[0], o[1], o[2], o[3]);
       *reinterpret_cast<uint4*>(d + 16) = make_uint4(o[4], o[5], o[6], o[7]);
@@ -250,7 +257,7 @@ __global__ __launch_bounds__(512, 4) void k_norm_dual(mxq_norm g) {
 // s and rstd, in LDS, each wavefront a block of 32 rows, a column a lane; the codes leave as
 // 128-byte lines of the transpose.  The next columns' loads are under way meanwhile.
 // Measured, 16384 x 2048: 22 us for 101 MB (4.6 TB/s; 25 without the loads ahead), after 41 us of
-// k_norm_rows for 167 MB more (5.5).  One kernel for both with 32 whole rows a workgroup in registers took
+// k_norm_rows for 235 MB more (5.6).  One kernel for both with 32 whole rows a workgroup in registers took
 // 73: it reads s once, but 8 wavefronts a CU are too few to load and store at once.
 constexpr int kNcRows = 128, kNcCols = 64, kNcLd = kNcCols + 1;
 
@@ -323,7 +330,8 @@ __global__ __launch_bounds__(256) void k_norm_columns(mxq_norm g, uint32_t width
 // Workgroup b takes rows b, b + grid, ...; a row is held as in k_norm_rows.
 // dw's sums stay in registers over a wavefront's rows; the workgroup's wavefronts
 // add theirs in order, and k_norm_join the workgroups', so the result
-// does not depend on timing.
+// does not depend on timing.  Measured, 16384 x 2048 with ds: 51 us for 268 MB
+// (5.3 TB/s), then 4.8 us for the join of 512 sums.
 template <int W, int CH>
 __global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_grad(mxq_norm_grad g) {
   constexpr int ROWS = W >= 4 ? 1 : 4 / W;
@@ -498,6 +506,8 @@ extern "C" int mx_rms_norm(const mxq_norm* norm, hipStream_t stream) {
     if (!aligned(g.weight, 16) || !aligned(g.rstd, 4) || g.ldq % 16 != 0 || !aligned(g.q, 16))
       return MXQ_ERR_ALIGN;
   }
+  // one kernel for both copies: 16384 x 1024 34.5 us and 38.7 as two, 16384 x 512 19.8 and 22.7; below
+  // some 3000 rows a microsecond longer than the two, but a launch less to wait for
   if (g.qT && K <= 1024) {
     const dim3 grid((uint32_t)(g.M_cap / 32)), block(512);
     if (K <= 512) hipLaunchKernelGGL(k_norm_dual<1>, grid, block, 0, stream, g);
@@ -509,7 +519,9 @@ extern "C" int mx_rms_norm(const mxq_norm* norm, hipStream_t stream) {
                      dim3(W == 16 ? 1024 : 256), 0, stream, g)
   if (M > 0) {
     if (K <= 512) MXQ_ROWS(1, 1);
-    else if (K <= 2048 && M >= 1024) MXQ_ROWS(1, 4);
+    // a wavefront a row once there are rows enough to fill the chip, a workgroup a row before (K =
+    // 2048: 512 rows 6.0 us and 4.5, 1024 6.6 and 5.2, 2048 9.6 both, 16384 41.7 and 46.3)
+    else if (K <= 2048 && M >= 2048) MXQ_ROWS(1, 4);
     else if (K <= 2048) MXQ_ROWS(4, 1);
     else if (K <= 4096) MXQ_ROWS(4, 2);
     else if (K <= 8192) MXQ_ROWS(4, 4);

@@ -570,8 +570,9 @@ MXQ_API int mx_grouped_gemm_swiglu_backward(
  * [offsets[e], offsets[e+1])
  *   h = silu(g) * u of the gate/up product (FP32), MX-quantized row-wise,
  *   y[rows, :] = h . W_down,eT,
- * as mx_grouped_gemm_swiglu and mx_grouped_gemm with MXQ_ACC_FP32 would form them:
- * products exact, sums FP32, y rounded to BF16 once.  For any number of rows, but
+ * the operators of mx_grouped_gemm_swiglu and mx_grouped_gemm with products exact
+ * and sums FP32 (MXQ_ACC_FP32), y rounded to BF16 once; operands beyond BF16's range
+ * (scale codes from 247) make a sum infinite or NaN.  For any number of rows, but
  * made for a few per group: each 64 rows of a group read its weights again.
  *   ffn         : host struct, read during the call only:
  *   x, x_scale  : device, [M, K] codes / [M, K/32] scales, strides ldx, ldsx.
@@ -587,13 +588,11 @@ MXQ_API int mx_grouped_gemm_swiglu_backward(
  *                 M, F, 0, 0) bytes, 16-byte aligned.
  * Requires K % 32 == 0, F % 32 == 0; code row and expert strides multiples of 16
  * with 16-byte aligned codes; scales have no alignment rule.  M <=
- * MXQ_FFN_DECODE_MAX_ROWS; K, F, N <= MXQ_FFN_DECODE_MAX_DIM; row strides of codes
- * and scales <= MXQ_FFN_DECODE_MAX_STRIDE.  Rows outside every
+ * MXQ_FFN_DECODE_MAX_ROWS; K, F, N <= MXQ_FFN_DECODE_MAX_DIM.  Rows outside every
  * group are not written.  M == 0 or N == 0 is a no-op; K == 0 or F == 0 writes zeros.
  */
 #define MXQ_FFN_DECODE_MAX_ROWS (1 << 20)
 #define MXQ_FFN_DECODE_MAX_DIM (1 << 20)
-#define MXQ_FFN_DECODE_MAX_STRIDE (1 << 26)
 typedef struct mxq_ffn_decode {
   const uint8_t* x;
   const uint8_t* x_scale;

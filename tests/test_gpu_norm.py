@@ -260,3 +260,42 @@ def test_repeated_calls_give_the_same_bits():
     for _ in range(3):
         b = mxq.mx_rms_norm_backward(dy, x, out[1], w)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("K,columns", [(96, False), (96, True), (544, True), (1056, True), (4128, False)])
+def test_values_past_the_range_of_bfloat16(K, columns):
+    """total and y that FP32 holds and BF16 does not are infinite, with the column copy too;
+    their codes come from the FP32 value."""
+    M = 33
+    top = 0x7F7F                                            # (2 - 2^-7) 2^127
+    x = np.zeros((M, K), np.uint16)
+    r = np.zeros((M, K), np.uint16)
+    x[5, 40], r[5, 40] = top, 0x7B00                        # + 2^119: a tie, to the even 2^128
+    x[6, 40], r[6, 40] = top | 0x8000, 0xFB00
+    x[7, 40], r[7, 40] = top, 0x7A80                        # + 2^118: back to the largest value
+    w = np.full(K, 0x3F80, np.uint16)
+    total, rstd, y, *_ = [None if t is None else host(t) for t in mxq.mx_rms_norm(
+        to_dev_bf16(x), to_dev_bf16(w[None])[0].contiguous(), residual=to_dev_bf16(r), eps=EPS, y=True,
+        columns=columns)]
+    assert (total[5, 40], total[6, 40], total[7, 40]) == (0x7F80, 0xFF80, top)
+    assert np.isnan(bf16_bits_to_f64(y[5:7])).any(axis=1).all()
+    # y = s w / rms.  Rows of ones: rms just above 1, y just below w's largest value
+    s = np.full((M, K), 0x3F80, np.uint16)
+    s[3, 64], w[64] = 0x3FC0, top                           # 1.5: past FP32's range too
+    s[4, 64] = 0x3F81                                       # (1 + 2^-7) (2 - 2^-7) > 2: as well
+    # 181^2 / 2^14 = 1.99957 is between BF16's largest (2 - 2^-7, up to 2 - 2^-8 rounding to it) and
+    # FP32's; the row's squares are K - 2 + 0 + 1.99945, so rms is 1 to 3 / K 10^-4
+    s[8, 65], s[8, 66], w[65] = 0x3FB5, 0, 0x7F35
+    v = bf16_bits_to_f64(s)
+    ref = norm.rms_norm(v, bf16_bits_to_f64(w), EPS)[1]
+    assert (2 - 2.0 ** -8) * 2.0 ** 127 < ref[8, 65] < (2 - 2.0 ** -13) * 2.0 ** 127
+    assert (ref[[3, 4], 64] > 2.0 ** 128).all()
+    out = mxq.mx_rms_norm(to_dev_bf16(s), to_dev_bf16(w[None])[0].contiguous(), eps=EPS, y=True, columns=columns)
+    got = bf16_bits_to_f64(host(out[2]))
+    big = np.zeros((M, K), bool)
+    big[[3, 4], 64] = big[8, 65] = True
+    assert np.isinf(got[big]).all() and np.isfinite(got[~big]).all()
+    scale = host(out[4])
+    assert (scale[[3, 4], 2] == 0xFF).all() and scale[8, 2] == 127 + 119 and host(out[3])[8, 65] == 0x7E
+    if columns:
+        assert host(out[6])[64, 0] == 0xFF and host(out[6])[65, 0] == 127 + 119 and host(out[5])[65, 8] == 0x7E

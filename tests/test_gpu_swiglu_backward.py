@@ -287,3 +287,23 @@ def test_equals_the_unfused_chain():
     top = np.repeat(np.abs(b).reshape(512, -1, 32).max(2), 32, axis=1)
     assert (np.abs(a - b) <= 2.0 ** -3 * np.abs(b) + 2.0 ** -3 * top).all()
     assert (a == b).mean() > 0.9
+
+
+@pytest.mark.parametrize("accum", [mxq.ACC_MFMA_FP8, mxq.ACC_FP32])
+def test_values_past_the_range_of_bfloat16(accum):
+    """A gradient that FP32 holds and BF16 does not is infinite in dgu; its codes come from
+    the FP32 value.  dh = 1.75 + 0.25 - 2^-9 and g = u = 2^127, so sg = 1 and both
+    gradients are (2 - 2^-9) 2^127, which rounds to 2^128; every sum is exact."""
+    M, F, K = 70, 64, 32
+    dq, ds = np.zeros((M, K), np.uint8), np.full((M, 1), 127, np.uint8)
+    wq, ws = np.zeros((F, K), np.uint8), np.full((F, 1), 127, np.uint8)
+    dq[:, :3] = 0x38                                        # 1
+    wq[:, 0], wq[:, 1], wq[:, 2] = 0x3E, 0x28, 0x81         # 1.75, 0.25, -2^-9
+    gu = np.full((M, 2 * F), 0x3F80, np.uint16)
+    gu[[0, 33, 69]] = 0x7F00                                # 2^127
+    dgu, q, sc, qT, sT, _ = _run(np.array([0, M]), dq, ds, wq, ws, gu, accum=accum)
+    v = bf16_bits_to_f64(dgu)
+    assert np.isposinf(v[[0, 33, 69]]).all() and np.isfinite(np.delete(v, [0, 33, 69], 0)).all()
+    # 1.998 2^127 = 448 * 2^119 * 1.14, saturated
+    assert (sc[[0, 33, 69]] == 127 + 119).all() and (q[[0, 33, 69]] == 0x7E).all()
+    assert (sT[:, :3] == 127 + 119).all() and (qT[:, [0, 33, 69]] == 0x7E).all()
