@@ -496,15 +496,16 @@ extern "C" int mx_rms_norm(const mxq_norm* norm, hipStream_t stream) {
     if (g.ldqT % 16 != 0 || !aligned(g.qT, 16)) return MXQ_ERR_ALIGN;
   }
   if (K == 0 || (M == 0 && (!g.qT || g.M_cap == 0))) return MXQ_OK;
+  if (!g.weight) return MXQ_ERR_NULL;               // the column copy's kernels read it without rows too
+  if (!aligned(g.weight, 16)) return MXQ_ERR_ALIGN;
   if (M > 0) {
     if ((st = check_rows(g.x, g.ldx, K))) return st;
     if (g.residual && (st = check_rows(g.residual, g.ldr, K))) return st;
     if (g.residual && (st = check_rows(g.total, g.ldt, K))) return st;
     if (g.y && (st = check_rows(g.y, g.ldy, K))) return st;
-    if (!g.weight || !g.rstd || !g.q || !g.scale) return MXQ_ERR_NULL;
+    if (!g.rstd || !g.q || !g.scale) return MXQ_ERR_NULL;
     if (g.ldq < K || g.lds < K / 32 || g.ldq > kMaxStride || g.lds > kMaxStride) return MXQ_ERR_SHAPE;
-    if (!aligned(g.weight, 16) || !aligned(g.rstd, 4) || g.ldq % 16 != 0 || !aligned(g.q, 16))
-      return MXQ_ERR_ALIGN;
+    if (!aligned(g.rstd, 4) || g.ldq % 16 != 0 || !aligned(g.q, 16)) return MXQ_ERR_ALIGN;
   }
   // one kernel for both copies: 16384 x 1024 34.5 us and 38.7 as two, 16384 x 512 19.8 and 22.7; below
   // some 3000 rows a microsecond longer than the two, but a launch less to wait for

@@ -729,7 +729,7 @@ MXQ_API int fp8_grouped_gemm_wgrad_per_group(const uint8_t* at, const float* a_s
  * Requires K % 32 == 0; ldx, ldr, ldt, ldy multiples of 8, ldq and ldqT of 16; all
  * pointers but rstd, scale and scaleT 16-byte aligned.  M <= MXQ_NORM_MAX_ROWS, K <=
  * MXQ_NORM_MAX_COLS.  Outputs other than total must not overlap inputs.  K == 0
- * is a no-op, M == 0 writes only the column copy's zeros.
+ * is a no-op, M == 0 writes only the column copy's zeros (and reads the weight).
  */
 #define MXQ_NORM_MAX_ROWS (1 << 25)
 #define MXQ_NORM_MAX_COLS 16384
