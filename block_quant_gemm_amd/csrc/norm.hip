@@ -467,6 +467,8 @@ using namespace mxq;
 static inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 constexpr int64_t kMaxStride = INT64_C(1) << 39;
+// Rows a launch of k_norm_rows: a grid holds less than 2^32 threads, a row takes up to 1024 of them.
+constexpr int64_t kRowsALaunch = INT64_C(1) << 21;
 
 // A row operand of K BF16 values: NULL, stride and alignment.
 static int check_rows(const void* p, int64_t ld, int64_t K) {
@@ -516,9 +518,17 @@ extern "C" int mx_rms_norm(const mxq_norm* norm, hipStream_t stream) {
     return hipGetLastError() == hipSuccess ? MXQ_OK : MXQ_ERR_HIP;
   }
 #define MXQ_ROWS(W, CH)                                                                        \
-  hipLaunchKernelGGL((k_norm_rows<W, CH>), dim3((uint32_t)(W >= 4 ? M : (M + 3) / 4)),         \
-                     dim3(W == 16 ? 1024 : 256), 0, stream, g)
-  if (M > 0) {
+  hipLaunchKernelGGL((k_norm_rows<W, CH>), dim3((uint32_t)(W >= 4 ? r.M : (r.M + 3) / 4)),     \
+                     dim3(W == 16 ? 1024 : 256), 0, stream, r)
+  for (int64_t m = 0; m < M; m += kRowsALaunch) {
+    mxq_norm r = g;
+    r.M = M - m < kRowsALaunch ? M - m : kRowsALaunch;
+    r.x += m * g.ldx;
+    if (g.residual) r.residual += m * g.ldr, r.total += m * g.ldt;
+    r.rstd += m;
+    if (g.y) r.y += m * g.ldy;
+    r.q += m * g.ldq;
+    r.scale += m * g.lds;
     if (K <= 512) MXQ_ROWS(1, 1);
     // a wavefront a row once there are rows enough to fill the chip, a workgroup a row before (K =
     // 2048: 512 rows 6.0 us and 4.5, 1024 6.6 and 5.2, 2048 9.6 both, 16384 41.7 and 46.3)
