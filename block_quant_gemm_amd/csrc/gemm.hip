@@ -1350,7 +1350,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
         const float sg = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.4426950408889634f));
         const float s = acc[i][e >> 4][e & 15] * sg;
         du[e] = s * x;
-        dg[e] = u * __builtin_fmaf(du[e], 1.0f - sg, s);
+        dg[e] = u * __builtin_fmaf(s, x * (1.0f - sg), s);     // not from du, which may be infinite
         if ((e & 7) == 7) __builtin_amdgcn_sched_barrier(0);   // few values in flight: registers
       }
       float* p = hst + (wm * 32 + r32) * LD + bn + 32 * half;
