@@ -1,12 +1,31 @@
-"""mx_rms_norm of more rows than one launch takes (2^21): each row is as in a call of its own."""
+"""mx_rms_norm's row copy alone, whose kernels for few columns no call with both copies takes, against
+the oracle; and of more rows than one launch takes (2^21): each row is as in a call of its own."""
 
 import pytest
 import torch
 
 from block_quant_gemm_amd import mxq
-from tests.gpu_helpers import say
+from oracle import norm
+from oracle.codec import bf16_bits_to_f64
+from tests.gpu_helpers import say, to_dev_bf16
+from tests.test_gpu_norm import EPS, _bits, _check_norm, _weight
 
 pytestmark = pytest.mark.gpu
+
+
+ROWS = [(1, 32), (3, 64), (33, 96), (5, 512), (130, 480), (2051, 288), (40, 1024), (2050, 992), (6, 2080)]
+
+
+@pytest.mark.parametrize("M,K", ROWS)
+@pytest.mark.parametrize("residual", [False, True])
+def test_row_copy_alone(M, K, residual):
+    say(f"rms norm, row copy, M={M} K={K} residual={residual}")
+    x, r, w = _bits((M, K), M + K, "nx"), _bits((M, K), M + K, "nr"), _weight(K, K)
+    out = mxq.mx_rms_norm(to_dev_bf16(x), to_dev_bf16(w), eps=EPS, y=True,
+                          residual=to_dev_bf16(r) if residual else None)
+    assert out[5] is None and out[6] is None
+    s = norm.residual_sum(x, r) if residual else bf16_bits_to_f64(x)
+    _check_norm(s, bf16_bits_to_f64(w), out)
 
 
 @pytest.mark.parametrize("K,residual", [(64, True), (64, False), (2080, False)])
