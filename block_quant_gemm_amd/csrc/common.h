@@ -247,10 +247,15 @@ __device__ __forceinline__ void quant8(uint4 v, uint32_t& lo, uint32_t& hi, uint
 // converted value into NaN.
 __device__ __forceinline__ float e8m0_f32(uint32_t c) { return __builtin_bit_cast(float, c << 23); }
 
-// E8M0 code of an MX block from its largest FP32 magnitude (NaN if it holds one).
+// E8M0 code of an MX block from its largest FP32 magnitude's pattern, sign cleared (NaN above
+// Inf above finite values).
+__device__ __forceinline__ uint32_t mx_code_of_bits(uint32_t am) {
+  const uint32_t E = am >> 23;
+  return am >= 0x7F800000u ? 0xFFu : (E > 8u ? E - 8u : 0u);
+}
+// The same from the magnitude itself (NaN, of either sign, if the block holds one).
 __device__ __forceinline__ uint32_t mx_code_of(float top) {
-  const uint32_t am = __builtin_bit_cast(uint32_t, top), E = am >> 23;
-  return (am & 0x7FFFFFFFu) >= 0x7F800000u ? 0xFFu : (E > 8u ? E - 8u : 0u);
+  return mx_code_of_bits(__builtin_bit_cast(uint32_t, top) & 0x7FFFFFFFu);
 }
 
 // Conversions of this wavefront to E4M3 saturate from here on, instead of giving NaN

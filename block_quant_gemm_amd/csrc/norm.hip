@@ -12,9 +12,6 @@
 
 namespace mxq {
 
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-
 __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
   f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
   f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
@@ -22,13 +19,6 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]), bf16x2_bits(f[4], f[5]),
                     bf16x2_bits(f[6], f[7]));
-}
-
-// MX scale code of a block from the FP32 pattern of its largest magnitude
-// (sign cleared; NaN above Inf above finite values).
-__device__ __forceinline__ uint32_t mx_scale_code_f32(uint32_t am) {
-  const uint32_t E = am >> 23;
-  return am >= 0x7F800000u ? 0xFFu : (E > 8u ? E - 8u : 0u);
 }
 
 // One MX block of 32 FP32 values held by a DPP quad, 8 a lane.
@@ -43,7 +33,7 @@ __device__ __forceinline__ uint2 quant8_f32(const float (&v)[8], uint32_t& code)
   am = am > o ? am : o;
   o = dpp_u32(am, kQuadXor2);
   am = am > o ? am : o;
-  code = mx_scale_code_f32(am);
+  code = mx_code_of_bits(am);
   if (code == 0xFFu) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
   const float inv = mx_inv_scale(code);
   uint32_t lo = cvt2_e4m3_sat<false>(v[0] * inv, v[1] * inv, 0u);
