@@ -8,9 +8,10 @@
 // each holding its weights in registers as they come from memory, and add their
 // sums in LDS in a fixed order.
 //
-// Bound: the bytes where there are many (64 experts of 2048 x 1408, 64 rows: gate/up 80 us for
-// 389 MB, 4.9 TB/s; down 35 us for 193 MB, 5.5 TB/s), else the chain of offsets, weights and sums
-// (one token, 2048 x 10944: gate/up 16 us for 46 MB, down 6 us for 23 MB; a workgroup alone takes
+// Bound: mostly the bytes where there are many (64 experts of 2048 x 1408, 96 rows over 56 of them:
+// gate/up 79 us for 333 MB of weights, 4.2 TB/s; down 35 us for 167 MB, 4.8 TB/s; a large copy 5.2),
+// else the chain of offsets, weights and sums (one token, 2048 x 10944: gate/up 16 us for 46 MB, down
+// 6 us for 23 MB; a workgroup alone takes
 // 7.6 us) and the rate at which a CU takes load instructions, some 50 cycles each.  Weights through
 // LDS, their scales through LDS or as dwords, 16 wavefronts for gate/up, and loads past the caches were
 // all slower.
@@ -291,8 +292,9 @@ extern "C" int mx_gated_ffn_decode(const mxq_ffn_decode* ffn, hipStream_t stream
             f.gus_estride, f.offsets, M, (uint32_t)(K / 32), F, hq, hq + M * F, F, F / 32, f.y,
             f.ldy, N};
   // Tokens a workgroup: the fewest tiles of 16 with which the workgroups still run at once, one a
-  // CU; where there are more anyway, as many as a group has on average, so that its weights are
-  // read once.
+  // CU; where there are more anyway, as many as a group has on average, so that an average group's
+  // weights are read once.  A larger group's tiles go one after another in the same workgroups (64 experts
+  // of 2048 x 1408: all 96 rows on one 61 us, 64 rows on one and 32 experts with one 79).
   const int64_t per = E == 1 ? M : M / E;
   auto tiles = [&](int64_t units) {
     for (const int T : {1, 2})

@@ -1239,10 +1239,13 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
     // to itself.  Both go to LDS in FP32 ([64 rows][256 columns] each, rows
     // padded), from which (column, 32-row block) items, one a lane, make the
     // column copy.  Rows past the group are zero: the column copy's padding.
-    // Bound: the product's loop, then the epilogue's vector instructions, some 16 us a tile (49152
-    // rows, 64 experts, 1408 x 2048: 326 us, the product alone 191; 2048 x 10944 x 2048: 107 and 65;
-    // one expert of 1501 rows in FP32 mode 52 and 43).  A lane to a block instead of 4 columns of 8
-    // rows halved it: no exchanges for the largest magnitude, codes four a dword.
+    // Bound: the product's loop, then the epilogue; they do not overlap (49152 rows, 64 experts, 1408 x
+    // 2048: 324 us, the product alone 191; 2048 x 10944 x 2048: 106 and 65; 1501 rows over 8 experts in
+    // FP32 mode 53 and 43).  Of the epilogue's 25 us a turn of tiles some 17 are its instructions and
+    // LDS and 8 its memory: 284 us with its reads and writes kept in L2, 315 with the reads alone, 301
+    // with the writes alone.  HBM carries 1.48 GB, 4.6 TB/s: operands are fetched twice and
+    // more.  A lane to a block instead of 4 columns of 8 rows halved the instructions: no exchanges for the
+    // largest magnitude, codes four a dword.
     saturate_conversions();
     constexpr int LD = TN + 4;
     static_assert(2 * 64 * LD * 4 <= kSmem && 512 * TMR <= kSmem, "staged gradients");
@@ -1571,6 +1574,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_swiglu_pg(GemmArgs g) {
   gemm_body<kVarM, true, MXQ_OUT_BF16, false, true, false>(g);
 }
 
+// The exact form with scale rows of any stride keeps 39 registers in scratch memory, four loads of
+// 16 bytes from it in each step of the loop: 82 us where the window form takes 52 (1501 rows, 8 experts,
+// 1408 x 2048), 686 and 457 (49152 rows, 64 experts).  The other three use no scratch.
 template <bool SW, bool XA>
 __global__ __launch_bounds__(kThreads, 1) void k_gemm_swiglu_grad(GemmArgs g) {
   gemm_body<kVarM, false, MXQ_OUT_BF16, SW, false, false, XA, 4, true>(g);

@@ -66,7 +66,7 @@ __device__ __forceinline__ void normed8(uint4 s, float rstd, uint4 w, float (&y)
 
 // A row is held by W wavefronts, CH chunks of 8 elements a lane, so it is read
 // once.  Lane l of wavefront v holds elements 8 (64 (W c + v) + l) .. + 8 of
-// chunk c.  Measured, 16384 x 2048 with a residual: 41.7 us for 235 MB (5.6 TB/s).
+// chunk c.  Measured, 16384 x 2048 with a residual: 42 us for 235 MB (5.6 TB/s; HBM carries 236).
 template <int W, int CH>
 __global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_rows(mxq_norm g) {
   constexpr int ROWS = W >= 4 ? 1 : 4 / W;          // rows a workgroup
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_rows(mxq_norm g) 
 // columns at a time, from which a lane makes a column's block.  A block is 32 bytes of
 // a column copy's row; the four that share a 128-byte line go to workgroups of one XCD, whose L2
 // then has the line whole (workgroup 32 q + 8 r + x takes block 32 q + 4 x + r).
-// Measured, 8190 x 512: 10 us, and 12.5 as two kernels.
+// Measured, 8190 x 512: 9.8 us; with a residual 12.9, and 17.8 as two kernels.
 template <int CH>
 __global__ __launch_bounds__(512, 4) void k_norm_dual(mxq_norm g) {
   constexpr int RW = 4, LD = 512 + 4;               // rows a wavefront; LDS row of floats
@@ -246,7 +246,7 @@ __global__ __launch_bounds__(512, 4) void k_norm_dual(mxq_norm g) {
 // The column copy of wider rows: `width` columns of 128 rows a workgroup, 64 at a time: y, formed again from
 // s and rstd, in LDS, each wavefront a block of 32 rows, a column a lane; the codes leave as
 // 128-byte lines of the transpose.  The next columns' loads are under way meanwhile.
-// Measured, 16384 x 2048: 22 us for 101 MB (4.6 TB/s; 25 without the loads ahead), after 41 us of
+// Measured, 16384 x 2048: 20 us for 101 MB (5.0 TB/s; 3 us more without the loads ahead), after 42 us of
 // k_norm_rows for 235 MB more (5.6).  One kernel for both with 32 whole rows a workgroup in registers took
 // 73: it reads s once, but 8 wavefronts a CU are too few to load and store at once.
 constexpr int kNcRows = 128, kNcCols = 64, kNcLd = kNcCols + 1;
@@ -499,8 +499,9 @@ extern "C" int mx_rms_norm(const mxq_norm* norm, hipStream_t stream) {
     if (g.ldq < K || g.lds < K / 32 || g.ldq > kMaxStride || g.lds > kMaxStride) return MXQ_ERR_SHAPE;
     if (!aligned(g.rstd, 4) || g.ldq % 16 != 0 || !aligned(g.q, 16)) return MXQ_ERR_ALIGN;
   }
-  // one kernel for both copies: 16384 x 1024 34.5 us and 38.7 as two, 16384 x 512 19.8 and 22.7; below
-  // some 3000 rows a microsecond longer than the two, but a launch less to wait for
+  // one kernel for both copies, with a residual: 16384 x 512 19.5 us and 21.8 as two, 16384 x 1024 34.9
+  // and 37.2, 3000 rows 9.5 and 9.5, 15.1 and 15.5; fewer rows take longer than as two (1024 rows 8.3 and
+  // 7.8, 12.3 and 8.9; 256 rows 8.1 and 7.5, 11.5 and 7.2), for a launch less of the host's time
   if (g.qT && K <= 1024) {
     const dim3 grid((uint32_t)(g.M_cap / 32)), block(512);
     if (K <= 512) hipLaunchKernelGGL(k_norm_dual<1>, grid, block, 0, stream, g);
@@ -520,8 +521,10 @@ extern "C" int mx_rms_norm(const mxq_norm* norm, hipStream_t stream) {
     r.q += m * g.ldq;
     r.scale += m * g.lds;
     if (K <= 512) MXQ_ROWS(1, 1);
-    // a wavefront a row once there are rows enough to fill the chip, a workgroup a row before (K =
-    // 2048: 512 rows 6.0 us and 4.5, 1024 6.6 and 5.2, 2048 9.6 both, 16384 41.7 and 46.3)
+    // a wavefront a row once there are rows enough to fill the chip, a workgroup a row before (K = 2048:
+    // 512 rows 6.0 us and 4.5, 1024 6.6 and 5.2, 2048 9.5 and 9.4, 4096 13.7 and 13.2, 16384 41.4 and
+    // 44.0; K = 1056: 2048 rows 7.2 and 6.6, 4096 11.0 and 10.8, 16384 27.4 and 30.3; K = 544, where
+    // one of the four chunks a lane is nearly full: 6.2 and 6.1, 8.8 and 9.8, 21.5 and 27.0)
     else if (K <= 2048 && M >= 2048) MXQ_ROWS(1, 4);
     else if (K <= 2048) MXQ_ROWS(4, 1);
     else if (K <= 4096) MXQ_ROWS(4, 2);

@@ -554,8 +554,10 @@ MXQ_API int mx_grouped_gemm_swiglu(const uint8_t* a, const uint8_t* a_scale, int
  * Requires F % 32 == 0, K % 32 == 0, M_cap % 32 == 0; ldq and ldqT multiples of 16
  * and ldgu, lddgu of 8, with 16-byte aligned q, qT, gu and dgu; the operand
  * requirements of mx_grouped_gemm; 257 rows of gu and of q within 2^31 bytes, ldqT
- * less than 2^32.  Rows outside every group are not written in q, scale and dgu.  F == 0 is a no-op; with M == 0 only offsets_padded and the
- * column copy's zeros are written.
+ * less than 2^32.  As for mx_gemm, scale row strides (of dy and wT) that are multiples
+ * of 16 take the faster path.  Rows outside every group are not written in q, scale
+ * and dgu.  F == 0 is a no-op; with M == 0 only offsets_padded and the column copy's
+ * zeros are written.
  */
 MXQ_API int mx_grouped_gemm_swiglu_backward(
     const uint8_t* dy, const uint8_t* dy_scale, int64_t ldd, int64_t ldsd, const uint8_t* wT,
@@ -573,7 +575,9 @@ MXQ_API int mx_grouped_gemm_swiglu_backward(
  * the operators of mx_grouped_gemm_swiglu and mx_grouped_gemm with products exact
  * and sums FP32 (MXQ_ACC_FP32), y rounded to BF16 once; operands beyond BF16's range
  * (scale codes from 247) make a sum infinite or NaN.  For any number of rows, but
- * made for a few per group: each 64 rows of a group read its weights again.
+ * made for a few per group: a group's rows go in tiles of 16, 32 or 64, by the
+ * average M / E of rows a group (not by this group's own), and each tile reads the
+ * group's weights again.
  *   ffn         : host struct, read during the call only:
  *   x, x_scale  : device, [M, K] codes / [M, K/32] scales, strides ldx, ldsx.
  *   w_gu, w_gu_scale : device, per expert the [2F, K] gate/up codes (gate rows
