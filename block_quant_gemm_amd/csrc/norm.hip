@@ -66,7 +66,7 @@ __device__ __forceinline__ void normed8(uint4 s, float rstd, uint4 w, float (&y)
 
 // A row is held by W wavefronts, CH chunks of 8 elements a lane, so it is read
 // once.  Lane l of wavefront v holds elements 8 (64 (W c + v) + l) .. + 8 of
-// chunk c.  Measured, 16384 x 2048 with a residual: 42 us for 235 MB (5.6 TB/s; HBM carries 236).
+// chunk c.  Measured, 16384 x 2048 with a residual: 42 us for 235 MB (5.6 TB/s).
 template <int W, int CH>
 __global__ __launch_bounds__(W == 16 ? 1024 : 256) void k_norm_rows(mxq_norm g) {
   constexpr int ROWS = W >= 4 ? 1 : 4 / W;          // rows a workgroup
