@@ -8,13 +8,13 @@
 // each holding its weights in registers as they come from memory, and add their
 // sums in LDS in a fixed order.
 //
-// Bound: mostly the bytes where there are many (64 experts of 2048 x 1408, 96 rows over 56 of them:
-// gate/up 79 us for 333 MB of weights, 4.2 TB/s; down 35 us for 167 MB, 4.8 TB/s; a large copy 5.2),
-// else the chain of offsets, weights and sums (one token, 2048 x 10944: gate/up 16 us for 46 MB, down
-// 6 us for 23 MB; a workgroup alone takes
-// 7.6 us) and the rate at which a CU takes load instructions, some 50 cycles each.  Weights through
-// LDS, their scales through LDS or as dwords, 16 wavefronts for gate/up, and loads past the caches were
-// all slower.
+// Bound: the bytes where there are many (64 experts of 2048 x 1408, 96 rows over 56 of them: gate/up 79 us
+// for 333 MB of weights, 4.2 TB/s, but L2 fetches 428 MB, 5.4 TB/s: two loads touch each 128-byte line, and
+// some have left L2 by the second; down 35 us for 167 MB, 4.8 TB/s, fetched once), else the chain
+// of offsets, weights and sums (one token, 2048 x 10944: gate/up 16 us for 46 MB, 61 fetched, down 6 us
+// for 23 MB; a workgroup alone takes 7.6 us) and the rate at which a CU takes load instructions, some 50
+// cycles each.  Weights through LDS, their scales through LDS or as dwords, 16 wavefronts for gate/up,
+// and loads past the caches were all slower.
 //
 // Products are exact: codes are widened to BF16 with the block's scale folded in
 // and multiplied on v_mfma_f32_16x16x32_bf16, which takes, per lane l, 8 values of row
@@ -108,7 +108,7 @@ __device__ __forceinline__ void rows_product(f32x4 (&acc)[R][T], const uint8_t* 
   }
 }
 
-// Waits out the last product before its sums are read: the compiler leaves no wait states between a
+// Waits out the last product before its sums are read: the compiler leaves too few wait states between a
 // matrix instruction at a loop's end and an LDS write of its result behind the loop, and the write
 // took the sums without that product (rows of 36 to 48 blocks over 4 wavefronts: off by 27 %).
 __device__ __forceinline__ void settle(f32x4& acc) { asm volatile("s_nop 15" : "+v"(acc)); }

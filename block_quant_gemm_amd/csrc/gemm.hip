@@ -1243,7 +1243,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& g) {
     // 2048: 324 us, the product alone 191; 2048 x 10944 x 2048: 106 and 65; 1501 rows over 8 experts in
     // FP32 mode 53 and 43).  Of the epilogue's 25 us a turn of tiles some 17 are its instructions and
     // LDS and 8 its memory: 284 us with its reads and writes kept in L2, 315 with the reads alone, 301
-    // with the writes alone.  L2 exchanges 1.48 GB with the memory side, 4.6 TB/s: the loop fetches its 294
+    // with the writes alone.  L2 exchanges 1.48 GB with the memory side, 4.6 TB/s: the loop fetches its 282
     // MB of operands three times.  A lane to a block instead of 4 columns of 8 rows halved the
     // instructions: no exchanges for the largest magnitude, codes four a dword.
     saturate_conversions();
